@@ -36,6 +36,11 @@ __all__ = [
     "spear_debug_mfma_rate",
     "library",
     "SpearError",
+    "spear_kv_cache",
+    "spear_kv_append",
+    "spear_kv_gather",
+    "spear_paged_attention",
+    "spear_verify_draft",
 ]
 
 
@@ -354,3 +359,7 @@ def spear_debug_mfma_rate(shape, waves_per_simd, iterations, sink):
                                          _stream(sink.device), ctypes.byref(flops))
     _binding.check(st, "spear_debug_mfma_rate")
     return flops.value
+
+
+from .serve import (  # noqa: E402,F401
+    spear_kv_cache, spear_kv_append, spear_kv_gather, spear_paged_attention, spear_verify_draft)

@@ -51,6 +51,16 @@ EXPORTS = (
     "spear_debug_mfma_rate",
 )
 
+# Entry points declared in include/spear_serve.h.
+SERVE_EXPORTS = (
+    "spear_kv_append",
+    "spear_kv_gather",
+    "spear_attention_workspace_bytes",
+    "spear_paged_attention",
+    "spear_verify_workspace_bytes",
+    "spear_verify_draft",
+)
+
 
 class LinearDesc(ctypes.Structure):
     _fields_ = [
@@ -83,6 +93,22 @@ class Plan(ctypes.Structure):
 class SchedLayer(ctypes.Structure):
     _fields_ = [("K", ctypes.c_int32), ("N", ctypes.c_int32), ("rank", ctypes.c_int32),
                 ("group_size", ctypes.c_int32), ("weight", ctypes.c_float)]
+
+
+class KvDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class AttentionDesc(ctypes.Structure):
+    _fields_ = [("kv", KvDesc), ("batch", ctypes.c_int32), ("total_q", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("device_cus", ctypes.c_int32)]
+
+
+class VerifyDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_drafts", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("device_cus", ctypes.c_int32)]
 
 
 class SpearError(RuntimeError):
@@ -150,6 +176,21 @@ def load(path=None):
     lib.spear_debug_stream_read.argtypes = [vp, sz, i32, vp, vp]
     lib.spear_debug_mfma_rate.restype = ctypes.c_int
     lib.spear_debug_mfma_rate.argtypes = [i32, i32, i32, vp, vp, ctypes.POINTER(ctypes.c_double)]
+    i64 = ctypes.c_int64
+    lib.spear_kv_append.restype = ctypes.c_int
+    lib.spear_kv_append.argtypes = [ctypes.POINTER(KvDesc), i32, vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, vp, vp]
+    lib.spear_kv_gather.restype = ctypes.c_int
+    lib.spear_kv_gather.argtypes = [ctypes.POINTER(KvDesc), i32, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.spear_attention_workspace_bytes.restype = ctypes.c_int
+    lib.spear_attention_workspace_bytes.argtypes = [ctypes.POINTER(AttentionDesc), ctypes.POINTER(sz)]
+    lib.spear_paged_attention.restype = ctypes.c_int
+    lib.spear_paged_attention.argtypes = [ctypes.POINTER(AttentionDesc), vp, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp,
+                                          vp, vp, sz, vp]
+    lib.spear_verify_workspace_bytes.restype = ctypes.c_int
+    lib.spear_verify_workspace_bytes.argtypes = [ctypes.POINTER(VerifyDesc), ctypes.POINTER(sz)]
+    lib.spear_verify_draft.restype = ctypes.c_int
+    lib.spear_verify_draft.argtypes = [ctypes.POINTER(VerifyDesc), vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, vp, vp,
+                                       vp, sz, vp]
     if path == LIB_PATH:
         _lib = lib
     return lib

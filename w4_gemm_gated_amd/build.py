@@ -23,7 +23,8 @@ LIB_NAME = "libspear_w4ec.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 ARCH = "gfx950"
 
-SOURCES = ["api.cpp", "plan.cpp", "sched.cpp", "pack.hip", "ec_project.hip", "gemm.hip", "skinny.hip", "util.hip", "noalloc.hip", "ec_init.hip"]
+SOURCES = ["api.cpp", "plan.cpp", "sched.cpp", "pack.hip", "ec_project.hip", "gemm.hip", "skinny.hip", "util.hip", "noalloc.hip", "ec_init.hip",
+           "serve_api.cpp", "kv_cache.hip", "paged_attn.hip", "verify.hip"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

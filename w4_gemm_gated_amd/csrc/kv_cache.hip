@@ -1,0 +1,192 @@
+// The paged key/value cache: new tokens written (fp16 as they are, or
+// quantised to 8 bits with one scale per token and head), and sequences read
+// back in fp16.
+//
+// Both kernels are bound by memory: a thread owns eight values of one head
+// (16 bytes of fp16, 8 of codes) of the keys and of the values, so every
+// fp16 access is 16 bytes wide and a head's row is one contiguous run of
+// head_dim / 8 lanes; the keys' and the values' loads are in flight together.
+#include "serve_internal.h"
+#include "device_common.h"
+
+namespace spear {
+namespace {
+
+constexpr int kThreads = 256;
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+struct AppendK {
+  const half_t *k, *v;
+  int64_t k_ts, k_hs, v_ts, v_hs;
+  const int64_t* slots;
+  void *kc, *vc;
+  float *ks, *vs;
+  int64_t units;       // tokens * heads * lanes
+  int64_t num_slots;
+  int32_t heads, page_log2;
+};
+
+// max over the LANES neighbouring lanes that share a head's row; a NaN stays.
+template <int LANES>
+__device__ __forceinline__ float row_max(float x) {
+#pragma unroll
+  for (int o = 1; o < LANES; o *= 2) {
+    const float y = __shfl_xor(x, o);
+    x = (y > x || y != y) ? y : x;
+  }
+  return x;
+}
+
+// Eight fp16 values -> codes, and the row's scale (float32 divisions, so that
+// the codes are the definition's; rint ties to even).
+template <int LANES>
+__device__ __forceinline__ u32x2_t quantise(const half8_t& h, float* scale) {
+  float x[8], m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = (float)h[i];
+    const float a = fabsf(x[i]);
+    m = (a > m || a != a) ? a : m;
+  }
+  m = row_max<LANES>(m);
+  const float s = m / 127.0f;
+  u32x2_t w = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // s = 0, infinite or NaN: code 0 (0 * s is then 0 or NaN)
+    float c = s > 0.0f ? rintf(x[i] / s) : 0.0f;
+    c = c == c ? fminf(fmaxf(c, -127.0f), 127.0f) : 0.0f;
+    w[i / 4] |= ((uint32_t)(int32_t)c & 0xFFu) << (8 * (i % 4));
+  }
+  *scale = s;
+  return w;
+}
+
+// LANES = head_dim / 8 threads per (token, head).  One pass over the rows: a
+// scale needs only its own row, which lies in the LANES threads' registers.
+template <int LANES, bool I8>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendK a) {
+  const int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (u >= a.units) return;   // units is a multiple of LANES: whole rows leave together
+  const int64_t row = u / LANES;
+  const int c = (int)(u % LANES);
+  const int64_t tok = row / a.heads;
+  const int head = (int)(row % a.heads);
+  const int64_t slot = a.slots[tok];
+  const half8_t kx = load_half8(a.k + tok * a.k_ts + head * a.k_hs + 8 * c);
+  const half8_t vx = load_half8(a.v + tok * a.v_ts + head * a.v_hs + 8 * c);
+  if (slot < 0 || slot >= a.num_slots) return;
+  const int64_t page = slot >> a.page_log2, place = slot & ((1 << a.page_log2) - 1);
+  const int64_t at = ((page * a.heads + head) << a.page_log2) + place;   // row of the cache
+  if constexpr (I8) {
+    float ks, vs;
+    const u32x2_t kw = quantise<LANES>(kx, &ks), vw = quantise<LANES>(vx, &vs);
+    ((u32x2_t*)a.kc)[at * LANES + c] = kw;
+    ((u32x2_t*)a.vc)[at * LANES + c] = vw;
+    if (c == 0) {
+      a.ks[at] = ks;
+      a.vs[at] = vs;
+    }
+  } else {
+    ((half8_t*)a.kc)[at * LANES + c] = kx;
+    ((half8_t*)a.vc)[at * LANES + c] = vx;
+  }
+}
+
+struct GatherK {
+  const int32_t *table, *cu;
+  int64_t table_stride;
+  const void *kc, *vc;
+  const float *ks, *vs;
+  half8_t *ko, *vo;
+  int64_t units;       // rows * heads * lanes
+  int32_t batch, rows, heads, page_log2, num_pages;
+};
+
+__device__ __forceinline__ half8_t dequantise(const u32x2_t& w, float s) {
+  half8_t h;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = (half_t)((float)(int8_t)(w[i / 4] >> (8 * (i % 4))) * s);
+  return h;
+}
+
+// A workgroup's rows belong to few sequences: its first row's is counted by the
+// whole wave (the rising entries of cu not above it), and a thread steps on
+// from there.
+template <int LANES, bool I8>
+__global__ void __launch_bounds__(kThreads) kv_gather_kernel(GatherK a) {
+  const int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int first = (int)((int64_t)blockIdx.x * kThreads / LANES / a.heads);
+  int b = -1;
+  for (int i = 0; i <= a.batch; i += kWave) {
+    const int j = i + (int)threadIdx.x % kWave;
+    b += __popcll(__ballot(j <= a.batch && a.cu[j] <= first));
+  }
+  if (u >= a.units) return;
+  const int row = (int)(u / LANES / a.heads);
+  const int head = (int)(u / LANES % a.heads), c = (int)(u % LANES);
+  while (b < a.batch && a.cu[b + 1] <= row) ++b;
+  half8_t kx = zero_half8(), vx = zero_half8();
+  if (b >= 0 && b < a.batch) {
+    const int i = row - a.cu[b];
+    const int64_t entry = min((int64_t)(i >> a.page_log2), a.table_stride - 1);
+    const uint32_t page = min((uint32_t)a.table[b * a.table_stride + entry], (uint32_t)a.num_pages - 1);
+    const int64_t at = (((int64_t)page * a.heads + head) << a.page_log2) + (i & ((1 << a.page_log2) - 1));
+    if constexpr (I8) {
+      kx = dequantise(((const u32x2_t*)a.kc)[at * LANES + c], a.ks[at]);
+      vx = dequantise(((const u32x2_t*)a.vc)[at * LANES + c], a.vs[at]);
+    } else {
+      kx = ((const half8_t*)a.kc)[at * LANES + c];
+      vx = ((const half8_t*)a.vc)[at * LANES + c];
+    }
+  }
+  a.ko[u] = kx;
+  a.vo[u] = vx;
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const KvAppendArgs& a, void* stream) {
+  AppendK k;
+  k.k = (const half_t*)a.k; k.v = (const half_t*)a.v;
+  k.k_ts = a.k_ts; k.k_hs = a.k_hs; k.v_ts = a.v_ts; k.v_hs = a.v_hs;
+  k.slots = a.slots;
+  k.kc = a.k_cache; k.vc = a.v_cache; k.ks = a.k_scale; k.vs = a.v_scale;
+  k.units = (int64_t)a.tokens * a.kv.heads * (a.kv.dim / 8);
+  k.num_slots = (int64_t)a.kv.num_pages << a.kv.page_log2;
+  k.heads = a.kv.heads; k.page_log2 = a.kv.page_log2;
+  const dim3 grid((unsigned)ceil_div(k.units, kThreads)), block(kThreads);
+  const hipStream_t st = (hipStream_t)stream;
+  const bool i8 = a.kv.dtype == SPEAR_KV_INT8;
+  if (a.kv.dim == 64) {
+    if (i8) kv_append_kernel<8, true><<<grid, block, 0, st>>>(k);
+    else kv_append_kernel<8, false><<<grid, block, 0, st>>>(k);
+  } else {
+    if (i8) kv_append_kernel<16, true><<<grid, block, 0, st>>>(k);
+    else kv_append_kernel<16, false><<<grid, block, 0, st>>>(k);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_gather(const KvGatherArgs& a, void* stream) {
+  GatherK k;
+  k.table = a.table; k.cu = a.cu; k.table_stride = a.table_stride;
+  k.kc = a.k_cache; k.vc = a.v_cache; k.ks = a.k_scale; k.vs = a.v_scale;
+  k.ko = (half8_t*)a.k_out; k.vo = (half8_t*)a.v_out;
+  k.units = (int64_t)a.rows * a.kv.heads * (a.kv.dim / 8);
+  k.batch = a.batch; k.rows = a.rows; k.heads = a.kv.heads;
+  k.page_log2 = a.kv.page_log2; k.num_pages = a.kv.num_pages;
+  const dim3 grid((unsigned)ceil_div(k.units, kThreads)), block(kThreads);
+  const hipStream_t st = (hipStream_t)stream;
+  const bool i8 = a.kv.dtype == SPEAR_KV_INT8;
+  if (a.kv.dim == 64) {
+    if (i8) kv_gather_kernel<8, true><<<grid, block, 0, st>>>(k);
+    else kv_gather_kernel<8, false><<<grid, block, 0, st>>>(k);
+  } else {
+    if (i8) kv_gather_kernel<16, true><<<grid, block, 0, st>>>(k);
+    else kv_gather_kernel<16, false><<<grid, block, 0, st>>>(k);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace spear

@@ -1,0 +1,85 @@
+// Internal interfaces of the serving operators (paged key/value cache, paged
+// attention, draft verification): launch arguments shared by serve_api.cpp and
+// the kernels.  Not installed; not part of the ABI.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <hip/hip_runtime_api.h>
+
+#include "../../include/spear_serve.h"
+#include "internal.h"
+
+namespace spear {
+
+struct KvShape {
+  int32_t dtype, num_pages, heads, dim, page_log2;
+};
+
+struct KvAppendArgs {
+  KvShape kv;
+  int32_t tokens;
+  const void *k, *v;
+  int64_t k_ts, k_hs, v_ts, v_hs;   // strides in elements
+  const int64_t* slots;
+  void *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+};
+hipError_t launch_kv_append(const KvAppendArgs& a, void* stream);
+
+struct KvGatherArgs {
+  KvShape kv;
+  int32_t batch, rows;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* cu;
+  const void *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  void *k_out, *v_out;
+};
+hipError_t launch_kv_gather(const KvGatherArgs& a, void* stream);
+
+// Launch shape of an attention call.
+struct AttnPlan {
+  int row_tiles;     // 16-row tiles a workgroup holds (1 or 2)
+  int target;        // split items aimed at, over all kv heads
+  int min_chunk;     // fewest keys of a split item
+  int grid;          // workgroups of the main launch
+  int combine_grid;  // workgroups of the launch that joins split items; 0: nothing can be split
+  size_t part;       // byte offset of the partial results in the workspace
+  size_t bytes;      // workspace (0: none)
+};
+AttnPlan attn_plan(const spear_attention_desc_t& d, int cus);
+
+struct AttnArgs {
+  KvShape kv;
+  int32_t batch, total_q, q_heads, group, max_kv;
+  float scale;
+  const void* q;
+  int64_t q_ts, q_hs;
+  const int32_t *cu_q, *kv_lens, *table;
+  int64_t table_stride;
+  const void *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  void* out;
+  float* part;
+};
+hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* stream);
+
+// Workgroups that share one sequence's vocabulary in a verification call.
+int verify_splits(const spear_verify_desc_t& d, int cus);
+struct VerifyArgs {
+  int32_t batch, drafts, vocab, splits;
+  const float *target, *draft;
+  int64_t target_bs, target_rs, draft_bs, draft_rs;
+  const int32_t* drafted;
+  const float *u, *noise;
+  const int32_t* num_drafts;
+  int32_t *accepted, *tokens;
+  uint32_t* counters;   // [batch], zero before and after
+  uint64_t* part;       // [batch][splits]
+};
+hipError_t launch_verify(const VerifyArgs& a, void* stream);
+
+}  // namespace spear
