@@ -104,9 +104,9 @@ typedef struct spear_attention_desc {
 
 /*
  * spear_attention_workspace_bytes -- device workspace of a call (host only).
- * The workspace is one of spear_w4ec_linear's kind: its 1 MiB header is left
- * as it is, the scratch after it needs no clearing, and calls that run
- * concurrently must not share it.
+ * The workspace is one of spear_w4ec_linear's kind: zero-filled before its first
+ * use, its 1 MiB header's counters returned to zero by the call, the rest
+ * scratch; calls that run concurrently must not share it.
  * Errors: NULL_POINTER, INVALID_SHAPE, INVALID_ARGUMENT, UNSUPPORTED, HIP.
  */
 spear_status_t spear_attention_workspace_bytes(const spear_attention_desc_t* desc, size_t* bytes);

@@ -27,11 +27,14 @@
 // above the scales that the row has seen so far (moved the same way), so that
 // the fp16 weights keep their range.
 //
-// Long sequences with few rows are split over workgroups.  The lengths are on
-// the device, so every workgroup finds its item by itself: the chunk length
-// follows from the total work and the GPU's size, and a scan over the
-// sequences locates the item (64 sequences a step).  Split items leave their
-// sums in the workspace in fp32; a second launch joins them in order.
+// The work is laid end to end, in steps of one key tile per wave, head after
+// head, sequence after sequence, and cut into equal shares, one per workgroup,
+// however the lengths differ.  The lengths are on the device, so every
+// workgroup finds its share by itself with a scan over the sequences (64 a
+// step).  A row tile that several workgroups share leaves one partial result
+// (fp32) per workgroup in the workspace; the last of them to arrive joins them
+// in order, so the result does not depend on scheduling.  Data passes between
+// workgroups as everywhere here: device-coherent stores, a drain, a counter.
 #include "serve_internal.h"
 #include "device_common.h"
 
@@ -54,109 +57,114 @@ struct AttnK {
   const void *kc, *vc;
   const float *ks, *vs;
   half_t* out;
-  float* part;
+  float* part;          // [2 x workgroups] partial results
+  uint32_t* counters;   // [workgroups], zero before and after
   int32_t batch, total_q, q_heads, kv_heads, group, max_kv, page_log2, num_pages;
-  int32_t target, min_chunk;   // per kv head
+  int32_t part_bytes;
   float scale;                 // scale * log2(e)
 };
 
 // ------------------------------------------------------------- the schedule
 
 struct Seq {
-  int q0, n, kv, tiles;   // first row of q, new tokens, cached tokens, row tiles
+  int q0, n, kv, tiles, steps;   // first row of q, new tokens, cached tokens, row tiles, steps of each
 };
 
-template <int R>
+// R rows a tile, KS keys a step.
+template <int R, int KS>
 __device__ __forceinline__ Seq sequence(const AttnK& a, int b) {
-  Seq s = {0, 0, 0, 0};
+  Seq s = {0, 0, 0, 0, 1};
   if (b < a.batch) {
-    s.q0 = min(max(a.cu[b], 0), a.total_q);
-    s.n = min(max(a.cu[b + 1], s.q0), a.total_q) - s.q0;
-    s.kv = min(max(a.lens[b], 0), a.max_kv);
-    s.tiles = (int)(((int64_t)s.n * a.group + R - 1) / R);
+    const int c0 = a.cu[b], c1 = a.cu[b + 1], len = a.lens[b];
+    s.q0 = min(max(c0, 0), a.total_q);
+    s.n = min(max(c1, s.q0), a.total_q) - s.q0;
+    s.kv = min(max(len, 0), a.max_kv);
+    s.tiles = (s.n * a.group + R - 1) / R;
+    s.steps = max((s.kv + KS - 1) / KS, 1);
   }
   return s;
 }
 
-__device__ __forceinline__ int64_t wave_sum(int64_t x) {
-#pragma unroll
-  for (int o = 1; o < kWave; o *= 2) x += __shfl_xor(x, o);
-  return x;
-}
-__device__ __forceinline__ int wave_scan(int x, int lane) {
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x, int lane) {
 #pragma unroll
   for (int o = 1; o < kWave; o *= 2) {
-    const int y = __shfl_up(x, o);
+    const uint32_t y = __shfl_up(x, o);
     if (lane >= o) x += y;
   }
   return x;
 }
 
-// Keys of a split item: the whole work over the items aimed at, whole rounds
-// of the four waves.
-template <int R, int KT>
-__device__ __forceinline__ int chunk_keys(const AttnK& a, int lane) {
-  int64_t work = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kWave) {
-    const Seq s = sequence<R>(a, b0 + lane);
-    work += (int64_t)s.tiles * s.kv;
-  }
-  work = wave_sum(work);
-  const int64_t c = (work + a.target - 1) / a.target;
-  const int64_t most = c > a.min_chunk ? c : a.min_chunk;
-  return (int)min((most + KT * kWaves - 1) / (KT * kWaves) * (KT * kWaves), (int64_t)1 << 30);
+// A value that all lanes hold alike, moved to a scalar register: addresses and
+// bounds made of it then are scalar too (a division leaves it in a vector one).
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
+
+// A buffer resource in scalar registers.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t p = (uint64_t)base;
+  return make_rsrc((const void*)((uint64_t)uniform((uint32_t)(p >> 32)) << 32 | uniform((uint32_t)p)), uniform(bytes));
 }
 
-__device__ __forceinline__ int pieces(int kv, int chunk) { return kv > chunk ? (kv + chunk - 1) / chunk : 1; }
-
-// What one item covers.  COUNT 0: items of the main launch (index = row tile x
-// piece); 1: rows of split sequences (the joining launch).  The first partial
-// slot of the sequence and of its pieces counts split sequences only.
-struct Item {
-  int b, q0, n, kv, at, pieces, slot;   // at: index within the sequence
-  bool found;
+// Equal shares of n steps for w workgroups: the first `more` take one step more.
+struct Shares {
+  uint32_t each, more;
+  __device__ uint32_t begin(uint32_t w) const { return w * each + min(w, more); }
+  __device__ uint32_t owner(uint32_t s) const {
+    const uint32_t head = more * (each + 1);
+    return s < head ? s / (each + 1) : more + (s - head) / each;
+  }
 };
-template <int R, int COUNT>
-__device__ __forceinline__ Item find(const AttnK& a, int chunk, int index, int lane) {
-  Item it;
-  it.found = false;
-  int before = 0, slots = 0;
+
+// The row tile that holds step p of a head's steps.
+struct Unit {
+  int b, q0, n, kv, steps, rt;
+  uint32_t first;   // its first step within the head
+};
+// `s0` holds the lanes' sequences of the first 64.
+template <int R, int KS>
+__device__ __forceinline__ Unit find(const AttnK& a, const Seq& s0, uint32_t p, int lane) {
+  Unit u = {0, 0, 0, 0, 1, 0, 0};
+  uint32_t before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += kWave) {
-    const Seq s = sequence<R>(a, b0 + lane);
-    const int np = pieces(s.kv, chunk);
-    const int split = np > 1 ? s.tiles * np : 0;
-    const int mine = COUNT == 0 ? s.tiles * np : np > 1 ? s.n * a.group : 0;
-    const int upto = before + wave_scan(mine, lane);
-    const uint64_t past = __ballot(upto > index);
-    const int slot_upto = slots + wave_scan(split, lane);
+    const Seq s = b0 == 0 ? s0 : sequence<R, KS>(a, b0 + lane);
+    const uint32_t mine = (uint32_t)s.tiles * (uint32_t)s.steps;
+    const uint32_t upto = before + wave_scan(mine, lane);
+    const uint64_t past = __ballot(upto > p);
     if (past) {
       const int l = __builtin_ctzll(past);
-      it.found = true;
-      it.b = b0 + l;
-      it.q0 = __shfl(s.q0, l);
-      it.n = __shfl(s.n, l);
-      it.kv = __shfl(s.kv, l);
-      it.pieces = __shfl(np, l);
-      it.at = index - __shfl(upto - mine, l);
-      it.slot = __shfl(slot_upto - split, l);
+      u.b = b0 + l;
+      u.q0 = __builtin_amdgcn_readlane(s.q0, l);
+      u.n = __builtin_amdgcn_readlane(s.n, l);
+      u.kv = __builtin_amdgcn_readlane(s.kv, l);
+      u.steps = __builtin_amdgcn_readlane(s.steps, l);
+      const uint32_t start = (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), l);
+      u.rt = (int)uniform((p - start) / (uint32_t)u.steps);
+      u.first = start + (uint32_t)u.rt * (uint32_t)u.steps;
       break;
     }
-    before = __shfl(upto, kWave - 1);
-    slots = __shfl(slot_upto, kWave - 1);
+    before = (uint32_t)__builtin_amdgcn_readlane((int)upto, kWave - 1);
   }
-  return it;
+  return u;
 }
 
 // -------------------------------------------------------------- small pieces
 
-// Over the four lanes (c, 0..3) that hold row c.
+// Over the four lanes (c, 0..3) that hold row c: swaps of 16- and 32-lane halves
+// (each returns the two halves' values in both).
+typedef uint32_t pair_t __attribute__((ext_vector_type(2)));
+template <typename F>
+__device__ __forceinline__ float over_row(float x, F f) {
+  const uint32_t v = float_bits(x);
+  const pair_t a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  const uint32_t w = float_bits(f(bits_float(a.x), bits_float(a.y)));
+  const pair_t b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  return f(bits_float(b.x), bits_float(b.y));
+}
 __device__ __forceinline__ float row_max4(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16));
-  return fmaxf(x, __shfl_xor(x, 32));
+  return over_row(x, [](float a, float b) { return fmaxf(a, b); });
 }
 __device__ __forceinline__ float row_sum4(float x) {
-  x += __shfl_xor(x, 16);
-  return x + __shfl_xor(x, 32);
+  return over_row(x, [](float a, float b) { return a + b; });
 }
 
 // Codes b0 and b1 (bytes i of two words, sign included) -> two fp16 values.
@@ -175,6 +183,8 @@ __device__ __forceinline__ half8_t codes_to_half8(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(half8_t, r);
 }
 
+typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(4))) int32_t scalar_i32_t;
 template <int BYTES> struct Vec;
 template <> struct Vec<4> { typedef uint32_t type __attribute__((ext_vector_type(1))); };
 template <> struct Vec<8> { typedef uint32_t type __attribute__((ext_vector_type(2))); };
@@ -184,52 +194,178 @@ __device__ __forceinline__ bool half2_not_finite(uint32_t w) {
   return (w & 0x7C00u) == 0x7C00u || (w & 0x7C000000u) == 0x7C000000u;
 }
 
+// An fp16 number's kind as an fp16 number: 0 finite, 1 infinity, 64 -infinity,
+// 4096 NaN.
+__device__ __forceinline__ uint32_t kind_of(uint32_t h) {
+  if ((h & 0x7C00u) != 0x7C00u) return 0u;
+  return (h & 0x03FFu) ? 0x6C00u : (h & 0x8000u) ? 0x5400u : 0x3C00u;
+}
+
 // ------------------------------------------------------------ the main kernel
 
+// Lanes' 4, 8 or 16 bytes of a buffer.
+template <int BYTES>
+__device__ __forceinline__ typename Vec<BYTES>::type buffer_vec(__amdgpu_buffer_rsrc_t r, uint32_t offset) {
+  typedef typename Vec<BYTES>::type vec_t;
+  if constexpr (BYTES == 4) return vec_t{(uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, offset, 0, 0)};
+  else if constexpr (BYTES == 8) return __builtin_bit_cast(vec_t, __builtin_amdgcn_raw_buffer_load_b64(r, offset, 0, 0));
+  else return __builtin_bit_cast(vec_t, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0));
+}
+
 template <int D, bool I8, int RT>
-__global__ void __launch_bounds__(kThreads) attn_kernel(AttnK a) {
-  constexpr int R = 16 * RT;
-  constexpr int KT = I8 ? 64 : 32;            // keys of a wave's tile: the same bytes in flight
+struct Shape {
+  static constexpr int R = 16 * RT;
+  static constexpr int KT = 32;                  // keys of a wave's tile
+  static constexpr int KS = KT * kWaves;         // keys of a step
+  static constexpr int SLOT = R * (D + 2);       // floats of a partial result: sums [R][D], references, totals
+};
+
+// Joins the `pieces` partial results of a row tile (rows `rows_here` of them in
+// use) and writes the result.  Threads take four columns of a row each; with few
+// columns, several groups of threads take every so many pieces.  Loads of
+// eight pieces are in flight together.
+template <int D, int R, int SLOT>
+__device__ __forceinline__ void join(const AttnK& a, float* lds, int rows_here, int r0, int q0, int head, uint32_t w0,
+                                     int pieces) {
+  const __amdgpu_buffer_rsrc_t pr = make_rsrc(a.part, (uint32_t)a.part_bytes);
+  const int cols = rows_here * (D / 4);
+  const int groups = cols < kThreads ? kThreads / cols : 1;
+  constexpr int BATCH = 8;
+  for (int c0 = 0; c0 < cols; c0 += kThreads) {
+    const int col = groups > 1 ? (int)threadIdx.x % cols : c0 + (int)threadIdx.x;
+    const int grp = groups > 1 ? (int)threadIdx.x / cols : 0;
+    const bool on = col < cols && grp < groups;
+    const int row = col / (D / 4), d = col % (D / 4) * 4;
+    float M = kNone, sum = 0.0f;
+    float4_t o = zero_float4();
+    if (on) {
+      for (int i0 = grp; i0 < pieces; i0 += BATCH * groups) {
+        float4_t po[BATCH];
+        float pm[BATCH], pl[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int piece = i0 + i * groups;
+          // the first piece is its workgroup's second result, the others first ones
+          const uint32_t slot = 2 * (w0 + (uint32_t)piece) + (piece == 0 ? 1u : 0u);
+          const uint32_t at = piece < pieces ? slot * (uint32_t)(SLOT * 4) : kOutOfRange;
+          po[i] = buffer_load_f4_dev(pr, at + (uint32_t)(row * D + d) * 4);
+          pm[i] = bits_float(__builtin_amdgcn_raw_buffer_load_b32(pr, at + (uint32_t)(R * D + row) * 4, 0, kCachePolicySc1));
+          pl[i] = bits_float(__builtin_amdgcn_raw_buffer_load_b32(pr, at + (uint32_t)(R * D + R + row) * 4, 0, kCachePolicySc1));
+        }
+        float to = M;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          if (i0 + i * groups >= pieces) pm[i] = kNone;   // its sums read as zero
+          to = fmaxf(to, pm[i]);
+        }
+        const float f = __builtin_amdgcn_exp2f(M - to);
+        M = to;
+        sum *= f;
+        o *= f;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const float g = __builtin_amdgcn_exp2f(pm[i] - M);
+          sum += pl[i] * g;
+          o += po[i] * g;
+        }
+      }
+    }
+    if (groups > 1) {
+      float* mine = lds + threadIdx.x * 8;
+      *(float4_t*)mine = o;
+      mine[4] = M;
+      mine[5] = sum;
+      __syncthreads();
+      if (on && grp == 0) {
+        for (int g = 1; g < groups; ++g) {
+          const float* other = lds + (threadIdx.x + g * cols) * 8;
+          const float to = fmaxf(M, other[4]);
+          const float f = __builtin_amdgcn_exp2f(M - to), e = __builtin_amdgcn_exp2f(other[4] - to);
+          sum = sum * f + other[5] * e;
+          o = o * f + *(const float4_t*)other * e;
+          M = to;
+        }
+      }
+    }
+    if (on && grp == 0) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // nothing seen: zeros
+      half4_t h;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[k] = (half_t)(o[k] * inv);
+      const int r = r0 + row;
+      *(half4_t*)(a.out + ((q0 + (int64_t)(r / a.group)) * a.q_heads + head * a.group + r % a.group) * D + d) = h;
+    }
+  }
+}
+
+template <int D, bool I8, int RT>
+__global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a) {
+  typedef Shape<D, I8, RT> S;
+  constexpr int R = S::R, KT = S::KT, KS = S::KS, SLOT = S::SLOT;
   constexpr int NS = KT / 16;                 // 16-key tiles
   constexpr int NG = KT / 32;                 // 32-key groups
   constexpr int E = I8 ? 1 : 2;               // bytes of a cached value
+  constexpr int RB = D * E;                   // bytes of a cached row
   constexpr int NM = D / 32;                  // matrix instructions along d
-  constexpr int KL = D * E / 64;              // 16-byte K loads of a lane and 16-key tile
+  constexpr int KL = RB / 64;                 // 16-byte K loads of a lane and 16-key tile
   constexpr int DL = D / 16;                  // d values of a lane's V load
   typedef typename Vec<DL * E>::type vvec_t;
   constexpr int OS = D + 4;                   // row stride of the sums in LDS
-  __shared__ float s_o[kWaves][R][OS];
+  __shared__ __attribute__((aligned(16))) float s_o[kWaves][R][OS];
   __shared__ float s_m[kWaves][R], s_l[kWaves][R];
+  __shared__ uint32_t s_arrived;
+  static_assert(sizeof(s_o) >= kThreads * 32, "the join's exchange fits");
 
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane % 16, t = lane / 16;
-  const int head = blockIdx.x % a.kv_heads;
-  const int chunk = chunk_keys<R, KT>(a, lane);
 
-  for (int index = blockIdx.x / a.kv_heads;; index += gridDim.x / a.kv_heads) {
-    const Item it = find<R, 0>(a, chunk, index, lane);
-    if (!it.found) break;
-    const int rt = it.at / it.pieces, piece = it.at % it.pieces;
-    const int rows = it.n * a.group;                     // of the sequence
-    const int r0 = rt * R;
-    const int first_tok = r0 / a.group;
-    const int last_tok = min(r0 + R, rows) - 1 >= 0 ? (min(r0 + R, rows) - 1) / a.group : 0;
-    const int pos0 = it.kv - it.n;                       // position of token 0
-    const int see_all = min(pos0 + first_tok + 1, it.kv);          // keys below this are seen by every row
-    const int k_end = min(max(pos0 + last_tok + 1, 0), it.kv);     // .. from this on by none
-    const int k0 = piece * chunk;
-    const int k1 = it.pieces == 1 ? k_end : min(k0 + chunk, k_end);
+  // This workgroup's share.
+  const Seq seq0 = sequence<R, KS>(a, lane);
+  uint32_t per_head = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kWave) {
+    const Seq s = b0 == 0 ? seq0 : sequence<R, KS>(a, b0 + lane);
+    per_head += (uint32_t)s.tiles * (uint32_t)s.steps;
+  }
+#pragma unroll
+  for (int o = 1; o < kWave; o *= 2) per_head += __shfl_xor(per_head, o);
+  per_head = uniform(per_head);
+  const uint32_t total = per_head * (uint32_t)a.kv_heads;
+  const uint32_t groups = min((uint32_t)gridDim.x, total);
+  if (blockIdx.x >= groups) return;
+  const uint32_t each = uniform(total / groups);
+  const Shares shares = {each, total - each * groups};
+  uint32_t at = shares.begin(blockIdx.x);
+  const uint32_t end = shares.begin(blockIdx.x + 1);
 
-    // Queries as B operands; the k order follows the K loads' below.
+  const int place_mask = (1 << a.page_log2) - 1;
+  const uint32_t koff = (uint32_t)(c * RB + 16 * t), voff = (uint32_t)(4 * t * RB + c * (DL * E));
+
+  while (at < end) {
+    const int head = (int)uniform(at / per_head);
+    const Unit u = find<R, KS>(a, seq0, at - (uint32_t)head * per_head, lane);
+    const uint32_t unit0 = (uint32_t)head * per_head + u.first;    // its first step of all
+    const int step0 = (int)(at - unit0);
+    const int step1 = (int)min((uint32_t)u.steps, end - unit0);
+    at = unit0 + (uint32_t)step1;
+    const int rows = u.n * a.group;                                // of the sequence
+    const int r0 = u.rt * R;
+    const int rows_here = min(R, rows - r0);
+    const int pos0 = u.kv - u.n;                                   // position of token 0
+    const int see_all = uniform(min(pos0 + r0 / a.group + 1, u.kv));   // keys below this are seen by every row
+    const int k1 = uniform(min(max(pos0 + (r0 + rows_here - 1) / a.group + 1, 0), u.kv));   // .. from this on by none
+    const int k_stop = min(k1, step1 * KS);                        // this workgroup's keys end here
+
+    // Queries as B operands; the k order follows the K loads'.
     half8_t qf[RT][NM];
-    int lim[RT];                                         // keys below this are seen by the lane's row
+    int lim[RT];                                                   // keys below this are seen by the lane's row
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
       const int r = r0 + 16 * x + c;
-      const int tok = r / a.group, h = head * a.group + r % a.group;
       const bool ok = r < rows;
-      lim[x] = ok ? pos0 + tok + 1 : k_end;
-      const half_t* qp = a.q + (it.q0 + (int64_t)(ok ? tok : 0)) * a.q_ts + (ok ? h : 0) * a.q_hs;
+      const int tok = ok ? r / a.group : 0, h = ok ? head * a.group + r % a.group : 0;
+      lim[x] = ok ? min(pos0 + tok + 1, k1) : k1;
+      const half_t* qp = a.q + (u.q0 + (int64_t)tok) * a.q_ts + h * a.q_hs;
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
         const int d = I8 ? 64 * (m / 2) + 16 * t + 8 * (m % 2) : 32 * m + 8 * t;
@@ -248,37 +384,69 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnK a) {
       for (int j = 0; j < DL; ++j) acc[x][j] = zero_float4();
     }
 
-    const int32_t* table = a.table + (int64_t)it.b * a.table_stride;
-    const int place_mask = (1 << a.page_log2) - 1;
-    for (int base = k0 + wave * KT; base < k1; base += kWaves * KT) {
-      // Loads.  A 16-key tile lies within one page; tiles past the end read
-      // the last page that holds keys.
-      u32x4_t kr[NS][KL];
-      vvec_t vr[NG][8];
-      float4_t ksc[NS], vsc[NS];
-      const unsigned char* vbase[NS];
+    // Memory: a 16-key tile lies within one page, so its place is the same for
+    // all lanes.  Rows from k1 on lie outside the buffer and read as zeros; a
+    // tile past the share reads nothing.
+    // (constant address space and a scalar index: scalar loads, which the waits
+    // for keys and values do not count)
+    const scalar_i32_t* table = (const scalar_i32_t*)(uintptr_t)(a.table + (int64_t)uniform(u.b) * a.table_stride);
+    const int last_key = max(k1 - 1, 0);
+    auto page_of = [&](int key) {
+      return (uint32_t)table[uniform(min(key, last_key) >> a.page_log2)];
+    };
+    const int64_t head_row = (int64_t)head << a.page_log2;
+    const unsigned char* kc = (const unsigned char*)a.kc + head_row * RB;
+    const unsigned char* vc = (const unsigned char*)a.vc + head_row * RB;
+    const float* ks = I8 ? a.ks + head_row : nullptr;
+    const float* vs = I8 ? a.vs + head_row : nullptr;
+    const uint32_t page_rows = (uint32_t)a.kv_heads << a.page_log2;
+    u32x4_t kr[NS][KL];
+    vvec_t vr[NG][8];
+    float4_t ksc[NS], vsc[NS];
+    uint32_t page[NS], later_page[NS];   // of the tile requested next, and of the one after it
+    // Bytes of a 16-key tile's rows that hold keys of this workgroup's share.
+    auto load_k = [&](int base, const uint32_t* pages) {
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
-        const int key = min(base + 16 * n, (k1 - 1) & ~15);
-        const uint32_t page = min((uint32_t)table[key >> a.page_log2], (uint32_t)a.num_pages - 1);
-        const int64_t row = (((int64_t)page * a.kv_heads + head) << a.page_log2) + (key & place_mask);
-        const unsigned char* kb = (const unsigned char*)a.kc + row * (D * E);
-        vbase[n] = (const unsigned char*)a.vc + row * (D * E);
+        const int key = base + 16 * n;
+        const uint64_t row = (uint64_t)min(pages[n], (uint32_t)a.num_pages - 1) * page_rows + (uint32_t)(key & place_mask);
+        const uint32_t rows = base < k_stop ? (uint32_t)min(max(k1 - key, 0), 16) : 0u;
+        const __amdgpu_buffer_rsrc_t r = uniform_rsrc(kc + row * RB, rows * RB);
 #pragma unroll
-        for (int i = 0; i < KL; ++i) kr[n][i] = *(const u32x4_t*)(kb + c * (D * E) + 64 * i + 16 * t);
-        if constexpr (I8) {
-          ksc[n] = *(const float4_t*)(a.ks + row + 4 * t);
-          vsc[n] = *(const float4_t*)(a.vs + row + 4 * t);
-        }
+        for (int i = 0; i < KL; ++i) kr[n][i] = buffer_vec<16>(r, koff + 64 * i);
+        if constexpr (I8) ksc[n] = __builtin_bit_cast(float4_t, buffer_vec<16>(uniform_rsrc(ks + row, rows ? 64u : 0u), 16 * t));
       }
+    };
+    auto load_v = [&](int base, const uint32_t* pages) {
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+      for (int n = 0; n < NS; ++n) {
+        const int key = base + 16 * n;
+        const uint64_t row = (uint64_t)min(pages[n], (uint32_t)a.num_pages - 1) * page_rows + (uint32_t)(key & place_mask);
+        const uint32_t rows = base < k_stop ? (uint32_t)min(max(k1 - key, 0), 16) : 0u;
+        const __amdgpu_buffer_rsrc_t r = uniform_rsrc(vc + row * RB, rows * RB);
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-          vr[g][s] = *(const vvec_t*)(vbase[2 * g + s / 4] + (4 * t + s % 4) * (D * E) + c * (DL * E));
+        for (int s = 0; s < 4; ++s) vr[n / 2][4 * (n % 2) + s] = buffer_vec<DL * E>(r, voff + s * RB);
+        if constexpr (I8) vsc[n] = __builtin_bit_cast(float4_t, buffer_vec<16>(uniform_rsrc(vs + row, rows ? 64u : 0u), 16 * t));
+      }
+    };
 
-      // Scores.
+    int base = (step0 * kWaves + wave) * KT;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) page[n] = page_of(base + 16 * n);
+#pragma unroll
+    for (int n = 0; n < NS; ++n) later_page[n] = page_of(base + KS + 16 * n);
+    // (the order is that of the loop: with another one the compiler's wait for
+    // the keys at its top would also wait for the values)
+    load_k(base, page);
+    __builtin_amdgcn_sched_barrier(0);
+    load_v(base, page);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < NS; ++n) page[n] = later_page[n];
+    for (; base < k_stop; base += KS) {
+      // Scores; the next tile's keys are requested as soon as these are used.
       float4_t st[RT][NS];
+      float4_t kscale[NS];
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
 #pragma unroll
@@ -291,8 +459,15 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnK a) {
 #pragma unroll
           for (int x = 0; x < RT; ++x) st[x][n] = mfma16x16x32(kf, qf[x][m], st[x][n]);
         }
+        if constexpr (I8) kscale[n] = ksc[n] * a.scale;
       }
-      const bool edge = base + KT > min(see_all, k1);
+      __builtin_amdgcn_sched_barrier(0);
+      load_k(base + KS, page);
+#pragma unroll
+      for (int n = 0; n < NS; ++n) later_page[n] = page_of(base + 2 * KS + 16 * n);
+      __builtin_amdgcn_sched_barrier(0);
+
+      const bool edge = base + KT > see_all;
       float top[RT], vmax[RT];
       bool move = false;
 #pragma unroll
@@ -305,7 +480,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnK a) {
           for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const bool out = vsc[n][i] > kMaxScale || (edge && base + 16 * n + 4 * t + i >= min(lim[x], k1));
+              const bool out = vsc[n][i] > kMaxScale || (edge && base + 16 * n + 4 * t + i >= lim[x]);
               vmax[x] = fmaxf(vmax[x], out ? 0.0f : vsc[n][i]);
             }
           vmax[x] = row_max4(vmax[x]);
@@ -316,9 +491,10 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnK a) {
         for (int n = 0; n < NS; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float s = st[x][n][i] * a.scale;
-            if constexpr (I8) s *= ksc[n][i];
-            if (edge && base + 16 * n + 4 * t + i >= min(lim[x], k1)) s = -INFINITY;
+            float s = st[x][n][i];
+            if constexpr (I8) s *= kscale[n][i];
+            else s *= a.scale;
+            if (edge && base + 16 * n + 4 * t + i >= lim[x]) s = -INFINITY;
             st[x][n][i] = s;
             top[x] = fmaxf(top[x], s);
           }
@@ -344,7 +520,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnK a) {
           for (int j = 0; j < DL; ++j) acc[x][j] *= f * vscale;
         }
       }
-      // Weights (B operands) and, for V's edge, which lanes see which keys.
+      // Weights (B operands).
       half8_t pf[RT][NG];
 #pragma unroll
       for (int x = 0; x < RT; ++x) {
@@ -358,7 +534,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnK a) {
             l[x] += p;
             if constexpr (I8) {
               const float w = p * (vsc[n][i] * vinv);
-              p = edge && base + 16 * n + 4 * t + i >= min(lim[x], k1) ? 0.0f : w;
+              p = edge && base + 16 * n + 4 * t + i >= lim[x] ? 0.0f : w;
             }
             pf[x][n / 2][4 * (n % 2) + i] = (half_t)p;
           }
@@ -371,41 +547,52 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnK a) {
 #pragma unroll
           for (int g = 0; g < NG; ++g)
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-              const int key = base + 32 * g + 16 * (s / 4) + 4 * t + s % 4;
+            for (int s = 0; s < 8; ++s)
 #pragma unroll
-              for (int w = 0; w < DL / 2; ++w) {
-                if (key >= k1) vr[g][s][w] = 0u;
-                else if (key >= see_all) odd |= half2_not_finite(vr[g][s][w]);
-              }
-            }
+              for (int w = 0; w < DL / 2; ++w) odd |= half2_not_finite(vr[g][s][w]);
           if (__ballot(odd)) {
-            // Rare: such keys leave the matrix product, and each row that sees
-            // them adds them by itself.
+            // Rare.  Such values leave the matrix product; a product of their
+            // kinds (1: inf, 64: -inf, 4096: NaN; exact for 32 keys) with what
+            // each row sees says which reach it.
+            half8_t seen[RT][NG];
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
+            for (int x = 0; x < RT; ++x)
 #pragma unroll
-              for (int s = 0; s < 8; ++s) {
-                const int n = 2 * g + s / 4, i = s % 4;
-                if (base + 16 * n + 4 * t + i >= see_all)
+              for (int g = 0; g < NG; ++g)
 #pragma unroll
-                  for (int w = 0; w < DL / 2; ++w) vr[g][s][w] = 0u;
+                for (int s = 0; s < 8; ++s)
+                  seen[x][g][s] = (half_t)(base + 32 * g + 16 * (s / 4) + 4 * t + s % 4 < lim[x] ? 1.0f : 0.0f);
 #pragma unroll
-                for (int tt = 0; tt < 4; ++tt) {
-                  const int key = base + 16 * n + 4 * tt + i;
-                  if (key < see_all || key >= k1) continue;
-                  const half_t* row = (const half_t*)(vbase[n] + (4 * tt + i) * (D * E));
+            for (int j = 0; j < DL; ++j)
 #pragma unroll
-                  for (int x = 0; x < RT; ++x) {
-                    const float p = __shfl((float)pf[x][g][s], c + 16 * tt);
-                    if (key < lim[x])
+              for (int g = 0; g < NG; ++g) {
+                u32x4_t w;
 #pragma unroll
-                      for (int j = 0; j < DL; ++j)
+                for (int k = 0; k < 4; ++k)
+                  w[k] = kind_of((vr[g][2 * k][j / 2] >> (16 * (j % 2))) & 0xFFFFu) |
+                         kind_of((vr[g][2 * k + 1][j / 2] >> (16 * (j % 2))) & 0xFFFFu) << 16;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) acc[x][j][k] += p * (float)row[DL * (4 * t + k) + j];
+                for (int x = 0; x < RT; ++x) {
+                  const float4_t kinds = mfma16x16x32(__builtin_bit_cast(half8_t, w), seen[x][g], zero_float4());
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const int n = (int)kinds[k];
+                    if (n & 63) acc[x][j][k] += INFINITY;
+                    if (n & 4032) acc[x][j][k] -= INFINITY;
+                    if (n >> 12) acc[x][j][k] = NAN;
                   }
                 }
               }
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+              for (int s = 0; s < 8; ++s)
+#pragma unroll
+                for (int w = 0; w < DL / 2; ++w) {
+                  const uint32_t v = vr[g][s][w];
+                  vr[g][s][w] = ((v & 0x7C00u) == 0x7C00u ? 0u : v & 0xFFFFu) |
+                                ((v & 0x7C000000u) == 0x7C000000u ? 0u : v & 0xFFFF0000u);
+                }
           }
         }
       }
@@ -430,6 +617,11 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnK a) {
 #pragma unroll
           for (int x = 0; x < RT; ++x) acc[x][j] = mfma16x16x32(vf, pf[x][g], acc[x][j]);
         }
+      __builtin_amdgcn_sched_barrier(0);
+      load_v(base + KS, page);
+#pragma unroll
+      for (int n = 0; n < NS; ++n) page[n] = later_page[n];
+      __builtin_amdgcn_sched_barrier(0);
     }
 
     // Join the waves.  Lane (c, t) holds row c at d = DL (4 t + k) + j.
@@ -450,116 +642,51 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnK a) {
       }
     }
     __syncthreads();
-    constexpr int UNITS = R * D / 8;
-    for (int u = threadIdx.x; u < UNITS; u += kThreads) {
-      const int row = u / (D / 8), d = u % (D / 8) * 8;
-      const int r = r0 + row;
-      if (r >= rows) break;
+    const bool whole = step0 == 0 && step1 == u.steps;
+    const uint32_t slot = 2 * blockIdx.x + (step0 == 0 ? 1u : 0u);
+    for (int v = threadIdx.x; v < rows_here * (D / 4); v += kThreads) {
+      const int row = v / (D / 4), d = v % (D / 4) * 4;
       float M = s_m[0][row];
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) M = fmaxf(M, s_m[w][row]);
-      float sum = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      float sum = 0.0f;
+      float4_t o = zero_float4();
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
         const float f = __builtin_amdgcn_exp2f(s_m[w][row] - M);
         sum += s_l[w][row] * f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] += s_o[w][row][d + k] * f;
+        o += *(const float4_t*)&s_o[w][row][d] * f;
       }
-      if (it.pieces == 1) {
+      if (whole) {
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // nothing seen: zeros
-        half8_t h;
+        half4_t h;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[k] = (half_t)(o[k] * inv);
-        const int tok = r / a.group, qh = head * a.group + r % a.group;
-        *(half8_t*)(a.out + ((it.q0 + (int64_t)tok) * a.q_heads + qh) * D + d) = h;
+        for (int k = 0; k < 4; ++k) h[k] = (half_t)(o[k] * inv);
+        const int r = r0 + row;
+        *(half4_t*)(a.out + ((u.q0 + (int64_t)(r / a.group)) * a.q_heads + head * a.group + r % a.group) * D + d) = h;
       } else {
-        const int64_t slot = (int64_t)(it.slot + it.at) * a.kv_heads + head;
-        float* p = a.part + slot * (R * (D + 2));
-        *(float4_t*)(p + row * D + d) = *(float4_t*)&o[0];
-        *(float4_t*)(p + row * D + d + 4) = *(float4_t*)&o[4];
+        const __amdgpu_buffer_rsrc_t pr = make_rsrc(a.part, (uint32_t)a.part_bytes);
+        const uint32_t p = slot * (uint32_t)(SLOT * 4);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o), pr, p + (uint32_t)(row * D + d) * 4, 0,
+                                               kCachePolicySc1);
         if (d == 0) {
-          p[R * D + row] = M;
-          p[R * D + R + row] = sum;
+          __builtin_amdgcn_raw_buffer_store_b32(float_bits(M), pr, p + (uint32_t)(R * D + row) * 4, 0, kCachePolicySc1);
+          __builtin_amdgcn_raw_buffer_store_b32(float_bits(sum), pr, p + (uint32_t)(R * D + R + row) * 4, 0,
+                                                kCachePolicySc1);
         }
       }
     }
-    __syncthreads();
-  }
-}
-
-// Joins the pieces of split rows: a workgroup takes one row of one kv head, its
-// waves a quarter of the pieces each, all in a fixed order.
-template <int D, int KT, int R>
-__global__ void __launch_bounds__(kThreads) attn_combine_kernel(AttnK a) {
-  constexpr int DL = D / kWave;
-  __shared__ float s_o[kWaves][D], s_m[kWaves], s_l[kWaves];
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int head = blockIdx.x % a.kv_heads;
-  const int chunk = chunk_keys<R, KT>(a, lane);
-  for (int index = blockIdx.x / a.kv_heads;; index += gridDim.x / a.kv_heads) {
-    const Item it = find<R, 1>(a, chunk, index, lane);
-    if (!it.found) break;
-    const int rt = it.at / R, row = it.at % R;
-    const float* base = a.part + ((int64_t)(it.slot + rt * it.pieces) * a.kv_heads + head) * (R * (D + 2));
-    const int64_t step = (int64_t)a.kv_heads * (R * (D + 2));
-    float M = kNone, sum = 0.0f, o[DL];
-#pragma unroll
-    for (int k = 0; k < DL; ++k) o[k] = 0.0f;
-    for (int i0 = wave; i0 < it.pieces; i0 += 8 * kWaves) {
-      float pm[8], pl[8], po[8][DL];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int piece = i0 + i * kWaves;
-        const float* p = base + min(piece, it.pieces - 1) * step;
-        pm[i] = p[R * D + row];
-        pl[i] = p[R * D + R + row];
-#pragma unroll
-        for (int k = 0; k < DL; ++k) po[i][k] = p[row * D + lane * DL + k];
-        if (piece >= it.pieces) {
-          pm[i] = kNone;
-          pl[i] = 0.0f;
-#pragma unroll
-          for (int k = 0; k < DL; ++k) po[i][k] = 0.0f;
-        }
+    if (!whole) {
+      drain_vm();
+      __syncthreads();
+      const uint32_t w0 = shares.owner(unit0);
+      const int pieces = (int)(shares.owner(unit0 + (uint32_t)u.steps - 1) - w0) + 1;
+      if (threadIdx.x == 0) s_arrived = add_dev_u32(&a.counters[w0], 1u);
+      __syncthreads();
+      if (s_arrived == (uint32_t)pieces - 1) {
+        if (threadIdx.x == 0) st_dev_u32(&a.counters[w0], 0u);
+        join<D, R, SLOT>(a, &s_o[0][0][0], rows_here, r0, u.q0, head, w0, pieces);
       }
-      float to = M;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) to = fmaxf(to, pm[i]);
-      const float f = __builtin_amdgcn_exp2f(M - to);
-      M = to;
-      sum *= f;
-#pragma unroll
-      for (int k = 0; k < DL; ++k) o[k] *= f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float g = __builtin_amdgcn_exp2f(pm[i] - M);
-        sum += pl[i] * g;
-#pragma unroll
-        for (int k = 0; k < DL; ++k) o[k] += po[i][k] * g;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < DL; ++k) s_o[wave][lane * DL + k] = o[k];
-    if (lane == 0) {
-      s_m[wave] = M;
-      s_l[wave] = sum;
-    }
-    __syncthreads();
-    if (threadIdx.x < D) {
-      const int d = threadIdx.x;
-      float to = s_m[0];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) to = fmaxf(to, s_m[w]);
-      float total = 0.0f, v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float g = __builtin_amdgcn_exp2f(s_m[w] - to);
-        total += s_l[w] * g;
-        v += s_o[w][d] * g;
-      }
-      const int tok = it.at / a.group, qh = head * a.group + it.at % a.group;
-      a.out[((it.q0 + (int64_t)tok) * a.q_heads + qh) * D + d] = (half_t)(total == 0.0f ? 0.0f : v / total);
     }
     __syncthreads();
   }
@@ -568,9 +695,6 @@ __global__ void __launch_bounds__(kThreads) attn_combine_kernel(AttnK a) {
 template <int D, bool I8, int RT>
 hipError_t launch(const AttnK& k, const AttnPlan& p, hipStream_t st) {
   attn_kernel<D, I8, RT><<<dim3(p.grid), dim3(kThreads), 0, st>>>(k);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.combine_grid == 0) return e;
-  attn_combine_kernel<D, I8 ? 64 : 32, 16 * RT><<<dim3(p.combine_grid), dim3(kThreads), 0, st>>>(k);
   return hipGetLastError();
 }
 
@@ -580,28 +704,19 @@ AttnPlan attn_plan(const spear_attention_desc_t& d, int cus) {
   AttnPlan p;
   const int64_t H = d.kv.kv_heads, group = d.q_heads / H;
   p.row_tiles = (int64_t)d.max_q * group > 16 ? 2 : 1;
-  const int64_t R = 16 * p.row_tiles;
-  const int64_t per_head = ceil_div((int64_t)4 * cus, H);   // split items aimed at
-  p.target = (int)per_head;
-  p.min_chunk = d.kv.dtype == SPEAR_KV_INT8 ? 256 : 128;     // one tile for each wave
-  // Row tiles: no sequence has more than its rows need, nor more than one not full.
-  int64_t tiles = d.batch + (int64_t)d.total_q * group / R;
-  const int64_t most = d.batch * ceil_div((int64_t)d.max_q * group, R);
-  if (most < tiles) tiles = most;
-  const int64_t max_kv = (int64_t)d.max_pages * d.kv.page_size;
-  const bool split = max_kv > p.min_chunk;
-  const int64_t cap = (int64_t)16 * cus * 4;                 // workgroups; the rest in turns
-  int64_t items = tiles + (split ? per_head : 0);
-  if (items * H > cap) items = ceil_div(cap, H);
-  p.grid = (int)(items * H);
-  // A sequence is split when it is longer than the chunk, so its pieces are
-  // fewer than twice its share of the target.
-  const int64_t slots = split ? 2 * per_head : 0;
-  int64_t rows = (int64_t)d.total_q * group;
-  if (rows * H > 4 * cus) rows = ceil_div((int64_t)4 * cus, H);
-  p.combine_grid = split ? (int)(rows * H) : 0;
+  const int64_t R = 16 * p.row_tiles, KS = 32 * kWaves;
+  // One share for each workgroup that the GPU holds at once; no more of them
+  // than there can be steps.
+  const int64_t held = (int64_t)(p.row_tiles == 1 ? 3 : 2) * cus;
+  const int64_t steps = ceil_div((int64_t)d.max_pages * d.kv.page_size, KS);
+  const int64_t tiles = d.batch + (int64_t)d.total_q * group / R;
+  p.fits = tiles * steps <= (INT32_MAX / H);
+  const int64_t most = tiles * steps * H;
+  p.grid = (int)(most < held ? most : held);
+  if (p.grid > kMaxEcTiles) p.grid = kMaxEcTiles;
   p.part = kSyncHeaderBytes;
-  p.bytes = split ? p.part + (size_t)(slots * H * R * (d.kv.head_dim + 2) * 4) : 0;
+  p.part_bytes = (size_t)2 * p.grid * R * (d.kv.head_dim + 2) * 4;
+  p.bytes = p.part + p.part_bytes;
   return p;
 }
 
@@ -610,10 +725,9 @@ hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* stream) 
   k.q = (const half_t*)a.q; k.q_ts = a.q_ts; k.q_hs = a.q_hs;
   k.cu = a.cu_q; k.lens = a.kv_lens; k.table = a.table; k.table_stride = a.table_stride;
   k.kc = a.k_cache; k.vc = a.v_cache; k.ks = a.k_scale; k.vs = a.v_scale;
-  k.out = (half_t*)a.out; k.part = a.part;
+  k.out = (half_t*)a.out; k.part = a.part; k.part_bytes = (int32_t)p.part_bytes; k.counters = a.counters;
   k.batch = a.batch; k.total_q = a.total_q; k.q_heads = a.q_heads; k.kv_heads = a.kv.heads;
   k.group = a.group; k.max_kv = a.max_kv; k.page_log2 = a.kv.page_log2; k.num_pages = a.kv.num_pages;
-  k.target = p.target; k.min_chunk = p.min_chunk;
   k.scale = a.scale * kLog2e;
   const hipStream_t st = (hipStream_t)stream;
   const bool i8 = a.kv.dtype == SPEAR_KV_INT8, two = p.row_tiles == 2;

@@ -90,7 +90,7 @@ spear_status_t plan_attention(const spear_attention_desc_t& d, AttnPlan* p) {
   spear_attention_desc_t e = d;
   if (e.max_q > e.total_q) e.max_q = e.total_q;
   *p = attn_plan(e, cus);
-  return SPEAR_OK;
+  return p->fits ? SPEAR_OK : SPEAR_ERR_UNSUPPORTED;
 }
 
 spear_status_t check_verify(const spear_verify_desc_t& d) {
@@ -184,9 +184,9 @@ spear_status_t spear_paged_attention(const spear_attention_desc_t* desc, const v
   AttnPlan p;
   st = plan_attention(*desc, &p);
   if (st != SPEAR_OK) return st;
-  if (p.bytes > 0 && !workspace) return SPEAR_ERR_NULL_POINTER;
+  if (!workspace) return SPEAR_ERR_NULL_POINTER;
   if (workspace_bytes < p.bytes) return SPEAR_ERR_WORKSPACE_TOO_SMALL;
-  if (workspace && !aligned(workspace, 16)) return SPEAR_ERR_MISALIGNED;
+  if (!aligned(workspace, 16)) return SPEAR_ERR_MISALIGNED;
   a.batch = desc->batch; a.total_q = desc->total_q; a.q_heads = desc->q_heads;
   a.group = desc->q_heads / desc->kv.kv_heads;
   a.max_kv = desc->max_pages * desc->kv.page_size;
@@ -195,7 +195,8 @@ spear_status_t spear_paged_attention(const spear_attention_desc_t* desc, const v
   a.cu_q = cu_q; a.kv_lens = kv_lens; a.table = block_table; a.table_stride = table_stride;
   a.k_cache = k_cache; a.v_cache = v_cache; a.k_scale = k_scale; a.v_scale = v_scale;
   a.out = out;
-  a.part = p.bytes > 0 ? (float*)((char*)workspace + p.part) : nullptr;
+  a.part = (float*)((char*)workspace + p.part);
+  a.counters = (uint32_t*)workspace;   // the first counters of the header
   return hip_status(launch_attention(a, p, stream));
 }
 

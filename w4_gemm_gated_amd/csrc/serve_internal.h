@@ -42,13 +42,12 @@ hipError_t launch_kv_gather(const KvGatherArgs& a, void* stream);
 
 // Launch shape of an attention call.
 struct AttnPlan {
-  int row_tiles;     // 16-row tiles a workgroup holds (1 or 2)
-  int target;        // split items aimed at, over all kv heads
-  int min_chunk;     // fewest keys of a split item
-  int grid;          // workgroups of the main launch
-  int combine_grid;  // workgroups of the launch that joins split items; 0: nothing can be split
-  size_t part;       // byte offset of the partial results in the workspace
-  size_t bytes;      // workspace (0: none)
+  int row_tiles;      // 16-row tiles a workgroup holds (1 or 2)
+  int grid;           // workgroups, each with an equal share of the work
+  bool fits;          // the work can be counted in 32 bits
+  size_t part;        // byte offset of the partial results in the workspace
+  size_t part_bytes;  // two results per workgroup
+  size_t bytes;       // workspace
 };
 AttnPlan attn_plan(const spear_attention_desc_t& d, int cus);
 
@@ -64,6 +63,7 @@ struct AttnArgs {
   const float *k_scale, *v_scale;
   void* out;
   float* part;
+  uint32_t* counters;   // [grid], zero before and after
 };
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* stream);
 
