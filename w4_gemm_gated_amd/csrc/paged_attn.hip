@@ -35,34 +35,12 @@
 // (fp32) per workgroup in the workspace; the last of them to arrive joins them
 // in order, so the result does not depend on scheduling.  Data passes between
 // workgroups as everywhere here: device-coherent stores, a drain, a counter.
-#include "serve_internal.h"
-#include "device_common.h"
+#include <algorithm>
+
+#include "attn_common.h"
 
 namespace spear {
 namespace {
-
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
-constexpr float kLog2e = 1.44269504088896341f;
-constexpr float kNone = -1e30f;      // reference of a row that has seen no key
-constexpr float kHead = 14.0f;       // a maximum this far above the reference moves it
-constexpr float kStart = 6.0f;       // .. to this far below the maximum
-constexpr float kMaxScale = 1e30f;   // scales above this do not move the common one
-
-struct AttnK {
-  const half_t* q;
-  int64_t q_ts, q_hs;
-  const int32_t *cu, *lens, *table;
-  int64_t table_stride;
-  const void *kc, *vc;
-  const float *ks, *vs;
-  half_t* out;
-  float* part;          // [2 x workgroups] partial results
-  uint32_t* counters;   // [workgroups], zero before and after
-  int32_t batch, total_q, q_heads, kv_heads, group, max_kv, page_log2, num_pages;
-  int32_t part_bytes;
-  float scale;                 // scale * log2(e)
-};
 
 // ------------------------------------------------------------- the schedule
 
@@ -79,30 +57,11 @@ __device__ __forceinline__ Seq sequence(const AttnK& a, int b) {
     s.q0 = min(max(c0, 0), a.total_q);
     s.n = min(max(c1, s.q0), a.total_q) - s.q0;
     s.kv = min(max(len, 0), a.max_kv);
-    s.tiles = (s.n * a.group + R - 1) / R;
+    const int rows = s.n * a.group;
+    s.tiles = rows > a.rows_from && rows <= a.rows_to ? (rows + R - 1) / R : 0;
     s.steps = max((s.kv + KS - 1) / KS, 1);
   }
   return s;
-}
-
-__device__ __forceinline__ uint32_t wave_scan(uint32_t x, int lane) {
-#pragma unroll
-  for (int o = 1; o < kWave; o *= 2) {
-    const uint32_t y = __shfl_up(x, o);
-    if (lane >= o) x += y;
-  }
-  return x;
-}
-
-// A value that all lanes hold alike, moved to a scalar register: addresses and
-// bounds made of it then are scalar too (a division leaves it in a vector one).
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-__device__ __forceinline__ uint32_t uniform(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
-
-// A buffer resource in scalar registers.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base, uint32_t bytes) {
-  const uint64_t p = (uint64_t)base;
-  return make_rsrc((const void*)((uint64_t)uniform((uint32_t)(p >> 32)) << 32 | uniform((uint32_t)p)), uniform(bytes));
 }
 
 // Equal shares of n steps for w workgroups: the first `more` take one step more.
@@ -147,70 +106,7 @@ __device__ __forceinline__ Unit find(const AttnK& a, const Seq& s0, uint32_t p, 
   return u;
 }
 
-// -------------------------------------------------------------- small pieces
-
-// Over the four lanes (c, 0..3) that hold row c: swaps of 16- and 32-lane halves
-// (each returns the two halves' values in both).
-typedef uint32_t pair_t __attribute__((ext_vector_type(2)));
-template <typename F>
-__device__ __forceinline__ float over_row(float x, F f) {
-  const uint32_t v = float_bits(x);
-  const pair_t a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  const uint32_t w = float_bits(f(bits_float(a.x), bits_float(a.y)));
-  const pair_t b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-  return f(bits_float(b.x), bits_float(b.y));
-}
-__device__ __forceinline__ float row_max4(float x) {
-  return over_row(x, [](float a, float b) { return fmaxf(a, b); });
-}
-__device__ __forceinline__ float row_sum4(float x) {
-  return over_row(x, [](float a, float b) { return a + b; });
-}
-
-// Codes b0 and b1 (bytes i of two words, sign included) -> two fp16 values.
-// Byte | 0x6400 with the sign bit flipped is the fp16 number 1024 + 128 + code.
-__device__ __forceinline__ uint32_t codes_to_half2(uint32_t bytes) {   // bytes 0x00b1'00b0
-  const half2_t bias = {(half_t)1152.0f, (half_t)1152.0f};
-  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, bytes ^ 0x64806480u) - bias);
-}
-// Eight codes of two words, in order.
-__device__ __forceinline__ half8_t codes_to_half8(uint32_t lo, uint32_t hi) {
-  u32x4_t r;
-  r[0] = codes_to_half2(__builtin_amdgcn_perm(lo, lo, 0x0c010c00u));
-  r[1] = codes_to_half2(__builtin_amdgcn_perm(lo, lo, 0x0c030c02u));
-  r[2] = codes_to_half2(__builtin_amdgcn_perm(hi, hi, 0x0c010c00u));
-  r[3] = codes_to_half2(__builtin_amdgcn_perm(hi, hi, 0x0c030c02u));
-  return __builtin_bit_cast(half8_t, r);
-}
-
-typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(4))) int32_t scalar_i32_t;
-template <int BYTES> struct Vec;
-template <> struct Vec<4> { typedef uint32_t type __attribute__((ext_vector_type(1))); };
-template <> struct Vec<8> { typedef uint32_t type __attribute__((ext_vector_type(2))); };
-template <> struct Vec<16> { typedef uint32_t type __attribute__((ext_vector_type(4))); };
-
-__device__ __forceinline__ bool half2_not_finite(uint32_t w) {
-  return (w & 0x7C00u) == 0x7C00u || (w & 0x7C000000u) == 0x7C000000u;
-}
-
-// An fp16 number's kind as an fp16 number: 0 finite, 1 infinity, 64 -infinity,
-// 4096 NaN.
-__device__ __forceinline__ uint32_t kind_of(uint32_t h) {
-  if ((h & 0x7C00u) != 0x7C00u) return 0u;
-  return (h & 0x03FFu) ? 0x6C00u : (h & 0x8000u) ? 0x5400u : 0x3C00u;
-}
-
 // ------------------------------------------------------------ the main kernel
-
-// Lanes' 4, 8 or 16 bytes of a buffer.
-template <int BYTES>
-__device__ __forceinline__ typename Vec<BYTES>::type buffer_vec(__amdgpu_buffer_rsrc_t r, uint32_t offset) {
-  typedef typename Vec<BYTES>::type vec_t;
-  if constexpr (BYTES == 4) return vec_t{(uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, offset, 0, 0)};
-  else if constexpr (BYTES == 8) return __builtin_bit_cast(vec_t, __builtin_amdgcn_raw_buffer_load_b64(r, offset, 0, 0));
-  else return __builtin_bit_cast(vec_t, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0));
-}
 
 template <int D, bool I8, int RT>
 struct Shape {
@@ -369,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
         const int d = I8 ? 64 * (m / 2) + 16 * t + 8 * (m % 2) : 32 * m + 8 * t;
-        qf[x][m] = ok ? load_half8(qp + d) : zero_half8();
+        qf[x][m] = ok ? query(qp + d, a.negate) : zero_half8();
       }
     }
 
@@ -702,21 +598,37 @@ hipError_t launch(const AttnK& k, const AttnPlan& p, hipStream_t st) {
 
 AttnPlan attn_plan(const spear_attention_desc_t& d, int cus) {
   AttnPlan p;
-  const int64_t H = d.kv.kv_heads, group = d.q_heads / H;
-  p.row_tiles = (int64_t)d.max_q * group > 16 ? 2 : 1;
-  const int64_t R = 16 * p.row_tiles, KS = 32 * kWaves;
+  const int64_t H = d.kv.kv_heads, group = d.q_heads / H, dim = d.kv.head_dim;
+  const int64_t most_rows = (int64_t)d.max_q * group;
+  // Few rows: this kernel, 16 or 32 at a time.  More: tiles of 128, unless other
+  // sequences of the batch have few (a decode step beside a prompt's chunk);
+  // then each kernel takes its own.
+  p.tiles = most_rows > 32;
+  p.both = p.tiles && (int64_t)d.total_q < d.batch * (int64_t)d.max_q;
+  p.row_tiles = (p.tiles ? group : most_rows) > 16 ? 2 : 1;
+  p.few_rows = 16 * p.row_tiles;
+  const int64_t R = p.few_rows, KS = 32 * kWaves;
   // One share for each workgroup that the GPU holds at once; no more of them
   // than there can be steps.
   const int64_t held = (int64_t)(p.row_tiles == 1 ? 3 : 2) * cus;
-  const int64_t steps = ceil_div((int64_t)d.max_pages * d.kv.page_size, KS);
-  const int64_t tiles = d.batch + (int64_t)d.total_q * group / R;
-  p.fits = tiles * steps <= (INT32_MAX / H);
+  const int64_t max_kv = (int64_t)d.max_pages * d.kv.page_size;
+  const int64_t steps = ceil_div(max_kv, KS);
+  const int64_t tiles = p.tiles ? d.batch : d.batch + (int64_t)d.total_q * group / R;
   const int64_t most = tiles * steps * H;
-  p.grid = (int)(most < held ? most : held);
+  p.fits = most <= INT32_MAX;
+  p.grid = p.tiles && !p.both ? 0 : (int)(most < held ? most : held);
   if (p.grid > kMaxEcTiles) p.grid = kMaxEcTiles;
+  // Items of the tile kernel: row tiles, and their pieces where there are few:
+  // the pieces of split row tiles are fewer than twice the workgroups held.
+  p.tile_held = (int)std::min<int64_t>((int64_t)2 * cus, kMaxEcTiles / 2);
+  const int64_t row_tiles = d.batch + (int64_t)d.total_q * group / 128;
+  const int64_t items = std::min<int64_t>(row_tiles * H + p.tile_held, (int64_t)1 << 20);
+  p.tile_grid = !p.tiles ? 0 : (int)round_up(items, H);
   p.part = kSyncHeaderBytes;
-  p.part_bytes = (size_t)2 * p.grid * R * (d.kv.head_dim + 2) * 4;
-  p.bytes = p.part + p.part_bytes;
+  p.part_bytes = (size_t)2 * p.grid * R * (dim + 2) * 4;
+  p.tile_part = p.part + p.part_bytes;
+  p.tile_part_bytes = p.tiles ? (size_t)2 * p.tile_held * 128 * (dim + 2) * 4 : 0;
+  p.bytes = p.tile_part + p.tile_part_bytes;
   return p;
 }
 
@@ -725,12 +637,26 @@ hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* stream) 
   k.q = (const half_t*)a.q; k.q_ts = a.q_ts; k.q_hs = a.q_hs;
   k.cu = a.cu_q; k.lens = a.kv_lens; k.table = a.table; k.table_stride = a.table_stride;
   k.kc = a.k_cache; k.vc = a.v_cache; k.ks = a.k_scale; k.vs = a.v_scale;
-  k.out = (half_t*)a.out; k.part = a.part; k.part_bytes = (int32_t)p.part_bytes; k.counters = a.counters;
+  k.out = (half_t*)a.out; k.counters = (uint32_t*)a.workspace;
   k.batch = a.batch; k.total_q = a.total_q; k.q_heads = a.q_heads; k.kv_heads = a.kv.heads;
   k.group = a.group; k.max_kv = a.max_kv; k.page_log2 = a.kv.page_log2; k.num_pages = a.kv.num_pages;
-  k.scale = a.scale * kLog2e;
+  k.scale = (a.scale < 0.0f ? -a.scale : a.scale) * kLog2e;
+  k.negate = a.scale < 0.0f ? 1 : 0;
   const hipStream_t st = (hipStream_t)stream;
   const bool i8 = a.kv.dtype == SPEAR_KV_INT8, two = p.row_tiles == 2;
+  if (p.tiles) {
+    k.rows_from = p.both ? p.few_rows : 0;
+    k.rows_to = INT32_MAX;
+    k.part = (float*)((char*)a.workspace + p.tile_part);
+    k.part_bytes = (int32_t)p.tile_part_bytes;
+    k.held = p.tile_held;
+    const hipError_t e = launch_attention_tiles(k, a.kv.dim, i8, p.tile_grid, st);
+    if (e != hipSuccess || !p.both) return e;
+  }
+  k.rows_from = 0;
+  k.rows_to = p.both ? p.few_rows : INT32_MAX;
+  k.part = (float*)((char*)a.workspace + p.part);
+  k.part_bytes = (int32_t)p.part_bytes;
   if (a.kv.dim == 64) {
     if (i8) return two ? launch<64, true, 2>(k, p, st) : launch<64, true, 1>(k, p, st);
     return two ? launch<64, false, 2>(k, p, st) : launch<64, false, 1>(k, p, st);

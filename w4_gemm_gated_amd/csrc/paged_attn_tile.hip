@@ -1,0 +1,509 @@
+// Attention of many new tokens (a prompt's chunk) over a paged key/value cache.
+//
+// As in paged_attn.hip, rows are r = token * group + head of the query heads
+// that share a kv head, S^T = K Q^T and O^T = V^T P^T, so that P goes from one
+// product's result registers into the other's operand without leaving its lane.
+// Here the matrix cores bound the work: a workgroup takes 128 rows, 32 for each of
+// its four waves, and all waves share a tile of 64 keys in LDS (two stages:
+// the next tile is copied in while this one is used).
+//
+//   - fp16 tiles go straight from memory to LDS; 16-byte units are permuted
+//     within their row by the row's number on the way (the lane's source
+//     address), so the fragment reads hit all banks.  8-bit tiles pass through
+//     registers, where codes become fp16 once for all four waves.
+//   - K fragments are 16-byte reads of a row; V^T fragments are transposing
+//     reads (within 16 lanes, lane 4e + q gives the address of row e's four
+//     values at 4q, and lane i receives column i of the four rows).
+//   - the softmax reference moves rarely, the 8-bit scales enter the scores and
+//     the weights, and infinities in values that some row must not see are kept
+//     out, all as described in paged_attn.hip.
+//
+// The matrix work of a key and row is 4 D flops, the vector work about seven
+// instructions, nearly the same time: two workgroups per CU let one's softmax
+// run under the other's products.
+//
+// A workgroup's item is a row tile of a kv head and its keys, or a piece of
+// them where there are too few tiles for the GPU (all pieces of a call have the
+// same length, so that the workgroups of a piece read the same keys).  Items
+// are numbered with the kv head fastest and a sequence's last row tile, which
+// sees the most keys, first: workgroups are dealt to the eight XCDs in turn, so
+// those that run at a time on one XCD walk the same head's keys together and
+// its L2 serves all but the first of them.  (Equal shares as in paged_attn.hip
+// were measured on 2048 tokens over 8192 keys: the workgroups of a head stood at
+// different keys, 4 MB of them, and 2.7 GB instead of 0.3 came from beyond the
+// L2: 633 us.)  Pieces leave their sums in the workspace; the last of a row
+// tile's to arrive joins them in order.
+#include "attn_common.h"
+
+namespace spear {
+namespace {
+
+constexpr int kRows = 128;                  // of a workgroup
+constexpr int kWaveRows = kRows / kWaves;   // 32: two 16-row operands
+constexpr int kKeys = 64;                   // of a tile
+constexpr int kNS = kKeys / 16;             // 16-key tiles
+constexpr int kNG = kKeys / 32;             // 32-key groups
+constexpr int kRT = kWaveRows / 16;
+constexpr uint64_t kMinPiece = 256;         // keys: a shorter piece costs more in its partial sums than it saves
+
+struct SeqT {
+  int q0, n, kv, tiles;
+};
+__device__ __forceinline__ SeqT sequence(const AttnK& a, int b) {
+  SeqT s = {0, 0, 0, 0};
+  if (b < a.batch) {
+    const int c0 = a.cu[b], c1 = a.cu[b + 1], len = a.lens[b];
+    s.q0 = min(max(c0, 0), a.total_q);
+    s.n = min(max(c1, s.q0), a.total_q) - s.q0;
+    s.kv = min(max(len, 0), a.max_kv);
+    const int rows = s.n * a.group;
+    s.tiles = rows > a.rows_from && rows <= a.rows_to ? (rows + kRows - 1) / kRows : 0;
+  }
+  return s;
+}
+
+__device__ __forceinline__ int pieces_of(int kv, int piece) { return kv > piece ? (kv + piece - 1) / piece : 1; }
+
+// Item `index` of a kv head: sequence, row tile and piece.  `slot` numbers the
+// split row tiles' pieces: this row tile's first.
+struct ItemT {
+  int b, q0, n, kv, rt, piece, slot;
+};
+__device__ __forceinline__ bool find(const AttnK& a, const SeqT& s0, int piece, uint32_t index, int lane, ItemT* it) {
+  uint32_t before = 0, slots = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kWave) {
+    const SeqT s = b0 == 0 ? s0 : sequence(a, b0 + lane);
+    const int np = pieces_of(s.kv, piece);
+    const uint32_t mine = (uint32_t)s.tiles * (uint32_t)np, split = np > 1 ? mine : 0;
+    const uint32_t upto = before + wave_scan(mine, lane), slot_upto = slots + wave_scan(split, lane);
+    const uint64_t past = __ballot(upto > index);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      const int tiles = __builtin_amdgcn_readlane(s.tiles, l), n = __builtin_amdgcn_readlane(np, l);
+      const int at = (int)(index - (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), l));
+      it->b = b0 + l;
+      it->q0 = __builtin_amdgcn_readlane(s.q0, l);
+      it->n = __builtin_amdgcn_readlane(s.n, l);
+      it->kv = __builtin_amdgcn_readlane(s.kv, l);
+      it->piece = uniform(at / tiles);
+      it->rt = tiles - 1 - (at - it->piece * tiles);
+      it->slot = __builtin_amdgcn_readlane((int)(slot_upto - split), l) + it->rt * n;
+      return true;
+    }
+    before = (uint32_t)__builtin_amdgcn_readlane((int)upto, kWave - 1);
+    slots = (uint32_t)__builtin_amdgcn_readlane((int)slot_upto, kWave - 1);
+  }
+  return false;
+}
+
+typedef __attribute__((address_space(3))) void lds_void_t;
+typedef __fp16 fp16x4_t __attribute__((__vector_size__(4 * sizeof(__fp16))));
+typedef __attribute__((address_space(3))) fp16x4_t lds_fp16x4_t;
+
+template <int D, bool I8>
+__global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
+  constexpr int RB = D * (I8 ? 1 : 2);        // bytes of a cached row
+  constexpr int NM = D / 32, NJ = D / 16;     // matrix instructions along d: of S and of O
+  constexpr int UPR = D / 8;                  // 16-byte units of a row in LDS
+  constexpr int SLOT = kRows * (D + 2);
+  constexpr int CR = I8 ? RB / 64 : 1;        // 16-byte code loads of a lane and 16-key share
+  __shared__ __attribute__((aligned(16))) half_t s_k[2][kKeys * D], s_v[2][kKeys * D];
+  __shared__ __attribute__((aligned(16))) float s_ks[2][I8 ? kKeys : 4], s_vs[2][I8 ? kKeys : 4];
+  __shared__ uint32_t s_arrived;
+
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int c = lane % 16, t = lane / 16;
+  auto swizzle = [](int row) { return UPR == 16 ? row & 15 : (row >> 1) & 7; };
+
+  // The pieces' length: none where the row tiles come near to filling the GPU.
+  const SeqT seq0 = sequence(a, lane);
+  uint64_t work = 0;
+  int tiles = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kWave) {
+    const SeqT s = b0 == 0 ? seq0 : sequence(a, b0 + lane);
+    work += (uint64_t)s.tiles * (uint64_t)s.kv;
+    tiles += s.tiles;
+  }
+#pragma unroll
+  for (int o = 1; o < kWave; o *= 2) {
+    work += __shfl_xor(work, o);
+    tiles += __shfl_xor(tiles, o);
+  }
+  int piece = 1 << 30;
+  if ((int64_t)tiles * a.kv_heads * 4 < (int64_t)a.held * 3) {
+    const uint64_t keys = (work * (uint64_t)a.kv_heads + (uint64_t)a.held - 1) / (uint64_t)a.held;
+    piece = (int)min(max((keys + kKeys - 1) / kKeys * kKeys, kMinPiece), (uint64_t)1 << 30);
+  }
+  piece = uniform(piece);
+
+  const int place_mask = (1 << a.page_log2) - 1;
+  const uint32_t page_rows = (uint32_t)a.kv_heads << a.page_log2;
+  const int head = (int)uniform(blockIdx.x % (uint32_t)a.kv_heads);
+
+  for (uint32_t index = blockIdx.x / (uint32_t)a.kv_heads;; index += gridDim.x / (uint32_t)a.kv_heads) {
+    ItemT u;
+    if (!find(a, seq0, piece, uniform(index), lane, &u)) break;
+    const int rows = u.n * a.group, r0 = u.rt * kRows;
+    const int rows_here = min(kRows, rows - r0);
+    const int pos0 = u.kv - u.n;
+    const int k1 = uniform(min(max(pos0 + (r0 + rows_here - 1) / a.group + 1, 0), u.kv));
+    const int pieces = uniform(pieces_of(k1, piece));          // of this row tile: those that hold keys
+    if (u.piece >= pieces) continue;
+    const int step0 = u.piece * (piece / kKeys);
+    const int steps = (k1 + kKeys - 1) / kKeys;
+    const int step1 = pieces == 1 ? steps : min(steps, step0 + piece / kKeys);
+
+    // This wave's rows.
+    const int w0 = r0 + wave * kWaveRows;
+    const bool busy = w0 < rows;
+    const int see_all = uniform(busy ? min(pos0 + w0 / a.group + 1, u.kv) : 0);
+    const int see_any = uniform(busy ? min(max(pos0 + (min(w0 + kWaveRows, rows) - 1) / a.group + 1, 0), u.kv) : 0);
+    half8_t qf[kRT][NM];
+    int lim[kRT];
+#pragma unroll
+    for (int x = 0; x < kRT; ++x) {
+      const int r = w0 + 16 * x + c;
+      const bool ok = r < rows;
+      const int tok = ok ? r / a.group : 0, h = ok ? head * a.group + r % a.group : 0;
+      lim[x] = ok ? min(pos0 + tok + 1, k1) : see_any;
+      const half_t* qp = a.q + (u.q0 + (int64_t)tok) * a.q_ts + h * a.q_hs;
+#pragma unroll
+      for (int m = 0; m < NM; ++m) qf[x][m] = ok ? query(qp + 32 * m + 8 * t, a.negate) : zero_half8();
+    }
+
+    float4_t acc[kRT][NJ];
+    float mref[kRT], l[kRT], vref[kRT];
+#pragma unroll
+    for (int x = 0; x < kRT; ++x) {
+      mref[x] = kNone;
+      l[x] = 0.0f;
+      vref[x] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[x][j] = zero_float4();
+    }
+
+    // A wave brings 16 keys of a tile, which lie within one page.  Rows from k1
+    // on lie outside the buffer and become zeros.
+    const scalar_i32_t* table = (const scalar_i32_t*)(uintptr_t)(a.table + (int64_t)uniform(u.b) * a.table_stride);
+    const int last_key = max(k1 - 1, 0);
+    auto page_of = [&](int step) {
+      return (uint32_t)table[uniform(min(step * kKeys + 16 * wave, last_key) >> a.page_log2)];
+    };
+    const int64_t head_row = (int64_t)head << a.page_log2;
+    const unsigned char* kc = (const unsigned char*)a.kc + head_row * RB;
+    const unsigned char* vc = (const unsigned char*)a.vc + head_row * RB;
+    u32x4_t kcode[CR], vcode[CR];
+    float kscale, vscale;
+    auto fetch = [&](int step, uint32_t page, int buf) {
+      const int key = step * kKeys + 16 * wave;
+      const uint64_t row = (uint64_t)min(page, (uint32_t)a.num_pages - 1) * page_rows + (uint32_t)(key & place_mask);
+      const uint32_t in = (uint32_t)min(max(k1 - key, 0), 16);
+      const __amdgpu_buffer_rsrc_t kr = uniform_rsrc(kc + row * RB, in * RB), vr = uniform_rsrc(vc + row * RB, in * RB);
+      if constexpr (I8) {
+#pragma unroll
+        for (int i = 0; i < CR; ++i) {
+          kcode[i] = buffer_vec<16>(kr, 1024 * i + 16 * lane);
+          vcode[i] = buffer_vec<16>(vr, 1024 * i + 16 * lane);
+        }
+        const uint32_t so = lane < 16 ? 4 * lane : kOutOfRange;
+        const __amdgpu_buffer_rsrc_t ksr = uniform_rsrc(a.ks + head_row + row, in * 4);
+        const __amdgpu_buffer_rsrc_t vsr = uniform_rsrc(a.vs + head_row + row, in * 4);
+        kscale = bits_float(__builtin_amdgcn_raw_buffer_load_b32(ksr, so, 0, 0));
+        vscale = bits_float(__builtin_amdgcn_raw_buffer_load_b32(vsr, so, 0, 0));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16 * RB / 1024; ++i) {
+          const int r = i * (1024 / RB) + lane / UPR;
+          const uint32_t off = (uint32_t)(r * RB + ((lane % UPR) ^ swizzle(r)) * 16);
+          const int to = (16 * wave + i * (1024 / RB)) * D;
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(kr, (lds_void_t*)(s_k[buf] + to), 16, off, 0, 0, 0);
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(vr, (lds_void_t*)(s_v[buf] + to), 16, off, 0, 0, 0);
+        }
+      }
+    };
+    // 8-bit tiles: codes to fp16, into LDS.
+    auto put = [&](int buf) {
+      if constexpr (I8) {
+#pragma unroll
+        for (int i = 0; i < CR; ++i) {
+          const int r = 16 * wave + i * (1024 / RB) + lane / (RB / 16), unit = 2 * (lane % (RB / 16));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int to = r * D + ((unit + h) ^ swizzle(r)) * 8;
+            *(half8_t*)(s_k[buf] + to) = codes_to_half8(kcode[i][2 * h], kcode[i][2 * h + 1]);
+            *(half8_t*)(s_v[buf] + to) = codes_to_half8(vcode[i][2 * h], vcode[i][2 * h + 1]);
+          }
+        }
+        if (lane < 16) {
+          s_ks[buf][16 * wave + lane] = kscale * a.scale;
+          s_vs[buf][16 * wave + lane] = vscale;
+        }
+      }
+    };
+
+    auto compute = [&](int step, int buf, auto edge_tag) {
+      constexpr bool EDGE = decltype(edge_tag)::value;
+      const int base = step * kKeys + 4 * t;            // the lane's first key
+      // Scores.
+      float4_t st[kRT][kNS];
+#pragma unroll
+      for (int n = 0; n < kNS; ++n) {
+        const int row = 16 * n + c;
+#pragma unroll
+        for (int x = 0; x < kRT; ++x) st[x][n] = zero_float4();
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+          const half8_t kf = *(const half8_t*)(s_k[buf] + row * D + ((4 * m + t) ^ swizzle(row)) * 8);
+#pragma unroll
+          for (int x = 0; x < kRT; ++x) st[x][n] = mfma16x16x32(kf, qf[x][m], st[x][n]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      float4_t vs[kNS];
+      if constexpr (I8) {
+#pragma unroll
+        for (int n = 0; n < kNS; ++n) {
+          const float4_t ks = *(const float4_t*)(s_ks[buf] + 16 * n + 4 * t);
+          vs[n] = *(const float4_t*)(s_vs[buf] + 16 * n + 4 * t);
+#pragma unroll
+          for (int x = 0; x < kRT; ++x) st[x][n] *= ks;
+        }
+      }
+      float top[kRT], vmax[kRT];
+      bool move = false;
+#pragma unroll
+      for (int x = 0; x < kRT; ++x) {
+        top[x] = -INFINITY;
+        vmax[x] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < kNS; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool out = EDGE && base + 16 * n + i >= lim[x];
+            if (EDGE) st[x][n][i] = out ? -INFINITY : st[x][n][i];
+            top[x] = fmaxf(top[x], st[x][n][i]);
+            if constexpr (I8) vmax[x] = fmaxf(vmax[x], out || vs[n][i] > kMaxScale ? 0.0f : vs[n][i]);
+          }
+        top[x] = row_max4(top[x]);
+        if constexpr (I8) {
+          vmax[x] = row_max4(vmax[x]);
+          move |= vmax[x] > vref[x];
+        } else {
+          // (a scale of zero makes every visible score zero, or NaN)
+          top[x] = top[x] == -INFINITY ? top[x] : top[x] * a.scale;
+        }
+        move |= top[x] > mref[x] + kHead;
+      }
+      if (__ballot(move)) {
+#pragma unroll
+        for (int x = 0; x < kRT; ++x) {
+          float vscale = 1.0f;
+          if constexpr (I8) {
+            if (vmax[x] > vref[x]) {
+              const float to = bits_float((float_bits(vmax[x]) & 0x7F800000u) + 0x00800000u);
+              vscale = vref[x] > 0.0f ? vref[x] / to : 0.0f;
+              vref[x] = to;
+            }
+          }
+          const float to = top[x] > mref[x] + kHead ? top[x] - kStart : mref[x];
+          const float f = __builtin_amdgcn_exp2f(mref[x] - to);
+          mref[x] = to;
+          l[x] *= f;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) acc[x][j] *= f * vscale;
+        }
+      }
+      half8_t pf[kRT][kNG];
+#pragma unroll
+      for (int x = 0; x < kRT; ++x) {
+        const float vinv = I8 && vref[x] > 0.0f ? bits_float(0x7F000000u - float_bits(vref[x])) : 0.0f;
+#pragma unroll
+        for (int n = 0; n < kNS; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float s = st[x][n][i];
+            float p;
+            if constexpr (I8) p = __builtin_amdgcn_exp2f(s - mref[x]);
+            else if (EDGE) p = s == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(__builtin_fmaf(s, a.scale, -mref[x]));
+            else p = __builtin_amdgcn_exp2f(__builtin_fmaf(s, a.scale, -mref[x]));
+            l[x] += p;
+            if constexpr (I8) {
+              p *= vs[n][i] * vinv;
+              if (EDGE) p = base + 16 * n + i >= lim[x] ? 0.0f : p;
+            }
+            pf[x][n / 2][4 * (n % 2) + i] = (half_t)p;
+          }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      // O^T += V^T P^T.
+      const int e = c / 4, q = c % 4;
+#pragma unroll
+      for (int g = 0; g < kNG; ++g)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          half8_t vf;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = 32 * g + 16 * h + 4 * t + e;
+            const half_t* p = s_v[buf] + row * D + ((2 * j + q / 2) ^ swizzle(row)) * 8 + (q % 2) * 4;
+            const half4_t v = __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_fp16x4_t*)p));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) vf[4 * h + k] = v[k];
+          }
+          if constexpr (EDGE && !I8) {
+            u32x4_t w = __builtin_bit_cast(u32x4_t, vf);
+            if (__ballot(half2_not_finite(w[0]) || half2_not_finite(w[1]) || half2_not_finite(w[2]) ||
+                         half2_not_finite(w[3]))) {
+              // Rare: infinities and NaN leave the product; their kinds times what
+              // each row sees say which reach it (paged_attn.hip).
+              u32x4_t kind;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                kind[k] = kind_of(w[k] & 0xFFFFu) | kind_of(w[k] >> 16) << 16;
+                w[k] = ((w[k] & 0x7C00u) == 0x7C00u ? 0u : w[k] & 0xFFFFu) |
+                       ((w[k] & 0x7C000000u) == 0x7C000000u ? 0u : w[k] & 0xFFFF0000u);
+              }
+              vf = __builtin_bit_cast(half8_t, w);
+#pragma unroll
+              for (int x = 0; x < kRT; ++x) {
+                half8_t seen;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  seen[k] = (half_t)(base + 32 * g + 16 * (k / 4) + k % 4 < lim[x] ? 1.0f : 0.0f);
+                const float4_t kinds = mfma16x16x32(__builtin_bit_cast(half8_t, kind), seen, zero_float4());
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int n = (int)kinds[k];
+                  if (n & 63) acc[x][j][k] += INFINITY;
+                  if (n & 4032) acc[x][j][k] -= INFINITY;
+                  if (n >> 12) acc[x][j][k] = NAN;
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < kRT; ++x) acc[x][j] = mfma16x16x32(vf, pf[x][g], acc[x][j]);
+        }
+    };
+
+    uint32_t page = page_of(step0);
+    if (step0 < step1) fetch(step0, page, step0 & 1);
+    page = page_of(step0 + 1);
+    for (int step = step0; step < step1; ++step) {
+      const int buf = step & 1;
+      put(buf);
+      __syncthreads();                          // the tile is in LDS; the other stage is free
+      if (step + 1 < step1) {
+        fetch(step + 1, page, buf ^ 1);
+        page = page_of(step + 2);
+      }
+      if (step * kKeys < see_any) {
+        if (step * kKeys + kKeys > see_all) compute(step, buf, std::integral_constant<bool, true>());
+        else compute(step, buf, std::integral_constant<bool, false>());
+      }
+    }
+
+    // Lane (c, t) holds row c at d = 16 j + 4 t + i.
+#pragma unroll
+    for (int x = 0; x < kRT; ++x) {
+      l[x] = row_sum4(l[x]);
+      if constexpr (I8)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[x][j] *= vref[x];
+    }
+    auto write = [&]() {
+#pragma unroll
+      for (int x = 0; x < kRT; ++x) {
+        const int r = w0 + 16 * x + c;
+        if (r >= rows) continue;
+        const float inv = l[x] == 0.0f ? 0.0f : 1.0f / l[x];   // nothing seen: zeros
+        half_t* o = a.out + ((u.q0 + (int64_t)(r / a.group)) * a.q_heads + head * a.group + r % a.group) * D + 4 * t;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          half4_t h;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) h[k] = (half_t)(acc[x][j][k] * inv);
+          *(half4_t*)(o + 16 * j) = h;
+        }
+      }
+    };
+    if (pieces == 1) {
+      write();
+    } else {
+      // A partial result, in the lanes' own order.
+      const __amdgpu_buffer_rsrc_t pr = make_rsrc(a.part, (uint32_t)a.part_bytes);
+      const uint32_t slot0 = (uint32_t)u.slot * (uint32_t)a.kv_heads + (uint32_t)head;   // pieces: kv_heads apart
+      const uint32_t own = (slot0 + (uint32_t)(u.piece * a.kv_heads)) * (uint32_t)(SLOT * 4);
+      const uint32_t sums = (uint32_t)wave * (kRT * NJ * 1024) + (uint32_t)lane * 16;
+      const uint32_t stats = (uint32_t)(kRows * D + wave * kWaveRows + c) * 4;
+      if (busy) {
+#pragma unroll
+        for (int x = 0; x < kRT; ++x) {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[x][j]), pr,
+                                                   own + sums + (x * NJ + j) * 1024, 0, kCachePolicySc1);
+          if (t == 0) {
+            __builtin_amdgcn_raw_buffer_store_b32(float_bits(mref[x]), pr, own + stats + 64 * x, 0, kCachePolicySc1);
+            __builtin_amdgcn_raw_buffer_store_b32(float_bits(l[x]), pr, own + stats + 64 * x + kRows * 4, 0,
+                                                  kCachePolicySc1);
+          }
+        }
+      }
+      drain_vm();
+      __syncthreads();
+      if (threadIdx.x == 0) s_arrived = add_dev_u32(&a.counters[slot0], 1u);
+      __syncthreads();
+      if (s_arrived == (uint32_t)pieces - 1) {
+        if (threadIdx.x == 0) st_dev_u32(&a.counters[slot0], 0u);
+        if (busy) {
+          // All pieces in order, this workgroup's own among them.
+#pragma unroll
+          for (int x = 0; x < kRT; ++x) {
+            mref[x] = kNone;
+            l[x] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) acc[x][j] = zero_float4();
+          }
+          for (int i = 0; i < pieces; ++i) {
+            const uint32_t p = (slot0 + (uint32_t)(i * a.kv_heads)) * (uint32_t)(SLOT * 4);
+#pragma unroll
+            for (int x = 0; x < kRT; ++x) {
+              float4_t o[NJ];
+#pragma unroll
+              for (int j = 0; j < NJ; ++j) o[j] = buffer_load_f4_dev(pr, p + sums + (x * NJ + j) * 1024);
+              const float m = bits_float(__builtin_amdgcn_raw_buffer_load_b32(pr, p + stats + 64 * x, 0, kCachePolicySc1));
+              const float n = bits_float(
+                  __builtin_amdgcn_raw_buffer_load_b32(pr, p + stats + 64 * x + kRows * 4, 0, kCachePolicySc1));
+              const float to = fmaxf(mref[x], m);
+              const float f = __builtin_amdgcn_exp2f(mref[x] - to), g = __builtin_amdgcn_exp2f(m - to);
+              mref[x] = to;
+              l[x] = l[x] * f + n * g;
+#pragma unroll
+              for (int j = 0; j < NJ; ++j) acc[x][j] = acc[x][j] * f + o[j] * g;
+            }
+          }
+          write();
+        }
+      }
+    }
+    __syncthreads();                            // the stages are free for the next unit
+  }
+}
+
+}  // namespace
+
+hipError_t launch_attention_tiles(const AttnK& k, int dim, bool i8, int grid, hipStream_t st) {
+  const dim3 g(grid), b(kThreads);
+  if (dim == 64) {
+    if (i8) attn_tile_kernel<64, true><<<g, b, 0, st>>>(k);
+    else attn_tile_kernel<64, false><<<g, b, 0, st>>>(k);
+  } else {
+    if (i8) attn_tile_kernel<128, true><<<g, b, 0, st>>>(k);
+    else attn_tile_kernel<128, false><<<g, b, 0, st>>>(k);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace spear

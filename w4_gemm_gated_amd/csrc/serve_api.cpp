@@ -195,8 +195,7 @@ spear_status_t spear_paged_attention(const spear_attention_desc_t* desc, const v
   a.cu_q = cu_q; a.kv_lens = kv_lens; a.table = block_table; a.table_stride = table_stride;
   a.k_cache = k_cache; a.v_cache = v_cache; a.k_scale = k_scale; a.v_scale = v_scale;
   a.out = out;
-  a.part = (float*)((char*)workspace + p.part);
-  a.counters = (uint32_t*)workspace;   // the first counters of the header
+  a.workspace = workspace;
   return hip_status(launch_attention(a, p, stream));
 }
 

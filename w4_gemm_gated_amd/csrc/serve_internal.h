@@ -42,11 +42,16 @@ hipError_t launch_kv_gather(const KvGatherArgs& a, void* stream);
 
 // Launch shape of an attention call.
 struct AttnPlan {
-  int row_tiles;      // 16-row tiles a workgroup holds (1 or 2)
-  int grid;           // workgroups, each with an equal share of the work
+  bool tiles;         // sequences of many rows go to the kernel of 128-row tiles ..
+  bool both;          // .. and those of at most few_rows to the other one
+  int row_tiles;      // 16-row operands a workgroup of the latter holds (1 or 2)
+  int few_rows;       // 16 * row_tiles
+  int grid;           // workgroups of the latter, each with an equal share of the work
+  int tile_grid;      // workgroups of the former
+  int tile_held;      // .. that the GPU holds at once
   bool fits;          // the work can be counted in 32 bits
-  size_t part;        // byte offset of the partial results in the workspace
-  size_t part_bytes;  // two results per workgroup
+  size_t part, part_bytes;            // partial results in the workspace
+  size_t tile_part, tile_part_bytes;
   size_t bytes;       // workspace
 };
 AttnPlan attn_plan(const spear_attention_desc_t& d, int cus);
@@ -62,8 +67,7 @@ struct AttnArgs {
   const void *k_cache, *v_cache;
   const float *k_scale, *v_scale;
   void* out;
-  float* part;
-  uint32_t* counters;   // [grid], zero before and after
+  void* workspace;      // its header's first counters are zero before and after
 };
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* stream);
 
