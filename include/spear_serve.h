@@ -98,7 +98,7 @@ typedef struct spear_attention_desc {
   int32_t max_q;      /* the longest sequence's new tokens (>= 1; a smaller value is slower, not wrong) */
   int32_t max_pages;  /* entries of a block table row; >= 1 */
   int32_t q_heads;    /* a multiple of kv_heads */
-  float scale;        /* factor of the scores, finite; usually 1 / sqrt(head_dim) */
+  float scale;        /* factor of the scores, |scale| <= 1e30; usually 1 / sqrt(head_dim) */
   int32_t device_cus; /* 0: query the current device; > 0: plan for that many CUs, no device access */
 } spear_attention_desc_t;
 

@@ -3,8 +3,6 @@
 // softmax, lane exchanges and the 8-bit codes' way into the matrix cores.
 #pragma once
 
-#include <type_traits>
-
 #include "serve_internal.h"
 #include "device_common.h"
 

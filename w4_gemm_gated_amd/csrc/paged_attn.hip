@@ -640,7 +640,9 @@ hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* stream) 
   k.out = (half_t*)a.out; k.counters = (uint32_t*)a.workspace;
   k.batch = a.batch; k.total_q = a.total_q; k.q_heads = a.q_heads; k.kv_heads = a.kv.heads;
   k.group = a.group; k.max_kv = a.max_kv; k.page_log2 = a.kv.page_log2; k.num_pages = a.kv.num_pages;
-  k.scale = (a.scale < 0.0f ? -a.scale : a.scale) * kLog2e;
+  // (a scale of zero: so small that every score counts as zero, yet a masked
+  // one, minus infinity, stays one)
+  k.scale = a.scale == 0.0f ? 1e-37f : (a.scale < 0.0f ? -a.scale : a.scale) * kLog2e;
   k.negate = a.scale < 0.0f ? 1 : 0;
   const hipStream_t st = (hipStream_t)stream;
   const bool i8 = a.kv.dtype == SPEAR_KV_INT8, two = p.row_tiles == 2;

@@ -109,12 +109,15 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
   constexpr int CR = I8 ? RB / 64 : 1;        // 16-byte code loads of a lane and 16-key share
   __shared__ __attribute__((aligned(16))) half_t s_k[2][kKeys * D], s_v[2][kKeys * D];
   __shared__ __attribute__((aligned(16))) float s_ks[2][I8 ? kKeys : 4], s_vs[2][I8 ? kKeys : 4];
+  __shared__ uint32_t s_odd[I8 ? 1 : 6][kThreads];   // see note_odd
   __shared__ uint32_t s_arrived;
 
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane % 16, t = lane / 16;
-  auto swizzle = [](int row) { return UPR == 16 ? row & 15 : (row >> 1) & 7; };
+  // Rows 0 .. 7 put a pair of units in different bank groups (the transposing
+  // reads), rows 0 .. 15 one unit (the plain ones).
+  auto swizzle = [](int row) { return (UPR == 16 ? (row & 7) << 1 : (row & 6)) | ((row >> 3) & 1); };
 
   // The pieces' length: none where the row tiles come near to filling the GPU.
   const SeqT seq0 = sequence(a, lane);
@@ -153,6 +156,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
     const int step0 = u.piece * (piece / kKeys);
     const int steps = (k1 + kKeys - 1) / kKeys;
     const int step1 = pieces == 1 ? steps : min(steps, step0 + piece / kKeys);
+
+    const int tile_see_all = uniform(min(pos0 + r0 / a.group + 1, u.kv));   // keys below this are seen by all rows
 
     // This wave's rows.
     const int w0 = r0 + wave * kWaveRows;
@@ -242,9 +247,23 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
       }
     };
 
-    auto compute = [&](int step, int buf, auto edge_tag) {
-      constexpr bool EDGE = decltype(edge_tag)::value;
+    auto v_fragment = [&](int buf, int g, int j) {
+      const int e = c / 4, q = c % 4;
+      half8_t vf;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = 32 * g + 16 * h + 4 * t + e;
+        const half_t* p = s_v[buf] + row * D + ((2 * j + q / 2) ^ swizzle(row)) * 8 + (q % 2) * 4;
+        const half4_t v = __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_fp16x4_t*)p));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) vf[4 * h + k] = v[k];
+      }
+      return vf;
+    };
+
+    auto compute = [&](int step, int buf) {
       const int base = step * kKeys + 4 * t;            // the lane's first key
+      const bool edge = step * kKeys + kKeys > see_all;
       // Scores.
       float4_t st[kRT][kNS];
 #pragma unroll
@@ -270,30 +289,46 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
           for (int x = 0; x < kRT; ++x) st[x][n] *= ks;
         }
       }
+      if (edge) {
+#pragma unroll
+        for (int x = 0; x < kRT; ++x)
+#pragma unroll
+          for (int n = 0; n < kNS; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (base + 16 * n + i >= lim[x]) st[x][n][i] = -INFINITY;
+      }
       float top[kRT], vmax[kRT];
       bool move = false;
 #pragma unroll
       for (int x = 0; x < kRT; ++x) {
         top[x] = -INFINITY;
-        vmax[x] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < kNS; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[x] = fmaxf(top[x], st[x][n][i]);
+        top[x] = row_max4(top[x]);
+        if constexpr (!I8) top[x] *= a.scale;
+        move |= top[x] > mref[x] + kHead;
+      }
+      if constexpr (I8) {
+        // The largest finite scale of the values that each row sees.
+#pragma unroll
+        for (int x = 0; x < kRT; ++x) vmax[x] = 0.0f;
 #pragma unroll
         for (int n = 0; n < kNS; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const bool out = EDGE && base + 16 * n + i >= lim[x];
-            if (EDGE) st[x][n][i] = out ? -INFINITY : st[x][n][i];
-            top[x] = fmaxf(top[x], st[x][n][i]);
-            if constexpr (I8) vmax[x] = fmaxf(vmax[x], out || vs[n][i] > kMaxScale ? 0.0f : vs[n][i]);
+            const float v = vs[n][i] > kMaxScale ? 0.0f : vs[n][i];
+#pragma unroll
+            for (int x = 0; x < kRT; ++x)
+              vmax[x] = fmaxf(vmax[x], edge && base + 16 * n + i >= lim[x] ? 0.0f : v);
           }
-        top[x] = row_max4(top[x]);
-        if constexpr (I8) {
+#pragma unroll
+        for (int x = 0; x < kRT; ++x) {
           vmax[x] = row_max4(vmax[x]);
           move |= vmax[x] > vref[x];
-        } else {
-          // (a scale of zero makes every visible score zero, or NaN)
-          top[x] = top[x] == -INFINITY ? top[x] : top[x] * a.scale;
         }
-        move |= top[x] > mref[x] + kHead;
       }
       if (__ballot(move)) {
 #pragma unroll
@@ -323,68 +358,111 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float s = st[x][n][i];
-            float p;
-            if constexpr (I8) p = __builtin_amdgcn_exp2f(s - mref[x]);
-            else if (EDGE) p = s == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(__builtin_fmaf(s, a.scale, -mref[x]));
-            else p = __builtin_amdgcn_exp2f(__builtin_fmaf(s, a.scale, -mref[x]));
+            float p = __builtin_amdgcn_exp2f(I8 ? s - mref[x] : __builtin_fmaf(s, a.scale, -mref[x]));
             l[x] += p;
-            if constexpr (I8) {
-              p *= vs[n][i] * vinv;
-              if (EDGE) p = base + 16 * n + i >= lim[x] ? 0.0f : p;
-            }
+            if constexpr (I8) p *= vs[n][i] * vinv;
             pf[x][n / 2][4 * (n % 2) + i] = (half_t)p;
           }
       }
+      if constexpr (I8) {
+        if (edge) {   // a scale that a row must not see may be infinite or NaN
+#pragma unroll
+          for (int x = 0; x < kRT; ++x)
+#pragma unroll
+            for (int n = 0; n < kNS; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (base + 16 * n + i >= lim[x]) pf[x][n / 2][4 * (n % 2) + i] = (half_t)0.0f;
+        }
+      }
       __builtin_amdgcn_sched_barrier(0);
       // O^T += V^T P^T.
-      const int e = c / 4, q = c % 4;
 #pragma unroll
       for (int g = 0; g < kNG; ++g)
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          half8_t vf;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int row = 32 * g + 16 * h + 4 * t + e;
-            const half_t* p = s_v[buf] + row * D + ((2 * j + q / 2) ^ swizzle(row)) * 8 + (q % 2) * 4;
-            const half4_t v = __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_fp16x4_t*)p));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) vf[4 * h + k] = v[k];
-          }
-          if constexpr (EDGE && !I8) {
-            u32x4_t w = __builtin_bit_cast(u32x4_t, vf);
-            if (__ballot(half2_not_finite(w[0]) || half2_not_finite(w[1]) || half2_not_finite(w[2]) ||
-                         half2_not_finite(w[3]))) {
-              // Rare: infinities and NaN leave the product; their kinds times what
-              // each row sees say which reach it (paged_attn.hip).
-              u32x4_t kind;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                kind[k] = kind_of(w[k] & 0xFFFFu) | kind_of(w[k] >> 16) << 16;
-                w[k] = ((w[k] & 0x7C00u) == 0x7C00u ? 0u : w[k] & 0xFFFFu) |
-                       ((w[k] & 0x7C000000u) == 0x7C000000u ? 0u : w[k] & 0xFFFF0000u);
-              }
-              vf = __builtin_bit_cast(half8_t, w);
-#pragma unroll
-              for (int x = 0; x < kRT; ++x) {
-                half8_t seen;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  seen[k] = (half_t)(base + 32 * g + 16 * (k / 4) + k % 4 < lim[x] ? 1.0f : 0.0f);
-                const float4_t kinds = mfma16x16x32(__builtin_bit_cast(half8_t, kind), seen, zero_float4());
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const int n = (int)kinds[k];
-                  if (n & 63) acc[x][j][k] += INFINITY;
-                  if (n & 4032) acc[x][j][k] -= INFINITY;
-                  if (n >> 12) acc[x][j][k] = NAN;
-                }
-              }
-            }
-          }
+          const half8_t vf = v_fragment(buf, g, j);
 #pragma unroll
           for (int x = 0; x < kRT; ++x) acc[x][j] = mfma16x16x32(vf, pf[x][g], acc[x][j]);
         }
+    };
+
+    // Infinities and NaN among values that some row must not see (a weight of
+    // zero would not remove them): all waves look through the tile, alike; if
+    // there are any (rarely), each notes which of its sums they reach (the
+    // product of their kinds with what each row sees), bits that `spread` turns
+    // into the values when the sums are complete, and they leave the tile.
+    bool noted = false;
+    auto note_odd = [&](int step, int buf) {
+      bool odd = false;
+#pragma unroll
+      for (int i = 0; i < kKeys * D / 8 / kWave; ++i) {
+        const u32x4_t w = *(const u32x4_t*)(s_v[buf] + (i * kWave + lane) * 8);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) odd |= half2_not_finite(w[k]);
+      }
+      if (!__ballot(odd)) return;
+      uint32_t bits[6];
+#pragma unroll
+      for (int i = 0; i < 6; ++i) bits[i] = noted ? s_odd[i][threadIdx.x] : 0u;
+      noted = true;
+      if (busy) {
+        const int base = step * kKeys + 4 * t;
+#pragma unroll
+        for (int g = 0; g < kNG; ++g)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const u32x4_t w = __builtin_bit_cast(u32x4_t, v_fragment(buf, g, j));
+            u32x4_t kind;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) kind[k] = kind_of(w[k] & 0xFFFFu) | kind_of(w[k] >> 16) << 16;
+#pragma unroll
+            for (int x = 0; x < kRT; ++x) {
+              half8_t seen;
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                seen[k] = (half_t)(base + 32 * g + 16 * (k / 4) + k % 4 < lim[x] ? 1.0f : 0.0f);
+              const float4_t kinds = mfma16x16x32(__builtin_bit_cast(half8_t, kind), seen, zero_float4());
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int n = (int)kinds[k];
+                const uint32_t bit = 1u << (4 * j + k);
+                bits[x] |= n & 63 ? bit : 0u;
+                bits[2 + x] |= n & 4032 ? bit : 0u;
+                bits[4 + x] |= n >> 12 ? bit : 0u;
+              }
+            }
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 6; ++i) s_odd[i][threadIdx.x] = bits[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kKeys * D / 8 / kThreads; ++i) {
+        u32x4_t* p = (u32x4_t*)(s_v[buf] + (i * kThreads + threadIdx.x) * 8);
+        u32x4_t w = *p;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[k] = ((w[k] & 0x7C00u) == 0x7C00u ? 0u : w[k] & 0xFFFFu) |
+                 ((w[k] & 0x7C000000u) == 0x7C000000u ? 0u : w[k] & 0xFFFF0000u);
+        *p = w;
+      }
+      __syncthreads();
+    };
+    auto spread = [&]() {
+#pragma unroll
+      for (int x = 0; x < kRT; ++x) {
+        const uint32_t inf = s_odd[x][threadIdx.x], minus = s_odd[2 + x][threadIdx.x], nan = s_odd[4 + x][threadIdx.x];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t bit = 1u << (4 * j + k);
+            if (inf & bit) acc[x][j][k] += INFINITY;
+            if (minus & bit) acc[x][j][k] -= INFINITY;
+            if (nan & bit) acc[x][j][k] = NAN;
+          }
+      }
     };
 
     uint32_t page = page_of(step0);
@@ -398,13 +476,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
         fetch(step + 1, page, buf ^ 1);
         page = page_of(step + 2);
       }
-      if (step * kKeys < see_any) {
-        if (step * kKeys + kKeys > see_all) compute(step, buf, std::integral_constant<bool, true>());
-        else compute(step, buf, std::integral_constant<bool, false>());
-      }
+      if constexpr (!I8)
+        if (step * kKeys + kKeys > tile_see_all) note_odd(step, buf);
+      if (step * kKeys < see_any) compute(step, buf);
     }
 
     // Lane (c, t) holds row c at d = 16 j + 4 t + i.
+    if constexpr (!I8)
+      if (noted) spread();
 #pragma unroll
     for (int x = 0; x < kRT; ++x) {
       l[x] = row_sum4(l[x]);

@@ -74,7 +74,7 @@ spear_status_t check_attention(const spear_attention_desc_t& d, KvShape* s) {
   if (st != SPEAR_OK) return st;
   if (d.batch < 0 || d.total_q < 0 || d.max_q < 1 || d.max_pages < 1 || d.q_heads < 1 || d.q_heads % d.kv.kv_heads != 0)
     return SPEAR_ERR_INVALID_SHAPE;
-  if (!std::isfinite(d.scale) || d.device_cus < 0) return SPEAR_ERR_INVALID_ARGUMENT;
+  if (!(std::fabs(d.scale) <= 1e30f) || d.device_cus < 0) return SPEAR_ERR_INVALID_ARGUMENT;
   // 32-bit counts of rows and keys inside the kernels
   const int64_t most = (int64_t)1 << 30;
   if ((int64_t)d.total_q * d.q_heads > most || (int64_t)d.max_pages * d.kv.page_size > most ||
