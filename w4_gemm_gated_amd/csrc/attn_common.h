@@ -36,7 +36,7 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kNone = -1e30f;      // reference of a row that has seen no key
 constexpr float kHead = 14.0f;       // a maximum this far above the reference moves it
 constexpr float kStart = 6.0f;       // .. to this far below the maximum
-constexpr float kMaxScale = 1e30f;   // scales above this do not move the common one
+constexpr float kMaxScale = 1e30f;   // scales above this do not enter the reference
 
 __device__ __forceinline__ uint32_t wave_scan(uint32_t x, int lane) {
 #pragma unroll
@@ -119,6 +119,13 @@ __device__ __forceinline__ typename Vec<BYTES>::type buffer_vec(__amdgpu_buffer_
   if constexpr (BYTES == 4) return vec_t{(uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, offset, 0, 0)};
   else if constexpr (BYTES == 8) return __builtin_bit_cast(vec_t, __builtin_amdgcn_raw_buffer_load_b64(r, offset, 0, 0));
   else return __builtin_bit_cast(vec_t, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0));
+}
+
+// Of an 8-bit cache's values: a power of two above their scales, as its exponent.
+// It enters the reference, so that weights times scales keep to fp16's range
+// (with a bound for values that vanish in an fp16 result anyway).
+__device__ __forceinline__ float scale_exponent(float largest) {
+  return fmaxf((float)((int)(float_bits(largest) >> 23) - 126), -40.0f);
 }
 
 // Queries of a row as a B operand; a negative scale's sign goes here.

@@ -23,9 +23,10 @@
 // stay below 2^14, and m starts 6 below the first maximum, which keeps the
 // fp16 rounding of small weights relative (subnormals start 2^-20 below the
 // largest).  An 8-bit cache: codes become fp16 exactly; a key's scale
-// multiplies its scores, a value's scale its weight, divided by a power of two
-// above the scales that the row has seen so far (moved the same way), so that
-// the fp16 weights keep their range.
+// multiplies its scores, a value's scale its weight, and the exponent of the
+// largest such scale that the row sees in a tile counts with the tile's maximum,
+// so that the fp16 weights keep their range (sums and totals share the
+// reference, so it cancels in the end).
 //
 // The work is laid end to end, in steps of one key tile per wave, head after
 // head, sequence after sequence, and cut into equal shares, one per workgroup,
@@ -270,12 +271,11 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
     }
 
     float4_t acc[RT][DL];
-    float mref[RT], l[RT], vref[RT];
+    float mref[RT], l[RT];
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
       mref[x] = kNone;
       l[x] = 0.0f;
-      vref[x] = 0.0f;
 #pragma unroll
       for (int j = 0; j < DL; ++j) acc[x][j] = zero_float4();
     }
@@ -326,6 +326,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
       }
     };
 
+    bool noted = false;
     int base = (step0 * kWaves + wave) * KT;
 #pragma unroll
     for (int n = 0; n < NS; ++n) page[n] = page_of(base + 16 * n);
@@ -364,24 +365,17 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
       __builtin_amdgcn_sched_barrier(0);
 
       const bool edge = base + KT > see_all;
-      float top[RT], vmax[RT];
+      float top[RT], tall = 0.0f;
       bool move = false;
+      if constexpr (I8) {   // the largest finite scale of the tile's values
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tall = fmaxf(tall, vsc[n][i] > kMaxScale ? 0.0f : vsc[n][i]);
+        tall = scale_exponent(row_max4(tall));
+      }
 #pragma unroll
       for (int x = 0; x < RT; ++x) {
-        if constexpr (I8) {
-          // The largest finite scale among the values the row sees: others must
-          // not take the range from its weights.
-          vmax[x] = 0.0f;
-#pragma unroll
-          for (int n = 0; n < NS; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const bool out = vsc[n][i] > kMaxScale || (edge && base + 16 * n + 4 * t + i >= lim[x]);
-              vmax[x] = fmaxf(vmax[x], out ? 0.0f : vsc[n][i]);
-            }
-          vmax[x] = row_max4(vmax[x]);
-          move |= vmax[x] > vref[x];
-        }
         top[x] = -INFINITY;
 #pragma unroll
         for (int n = 0; n < NS; ++n)
@@ -395,33 +389,36 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
             top[x] = fmaxf(top[x], s);
           }
         top[x] = row_max4(top[x]);
+        if constexpr (I8) {
+          float e = tall;
+          if (edge) {         // of those that the row sees
+            e = 0.0f;
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                e = fmaxf(e, vsc[n][i] > kMaxScale || base + 16 * n + 4 * t + i >= lim[x] ? 0.0f : vsc[n][i]);
+            e = scale_exponent(row_max4(e));
+          }
+          top[x] += e;
+        }
         move |= top[x] > mref[x] + kHead;
       }
       if (__ballot(move)) {
 #pragma unroll
         for (int x = 0; x < RT; ++x) {
-          float vscale = 1.0f;
-          if constexpr (I8) {
-            if (vmax[x] > vref[x]) {   // the next power of two
-              const float to = bits_float((float_bits(vmax[x]) & 0x7F800000u) + 0x00800000u);
-              vscale = vref[x] > 0.0f ? vref[x] / to : 0.0f;
-              vref[x] = to;
-            }
-          }
           const float to = top[x] > mref[x] + kHead ? top[x] - kStart : mref[x];
           const float f = __builtin_amdgcn_exp2f(mref[x] - to);
           mref[x] = to;
           l[x] *= f;
 #pragma unroll
-          for (int j = 0; j < DL; ++j) acc[x][j] *= f * vscale;
+          for (int j = 0; j < DL; ++j) acc[x][j] *= f;
         }
       }
       // Weights (B operands).
       half8_t pf[RT][NG];
 #pragma unroll
       for (int x = 0; x < RT; ++x) {
-        // the reciprocal of a power of two, exactly
-        const float vinv = I8 && vref[x] > 0.0f ? bits_float(0x7F000000u - float_bits(vref[x])) : 0.0f;
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -429,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
             float p = __builtin_amdgcn_exp2f(st[x][n][i] - mref[x]);
             l[x] += p;
             if constexpr (I8) {
-              const float w = p * (vsc[n][i] * vinv);
+              const float w = p * vsc[n][i];
               p = edge && base + 16 * n + 4 * t + i >= lim[x] ? 0.0f : w;
             }
             pf[x][n / 2][4 * (n % 2) + i] = (half_t)p;
@@ -447,38 +444,43 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
 #pragma unroll
               for (int w = 0; w < DL / 2; ++w) odd |= half2_not_finite(vr[g][s][w]);
           if (__ballot(odd)) {
-            // Rare.  Such values leave the matrix product; a product of their
-            // kinds (1: inf, 64: -inf, 4096: NaN; exact for 32 keys) with what
-            // each row sees says which reach it.
-            half8_t seen[RT][NG];
+            // Rare.  A product of their kinds (1: inf, 64: -inf, 4096: NaN; exact
+            // for 32 keys) with what each row sees says which sums they reach:
+            // bits, kept in this wave's part of s_o, that become values when the
+            // sums are complete.  Then they leave the tile.
+            uint32_t* note = (uint32_t*)s_o[wave] + lane;
+            uint32_t bits[3 * RT];
+#pragma unroll
+            for (int i = 0; i < 3 * RT; ++i) bits[i] = noted ? note[i * kWave] : 0u;
+            noted = true;
 #pragma unroll
             for (int x = 0; x < RT; ++x)
 #pragma unroll
-              for (int g = 0; g < NG; ++g)
+              for (int g = 0; g < NG; ++g) {
+                half8_t seen;
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                  seen[x][g][s] = (half_t)(base + 32 * g + 16 * (s / 4) + 4 * t + s % 4 < lim[x] ? 1.0f : 0.0f);
+                  seen[s] = (half_t)(base + 32 * g + 16 * (s / 4) + 4 * t + s % 4 < lim[x] ? 1.0f : 0.0f);
 #pragma unroll
-            for (int j = 0; j < DL; ++j)
+                for (int j = 0; j < DL; ++j) {
+                  u32x4_t w;
 #pragma unroll
-              for (int g = 0; g < NG; ++g) {
-                u32x4_t w;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  w[k] = kind_of((vr[g][2 * k][j / 2] >> (16 * (j % 2))) & 0xFFFFu) |
-                         kind_of((vr[g][2 * k + 1][j / 2] >> (16 * (j % 2))) & 0xFFFFu) << 16;
-#pragma unroll
-                for (int x = 0; x < RT; ++x) {
-                  const float4_t kinds = mfma16x16x32(__builtin_bit_cast(half8_t, w), seen[x][g], zero_float4());
+                  for (int k = 0; k < 4; ++k)
+                    w[k] = kind_of((vr[g][2 * k][j / 2] >> (16 * (j % 2))) & 0xFFFFu) |
+                           kind_of((vr[g][2 * k + 1][j / 2] >> (16 * (j % 2))) & 0xFFFFu) << 16;
+                  const float4_t kinds = mfma16x16x32(__builtin_bit_cast(half8_t, w), seen, zero_float4());
 #pragma unroll
                   for (int k = 0; k < 4; ++k) {
                     const int n = (int)kinds[k];
-                    if (n & 63) acc[x][j][k] += INFINITY;
-                    if (n & 4032) acc[x][j][k] -= INFINITY;
-                    if (n >> 12) acc[x][j][k] = NAN;
+                    const uint32_t bit = 1u << (4 * j + k);
+                    bits[3 * x] |= n & 63 ? bit : 0u;
+                    bits[3 * x + 1] |= n & 4032 ? bit : 0u;
+                    bits[3 * x + 2] |= n >> 12 ? bit : 0u;
                   }
                 }
               }
+#pragma unroll
+            for (int i = 0; i < 3 * RT; ++i) note[i * kWave] = bits[i];
 #pragma unroll
             for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -520,16 +522,31 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
       __builtin_amdgcn_sched_barrier(0);
     }
 
+    if (!I8 && noted) {
+      const uint32_t* note = (const uint32_t*)s_o[wave] + lane;
+#pragma unroll
+      for (int x = 0; x < RT; ++x) {
+        const uint32_t inf = note[3 * x * kWave], minus = note[(3 * x + 1) * kWave], nan = note[(3 * x + 2) * kWave];
+#pragma unroll
+        for (int j = 0; j < DL; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t bit = 1u << (4 * j + k);
+            if (inf & bit) acc[x][j][k] += INFINITY;
+            if (minus & bit) acc[x][j][k] -= INFINITY;
+            if (nan & bit) acc[x][j][k] = NAN;
+          }
+      }
+    }
     // Join the waves.  Lane (c, t) holds row c at d = DL (4 t + k) + j.
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
       l[x] = row_sum4(l[x]);
-      const float f = I8 ? vref[x] : 1.0f;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int j = 0; j < DL; j += 4) {
-          float4_t o = {acc[x][j][k] * f, acc[x][j + 1][k] * f, acc[x][j + 2][k] * f, acc[x][j + 3][k] * f};
+          float4_t o = {acc[x][j][k], acc[x][j + 1][k], acc[x][j + 2][k], acc[x][j + 3][k]};
           *(float4_t*)&s_o[wave][16 * x + c][DL * (4 * t + k) + j] = o;
         }
       if (t == 0) {

@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
   constexpr int CR = I8 ? RB / 64 : 1;        // 16-byte code loads of a lane and 16-key share
   __shared__ __attribute__((aligned(16))) half_t s_k[2][kKeys * D], s_v[2][kKeys * D];
   __shared__ __attribute__((aligned(16))) float s_ks[2][I8 ? kKeys : 4], s_vs[2][I8 ? kKeys : 4];
+  __shared__ __attribute__((aligned(16))) float s_tall[2][kWaves];   // largest finite scale of each wave's 16 values
   __shared__ uint32_t s_odd[I8 ? 1 : 6][kThreads];   // see note_odd
   __shared__ uint32_t s_arrived;
 
@@ -178,12 +179,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
     }
 
     float4_t acc[kRT][NJ];
-    float mref[kRT], l[kRT], vref[kRT];
+    float mref[kRT], l[kRT];
 #pragma unroll
     for (int x = 0; x < kRT; ++x) {
       mref[x] = kNone;
       l[x] = 0.0f;
-      vref[x] = 0.0f;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[x][j] = zero_float4();
     }
@@ -198,9 +198,15 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
     const int64_t head_row = (int64_t)head << a.page_log2;
     const unsigned char* kc = (const unsigned char*)a.kc + head_row * RB;
     const unsigned char* vc = (const unsigned char*)a.vc + head_row * RB;
-    u32x4_t kcode[CR], vcode[CR];
-    float kscale, vscale;
-    auto fetch = [&](int step, uint32_t page, int buf) {
+    // 8-bit tiles on their way: two sets of registers, so that a tile is
+    // requested two steps ahead.
+    struct Codes {
+      u32x4_t k[CR], v[CR];
+      float ks, vs;
+      uint32_t page;   // of the tile requested next into this set
+    };
+    Codes set[2];
+    auto fetch = [&](int step, uint32_t page, int buf, Codes& r8) {
       const int key = step * kKeys + 16 * wave;
       const uint64_t row = (uint64_t)min(page, (uint32_t)a.num_pages - 1) * page_rows + (uint32_t)(key & place_mask);
       const uint32_t in = (uint32_t)min(max(k1 - key, 0), 16);
@@ -208,14 +214,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
       if constexpr (I8) {
 #pragma unroll
         for (int i = 0; i < CR; ++i) {
-          kcode[i] = buffer_vec<16>(kr, 1024 * i + 16 * lane);
-          vcode[i] = buffer_vec<16>(vr, 1024 * i + 16 * lane);
+          r8.k[i] = buffer_vec<16>(kr, 1024 * i + 16 * lane);
+          r8.v[i] = buffer_vec<16>(vr, 1024 * i + 16 * lane);
         }
         const uint32_t so = lane < 16 ? 4 * lane : kOutOfRange;
         const __amdgpu_buffer_rsrc_t ksr = uniform_rsrc(a.ks + head_row + row, in * 4);
         const __amdgpu_buffer_rsrc_t vsr = uniform_rsrc(a.vs + head_row + row, in * 4);
-        kscale = bits_float(__builtin_amdgcn_raw_buffer_load_b32(ksr, so, 0, 0));
-        vscale = bits_float(__builtin_amdgcn_raw_buffer_load_b32(vsr, so, 0, 0));
+        r8.ks = bits_float(__builtin_amdgcn_raw_buffer_load_b32(ksr, so, 0, 0));
+        r8.vs = bits_float(__builtin_amdgcn_raw_buffer_load_b32(vsr, so, 0, 0));
       } else {
 #pragma unroll
         for (int i = 0; i < 16 * RB / 1024; ++i) {
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
       }
     };
     // 8-bit tiles: codes to fp16, into LDS.
-    auto put = [&](int buf) {
+    auto put = [&](int buf, const Codes& r8) {
       if constexpr (I8) {
 #pragma unroll
         for (int i = 0; i < CR; ++i) {
@@ -236,14 +242,18 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int to = r * D + ((unit + h) ^ swizzle(r)) * 8;
-            *(half8_t*)(s_k[buf] + to) = codes_to_half8(kcode[i][2 * h], kcode[i][2 * h + 1]);
-            *(half8_t*)(s_v[buf] + to) = codes_to_half8(vcode[i][2 * h], vcode[i][2 * h + 1]);
+            *(half8_t*)(s_k[buf] + to) = codes_to_half8(r8.k[i][2 * h], r8.k[i][2 * h + 1]);
+            *(half8_t*)(s_v[buf] + to) = codes_to_half8(r8.v[i][2 * h], r8.v[i][2 * h + 1]);
           }
         }
         if (lane < 16) {
-          s_ks[buf][16 * wave + lane] = kscale * a.scale;
-          s_vs[buf][16 * wave + lane] = vscale;
+          s_ks[buf][16 * wave + lane] = r8.ks * a.scale;
+          s_vs[buf][16 * wave + lane] = r8.vs;
         }
+        float tall = r8.vs > kMaxScale ? 0.0f : fmaxf(r8.vs, 0.0f);   // (lanes from 16 on hold zero)
+#pragma unroll
+        for (int o = 1; o < 16; o *= 2) tall = fmaxf(tall, __shfl_xor(tall, o));
+        if (lane == 0) s_tall[buf][wave] = tall;
       }
     };
 
@@ -298,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
             for (int i = 0; i < 4; ++i)
               if (base + 16 * n + i >= lim[x]) st[x][n][i] = -INFINITY;
       }
-      float top[kRT], vmax[kRT];
+      float top[kRT];
       bool move = false;
 #pragma unroll
       for (int x = 0; x < kRT; ++x) {
@@ -308,51 +318,44 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) top[x] = fmaxf(top[x], st[x][n][i]);
         top[x] = row_max4(top[x]);
-        if constexpr (!I8) top[x] *= a.scale;
-        move |= top[x] > mref[x] + kHead;
       }
       if constexpr (I8) {
-        // The largest finite scale of the values that each row sees.
-#pragma unroll
-        for (int x = 0; x < kRT; ++x) vmax[x] = 0.0f;
-#pragma unroll
-        for (int n = 0; n < kNS; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float v = vs[n][i] > kMaxScale ? 0.0f : vs[n][i];
-#pragma unroll
-            for (int x = 0; x < kRT; ++x)
-              vmax[x] = fmaxf(vmax[x], edge && base + 16 * n + i >= lim[x] ? 0.0f : v);
-          }
+        const float4_t w = *(const float4_t*)s_tall[buf];
+        const float tall = scale_exponent(fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])));
 #pragma unroll
         for (int x = 0; x < kRT; ++x) {
-          vmax[x] = row_max4(vmax[x]);
-          move |= vmax[x] > vref[x];
+          float e = tall;
+          if (edge) {         // of the values that the row sees
+            e = 0.0f;
+#pragma unroll
+            for (int n = 0; n < kNS; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                e = fmaxf(e, vs[n][i] > kMaxScale || base + 16 * n + i >= lim[x] ? 0.0f : vs[n][i]);
+            e = scale_exponent(row_max4(e));
+          }
+          top[x] += e;
         }
+      } else {
+#pragma unroll
+        for (int x = 0; x < kRT; ++x) top[x] *= a.scale;
       }
+#pragma unroll
+      for (int x = 0; x < kRT; ++x) move |= top[x] > mref[x] + kHead;
       if (__ballot(move)) {
 #pragma unroll
         for (int x = 0; x < kRT; ++x) {
-          float vscale = 1.0f;
-          if constexpr (I8) {
-            if (vmax[x] > vref[x]) {
-              const float to = bits_float((float_bits(vmax[x]) & 0x7F800000u) + 0x00800000u);
-              vscale = vref[x] > 0.0f ? vref[x] / to : 0.0f;
-              vref[x] = to;
-            }
-          }
           const float to = top[x] > mref[x] + kHead ? top[x] - kStart : mref[x];
           const float f = __builtin_amdgcn_exp2f(mref[x] - to);
           mref[x] = to;
           l[x] *= f;
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) acc[x][j] *= f * vscale;
+          for (int j = 0; j < NJ; ++j) acc[x][j] *= f;
         }
       }
       half8_t pf[kRT][kNG];
 #pragma unroll
       for (int x = 0; x < kRT; ++x) {
-        const float vinv = I8 && vref[x] > 0.0f ? bits_float(0x7F000000u - float_bits(vref[x])) : 0.0f;
 #pragma unroll
         for (int n = 0; n < kNS; ++n)
 #pragma unroll
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
             const float s = st[x][n][i];
             float p = __builtin_amdgcn_exp2f(I8 ? s - mref[x] : __builtin_fmaf(s, a.scale, -mref[x]));
             l[x] += p;
-            if constexpr (I8) p *= vs[n][i] * vinv;
+            if constexpr (I8) p *= vs[n][i];
             pf[x][n / 2][4 * (n % 2) + i] = (half_t)p;
           }
       }
@@ -465,32 +468,45 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
       }
     };
 
-    uint32_t page = page_of(step0);
-    if (step0 < step1) fetch(step0, page, step0 & 1);
-    page = page_of(step0 + 1);
-    for (int step = step0; step < step1; ++step) {
-      const int buf = step & 1;
-      put(buf);
-      __syncthreads();                          // the tile is in LDS; the other stage is free
-      if (step + 1 < step1) {
-        fetch(step + 1, page, buf ^ 1);
-        page = page_of(step + 2);
+    if constexpr (I8) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        set[i].page = page_of(step0 + i);
+        if (step0 + i < step1) fetch(step0 + i, set[i].page, 0, set[i]);
+        set[i].page = page_of(step0 + 2 + i);
       }
-      if constexpr (!I8)
+      auto one = [&](int step, int buf, Codes& r8) {
+        put(buf, r8);
+        __syncthreads();                        // the tile is in LDS; the other stage is free
+        if (step + 2 < step1) fetch(step + 2, r8.page, 0, r8);
+        r8.page = page_of(step + 4);
+        if (step * kKeys < see_any) compute(step, buf);
+      };
+      for (int step = step0; step < step1; step += 2) {
+        one(step, 0, set[0]);
+        if (step + 1 < step1) one(step + 1, 1, set[1]);
+      }
+    } else {
+      uint32_t page = page_of(step0);
+      if (step0 < step1) fetch(step0, page, step0 & 1, set[0]);
+      page = page_of(step0 + 1);
+      for (int step = step0; step < step1; ++step) {
+        const int buf = step & 1;
+        __syncthreads();                        // the tile is in LDS; the other stage is free
+        if (step + 1 < step1) {
+          fetch(step + 1, page, buf ^ 1, set[0]);
+          page = page_of(step + 2);
+        }
         if (step * kKeys + kKeys > tile_see_all) note_odd(step, buf);
-      if (step * kKeys < see_any) compute(step, buf);
+        if (step * kKeys < see_any) compute(step, buf);
+      }
     }
 
     // Lane (c, t) holds row c at d = 16 j + 4 t + i.
     if constexpr (!I8)
       if (noted) spread();
 #pragma unroll
-    for (int x = 0; x < kRT; ++x) {
-      l[x] = row_sum4(l[x]);
-      if constexpr (I8)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[x][j] *= vref[x];
-    }
+    for (int x = 0; x < kRT; ++x) l[x] = row_sum4(l[x]);
     auto write = [&]() {
 #pragma unroll
       for (int x = 0; x < kRT; ++x) {
