@@ -121,6 +121,13 @@ __device__ __forceinline__ typename Vec<BYTES>::type buffer_vec(__amdgpu_buffer_
   else return __builtin_bit_cast(vec_t, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0));
 }
 
+// A value the compiler knows nothing about: keeps the comparisons of a tile's
+// edge inside the (uniform) branches that need them.
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // Of an 8-bit cache's values: a power of two above their scales, as its exponent.
 // It enters the reference, so that weights times scales keep to fp16's range
 // (with a bound for values that vanish in an fp16 result anyway).

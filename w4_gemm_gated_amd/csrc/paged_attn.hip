@@ -381,23 +381,31 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
         for (int n = 0; n < NS; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float s = st[x][n][i];
-            if constexpr (I8) s *= kscale[n][i];
-            else s *= a.scale;
-            if (edge && base + 16 * n + 4 * t + i >= lim[x]) s = -INFINITY;
-            st[x][n][i] = s;
-            top[x] = fmaxf(top[x], s);
+            if constexpr (I8) st[x][n][i] *= kscale[n][i];
+            else st[x][n][i] *= a.scale;
           }
+        if (edge) {
+          const int left = opaque(lim[x] - base - 4 * t);
+#pragma unroll
+          for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (16 * n + i >= left) st[x][n][i] = -INFINITY;
+        }
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[x] = fmaxf(top[x], st[x][n][i]);
         top[x] = row_max4(top[x]);
         if constexpr (I8) {
           float e = tall;
           if (edge) {         // of those that the row sees
             e = 0.0f;
+            const int left = opaque(lim[x] - base - 4 * t);
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                e = fmaxf(e, vsc[n][i] > kMaxScale || base + 16 * n + 4 * t + i >= lim[x] ? 0.0f : vsc[n][i]);
+              for (int i = 0; i < 4; ++i) e = fmaxf(e, vsc[n][i] > kMaxScale || 16 * n + i >= left ? 0.0f : vsc[n][i]);
             e = scale_exponent(row_max4(e));
           }
           top[x] += e;
@@ -425,12 +433,19 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
           for (int i = 0; i < 4; ++i) {
             float p = __builtin_amdgcn_exp2f(st[x][n][i] - mref[x]);
             l[x] += p;
-            if constexpr (I8) {
-              const float w = p * vsc[n][i];
-              p = edge && base + 16 * n + 4 * t + i >= lim[x] ? 0.0f : w;
-            }
+            if constexpr (I8) p *= vsc[n][i];
             pf[x][n / 2][4 * (n % 2) + i] = (half_t)p;
           }
+        if constexpr (I8) {
+          if (edge) {   // a scale that a row must not see may be infinite or NaN
+            const int left = opaque(lim[x] - base - 4 * t);
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (16 * n + i >= left) pf[x][n / 2][4 * (n % 2) + i] = (half_t)0.0f;
+          }
+        }
       }
       // Values that some row must not see may be infinite or NaN, which a weight
       // of zero would not remove (codes are always finite).

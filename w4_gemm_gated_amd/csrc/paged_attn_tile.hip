@@ -301,12 +301,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
       }
       if (edge) {
 #pragma unroll
-        for (int x = 0; x < kRT; ++x)
+        for (int x = 0; x < kRT; ++x) {
+          const int left = opaque(lim[x] - base);
 #pragma unroll
           for (int n = 0; n < kNS; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (base + 16 * n + i >= lim[x]) st[x][n][i] = -INFINITY;
+              if (16 * n + i >= left) st[x][n][i] = -INFINITY;
+        }
       }
       float top[kRT];
       bool move = false;
@@ -327,11 +329,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
           float e = tall;
           if (edge) {         // of the values that the row sees
             e = 0.0f;
+            const int left = opaque(lim[x] - base);
 #pragma unroll
             for (int n = 0; n < kNS; ++n)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                e = fmaxf(e, vs[n][i] > kMaxScale || base + 16 * n + i >= lim[x] ? 0.0f : vs[n][i]);
+              for (int i = 0; i < 4; ++i) e = fmaxf(e, vs[n][i] > kMaxScale || 16 * n + i >= left ? 0.0f : vs[n][i]);
             e = scale_exponent(row_max4(e));
           }
           top[x] += e;
@@ -370,12 +372,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
       if constexpr (I8) {
         if (edge) {   // a scale that a row must not see may be infinite or NaN
 #pragma unroll
-          for (int x = 0; x < kRT; ++x)
+          for (int x = 0; x < kRT; ++x) {
+            const int left = opaque(lim[x] - base);
 #pragma unroll
             for (int n = 0; n < kNS; ++n)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                if (base + 16 * n + i >= lim[x]) pf[x][n / 2][4 * (n % 2) + i] = (half_t)0.0f;
+                if (16 * n + i >= left) pf[x][n / 2][4 * (n % 2) + i] = (half_t)0.0f;
+          }
         }
       }
       __builtin_amdgcn_sched_barrier(0);
