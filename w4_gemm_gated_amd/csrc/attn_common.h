@@ -78,6 +78,12 @@ __device__ __forceinline__ float row_sum4(float x) {
   return over_row(x, [](float a, float b) { return a + b; });
 }
 
+// The value of the lane N further on among 16 (a rotation in the vector unit).
+template <int N>
+__device__ __forceinline__ float rotate16(float x) {
+  return bits_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)float_bits(x), 0x120 + N, 0xF, 0xF, true));
+}
+
 // Codes b0 and b1 (bytes i of two words, sign included) -> two fp16 values.
 // Byte | 0x6400 with the sign bit flipped is the fp16 number 1024 + 128 + code.
 __device__ __forceinline__ uint32_t codes_to_half2(uint32_t bytes) {   // bytes 0x00b1'00b0

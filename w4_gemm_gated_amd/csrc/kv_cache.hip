@@ -37,8 +37,11 @@ __device__ __forceinline__ float row_max(float x) {
   return x;
 }
 
-// Eight fp16 values -> codes, and the row's scale (float32 divisions, so that
-// the codes are the definition's; rint ties to even).
+// Eight fp16 values -> codes, and the row's scale.  The codes are those of the
+// definition's float32 division: the product with the reciprocal is off by less
+// than 2^-15 (127 x three roundings of 2^-24), so it gives the same integer
+// unless it lies that near the middle of two, and only then (one wave in eight)
+// does the wave divide.
 template <int LANES>
 __device__ __forceinline__ u32x2_t quantise(const half8_t& h, float* scale) {
   float x[8], m = 0.0f;
@@ -50,15 +53,25 @@ __device__ __forceinline__ u32x2_t quantise(const half8_t& h, float* scale) {
   }
   m = row_max<LANES>(m);
   const float s = m / 127.0f;
-  u32x2_t w = {0u, 0u};
+  *scale = s;
+  const float r = 1.0f / s;
+  float c[8];
+  bool near = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    // s = 0, infinite or NaN: code 0 (0 * s is then 0 or NaN)
-    float c = s > 0.0f ? rintf(x[i] / s) : 0.0f;
-    c = c == c ? fminf(fmaxf(c, -127.0f), 127.0f) : 0.0f;
-    w[i / 4] |= ((uint32_t)(int32_t)c & 0xFFu) << (8 * (i % 4));
+    const float q = x[i] * r;
+    c[i] = rintf(q);
+    near |= !(fabsf(q - c[i]) < 0.5f - 0x1p-14f);   // (also s = 0, infinite or NaN)
   }
-  *scale = s;
+  if (near)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = s > 0.0f ? rintf(x[i] / s) : 0.0f;
+      c[i] = c[i] == c[i] ? fminf(fmaxf(c[i], -127.0f), 127.0f) : 0.0f;   // 0 * s is then 0 or NaN
+    }
+  u32x2_t w = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i / 4] |= ((uint32_t)(int32_t)c[i] & 0xFFu) << (8 * (i % 4));
   return w;
 }
 
@@ -140,8 +153,8 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(GatherK a) {
       vx = ((const half8_t*)a.vc)[at * LANES + c];
     }
   }
-  a.ko[u] = kx;
-  a.vo[u] = vx;
+  __builtin_nontemporal_store(kx, &a.ko[u]);   // written once, not read here
+  __builtin_nontemporal_store(vx, &a.vo[u]);
 }
 
 }  // namespace

@@ -44,6 +44,7 @@ constexpr int kKeys = 64;                   // of a tile
 constexpr int kNS = kKeys / 16;             // 16-key tiles
 constexpr int kNG = kKeys / 32;             // 32-key groups
 constexpr int kRT = kWaveRows / 16;
+constexpr int kSchedMatrix = 0x8, kSchedLdsRead = 0x100;   // instruction classes of the issue order
 constexpr uint64_t kMinPiece = 256;         // keys: a shorter piece costs more in its partial sums than it saves
 
 struct SeqT {
@@ -251,8 +252,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
           s_vs[buf][16 * wave + lane] = r8.vs;
         }
         float tall = r8.vs > kMaxScale ? 0.0f : fmaxf(r8.vs, 0.0f);   // (lanes from 16 on hold zero)
-#pragma unroll
-        for (int o = 1; o < 16; o *= 2) tall = fmaxf(tall, __shfl_xor(tall, o));
+        tall = fmaxf(tall, rotate16<8>(tall));
+        tall = fmaxf(tall, rotate16<4>(tall));
+        tall = fmaxf(tall, rotate16<2>(tall));
+        tall = fmaxf(tall, rotate16<1>(tall));
         if (lane == 0) s_tall[buf][wave] = tall;
       }
     };
@@ -288,7 +291,20 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
           for (int x = 0; x < kRT; ++x) st[x][n] = mfma16x16x32(kf, qf[x][m], st[x][n]);
         }
       }
+      // Issue order: four fragment reads ahead of the products that use them.
+      __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 4, 0);
+#pragma unroll
+      for (int i = 0; i < kNS * NM - 4; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kSchedMatrix, kRT, 0);
+        __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 1, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(kSchedMatrix, 4 * kRT, 0);
       __builtin_amdgcn_sched_barrier(0);
+      // The first values are requested under the softmax.
+      constexpr int AHEAD = 4;
+      half8_t first[AHEAD];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) first[j] = v_fragment(buf, 0, j);
       float4_t vs[kNS];
       if constexpr (I8) {
 #pragma unroll
@@ -388,10 +404,16 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
       for (int g = 0; g < kNG; ++g)
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          const half8_t vf = v_fragment(buf, g, j);
+          const half8_t vf = g == 0 && j < AHEAD ? first[j] : v_fragment(buf, g, j);
 #pragma unroll
           for (int x = 0; x < kRT; ++x) acc[x][j] = mfma16x16x32(vf, pf[x][g], acc[x][j]);
         }
+#pragma unroll
+      for (int i = 0; i < kNG * NJ - AHEAD; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 2, 1);
+        __builtin_amdgcn_sched_group_barrier(kSchedMatrix, kRT, 1);
+      }
+      __builtin_amdgcn_sched_group_barrier(kSchedMatrix, AHEAD * kRT, 1);
     };
 
     // Infinities and NaN among values that some row must not see (a weight of

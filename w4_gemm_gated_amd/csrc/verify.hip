@@ -26,18 +26,29 @@ constexpr int kUnroll = 4;                       // 16-byte loads per row in fli
 constexpr int kStep = kThreads * 4 * kUnroll;    // entries of one round
 typedef float f4u_t __attribute__((ext_vector_type(4), aligned(4)));   // rows start at any entry
 
-__device__ __forceinline__ uint64_t key_of(float w, float noise, int j) {
-  const float s = w / noise;
-  return w > 0.0f && s >= 0.0f ? ((uint64_t)float_bits(s) << 32) | (uint32_t)~j : 0ull;
-}
 __device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+
+// A thread's best entry so far; it sees rising j, so a tie keeps the lower one.
+struct Best {
+  float score = -1.0f;
+  int j = 0;
+  __device__ __forceinline__ void see(float w, float noise, int at) {
+    const float s = w / noise;
+    const bool better = w > 0.0f && s > score;
+    score = better ? s : score;
+    j = better ? at : j;
+  }
+  __device__ __forceinline__ uint64_t key() const {
+    return score >= 0.0f ? ((uint64_t)float_bits(score) << 32) | (uint32_t)~j : 0ull;
+  }
+};
 
 // Best key of the entries [beg, end) of one row.  MODE 0: w = p; 1: w = p - q;
 // 2: w = p - [j = x].
 template <int MODE>
-__device__ uint64_t scan(const float* __restrict__ p, const float* __restrict__ q, const float* __restrict__ e, int x,
-                         int beg, int end) {
-  uint64_t best = 0;
+__device__ __forceinline__ uint64_t scan(const float* __restrict__ p, const float* __restrict__ q,
+                                         const float* __restrict__ e, int x, int beg, int end) {
+  Best best;
   int j0 = beg + 4 * (int)threadIdx.x;
   for (; j0 + 4 * kThreads * (kUnroll - 1) + 3 < end; j0 += kStep) {
     f4u_t pv[kUnroll], qv[kUnroll], ev[kUnroll];
@@ -54,7 +65,7 @@ __device__ uint64_t scan(const float* __restrict__ p, const float* __restrict__ 
       for (int k = 0; k < 4; ++k) {
         const int j = j0 + i * 4 * kThreads + k;
         const float w = MODE == 0 ? pv[i][k] : MODE == 1 ? pv[i][k] - qv[i][k] : j == x ? pv[i][k] - 1.0f : pv[i][k];
-        best = max64(best, key_of(w, ev[i][k], j));
+        best.see(w, ev[i][k], j);
       }
   }
   for (; j0 < end; j0 += 4 * kThreads)
@@ -63,10 +74,10 @@ __device__ uint64_t scan(const float* __restrict__ p, const float* __restrict__ 
       const int j = j0 + k;
       if (j < end) {
         const float w = MODE == 0 ? p[j] : MODE == 1 ? p[j] - q[j] : j == x ? p[j] - 1.0f : p[j];
-        best = max64(best, key_of(w, e[j], j));
+        best.see(w, e[j], j);
       }
     }
-  return best;
+  return best.key();
 }
 
 // The workgroup's maximum, in every thread.
@@ -88,33 +99,32 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
   const int b = blockIdx.x / a.splits, part = blockIdx.x % a.splits;
   const int lane = threadIdx.x % kWave;
   const int K = a.drafts;
-  const int n = a.num_drafts ? min(max(a.num_drafts[b], 0), K) : K;
   const float* target = a.target + b * a.target_bs;
   const float* draft = a.draft ? a.draft + b * a.draft_bs : nullptr;
   const int32_t* drafted = a.drafted + (int64_t)b * K;
 
   // Kept tokens: lanes take one drafted token each, the first refusal counts.
-  int kept = n;
-  for (int i0 = 0; i0 < n; i0 += kWave) {
-    const int i = i0 + lane;
-    bool ok = true;
-    if (i < n) {
-      const int x = drafted[i];
-      ok = x >= 0 && x < a.vocab;
-      if (ok) {
-        const float q = draft ? draft[i * a.draft_rs + x] : 1.0f;
-        ok = a.u[(int64_t)b * K + i] * q < target[i * a.target_rs + x];
-      }
-    }
-    const uint64_t refused = __ballot(!ok);
-    if (refused) {
-      kept = i0 + __builtin_ctzll(refused);
+  // (The token, its random number and the sequence's length are requested
+  // together, whether the length needs them or not.)
+  int n = K, kept = -1;
+  for (int i0 = 0; i0 < K; i0 += kWave) {
+    const int i = min(i0 + lane, K - 1);
+    const int x = drafted[i];
+    const float u = a.u[(int64_t)b * K + i];
+    if (i0 == 0 && a.num_drafts) n = min(max(a.num_drafts[b], 0), K);
+    const bool in = x >= 0 && x < a.vocab;
+    const float q = draft && in ? draft[i * a.draft_rs + x] : 1.0f;
+    const float p = in ? target[i * a.target_rs + x] : 0.0f;
+    const uint64_t stop = __ballot(i0 + lane >= n || !(u * q < p));
+    if (stop) {
+      kept = min(i0 + __builtin_ctzll(stop), n);
       break;
     }
   }
+  if (kept < 0) kept = n;
 
   // The race over this workgroup's share.
-  const int share = ((a.vocab + a.splits - 1) / a.splits + 3) / 4 * 4;
+  const int share = (int)((((int64_t)a.vocab + a.splits - 1) / a.splits + 3) / 4 * 4);
   const int beg = (int)min((int64_t)part * share, (int64_t)a.vocab);
   const int end = (int)min((int64_t)beg + share, (int64_t)a.vocab);
   const float* p = target + kept * a.target_rs;
@@ -154,12 +164,12 @@ hipError_t launch_verify(const VerifyArgs& a, void* stream) {
   return hipGetLastError();
 }
 
-// Workgroups per sequence: a round (kStep entries) each at least, and about
-// eight workgroups per CU in all.  Sequences past the header's counters have
+// Workgroups per sequence: a round (kStep entries) each at least, and the four
+// workgroups per CU that the GPU holds at once.  Sequences past the header's counters have
 // a workgroup each.
 int verify_splits(const spear_verify_desc_t& d, int cus) {
   if (d.batch > (int)kMaxEcTiles) return 1;
-  const int64_t rounds = ceil_div(d.vocab, kStep), fill = ceil_div((int64_t)8 * cus, d.batch > 0 ? d.batch : 1);
+  const int64_t rounds = ceil_div(d.vocab, kStep), fill = ceil_div((int64_t)4 * cus, d.batch > 0 ? d.batch : 1);
   return (int)(rounds < fill ? rounds : fill);
 }
 

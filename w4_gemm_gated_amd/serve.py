@@ -16,6 +16,8 @@ import math
 
 import torch
 
+import w4_gemm_gated_amd as _pkg
+
 from . import _binding
 from ._binding import AttentionDesc, KvDesc, VerifyDesc
 
@@ -24,8 +26,7 @@ __all__ = ["spear_kv_cache", "spear_kv_append", "spear_kv_gather", "spear_paged_
 _KV_DTYPES = {torch.float16: 0, torch.int8: 1}
 
 
-def _check(t, name, dtype, dims, device):
-    """A GPU tensor of this type; contiguity is checked apart, where it matters."""
+def _refuse(t, name, dtype, dims, device):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -34,12 +35,22 @@ def _check(t, name, dtype, dims, device):
         raise ValueError(f"{name} must have {dims} dimensions")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+# Small calls take about as long on the host as on the GPU: the checks look at
+# each tensor once, and only a failing one asks what is wrong with it.
+def _check(t, name, dtype, dims, device):
+    """A GPU tensor of this type."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == dims and t.device == device):
+        _refuse(t, name, dtype, dims, device)
 
 
 def _dense(t, name, dtype, dims, device):
-    _check(t, name, dtype, dims, device)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    """.. that is contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == dims and t.device == device
+            and t.is_contiguous()):
+        _refuse(t, name, dtype, dims, device)
 
 
 def _rows(t, name, dtype, device):
@@ -52,6 +63,8 @@ def _rows(t, name, dtype, device):
 
 
 def _kv_desc(k_cache, v_cache, k_scale, v_scale):
+    """The cache's (type, num_pages, kv_heads, page_size, head_dim), its device, and
+    its tensors' addresses."""
     if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda:
         raise ValueError("k_cache must be a GPU tensor")
     dev, dt = k_cache.device, k_cache.dtype
@@ -59,30 +72,62 @@ def _kv_desc(k_cache, v_cache, k_scale, v_scale):
         raise TypeError(f"k_cache must be torch.float16 or torch.int8, got {dt}")
     _dense(k_cache, "k_cache", dt, 4, dev)
     _dense(v_cache, "v_cache", dt, 4, dev)
-    if v_cache.shape != k_cache.shape:
+    shape = k_cache.shape
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have the same shape")
-    pages, heads, page, dim = k_cache.shape
+    at = (k_cache.data_ptr(), v_cache.data_ptr(), None, None)
     if dt is torch.int8:
         for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if s is None:
                 raise ValueError(f"{name} must be given with an int8 cache")
             _dense(s, name, torch.float32, 3, dev)
-            if s.shape != (pages, heads, page):
+            if s.shape != shape[:3]:
                 raise ValueError(f"{name} must be [num_pages, kv_heads, page_size]")
-    return KvDesc(_KV_DTYPES[dt], pages, heads, dim, page), dev
+        at = (at[0], at[1], k_scale.data_ptr(), v_scale.data_ptr())
+    return (_KV_DTYPES[dt], *shape), dev, at
 
 
 def _p(t):
     return t.data_ptr() if t is not None else None
 
 
+# torch.cuda.current_stream() makes an object of the stream; only its handle is
+# needed, which this gives in a thirtieth of the time where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
 
 
-def _scratch(nbytes, device):
-    from . import _workspace
-    return _workspace(nbytes, device)
+# What follows from a call's sizes alone is made once for them: the descriptor
+# (never written to again), and the bytes of workspace that it needs.
+_plans = {}
+
+
+def _plan(key, make):
+    p = _plans.get(key)
+    if p is None:
+        if len(_plans) >= 4096:
+            _plans.clear()
+        d, ask, where = make()
+        nb = ctypes.c_size_t(0)
+        if ask is not None:
+            _binding.check(ask(ctypes.byref(d), ctypes.byref(nb)), where)
+        p = _plans[key] = (d, ctypes.byref(d), nb.value)
+    return p
+
+
+def _kv_struct(kv):
+    return KvDesc(kv[0], kv[1], kv[2], kv[4], kv[3])
+
+
+def _scratch(n, device, stream):
+    """The cached workspace of the stream, as the linear layer's."""
+    if n == 0:
+        return None
+    ws = _pkg._workspaces.get((device.index, stream))
+    return ws if ws is not None and ws.numel() >= n else _pkg._workspace(n, device)
 
 
 def spear_kv_cache(num_pages, kv_heads, head_dim, page_size=16, dtype=torch.float16, device="cuda"):
@@ -103,15 +148,16 @@ def spear_kv_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
     a joint projection); slots int64 [T]: page * page_size + place, or -1 for
     rows that are not written.
     """
-    kv, dev = _kv_desc(k_cache, v_cache, k_scale, v_scale)
+    kv, dev, at = _kv_desc(k_cache, v_cache, k_scale, v_scale)
     kt, kh = _rows(k, "k", torch.float16, dev)
     vt, vh = _rows(v, "v", torch.float16, dev)
     _dense(slots, "slots", torch.int64, 1, dev)
     T = slots.shape[0]
-    if k.shape != (T, kv.kv_heads, kv.head_dim) or v.shape != k.shape:
+    if k.shape != (T, kv[2], kv[4]) or v.shape != k.shape:
         raise ValueError("k and v must be [T, kv_heads, head_dim] with T slots")
-    st = _binding.load().spear_kv_append(ctypes.byref(kv), T, _p(k), kt, kh, _p(v), vt, vh, _p(slots), _p(k_cache),
-                                         _p(v_cache), _p(k_scale), _p(v_scale), _stream(dev))
+    d = _plan(kv, lambda: (_kv_struct(kv), None, None))
+    st = _binding.load().spear_kv_append(d[1], T, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                                         slots.data_ptr(), *at, _stream(dev))
     _binding.check(st, "spear_kv_append")
 
 
@@ -121,13 +167,13 @@ def spear_kv_gather(k_cache, v_cache, block_table, cu_kv, rows, k_scale=None, v_
 
     block_table int32 [B, max_pages]; cu_kv int32 [B + 1].
     """
-    kv, dev = _kv_desc(k_cache, v_cache, k_scale, v_scale)
+    kv, dev, at = _kv_desc(k_cache, v_cache, k_scale, v_scale)
     _dense(block_table, "block_table", torch.int32, 2, dev)
     _dense(cu_kv, "cu_kv", torch.int32, 1, dev)
     B, rows = block_table.shape[0], int(rows)
     if cu_kv.shape[0] != B + 1:
         raise ValueError("cu_kv must have one entry more than block_table has rows")
-    shape = (rows, kv.kv_heads, kv.head_dim)
+    shape = (rows, kv[2], kv[4])
     out = []
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         if t is None:
@@ -137,9 +183,9 @@ def spear_kv_gather(k_cache, v_cache, block_table, cu_kv, rows, k_scale=None, v_
             if t.shape != shape:
                 raise ValueError(f"{name} must be [rows, kv_heads, head_dim]")
         out.append(t)
-    st = _binding.load().spear_kv_gather(ctypes.byref(kv), B, rows, _p(block_table), block_table.shape[1], _p(cu_kv),
-                                         _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale), _p(out[0]), _p(out[1]),
-                                         _stream(dev))
+    d = _plan(kv, lambda: (_kv_struct(kv), None, None))
+    st = _binding.load().spear_kv_gather(d[1], B, rows, block_table.data_ptr(), block_table.shape[1],
+                                         cu_kv.data_ptr(), *at, out[0].data_ptr(), out[1].data_ptr(), _stream(dev))
     _binding.check(st, "spear_kv_gather")
     return out[0], out[1]
 
@@ -155,14 +201,14 @@ def spear_paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q
     sequence's new tokens; scale defaults to 1 / sqrt(head_dim).  `workspace`
     (uint8) defaults to the cached one of the current stream.
     """
-    kv, dev = _kv_desc(k_cache, v_cache, k_scale, v_scale)
+    kv, dev, at = _kv_desc(k_cache, v_cache, k_scale, v_scale)
     qt, qh = _rows(q, "q", torch.float16, dev)
     _dense(block_table, "block_table", torch.int32, 2, dev)
     _dense(cu_q, "cu_q", torch.int32, 1, dev)
     _dense(kv_lens, "kv_lens", torch.int32, 1, dev)
     B, pages = block_table.shape
     total, heads, dim = q.shape
-    if dim != kv.head_dim or kv_lens.shape[0] != B or cu_q.shape[0] != B + 1:
+    if dim != kv[4] or kv_lens.shape[0] != B or cu_q.shape[0] != B + 1:
         raise ValueError("need q [total_q, q_heads, head_dim], block_table [B, max_pages], cu_q [B + 1], kv_lens [B]")
     if out is None:
         out = torch.empty((total, heads, dim), dtype=torch.float16, device=dev)
@@ -172,18 +218,18 @@ def spear_paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q
             raise ValueError("out must have the shape of q")
     if B == 0 or total == 0:
         return out
-    lib = _binding.load()
-    d = AttentionDesc(kv, B, total, int(max_q), pages, heads, 1.0 / math.sqrt(dim) if scale is None else float(scale), 0)
+    lib, stream = _binding.load(), _stream(dev)
+    max_q, scale = int(max_q), 1.0 / math.sqrt(dim) if scale is None else float(scale)
+    d = _plan((kv, dev.index, B, total, max_q, pages, heads, scale), lambda: (
+        AttentionDesc(_kv_struct(kv), B, total, max_q, pages, heads, scale, 0),
+        lib.spear_attention_workspace_bytes, "spear_paged_attention"))
     if workspace is None:
-        nb = ctypes.c_size_t(0)
-        _binding.check(lib.spear_attention_workspace_bytes(ctypes.byref(d), ctypes.byref(nb)),
-                       "spear_attention_workspace_bytes")
-        workspace = _scratch(nb.value, dev)
+        workspace = _scratch(d[2], dev, stream)
     else:
         _dense(workspace, "workspace", torch.uint8, 1, dev)
-    st = lib.spear_paged_attention(ctypes.byref(d), _p(q), qt, qh, _p(cu_q), _p(kv_lens), _p(block_table), pages,
-                                   _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale), _p(out), _p(workspace),
-                                   workspace.numel() if workspace is not None else 0, _stream(dev))
+    st = lib.spear_paged_attention(d[1], q.data_ptr(), qt, qh, cu_q.data_ptr(), kv_lens.data_ptr(),
+                                   block_table.data_ptr(), pages, *at, out.data_ptr(), workspace.data_ptr(),
+                                   workspace.numel(), stream)
     _binding.check(st, "spear_paged_attention")
     return out
 
@@ -226,17 +272,16 @@ def spear_verify_draft(target, draft, drafted, u, noise, num_drafts=None, accept
                 raise ValueError(f"{name} must be {list(shape)}")
     accepted = torch.empty(B, dtype=torch.int32, device=dev) if accepted is None else accepted
     tokens = torch.empty((B, K1), dtype=torch.int32, device=dev) if tokens is None else tokens
-    lib = _binding.load()
-    d = VerifyDesc(B, K, V, 0)
+    lib, stream = _binding.load(), _stream(dev)
+    d = _plan(("verify", dev.index, B, K, V),
+              lambda: (VerifyDesc(B, K, V, 0), lib.spear_verify_workspace_bytes, "spear_verify_draft"))
     if workspace is None:
-        nb = ctypes.c_size_t(0)
-        _binding.check(lib.spear_verify_workspace_bytes(ctypes.byref(d), ctypes.byref(nb)),
-                       "spear_verify_workspace_bytes")
-        workspace = _scratch(nb.value, dev)
+        workspace = _scratch(d[2], dev, stream)
     else:
         _dense(workspace, "workspace", torch.uint8, 1, dev)
-    st = lib.spear_verify_draft(ctypes.byref(d), _p(target), tb, tr, _p(draft), db, dr, _p(drafted), _p(u), _p(noise),
-                                _p(num_drafts), _p(accepted), _p(tokens), _p(workspace),
-                                workspace.numel() if workspace is not None else 0, _stream(dev))
+    st = lib.spear_verify_draft(d[1], target.data_ptr(), tb, tr, _p(draft), db, dr, drafted.data_ptr(),
+                                u.data_ptr(), noise.data_ptr(), _p(num_drafts), accepted.data_ptr(),
+                                tokens.data_ptr(), _p(workspace), workspace.numel() if workspace is not None else 0,
+                                stream)
     _binding.check(st, "spear_verify_draft")
     return accepted, tokens
