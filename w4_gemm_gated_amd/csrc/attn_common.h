@@ -16,11 +16,11 @@ struct AttnK {
   const void *kc, *vc;
   const float *ks, *vs;
   half_t* out;
-  float* part;          // [2 x workgroups] partial results
-  uint32_t* counters;   // [workgroups], zero before and after
+  float* part;          // partial results, one for each piece of a split row tile
+  uint32_t* counters;   // zero before and after
   int32_t batch, total_q, q_heads, kv_heads, group, max_kv, page_log2, num_pages;
   int32_t part_bytes;
-  int32_t held;         // workgroups of 128-row tiles that the GPU holds at once
+  int32_t cus, min_piece;   // compute units planned for; fewest keys of a piece
   int32_t rows_from, rows_to;   // sequences with more rows than the one and no more than the other are this launch's
   float scale;                  // |scale| * log2(e)
   int32_t negate;               // the scale is negative: queries enter with the other sign
@@ -38,15 +38,6 @@ constexpr float kHead = 14.0f;       // a maximum this far above the reference m
 constexpr float kStart = 6.0f;       // .. to this far below the maximum
 constexpr float kMaxScale = 1e30f;   // scales above this do not enter the reference
 
-__device__ __forceinline__ uint32_t wave_scan(uint32_t x, int lane) {
-#pragma unroll
-  for (int o = 1; o < kWave; o *= 2) {
-    const uint32_t y = __shfl_up(x, o);
-    if (lane >= o) x += y;
-  }
-  return x;
-}
-
 // A value that all lanes hold alike, moved to a scalar register: addresses and
 // bounds made of it then are scalar too (a division leaves it in a vector one).
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -56,6 +47,128 @@ __device__ __forceinline__ uint32_t uniform(uint32_t x) { return (uint32_t)__bui
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base, uint32_t bytes) {
   const uint64_t p = (uint64_t)base;
   return make_rsrc((const void*)((uint64_t)uniform((uint32_t)(p >> 32)) << 32 | uniform((uint32_t)p)), uniform(bytes));
+}
+
+// ------------------------------------------------------------- the schedule
+//
+// An item of work is a row tile of a kv head and its keys, or a piece of them:
+// pieces of one call have the same length, which follows from the total work
+// and from how many items the GPU should get.  The lengths are on the device, so
+// every workgroup finds its item by itself, with a scan over the sequences (64 a
+// step).
+
+// Sum over the lanes up to and with this one, in the vector unit.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t add_from(uint32_t x) {
+  return x + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+  x = add_from<0x111, 0xF>(x);   // 1, 2, 4, 8 lanes below within 16
+  x = add_from<0x112, 0xF>(x);
+  x = add_from<0x114, 0xF>(x);
+  x = add_from<0x118, 0xF>(x);
+  x = add_from<0x142, 0xA>(x);   // lane 15 of the 16 below, then lane 31
+  return add_from<0x143, 0xC>(x);
+}
+__device__ __forceinline__ uint32_t wave_sum(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)wave_scan(x), kWave - 1);
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t max_from(uint32_t x) {
+  return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  x = max_from<0x111, 0xF>(x);
+  x = max_from<0x112, 0xF>(x);
+  x = max_from<0x114, 0xF>(x);
+  x = max_from<0x118, 0xF>(x);
+  x = max_from<0x142, 0xA>(x);
+  return (uint32_t)__builtin_amdgcn_readlane((int)max_from<0x143, 0xC>(x), kWave - 1);
+}
+
+struct Seq {
+  int q0, n, kv, tiles;   // first row of q, new tokens, cached tokens, row tiles
+};
+template <int R>
+__device__ __forceinline__ Seq sequence(const AttnK& a, int b) {
+  Seq s = {0, 0, 0, 0};
+  if (b < a.batch) {
+    const int c0 = a.cu[b], c1 = a.cu[b + 1], len = a.lens[b];
+    s.q0 = min(max(c0, 0), a.total_q);
+    s.n = min(max(c1, s.q0), a.total_q) - s.q0;
+    s.kv = min(max(len, 0), a.max_kv);
+    const int rows = s.n * a.group;
+    s.tiles = rows > a.rows_from && rows <= a.rows_to ? (rows + R - 1) / R : 0;
+  }
+  return s;
+}
+
+// The length of a piece in keys, a multiple of STEP: the work (in tiles times 64
+// keys) over `target` items, or kWhole for no pieces.
+constexpr int kWhole = 1 << 30;
+template <int STEP>
+__device__ __forceinline__ int piece_keys(const AttnK& a, uint32_t work, uint32_t target) {
+  // (a float's quotient, rounded up past its error: no 64-bit division)
+  const float q = (float)work * (float)a.kv_heads / (float)target;
+  const uint32_t per = uniform((uint32_t)fminf(q * (1.0f + 0x1p-20f) + 1.0f, 0x1p25f));
+  const uint32_t keys = max((min(per, (uint32_t)kWhole / 64) * 64 + STEP - 1) / STEP * STEP, (uint32_t)a.min_piece);
+  return (int)min(keys, (uint32_t)kWhole);
+}
+// What the sequences add up to: work, row tiles, and the most work of a tile.
+struct Load {
+  uint32_t work, tiles, longest;
+};
+template <int R>
+__device__ __forceinline__ Load load_of(const AttnK& a, const Seq& s0, int lane) {
+  Load l = {0, 0, 0};
+  for (int b0 = 0; b0 < a.batch; b0 += kWave) {
+    const Seq s = b0 == 0 ? s0 : sequence<R>(a, b0 + lane);
+    const uint32_t keys = (uint32_t)((s.kv + 63) / 64);
+    l.work += (uint32_t)s.tiles * keys;
+    l.tiles += (uint32_t)s.tiles;
+    l.longest = max(l.longest, s.tiles > 0 ? keys : 0u);
+  }
+  l.work = wave_sum(l.work);
+  l.tiles = wave_sum(l.tiles);
+  l.longest = wave_max(l.longest);
+  return l;
+}
+
+__device__ __forceinline__ int pieces_of(int kv, int piece) { return kv > piece ? (kv + piece - 1) / piece : 1; }
+
+// Item `index` of a kv head: sequence, row tile (the last, which sees the most
+// keys, first) and piece.  `slot` numbers the pieces of split row tiles: this
+// row tile's first.
+struct Item {
+  int b, q0, n, kv, rt, piece, slot;
+};
+template <int R>
+__device__ __forceinline__ bool find(const AttnK& a, const Seq& s0, int piece, uint32_t index, int lane, Item* it) {
+  uint32_t before = 0, slots = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kWave) {
+    const Seq s = b0 == 0 ? s0 : sequence<R>(a, b0 + lane);
+    const int np = pieces_of(s.kv, piece);
+    const uint32_t mine = (uint32_t)s.tiles * (uint32_t)np, split = np > 1 ? mine : 0;
+    const uint32_t upto = before + wave_scan(mine), slot_upto = slots + wave_scan(split);
+    const uint64_t past = __ballot(upto > index);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      const int tiles = __builtin_amdgcn_readlane(s.tiles, l), n = __builtin_amdgcn_readlane(np, l);
+      const int at = (int)(index - (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), l));
+      it->b = b0 + l;
+      it->q0 = __builtin_amdgcn_readlane(s.q0, l);
+      it->n = __builtin_amdgcn_readlane(s.n, l);
+      it->kv = __builtin_amdgcn_readlane(s.kv, l);
+      it->piece = tiles == 1 ? at : uniform(at / tiles);
+      it->rt = tiles - 1 - (at - it->piece * tiles);
+      it->slot = __builtin_amdgcn_readlane((int)(slot_upto - split), l) + it->rt * n;
+      return true;
+    }
+    before = (uint32_t)__builtin_amdgcn_readlane((int)upto, kWave - 1);
+    slots = (uint32_t)__builtin_amdgcn_readlane((int)slot_upto, kWave - 1);
+  }
+  return false;
 }
 
 // -------------------------------------------------------------- small pieces

@@ -28,14 +28,10 @@
 // so that the fp16 weights keep their range (sums and totals share the
 // reference, so it cancels in the end).
 //
-// The work is laid end to end, in steps of one key tile per wave, head after
-// head, sequence after sequence, and cut into equal shares, one per workgroup,
-// however the lengths differ.  The lengths are on the device, so every
-// workgroup finds its share by itself with a scan over the sequences (64 a
-// step).  A row tile that several workgroups share leaves one partial result
-// (fp32) per workgroup in the workspace; the last of them to arrive joins them
-// in order, so the result does not depend on scheduling.  Data passes between
-// workgroups as everywhere here: device-coherent stores, a drain, a counter.
+// Long sequences are cut into pieces (attn_common.h).  Pieces leave their sums in the workspace in
+// fp32, and the last of a row tile's to arrive joins them in order, so the result
+// does not depend on scheduling.  Data passes between workgroups as everywhere
+// here: device-coherent stores, a drain, a counter.
 #include <algorithm>
 
 #include "attn_common.h"
@@ -43,71 +39,9 @@
 namespace spear {
 namespace {
 
-// ------------------------------------------------------------- the schedule
-
-struct Seq {
-  int q0, n, kv, tiles, steps;   // first row of q, new tokens, cached tokens, row tiles, steps of each
-};
-
-// R rows a tile, KS keys a step.
-template <int R, int KS>
-__device__ __forceinline__ Seq sequence(const AttnK& a, int b) {
-  Seq s = {0, 0, 0, 0, 1};
-  if (b < a.batch) {
-    const int c0 = a.cu[b], c1 = a.cu[b + 1], len = a.lens[b];
-    s.q0 = min(max(c0, 0), a.total_q);
-    s.n = min(max(c1, s.q0), a.total_q) - s.q0;
-    s.kv = min(max(len, 0), a.max_kv);
-    const int rows = s.n * a.group;
-    s.tiles = rows > a.rows_from && rows <= a.rows_to ? (rows + R - 1) / R : 0;
-    s.steps = max((s.kv + KS - 1) / KS, 1);
-  }
-  return s;
-}
-
-// Equal shares of n steps for w workgroups: the first `more` take one step more.
-struct Shares {
-  uint32_t each, more;
-  __device__ uint32_t begin(uint32_t w) const { return w * each + min(w, more); }
-  __device__ uint32_t owner(uint32_t s) const {
-    const uint32_t head = more * (each + 1);
-    return s < head ? s / (each + 1) : more + (s - head) / each;
-  }
-};
-
-// The row tile that holds step p of a head's steps.
-struct Unit {
-  int b, q0, n, kv, steps, rt;
-  uint32_t first;   // its first step within the head
-};
-// `s0` holds the lanes' sequences of the first 64.
-template <int R, int KS>
-__device__ __forceinline__ Unit find(const AttnK& a, const Seq& s0, uint32_t p, int lane) {
-  Unit u = {0, 0, 0, 0, 1, 0, 0};
-  uint32_t before = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kWave) {
-    const Seq s = b0 == 0 ? s0 : sequence<R, KS>(a, b0 + lane);
-    const uint32_t mine = (uint32_t)s.tiles * (uint32_t)s.steps;
-    const uint32_t upto = before + wave_scan(mine, lane);
-    const uint64_t past = __ballot(upto > p);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      u.b = b0 + l;
-      u.q0 = __builtin_amdgcn_readlane(s.q0, l);
-      u.n = __builtin_amdgcn_readlane(s.n, l);
-      u.kv = __builtin_amdgcn_readlane(s.kv, l);
-      u.steps = __builtin_amdgcn_readlane(s.steps, l);
-      const uint32_t start = (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), l);
-      u.rt = (int)uniform((p - start) / (uint32_t)u.steps);
-      u.first = start + (uint32_t)u.rt * (uint32_t)u.steps;
-      break;
-    }
-    before = (uint32_t)__builtin_amdgcn_readlane((int)upto, kWave - 1);
-  }
-  return u;
-}
-
 // ------------------------------------------------------------ the main kernel
+
+constexpr uint32_t kMostItems = 4;   // items per CU aimed at, at most
 
 template <int D, bool I8, int RT>
 struct Shape {
@@ -122,8 +56,8 @@ struct Shape {
 // columns, several groups of threads take every so many pieces.  Loads of
 // eight pieces are in flight together.
 template <int D, int R, int SLOT>
-__device__ __forceinline__ void join(const AttnK& a, float* lds, int rows_here, int r0, int q0, int head, uint32_t w0,
-                                     int pieces) {
+__device__ __forceinline__ void join(const AttnK& a, float* lds, int rows_here, int r0, int q0, int head,
+                                     uint32_t slot0, int pieces) {
   const __amdgpu_buffer_rsrc_t pr = make_rsrc(a.part, (uint32_t)a.part_bytes);
   const int cols = rows_here * (D / 4);
   const int groups = cols < kThreads ? kThreads / cols : 1;
@@ -142,8 +76,7 @@ __device__ __forceinline__ void join(const AttnK& a, float* lds, int rows_here, 
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
           const int piece = i0 + i * groups;
-          // the first piece is its workgroup's second result, the others first ones
-          const uint32_t slot = 2 * (w0 + (uint32_t)piece) + (piece == 0 ? 1u : 0u);
+          const uint32_t slot = slot0 + (uint32_t)(piece * a.kv_heads);
           const uint32_t at = piece < pieces ? slot * (uint32_t)(SLOT * 4) : kOutOfRange;
           po[i] = buffer_load_f4_dev(pr, at + (uint32_t)(row * D + d) * 4);
           pm[i] = bits_float(__builtin_amdgcn_raw_buffer_load_b32(pr, at + (uint32_t)(R * D + row) * 4, 0, kCachePolicySc1));
@@ -217,41 +150,42 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane % 16, t = lane / 16;
 
-  // This workgroup's share.
-  const Seq seq0 = sequence<R, KS>(a, lane);
-  uint32_t per_head = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kWave) {
-    const Seq s = b0 == 0 ? seq0 : sequence<R, KS>(a, b0 + lane);
-    per_head += (uint32_t)s.tiles * (uint32_t)s.steps;
+  const Seq seq0 = sequence<R>(a, lane);
+  // Sequences of like length: no more than one item for each CU (two would share
+  // one), so the pieces are counted as if every row tile wasted one; and no
+  // pieces if the row tiles come out even on the CUs by themselves (64 sequences
+  // of 2k, two row tiles a CU: 111 us, 125 cut in two).  Otherwise four items for
+  // each CU, which end at different times, the next ones taking their places (96
+  // sequences of 64 .. 8192 at 1, 2, 3, 4, 7 items a CU: 120, 98, 99, 97, 95 us,
+  // and fp16 213, 200, 196, 191, 187; two of 54k and 60k at 200, 256, 264, 488,
+  // 720 items: 90, 93, 121, 99, 104).
+  const Load load = load_of<R>(a, seq0, lane);
+  const bool even = (uint64_t)load.longest * load.tiles * 2 <= (uint64_t)load.work * 3;
+  const uint32_t cus = (uint32_t)a.cus, units = load.tiles * (uint32_t)a.kv_heads;
+  uint32_t target = (RT == 1 ? kMostItems : 2) * cus;   // (two workgroups of 32 rows fill a CU)
+  if (even) {
+    if (units < cus) target = max(cus - units, cus / 4);
+    else if (((units + cus - 1) / cus) * cus * 7 <= units * 8) target = 0;
   }
-#pragma unroll
-  for (int o = 1; o < kWave; o *= 2) per_head += __shfl_xor(per_head, o);
-  per_head = uniform(per_head);
-  const uint32_t total = per_head * (uint32_t)a.kv_heads;
-  const uint32_t groups = min((uint32_t)gridDim.x, total);
-  if (blockIdx.x >= groups) return;
-  const uint32_t each = uniform(total / groups);
-  const Shares shares = {each, total - each * groups};
-  uint32_t at = shares.begin(blockIdx.x);
-  const uint32_t end = shares.begin(blockIdx.x + 1);
+  const int piece = target ? piece_keys<KS>(a, load.work, target) : kWhole;
+  const int head = (int)uniform(blockIdx.x % (uint32_t)a.kv_heads);
 
   const int place_mask = (1 << a.page_log2) - 1;
   const uint32_t koff = (uint32_t)(c * RB + 16 * t), voff = (uint32_t)(4 * t * RB + c * (DL * E));
 
-  while (at < end) {
-    const int head = (int)uniform(at / per_head);
-    const Unit u = find<R, KS>(a, seq0, at - (uint32_t)head * per_head, lane);
-    const uint32_t unit0 = (uint32_t)head * per_head + u.first;    // its first step of all
-    const int step0 = (int)(at - unit0);
-    const int step1 = (int)min((uint32_t)u.steps, end - unit0);
-    at = unit0 + (uint32_t)step1;
+  for (uint32_t index = blockIdx.x / (uint32_t)a.kv_heads;; index += gridDim.x / (uint32_t)a.kv_heads) {
+    Item u;
+    if (!find<R>(a, seq0, piece, uniform(index), lane, &u)) break;
     const int rows = u.n * a.group;                                // of the sequence
     const int r0 = u.rt * R;
     const int rows_here = min(R, rows - r0);
     const int pos0 = u.kv - u.n;                                   // position of token 0
     const int see_all = uniform(min(pos0 + r0 / a.group + 1, u.kv));   // keys below this are seen by every row
     const int k1 = uniform(min(max(pos0 + (r0 + rows_here - 1) / a.group + 1, 0), u.kv));   // .. from this on by none
-    const int k_stop = min(k1, step1 * KS);                        // this workgroup's keys end here
+    const int pieces = pieces_of(k1, piece);                       // of this row tile: those that hold keys
+    if (u.piece >= pieces) continue;
+    const int step0 = u.piece * (piece / KS);
+    const int k_stop = pieces == 1 ? k1 : min(k1, step0 * KS + piece);   // this workgroup's keys end here
 
     // Queries as B operands; the k order follows the K loads'.
     half8_t qf[RT][NM];
@@ -570,8 +504,9 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
       }
     }
     __syncthreads();
-    const bool whole = step0 == 0 && step1 == u.steps;
-    const uint32_t slot = 2 * blockIdx.x + (step0 == 0 ? 1u : 0u);
+    const bool whole = pieces == 1;
+    const uint32_t slot0 = (uint32_t)u.slot * (uint32_t)a.kv_heads + (uint32_t)head;   // pieces: kv_heads apart
+    const uint32_t slot = slot0 + (uint32_t)(u.piece * a.kv_heads);
     for (int v = threadIdx.x; v < rows_here * (D / 4); v += kThreads) {
       const int row = v / (D / 4), d = v % (D / 4) * 4;
       float M = s_m[0][row];
@@ -607,13 +542,13 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
     if (!whole) {
       drain_vm();
       __syncthreads();
-      const uint32_t w0 = shares.owner(unit0);
-      const int pieces = (int)(shares.owner(unit0 + (uint32_t)u.steps - 1) - w0) + 1;
-      if (threadIdx.x == 0) s_arrived = add_dev_u32(&a.counters[w0], 1u);
+      // (a split row tile has two slots at least)
+      uint32_t* counter = a.counters + (uint32_t)(u.slot / 2) * (uint32_t)a.kv_heads + (uint32_t)head;
+      if (threadIdx.x == 0) s_arrived = add_dev_u32(counter, 1u);
       __syncthreads();
       if (s_arrived == (uint32_t)pieces - 1) {
-        if (threadIdx.x == 0) st_dev_u32(&a.counters[w0], 0u);
-        join<D, R, SLOT>(a, &s_o[0][0][0], rows_here, r0, u.q0, head, w0, pieces);
+        if (threadIdx.x == 0) st_dev_u32(counter, 0u);
+        join<D, R, SLOT>(a, &s_o[0][0][0], rows_here, r0, u.q0, head, slot0, pieces);
       }
     }
     __syncthreads();
@@ -639,27 +574,27 @@ AttnPlan attn_plan(const spear_attention_desc_t& d, int cus) {
   p.both = p.tiles && (int64_t)d.total_q < d.batch * (int64_t)d.max_q;
   p.row_tiles = (p.tiles ? group : most_rows) > 16 ? 2 : 1;
   p.few_rows = 16 * p.row_tiles;
-  const int64_t R = p.few_rows, KS = 32 * kWaves;
-  // One share for each workgroup that the GPU holds at once; no more of them
-  // than there can be steps.
-  const int64_t held = (int64_t)(p.row_tiles == 1 ? 3 : 2) * cus;
+  const int64_t R = p.few_rows;
+  p.cus = std::min(cus, 512);
   const int64_t max_kv = (int64_t)d.max_pages * d.kv.page_size;
-  const int64_t steps = ceil_div(max_kv, KS);
-  const int64_t tiles = p.tiles ? d.batch : d.batch + (int64_t)d.total_q * group / R;
-  const int64_t most = tiles * steps * H;
-  p.fits = most <= INT32_MAX;
-  p.grid = p.tiles && !p.both ? 0 : (int)(most < held ? most : held);
-  if (p.grid > kMaxEcTiles) p.grid = kMaxEcTiles;
-  // Items of the tile kernel: row tiles, and their pieces where there are few:
-  // the pieces of split row tiles are fewer than twice the workgroups held.
-  p.tile_held = (int)std::min<int64_t>((int64_t)2 * cus, kMaxEcTiles / 2);
-  const int64_t row_tiles = d.batch + (int64_t)d.total_q * group / 128;
-  const int64_t items = std::min<int64_t>(row_tiles * H + p.tile_held, (int64_t)1 << 20);
-  p.tile_grid = !p.tiles ? 0 : (int)round_up(items, H);
+  const int64_t rows = (int64_t)d.total_q * group;
+  // The kernels count work (tiles times 64 keys) and items in 32 bits.
+  p.fits = (d.batch + rows / (p.tiles && !p.both ? 128 : R)) * ceil_div(max_kv, 64) <= INT32_MAX / 2;
+  const int64_t most = (int64_t)1 << 20;
+  // Items: row tiles, and the pieces of split ones: fewer than twice the items
+  // aimed at.  That many partial results have to fit, and half as many counters.
+  const int64_t pieces = (int64_t)kMostItems * p.cus, tile_pieces = (int64_t)2 * p.cus;
+  const int64_t tiles = p.tiles ? d.batch : d.batch + rows / R;
+  // (with few row tiles, items beyond two a CU are second ones of a workgroup:
+  // workgroups without any would only be in the others' way)
+  const int64_t items = tiles * H + pieces;
+  p.grid = p.tiles && !p.both ? 0
+           : (int)round_up(tiles * H < p.cus ? std::min(items, (int64_t)2 * p.cus) : std::min(items, most), H);
+  p.tile_grid = !p.tiles ? 0 : (int)round_up(std::min((d.batch + rows / 128) * H + tile_pieces, most), H);
   p.part = kSyncHeaderBytes;
-  p.part_bytes = (size_t)2 * p.grid * R * (dim + 2) * 4;
+  p.part_bytes = p.grid ? (size_t)2 * pieces * R * (dim + 2) * 4 : 0;
   p.tile_part = p.part + p.part_bytes;
-  p.tile_part_bytes = p.tiles ? (size_t)2 * p.tile_held * 128 * (dim + 2) * 4 : 0;
+  p.tile_part_bytes = p.tiles ? (size_t)2 * tile_pieces * 128 * (dim + 2) * 4 : 0;
   p.bytes = p.tile_part + p.tile_part_bytes;
   return p;
 }
@@ -674,6 +609,7 @@ hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* stream) 
   k.group = a.group; k.max_kv = a.max_kv; k.page_log2 = a.kv.page_log2; k.num_pages = a.kv.num_pages;
   // (a scale of zero: so small that every score counts as zero, yet a masked
   // one, minus infinity, stays one)
+  k.cus = p.cus;
   k.scale = a.scale == 0.0f ? 1e-37f : (a.scale < 0.0f ? -a.scale : a.scale) * kLog2e;
   k.negate = a.scale < 0.0f ? 1 : 0;
   const hipStream_t st = (hipStream_t)stream;
@@ -683,7 +619,7 @@ hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* stream) 
     k.rows_to = INT32_MAX;
     k.part = (float*)((char*)a.workspace + p.tile_part);
     k.part_bytes = (int32_t)p.tile_part_bytes;
-    k.held = p.tile_held;
+    k.min_piece = 256;   // shorter ones cost more in their partial sums than they save
     const hipError_t e = launch_attention_tiles(k, a.kv.dim, i8, p.tile_grid, st);
     if (e != hipSuccess || !p.both) return e;
   }
@@ -691,6 +627,7 @@ hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* stream) 
   k.rows_to = p.both ? p.few_rows : INT32_MAX;
   k.part = (float*)((char*)a.workspace + p.part);
   k.part_bytes = (int32_t)p.part_bytes;
+  k.min_piece = 512;   // four steps; 256 took 20 us instead of 15 for one sequence of 8k
   if (a.kv.dim == 64) {
     if (i8) return two ? launch<64, true, 2>(k, p, st) : launch<64, true, 1>(k, p, st);
     return two ? launch<64, false, 2>(k, p, st) : launch<64, false, 1>(k, p, st);

@@ -22,16 +22,14 @@
 // instructions, nearly the same time: two workgroups per CU let one's softmax
 // run under the other's products.
 //
-// A workgroup's item is a row tile of a kv head and its keys, or a piece of
-// them where there are too few tiles for the GPU (all pieces of a call have the
-// same length, so that the workgroups of a piece read the same keys).  Items
-// are numbered with the kv head fastest and a sequence's last row tile, which
+// Row tiles are cut into pieces (attn_common.h) where there are too few for the
+// GPU; workgroups of a piece read the same keys.  Items are numbered with the kv head fastest and a sequence's last row tile, which
 // sees the most keys, first: workgroups are dealt to the eight XCDs in turn, so
 // those that run at a time on one XCD walk the same head's keys together and
-// its L2 serves all but the first of them.  (Equal shares as in paged_attn.hip
-// were measured on 2048 tokens over 8192 keys: the workgroups of a head stood at
-// different keys, 4 MB of them, and 2.7 GB instead of 0.3 came from beyond the
-// L2: 633 us.)  Pieces leave their sums in the workspace; the last of a row
+// its L2 serves all but the first of them.  (Equal shares of the keys for all
+// workgroups were measured on 2048 tokens over 8192 keys: the workgroups of a
+// head stood at different keys, 4 MB of them, and 2.7 GB instead of 0.08 came
+// from beyond the L2: 633 us instead of 419 then.)  Pieces leave their sums in the workspace; the last of a row
 // tile's to arrive joins them in order.
 #include "attn_common.h"
 
@@ -45,57 +43,6 @@ constexpr int kNS = kKeys / 16;             // 16-key tiles
 constexpr int kNG = kKeys / 32;             // 32-key groups
 constexpr int kRT = kWaveRows / 16;
 constexpr int kSchedMatrix = 0x8, kSchedLdsRead = 0x100;   // instruction classes of the issue order
-constexpr uint64_t kMinPiece = 256;         // keys: a shorter piece costs more in its partial sums than it saves
-
-struct SeqT {
-  int q0, n, kv, tiles;
-};
-__device__ __forceinline__ SeqT sequence(const AttnK& a, int b) {
-  SeqT s = {0, 0, 0, 0};
-  if (b < a.batch) {
-    const int c0 = a.cu[b], c1 = a.cu[b + 1], len = a.lens[b];
-    s.q0 = min(max(c0, 0), a.total_q);
-    s.n = min(max(c1, s.q0), a.total_q) - s.q0;
-    s.kv = min(max(len, 0), a.max_kv);
-    const int rows = s.n * a.group;
-    s.tiles = rows > a.rows_from && rows <= a.rows_to ? (rows + kRows - 1) / kRows : 0;
-  }
-  return s;
-}
-
-__device__ __forceinline__ int pieces_of(int kv, int piece) { return kv > piece ? (kv + piece - 1) / piece : 1; }
-
-// Item `index` of a kv head: sequence, row tile and piece.  `slot` numbers the
-// split row tiles' pieces: this row tile's first.
-struct ItemT {
-  int b, q0, n, kv, rt, piece, slot;
-};
-__device__ __forceinline__ bool find(const AttnK& a, const SeqT& s0, int piece, uint32_t index, int lane, ItemT* it) {
-  uint32_t before = 0, slots = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kWave) {
-    const SeqT s = b0 == 0 ? s0 : sequence(a, b0 + lane);
-    const int np = pieces_of(s.kv, piece);
-    const uint32_t mine = (uint32_t)s.tiles * (uint32_t)np, split = np > 1 ? mine : 0;
-    const uint32_t upto = before + wave_scan(mine, lane), slot_upto = slots + wave_scan(split, lane);
-    const uint64_t past = __ballot(upto > index);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      const int tiles = __builtin_amdgcn_readlane(s.tiles, l), n = __builtin_amdgcn_readlane(np, l);
-      const int at = (int)(index - (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), l));
-      it->b = b0 + l;
-      it->q0 = __builtin_amdgcn_readlane(s.q0, l);
-      it->n = __builtin_amdgcn_readlane(s.n, l);
-      it->kv = __builtin_amdgcn_readlane(s.kv, l);
-      it->piece = uniform(at / tiles);
-      it->rt = tiles - 1 - (at - it->piece * tiles);
-      it->slot = __builtin_amdgcn_readlane((int)(slot_upto - split), l) + it->rt * n;
-      return true;
-    }
-    before = (uint32_t)__builtin_amdgcn_readlane((int)upto, kWave - 1);
-    slots = (uint32_t)__builtin_amdgcn_readlane((int)slot_upto, kWave - 1);
-  }
-  return false;
-}
 
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __fp16 fp16x4_t __attribute__((__vector_size__(4 * sizeof(__fp16))));
@@ -121,34 +68,20 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
   // reads), rows 0 .. 15 one unit (the plain ones).
   auto swizzle = [](int row) { return (UPR == 16 ? (row & 7) << 1 : (row & 6)) | ((row >> 3) & 1); };
 
-  // The pieces' length: none where the row tiles come near to filling the GPU.
-  const SeqT seq0 = sequence(a, lane);
-  uint64_t work = 0;
-  int tiles = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kWave) {
-    const SeqT s = b0 == 0 ? seq0 : sequence(a, b0 + lane);
-    work += (uint64_t)s.tiles * (uint64_t)s.kv;
-    tiles += s.tiles;
-  }
-#pragma unroll
-  for (int o = 1; o < kWave; o *= 2) {
-    work += __shfl_xor(work, o);
-    tiles += __shfl_xor(tiles, o);
-  }
-  int piece = 1 << 30;
-  if ((int64_t)tiles * a.kv_heads * 4 < (int64_t)a.held * 3) {
-    const uint64_t keys = (work * (uint64_t)a.kv_heads + (uint64_t)a.held - 1) / (uint64_t)a.held;
-    piece = (int)min(max((keys + kKeys - 1) / kKeys * kKeys, kMinPiece), (uint64_t)1 << 30);
-  }
-  piece = uniform(piece);
+  const Seq seq0 = sequence<kRows>(a, lane);
+  // Two workgroups run on a CU; no pieces if the row tiles alone are near to that.
+  const Load load = load_of<kRows>(a, seq0, lane);
+  const uint32_t held = 2 * (uint32_t)a.cus;
+  const int piece = (uint64_t)load.tiles * (uint32_t)a.kv_heads * 4 >= (uint64_t)held * 3
+                        ? kWhole : piece_keys<kKeys>(a, load.work, held);
 
   const int place_mask = (1 << a.page_log2) - 1;
   const uint32_t page_rows = (uint32_t)a.kv_heads << a.page_log2;
   const int head = (int)uniform(blockIdx.x % (uint32_t)a.kv_heads);
 
   for (uint32_t index = blockIdx.x / (uint32_t)a.kv_heads;; index += gridDim.x / (uint32_t)a.kv_heads) {
-    ItemT u;
-    if (!find(a, seq0, piece, uniform(index), lane, &u)) break;
+    Item u;
+    if (!find<kRows>(a, seq0, piece, uniform(index), lane, &u)) break;
     const int rows = u.n * a.group, r0 = u.rt * kRows;
     const int rows_here = min(kRows, rows - r0);
     const int pos0 = u.kv - u.n;
@@ -555,6 +488,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
       // A partial result, in the lanes' own order.
       const __amdgpu_buffer_rsrc_t pr = make_rsrc(a.part, (uint32_t)a.part_bytes);
       const uint32_t slot0 = (uint32_t)u.slot * (uint32_t)a.kv_heads + (uint32_t)head;   // pieces: kv_heads apart
+      // (a split row tile has two slots at least)
+      uint32_t* counter = a.counters + (uint32_t)(u.slot / 2) * (uint32_t)a.kv_heads + (uint32_t)head;
       const uint32_t own = (slot0 + (uint32_t)(u.piece * a.kv_heads)) * (uint32_t)(SLOT * 4);
       const uint32_t sums = (uint32_t)wave * (kRT * NJ * 1024) + (uint32_t)lane * 16;
       const uint32_t stats = (uint32_t)(kRows * D + wave * kWaveRows + c) * 4;
@@ -574,10 +509,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
       }
       drain_vm();
       __syncthreads();
-      if (threadIdx.x == 0) s_arrived = add_dev_u32(&a.counters[slot0], 1u);
+      if (threadIdx.x == 0) s_arrived = add_dev_u32(counter, 1u);
       __syncthreads();
       if (s_arrived == (uint32_t)pieces - 1) {
-        if (threadIdx.x == 0) st_dev_u32(&a.counters[slot0], 0u);
+        if (threadIdx.x == 0) st_dev_u32(counter, 0u);
         if (busy) {
           // All pieces in order, this workgroup's own among them.
 #pragma unroll

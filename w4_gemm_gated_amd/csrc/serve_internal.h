@@ -46,9 +46,8 @@ struct AttnPlan {
   bool both;          // .. and those of at most few_rows to the other one
   int row_tiles;      // 16-row operands a workgroup of the latter holds (1 or 2)
   int few_rows;       // 16 * row_tiles
-  int grid;           // workgroups of the latter, each with an equal share of the work
-  int tile_grid;      // workgroups of the former
-  int tile_held;      // .. that the GPU holds at once
+  int grid, tile_grid;   // workgroups of the latter and of the former
+  int cus;
   bool fits;          // the work can be counted in 32 bits
   size_t part, part_bytes;            // partial results in the workspace
   size_t tile_part, tile_part_bytes;
