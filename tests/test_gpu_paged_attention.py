@@ -338,3 +338,47 @@ def test_refusals():
     with pytest.raises(sp.SpearError, match="WORKSPACE"):
         call(table=big, workspace=torch.zeros(1 << 20, dtype=torch.uint8, device=DEV))
     assert call(q=a["q"][:0]).shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("batch,kv_heads,group,dim,q_most,kv_most", [
+    (150, 2, 4, 64, 1, 300), (300, 1, 1, 128, 1, 40), (90, 3, 20, 64, 1, 200), (70, 1, 40, 128, 1, 150),
+    (100, 2, 3, 128, 4, 120), (80, 1, 20, 64, 3, 90)])
+def test_large_batches(int8, batch, kv_heads, group, dim, q_most, kv_most):
+    """More sequences than one scan step takes; more query heads to a kv head than
+    16 and 32 rows; sequences without new tokens or without cached ones between."""
+    note(f"batch {batch} int8 {int8} kv_heads {kv_heads} group {group} dim {dim}")
+    rng = np.random.default_rng(batch + group)
+    q_lens = rng.integers(0 if batch != 90 else 1, q_most + 1, size=batch).tolist()
+    lens = np.exp(rng.uniform(0, math.log(kv_most), size=batch)).astype(int) + rng.integers(0, 2, size=batch)
+    lens[::17] = 0
+    c = make(rng, q_lens, lens.tolist(), kv_heads, group, dim, 16, int8)
+    check(c, run(c))
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("q_lens,lens,kv_heads,group,dim", [
+    ([300, 1, 1, 5, 1], [900, 2000, 30, 400, 1], 1, 2, 64),       # both kernels, the long one in pieces
+    ([300, 1, 1], [300, 700, 64], 2, 24, 64),                     # .. 32 rows for one token's heads
+    ([130, 90], [2500, 1300], 1, 1, 128),                         # row tiles in pieces, two lengths
+    ([64, 64, 64], [64, 1000, 129], 3, 4, 128),                   # tiles alone
+    ([33], [4000], 1, 1, 128), ([500], [500], 1, 5, 64)])
+def test_tiles_and_pieces(int8, q_lens, lens, kv_heads, group, dim):
+    note(f"tiles int8 {int8} q {q_lens} kv {lens} group {group} dim {dim}")
+    c = make(np.random.default_rng(sum(lens)), q_lens, lens, kv_heads, group, dim, 32, int8)
+    got = run(c)
+    check(c, got)
+    assert np.array_equal(got.view(np.uint16), run(c).view(np.uint16))
+
+
+def test_calls_on_one_workspace_do_not_meet():
+    """Calls of other shapes one after the other on the stream's workspace, which
+    the linear layer and the verification use too: counters are left at zero."""
+    note("shared workspace")
+    rng = np.random.default_rng(21)
+    cases = [make(rng, [1, 1], [4000, 90], 2, 4, 128, 16, True), make(rng, [200, 1], [1500, 2600], 1, 2, 64, 16, False),
+             make(rng, [6], [5000], 2, 4, 64, 16, True)]
+    want = [run(c) for c in cases]
+    for _ in range(3):
+        for c, w in zip(cases, want):
+            assert np.array_equal(run(c).view(np.uint16), w.view(np.uint16))
