@@ -87,7 +87,7 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
   return (uint32_t)__builtin_amdgcn_readlane((int)max_from<0x143, 0xC>(x), kWave - 1);
 }
 
-struct Seq {
+struct __attribute__((aligned(16))) Seq {
   int q0, n, kv, tiles;   // first row of q, new tokens, cached tokens, row tiles
 };
 template <int R>

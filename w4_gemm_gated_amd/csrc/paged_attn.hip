@@ -28,10 +28,17 @@
 // so that the fp16 weights keep their range (sums and totals share the
 // reference, so it cancels in the end).
 //
-// Long sequences are cut into pieces (attn_common.h).  Pieces leave their sums in the workspace in
-// fp32, and the last of a row tile's to arrive joins them in order, so the result
-// does not depend on scheduling.  Data passes between workgroups as everywhere
-// here: device-coherent stores, a drain, a counter.
+// The work is laid end to end, in steps of one key tile per wave, head after
+// head, sequence after sequence, and cut into equal shares, one per workgroup,
+// however the lengths differ.  The lengths are on the device, so every
+// workgroup finds its share by itself with a scan over the sequences.  Under
+// load a dependent load takes microseconds, so a workgroup finds the next row
+// tile of its share before it walks the present one, and requests the next one's
+// queries and first keys and values before it writes the present one's result.
+// A row tile that several workgroups share leaves one partial result (fp32) per
+// workgroup in the workspace; the last of them to arrive joins them in order, so
+// the result does not depend on scheduling.  Data passes between workgroups as
+// everywhere here: device-coherent stores, a drain, a counter.
 #include <algorithm>
 
 #include "attn_common.h"
@@ -41,7 +48,28 @@ namespace {
 
 // ------------------------------------------------------------ the main kernel
 
-constexpr uint32_t kMostItems = 4;   // items per CU aimed at, at most
+// Equal shares of n steps for w workgroups: the first `more` take one step more.
+struct Shares {
+  uint32_t each, more;
+  __device__ uint32_t begin(uint32_t w) const { return w * each + min(w, more); }
+  __device__ uint32_t owner(uint32_t s) const {
+    const uint32_t head = more * (each + 1);
+    return s < head ? s / (each + 1) : more + (s - head) / each;
+  }
+};
+
+constexpr int kSeqs = 512;   // sequences kept in LDS; more are read again where needed
+
+// Steps of KS keys that a sequence's row tile takes.
+template <int KS>
+__device__ __forceinline__ int steps_of(const Seq& s) { return max((s.kv + KS - 1) / KS, 1); }
+
+// A share's part of a row tile: steps [step0, step1) of its `steps`.
+struct Part {
+  int b, q0, head, pos0, rows, r0, rows_here, steps, step0, step1;
+  int see_all, k1, k_stop;   // keys below are seen by all rows; from here on by none; .. not this part's
+  uint32_t unit0;            // the row tile's first step of all
+};
 
 template <int D, bool I8, int RT>
 struct Shape {
@@ -51,13 +79,18 @@ struct Shape {
   static constexpr int SLOT = R * (D + 2);       // floats of a partial result: sums [R][D], references, totals
 };
 
+// A barrier for data in LDS alone: loads and stores in flight stay so.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // Joins the `pieces` partial results of a row tile (rows `rows_here` of them in
 // use) and writes the result.  Threads take four columns of a row each; with few
 // columns, several groups of threads take every so many pieces.  Loads of
 // eight pieces are in flight together.
 template <int D, int R, int SLOT>
-__device__ __forceinline__ void join(const AttnK& a, float* lds, int rows_here, int r0, int q0, int head,
-                                     uint32_t slot0, int pieces) {
+__device__ __forceinline__ void join(const AttnK& a, float* lds, int rows_here, int r0, int q0, int head, uint32_t w0,
+                                     int pieces) {
   const __amdgpu_buffer_rsrc_t pr = make_rsrc(a.part, (uint32_t)a.part_bytes);
   const int cols = rows_here * (D / 4);
   const int groups = cols < kThreads ? kThreads / cols : 1;
@@ -76,7 +109,8 @@ __device__ __forceinline__ void join(const AttnK& a, float* lds, int rows_here, 
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
           const int piece = i0 + i * groups;
-          const uint32_t slot = slot0 + (uint32_t)(piece * a.kv_heads);
+          // the first piece is its workgroup's second result, the others first ones
+          const uint32_t slot = 2 * (w0 + (uint32_t)piece) + (piece == 0 ? 1u : 0u);
           const uint32_t at = piece < pieces ? slot * (uint32_t)(SLOT * 4) : kOutOfRange;
           po[i] = buffer_load_f4_dev(pr, at + (uint32_t)(row * D + d) * 4);
           pm[i] = bits_float(__builtin_amdgcn_raw_buffer_load_b32(pr, at + (uint32_t)(R * D + row) * 4, 0, kCachePolicySc1));
@@ -143,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
   constexpr int OS = D + 4;                   // row stride of the sums in LDS
   __shared__ __attribute__((aligned(16))) float s_o[kWaves][R][OS];
   __shared__ float s_m[kWaves][R], s_l[kWaves][R];
+  __shared__ Seq s_seq[kSeqs];
   __shared__ uint32_t s_arrived;
   static_assert(sizeof(s_o) >= kThreads * 32, "the join's exchange fits");
 
@@ -150,92 +185,108 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane % 16, t = lane / 16;
 
-  const Seq seq0 = sequence<R>(a, lane);
-  // Sequences of like length: no more than one item for each CU (two would share
-  // one), so the pieces are counted as if every row tile wasted one; and no
-  // pieces if the row tiles come out even on the CUs by themselves (64 sequences
-  // of 2k, two row tiles a CU: 111 us, 125 cut in two).  Otherwise four items for
-  // each CU, which end at different times, the next ones taking their places (96
-  // sequences of 64 .. 8192 at 1, 2, 3, 4, 7 items a CU: 120, 98, 99, 97, 95 us,
-  // and fp16 213, 200, 196, 191, 187; two of 54k and 60k at 200, 256, 264, 488,
-  // 720 items: 90, 93, 121, 99, 104).
-  const Load load = load_of<R>(a, seq0, lane);
-  const bool even = (uint64_t)load.longest * load.tiles * 2 <= (uint64_t)load.work * 3;
-  const uint32_t cus = (uint32_t)a.cus, units = load.tiles * (uint32_t)a.kv_heads;
-  uint32_t target = (RT == 1 ? kMostItems : 2) * cus;   // (two workgroups of 32 rows fill a CU)
-  if (even) {
-    if (units < cus) target = max(cus - units, cus / 4);
-    else if (((units + cus - 1) / cus) * cus * 7 <= units * 8) target = 0;
+  // This workgroup's share.  Whole row tiles where those come out even on the
+  // workgroups: sequences of like length (64 of 2k, 512 row tiles: 112 us, 123 cut
+  // into 768 shares), or all so short that a join would cost more than it saves.
+  // Otherwise steps: as many shares as workgroups fit on the GPU (96 sequences of
+  // 64 .. 8192: 89 us, 97 in pieces of one length), or, with fewer row tiles than
+  // CUs, one for each CU, two where lengths differ much (two contexts of 54k and
+  // 60k at 200, 256, 488, 720: 90, 93, 99, 104 us; 24 drafts of 500 .. 6000 at 256,
+  // 340, 512, 800: 38, 36, 36, 38); but none of under four steps.
+  // (The sequences are kept in LDS: a load from memory for the next row tile would
+  // wait for all keys and values on their way.)
+  for (int b = threadIdx.x; b < kSeqs && b < (a.batch + kWave - 1) / kWave * kWave; b += kThreads)
+    s_seq[b] = sequence<R>(a, b);
+  __syncthreads();
+  auto seq_of = [&](int b) { return b < kSeqs ? s_seq[b] : sequence<R>(a, b); };
+  uint32_t steps = 0, tiles = 0, longest = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kWave) {
+    const Seq s = seq_of(b0 + lane);
+    const uint32_t n = (uint32_t)steps_of<KS>(s);
+    steps += (uint32_t)s.tiles * n;
+    tiles += (uint32_t)s.tiles;
+    longest = max(longest, s.tiles > 0 ? n : 0u);
   }
-  const int piece = target ? piece_keys<KS>(a, load.work, target) : kWhole;
-  const int head = (int)uniform(blockIdx.x % (uint32_t)a.kv_heads);
+  steps = wave_sum(steps);
+  tiles = wave_sum(tiles);
+  longest = wave_max(longest);
+  if (tiles == 0) return;
+  const uint32_t cus = (uint32_t)a.cus, units = tiles * (uint32_t)a.kv_heads;
+  const bool even = (uint64_t)longest * tiles * 2 <= (uint64_t)steps * 3;
+  const uint32_t rounds = (units + gridDim.x - 1) / gridDim.x;
+  const bool whole_tiles = longest <= 8 ? units <= gridDim.x
+                                        : even && units >= cus && (rounds == 1 || rounds * gridDim.x * 7 <= units * 8);
+  const uint32_t per_head = whole_tiles ? tiles : steps, total = per_head * (uint32_t)a.kv_heads;
+  uint32_t groups = whole_tiles ? min(units, gridDim.x)
+                    : min(min(gridDim.x, units >= cus ? gridDim.x : even ? cus : 2 * cus), max(units, total / 4));
+  if (blockIdx.x >= groups) return;
+  const uint32_t each = uniform(total / groups);
+  const Shares shares = {each, total - each * groups};
+  const uint32_t end = shares.begin(blockIdx.x + 1);
+
+  // The row tile that holds step (or is row tile) `at` of all.
+  auto find = [&](uint32_t at) {
+    Part u;
+    u.head = (int)uniform(at / per_head);
+    const uint32_t p = at - (uint32_t)u.head * per_head;
+    u.b = u.q0 = u.rows = u.r0 = u.pos0 = u.k1 = u.step0 = 0;
+    u.steps = 1;
+    u.unit0 = at;
+    int n = 0, kv = 0;
+    uint32_t before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kWave) {
+      const Seq s = seq_of(b0 + lane);
+      const uint32_t mine = (uint32_t)s.tiles * (whole_tiles ? 1u : (uint32_t)steps_of<KS>(s));
+      const uint32_t upto = before + wave_scan(mine);
+      const uint64_t past = __ballot(upto > p);
+      if (past) {
+        const int l = __builtin_ctzll(past);
+        n = __builtin_amdgcn_readlane(s.n, l);
+        kv = __builtin_amdgcn_readlane(s.kv, l);
+        u.b = b0 + l;
+        u.q0 = __builtin_amdgcn_readlane(s.q0, l);
+        u.steps = max((kv + KS - 1) / KS, 1);
+        const uint32_t off = p - (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), l);
+        const uint32_t rt = whole_tiles ? off
+                            : __builtin_amdgcn_readlane(s.tiles, l) == 1 ? 0u : uniform(off / (uint32_t)u.steps);
+        u.step0 = whole_tiles ? 0 : (int)(off - rt * (uint32_t)u.steps);
+        u.unit0 = at - (uint32_t)u.step0;
+        u.r0 = (int)rt * R;
+        break;
+      }
+      before = (uint32_t)__builtin_amdgcn_readlane((int)upto, kWave - 1);
+    }
+    u.rows = n * a.group;                                          // of the sequence
+    u.rows_here = min(R, u.rows - u.r0);
+    u.pos0 = kv - n;                                               // position of token 0
+    u.step1 = whole_tiles ? u.steps : (int)min((uint32_t)u.steps, end - u.unit0);
+    u.see_all = uniform(min(u.pos0 + u.r0 / a.group + 1, kv));
+    u.k1 = uniform(min(max(u.pos0 + (u.r0 + u.rows_here - 1) / a.group + 1, 0), kv));
+    u.k_stop = min(u.k1, u.step1 * KS);
+    return u;
+  };
 
   const int place_mask = (1 << a.page_log2) - 1;
   const uint32_t koff = (uint32_t)(c * RB + 16 * t), voff = (uint32_t)(4 * t * RB + c * (DL * E));
 
-  for (uint32_t index = blockIdx.x / (uint32_t)a.kv_heads;; index += gridDim.x / (uint32_t)a.kv_heads) {
-    Item u;
-    if (!find<R>(a, seq0, piece, uniform(index), lane, &u)) break;
-    const int rows = u.n * a.group;                                // of the sequence
-    const int r0 = u.rt * R;
-    const int rows_here = min(R, rows - r0);
-    const int pos0 = u.kv - u.n;                                   // position of token 0
-    const int see_all = uniform(min(pos0 + r0 / a.group + 1, u.kv));   // keys below this are seen by every row
-    const int k1 = uniform(min(max(pos0 + (r0 + rows_here - 1) / a.group + 1, 0), u.kv));   // .. from this on by none
-    const int pieces = pieces_of(k1, piece);                       // of this row tile: those that hold keys
-    if (u.piece >= pieces) continue;
-    const int step0 = u.piece * (piece / KS);
-    const int k_stop = pieces == 1 ? k1 : min(k1, step0 * KS + piece);   // this workgroup's keys end here
-
-    // Queries as B operands; the k order follows the K loads'.
-    half8_t qf[RT][NM];
-    int lim[RT];                                                   // keys below this are seen by the lane's row
-#pragma unroll
-    for (int x = 0; x < RT; ++x) {
-      const int r = r0 + 16 * x + c;
-      const bool ok = r < rows;
-      const int tok = ok ? r / a.group : 0, h = ok ? head * a.group + r % a.group : 0;
-      lim[x] = ok ? min(pos0 + tok + 1, k1) : k1;
-      const half_t* qp = a.q + (u.q0 + (int64_t)tok) * a.q_ts + h * a.q_hs;
-#pragma unroll
-      for (int m = 0; m < NM; ++m) {
-        const int d = I8 ? 64 * (m / 2) + 16 * t + 8 * (m % 2) : 32 * m + 8 * t;
-        qf[x][m] = ok ? query(qp + d, a.negate) : zero_half8();
-      }
-    }
-
-    float4_t acc[RT][DL];
-    float mref[RT], l[RT];
-#pragma unroll
-    for (int x = 0; x < RT; ++x) {
-      mref[x] = kNone;
-      l[x] = 0.0f;
-#pragma unroll
-      for (int j = 0; j < DL; ++j) acc[x][j] = zero_float4();
-    }
-
-    // Memory: a 16-key tile lies within one page, so its place is the same for
-    // all lanes.  Rows from k1 on lie outside the buffer and read as zeros; a
-    // tile past the share reads nothing.
-    // (constant address space and a scalar index: scalar loads, which the waits
-    // for keys and values do not count)
-    const scalar_i32_t* table = (const scalar_i32_t*)(uintptr_t)(a.table + (int64_t)uniform(u.b) * a.table_stride);
-    const int last_key = max(k1 - 1, 0);
-    auto page_of = [&](int key) {
-      return (uint32_t)table[uniform(min(key, last_key) >> a.page_log2)];
-    };
-    const int64_t head_row = (int64_t)head << a.page_log2;
-    const unsigned char* kc = (const unsigned char*)a.kc + head_row * RB;
-    const unsigned char* vc = (const unsigned char*)a.vc + head_row * RB;
-    const float* ks = I8 ? a.ks + head_row : nullptr;
-    const float* vs = I8 ? a.vs + head_row : nullptr;
-    const uint32_t page_rows = (uint32_t)a.kv_heads << a.page_log2;
-    u32x4_t kr[NS][KL];
-    vvec_t vr[NG][8];
-    float4_t ksc[NS], vsc[NS];
-    uint32_t page[NS], later_page[NS];   // of the tile requested next, and of the one after it
-    // Bytes of a 16-key tile's rows that hold keys of this workgroup's share.
-    auto load_k = [&](int base, const uint32_t* pages) {
+  // What is on its way: the queries as B operands (the k order follows the K
+  // loads'), and the next tile's keys and values.  A 16-key tile lies within one
+  // page, so its place is the same for all lanes; rows from k1 on lie outside the
+  // buffer and read as zeros, and a tile past the share reads nothing.
+  const uint32_t page_rows = (uint32_t)a.kv_heads << a.page_log2;
+  half8_t qf[RT][NM];
+  int lim[RT];                           // keys below this are seen by the lane's row
+  u32x4_t kr[NS][KL];
+  vvec_t vr[NG][8];
+  float4_t ksc[NS], vsc[NS];
+  uint32_t page[NS], later_page[NS];     // of the tile requested next, and of the one after it
+  const scalar_i32_t* table;             // (constant address space and a scalar index: scalar loads, which the
+                                         // waits for keys and values do not count)
+  const unsigned char *kc, *vc;
+  const float *ks, *vs;
+  int base, k1, k_stop, last_key;
+  auto page_of = [&](int key) { return (uint32_t)table[uniform(min(key, last_key) >> a.page_log2)]; };
+  auto load_k = [&](int base, const uint32_t* pages) {
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
         const int key = base + 16 * n;
@@ -260,12 +311,35 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
       }
     };
 
-    bool noted = false;
-    int base = (step0 * kWaves + wave) * KT;
+  auto begin = [&](const Part& u) {
+    k1 = u.k1;
+    k_stop = u.k_stop;
+    last_key = max(k1 - 1, 0);
+    base = (u.step0 * kWaves + wave) * KT;
+    table = (const scalar_i32_t*)(uintptr_t)(a.table + (int64_t)uniform(u.b) * a.table_stride);
+    const int64_t head_row = (int64_t)u.head << a.page_log2;
+    kc = (const unsigned char*)a.kc + head_row * RB;
+    vc = (const unsigned char*)a.vc + head_row * RB;
+    ks = I8 ? a.ks + head_row : nullptr;
+    vs = I8 ? a.vs + head_row : nullptr;
 #pragma unroll
     for (int n = 0; n < NS; ++n) page[n] = page_of(base + 16 * n);
 #pragma unroll
     for (int n = 0; n < NS; ++n) later_page[n] = page_of(base + KS + 16 * n);
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+      const int r = u.r0 + 16 * x + c;
+      const bool ok = r < u.rows;
+      const int tok = ok ? r / a.group : 0, h = ok ? u.head * a.group + r % a.group : 0;
+      lim[x] = ok ? min(u.pos0 + tok + 1, k1) : k1;
+      const half_t* qp = a.q + (u.q0 + (int64_t)tok) * a.q_ts + h * a.q_hs;
+#pragma unroll
+      for (int m = 0; m < NM; ++m) {
+        const int d = I8 ? 64 * (m / 2) + 16 * t + 8 * (m % 2) : 32 * m + 8 * t;
+        qf[x][m] = ok ? load_half8(qp + d) : zero_half8();
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
     // (the order is that of the loop: with another one the compiler's wait for
     // the keys at its top would also wait for the values)
     load_k(base, page);
@@ -274,6 +348,31 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int n = 0; n < NS; ++n) page[n] = later_page[n];
+  };
+
+  Part u = find(shares.begin(blockIdx.x));
+  begin(u);
+  for (;;) {
+    const uint32_t next = u.unit0 + (whole_tiles ? 1u : (uint32_t)u.step1);
+    const bool more = next < end;
+    const Part then = find(more ? next : u.unit0);
+    const int see_all = u.see_all;
+    if (a.negate) {
+#pragma unroll
+      for (int x = 0; x < RT; ++x)
+#pragma unroll
+        for (int m = 0; m < NM; ++m) qf[x][m] = -qf[x][m];
+    }
+    float4_t acc[RT][DL];
+    float mref[RT], l[RT];
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+      mref[x] = kNone;
+      l[x] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < DL; ++j) acc[x][j] = zero_float4();
+    }
+    bool noted = false;
     for (; base < k_stop; base += KS) {
       // Scores; the next tile's keys are requested as soon as these are used.
       float4_t st[RT][NS];
@@ -471,6 +570,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
       __builtin_amdgcn_sched_barrier(0);
     }
 
+    if (more) begin(then);
+
     if (!I8 && noted) {
       const uint32_t* note = (const uint32_t*)s_o[wave] + lane;
 #pragma unroll
@@ -503,11 +604,10 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
         s_l[wave][16 * x + c] = l[x];
       }
     }
-    __syncthreads();
-    const bool whole = pieces == 1;
-    const uint32_t slot0 = (uint32_t)u.slot * (uint32_t)a.kv_heads + (uint32_t)head;   // pieces: kv_heads apart
-    const uint32_t slot = slot0 + (uint32_t)(u.piece * a.kv_heads);
-    for (int v = threadIdx.x; v < rows_here * (D / 4); v += kThreads) {
+    lds_barrier();
+    const bool whole = u.step0 == 0 && u.step1 == u.steps;
+    const uint32_t slot = 2 * blockIdx.x + (u.step0 == 0 ? 1u : 0u);
+    for (int v = threadIdx.x; v < u.rows_here * (D / 4); v += kThreads) {
       const int row = v / (D / 4), d = v % (D / 4) * 4;
       float M = s_m[0][row];
 #pragma unroll
@@ -525,8 +625,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
         half4_t h;
 #pragma unroll
         for (int k = 0; k < 4; ++k) h[k] = (half_t)(o[k] * inv);
-        const int r = r0 + row;
-        *(half4_t*)(a.out + ((u.q0 + (int64_t)(r / a.group)) * a.q_heads + head * a.group + r % a.group) * D + d) = h;
+        const int r = u.r0 + row;
+        *(half4_t*)(a.out + ((u.q0 + (int64_t)(r / a.group)) * a.q_heads + u.head * a.group + r % a.group) * D + d) = h;
       } else {
         const __amdgpu_buffer_rsrc_t pr = make_rsrc(a.part, (uint32_t)a.part_bytes);
         const uint32_t p = slot * (uint32_t)(SLOT * 4);
@@ -541,17 +641,19 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
     }
     if (!whole) {
       drain_vm();
-      __syncthreads();
-      // (a split row tile has two slots at least)
-      uint32_t* counter = a.counters + (uint32_t)(u.slot / 2) * (uint32_t)a.kv_heads + (uint32_t)head;
-      if (threadIdx.x == 0) s_arrived = add_dev_u32(counter, 1u);
-      __syncthreads();
+      lds_barrier();
+      const uint32_t w0 = shares.owner(u.unit0);
+      const int pieces = (int)(shares.owner(u.unit0 + (uint32_t)u.steps - 1) - w0) + 1;
+      if (threadIdx.x == 0) s_arrived = add_dev_u32(&a.counters[w0], 1u);
+      lds_barrier();
       if (s_arrived == (uint32_t)pieces - 1) {
-        if (threadIdx.x == 0) st_dev_u32(counter, 0u);
-        join<D, R, SLOT>(a, &s_o[0][0][0], rows_here, r0, u.q0, head, slot0, pieces);
+        if (threadIdx.x == 0) st_dev_u32(&a.counters[w0], 0u);
+        join<D, R, SLOT>(a, &s_o[0][0][0], u.rows_here, u.r0, u.q0, u.head, w0, pieces);
       }
     }
-    __syncthreads();
+    if (!more) break;
+    lds_barrier();
+    u = then;
   }
 }
 
@@ -578,21 +680,22 @@ AttnPlan attn_plan(const spear_attention_desc_t& d, int cus) {
   p.cus = std::min(cus, 512);
   const int64_t max_kv = (int64_t)d.max_pages * d.kv.page_size;
   const int64_t rows = (int64_t)d.total_q * group;
-  // The kernels count work (tiles times 64 keys) and items in 32 bits.
-  p.fits = (d.batch + rows / (p.tiles && !p.both ? 128 : R)) * ceil_div(max_kv, 64) <= INT32_MAX / 2;
-  const int64_t most = (int64_t)1 << 20;
-  // Items: row tiles, and the pieces of split ones: fewer than twice the items
-  // aimed at.  That many partial results have to fit, and half as many counters.
-  const int64_t pieces = (int64_t)kMostItems * p.cus, tile_pieces = (int64_t)2 * p.cus;
-  const int64_t tiles = p.tiles ? d.batch : d.batch + rows / R;
-  // (with few row tiles, items beyond two a CU are second ones of a workgroup:
-  // workgroups without any would only be in the others' way)
-  const int64_t items = tiles * H + pieces;
-  p.grid = p.tiles && !p.both ? 0
-           : (int)round_up(tiles * H < p.cus ? std::min(items, (int64_t)2 * p.cus) : std::min(items, most), H);
-  p.tile_grid = !p.tiles ? 0 : (int)round_up(std::min((d.batch + rows / 128) * H + tile_pieces, most), H);
+  // The kernels count work in 32 bits: steps of 128 keys of all row tiles here,
+  // row tiles of a head times 64 keys in the other.
+  const int64_t few = p.tiles ? (p.both ? d.batch : 0) : d.batch + rows / R;
+  p.fits = few * ceil_div(max_kv, 32 * kWaves) * H <= INT32_MAX &&
+           (p.tiles ? d.batch + rows / 128 : 0) * ceil_div(max_kv, 64) <= INT32_MAX / 2;
+  // One share for each workgroup that the GPU holds at once; no more of them than
+  // there can be steps.
+  const int64_t held = (int64_t)(p.row_tiles == 1 ? 3 : 2) * p.cus;
+  p.grid = (int)std::min(held, few * ceil_div(max_kv, 32 * kWaves) * H);
+  // Items of the tile kernel: row tiles, and the pieces of split ones, fewer than
+  // twice the items aimed at.  That many partial results have to fit, and half as
+  // many counters.
+  const int64_t tile_pieces = (int64_t)2 * p.cus;
+  p.tile_grid = !p.tiles ? 0 : (int)round_up(std::min((d.batch + rows / 128) * H + tile_pieces, (int64_t)1 << 20), H);
   p.part = kSyncHeaderBytes;
-  p.part_bytes = p.grid ? (size_t)2 * pieces * R * (dim + 2) * 4 : 0;
+  p.part_bytes = (size_t)2 * p.grid * R * (dim + 2) * 4;
   p.tile_part = p.part + p.part_bytes;
   p.tile_part_bytes = p.tiles ? (size_t)2 * tile_pieces * 128 * (dim + 2) * 4 : 0;
   p.bytes = p.tile_part + p.tile_part_bytes;
@@ -627,7 +730,6 @@ hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* stream) 
   k.rows_to = p.both ? p.few_rows : INT32_MAX;
   k.part = (float*)((char*)a.workspace + p.part);
   k.part_bytes = (int32_t)p.part_bytes;
-  k.min_piece = 512;   // four steps; 256 took 20 us instead of 15 for one sequence of 8k
   if (a.kv.dim == 64) {
     if (i8) return two ? launch<64, true, 2>(k, p, st) : launch<64, true, 1>(k, p, st);
     return two ? launch<64, false, 2>(k, p, st) : launch<64, false, 1>(k, p, st);
