@@ -120,19 +120,23 @@ def test_attention_checks(lib, buf):
 
 
 def test_workspaces_follow_the_launch_shape(lib):
-    """Partial results are two per item aimed at, of 16, 32 or 128 rows: whatever
-    the lengths turn out to be, they fit (the kernels' own bound)."""
+    """Room for two partial results of 16 or 32 rows for each workgroup, which are
+    as many as the GPU holds or as there can be steps of 128 keys, and of 128 rows
+    for two pieces of each item aimed at: whatever the lengths turn out to be, they
+    fit (the kernels' own bound)."""
     n = ctypes.c_size_t(0)
 
     def size(**o):
         assert lib.spear_attention_workspace_bytes(ctypes.byref(attention(**o)), ctypes.byref(n)) == OK
         return n.value - (1 << 20)
     item = lambda rows, dim: rows * (dim + 2) * 4  # noqa: E731
-    assert size() == 2 * 4 * 256 * item(16, 64)
-    assert size(max_q=9, total_q=18, kv=kv(dim=128)) == 2 * 4 * 256 * item(32, 128)
+    assert size() == 2 * 4 * item(16, 64)                          # 2 sequences x 2 heads, 64 keys at most
+    assert size(max_pages=9) == 2 * 2 * 4 * item(16, 64)           # 144 keys: two steps
+    assert size(max_pages=10000) == 2 * 3 * 256 * item(16, 64)
+    assert size(max_pages=10000, max_q=9, total_q=18, kv=kv(dim=128)) == 2 * 2 * 256 * item(32, 128)
     assert size(max_q=100, total_q=200) == 2 * 2 * 256 * item(128, 64)                      # tiles alone
-    assert size(max_q=100, total_q=101) == 2 * 2 * 256 * item(128, 64) + 2 * 4 * 256 * item(16, 64)
-    assert size(device_cus=4096) == 2 * 4 * 512 * item(16, 64)      # no more than the counters allow
+    assert size(max_q=100, total_q=101) == 2 * 2 * 256 * item(128, 64) + 2 * 4 * item(16, 64)
+    assert size(max_pages=10000, device_cus=4096) == 2 * 3 * 512 * item(16, 64)   # no more than the counters allow
     v = _binding.VerifyDesc(2, 3, 100, 256)
     assert lib.spear_verify_workspace_bytes(ctypes.byref(v), ctypes.byref(n)) == OK and n.value == 0
     v = _binding.VerifyDesc(2, 3, 100000, 256)

@@ -587,6 +587,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
             if (nan & bit) acc[x][j][k] = NAN;
           }
       }
+      asm volatile("" ::: "memory");   // all notes are read before the sums take their place
     }
     // Join the waves.  Lane (c, t) holds row c at d = DL (4 t + k) + j.
 #pragma unroll
