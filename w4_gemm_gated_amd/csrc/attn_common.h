@@ -191,25 +191,32 @@ __device__ __forceinline__ float row_sum4(float x) {
   return over_row(x, [](float a, float b) { return a + b; });
 }
 
-// The value of the lane N further on among 16 (a rotation in the vector unit).
-template <int N>
-__device__ __forceinline__ float rotate16(float x) {
-  return bits_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)float_bits(x), 0x120 + N, 0xF, 0xF, true));
+// The largest of 16 lanes' values, none of them negative or NaN (whose bits are
+// ordered as the numbers are), by rotations in the vector unit.
+__device__ __forceinline__ float max16(float x) {
+  uint32_t v = float_bits(x);
+  v = max_from<0x128, 0xF>(v);   // 8, 4, 2 and 1 lanes on
+  v = max_from<0x124, 0xF>(v);
+  v = max_from<0x122, 0xF>(v);
+  return bits_float(max_from<0x121, 0xF>(v));
 }
 
-// Codes b0 and b1 (bytes i of two words, sign included) -> two fp16 values.
-// Byte | 0x6400 with the sign bit flipped is the fp16 number 1024 + 128 + code.
-__device__ __forceinline__ uint32_t codes_to_half2(uint32_t bytes) {   // bytes 0x00b1'00b0
+// Codes become fp16 values exactly: a code's byte with its sign bit flipped, under
+// the byte 0x64, is the fp16 number 1024 + 128 + code.
+constexpr uint32_t kCodeSigns = 0x80808080u, kCodeHigh = 0x64646464u;
+__device__ __forceinline__ uint32_t codes_to_half2(uint32_t biased) {   // 0x64b1'64b0, signs flipped
   const half2_t bias = {(half_t)1152.0f, (half_t)1152.0f};
-  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, bytes ^ 0x64806480u) - bias);
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, biased) - bias);
 }
 // Eight codes of two words, in order.
 __device__ __forceinline__ half8_t codes_to_half8(uint32_t lo, uint32_t hi) {
   u32x4_t r;
-  r[0] = codes_to_half2(__builtin_amdgcn_perm(lo, lo, 0x0c010c00u));
-  r[1] = codes_to_half2(__builtin_amdgcn_perm(lo, lo, 0x0c030c02u));
-  r[2] = codes_to_half2(__builtin_amdgcn_perm(hi, hi, 0x0c010c00u));
-  r[3] = codes_to_half2(__builtin_amdgcn_perm(hi, hi, 0x0c030c02u));
+  lo ^= kCodeSigns;
+  hi ^= kCodeSigns;
+  r[0] = codes_to_half2(__builtin_amdgcn_perm(kCodeHigh, lo, 0x04010400u));
+  r[1] = codes_to_half2(__builtin_amdgcn_perm(kCodeHigh, lo, 0x04030402u));
+  r[2] = codes_to_half2(__builtin_amdgcn_perm(kCodeHigh, hi, 0x04010400u));
+  r[3] = codes_to_half2(__builtin_amdgcn_perm(kCodeHigh, hi, 0x04030402u));
   return __builtin_bit_cast(half8_t, r);
 }
 

@@ -552,9 +552,9 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
           for (int k = 0; k < 4; ++k) {
             const uint32_t lo = vr[g][2 * k][j * E / 4], hi = vr[g][2 * k + 1][j * E / 4];
             if constexpr (I8) {
-              // bytes j % 4 of both words, zero extended to halves
+              // bytes j % 4 of both words, under 0x64, sign bits flipped
               const uint32_t sel = 0x0c000c04u + (uint32_t)(j % 4) * 0x00010001u;
-              w[k] = codes_to_half2(__builtin_amdgcn_perm(lo, hi, sel));
+              w[k] = codes_to_half2(__builtin_amdgcn_perm(lo, hi, sel) ^ 0x64806480u);
             } else {
               w[k] = __builtin_amdgcn_perm(hi, lo, j % 2 ? 0x07060302u : 0x05040100u);
             }

@@ -132,14 +132,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
     const int64_t head_row = (int64_t)head << a.page_log2;
     const unsigned char* kc = (const unsigned char*)a.kc + head_row * RB;
     const unsigned char* vc = (const unsigned char*)a.vc + head_row * RB;
-    // 8-bit tiles on their way: two sets of registers, so that a tile is
-    // requested two steps ahead.
+    // An 8-bit tile on its way, requested as soon as the one before is in LDS.
+    // (Two, in two sets of registers, gained nothing at D = 64 and spilled at 128:
+    // 8 x 2048 tokens over 4096 keys 1230 us, 1143 with one.)
     struct Codes {
       u32x4_t k[CR], v[CR];
       float ks, vs;
-      uint32_t page;   // of the tile requested next into this set
     };
-    Codes set[2];
+    Codes codes;
     auto fetch = [&](int step, uint32_t page, int buf, Codes& r8) {
       const int key = step * kKeys + 16 * wave;
       const uint64_t row = (uint64_t)min(page, (uint32_t)a.num_pages - 1) * page_rows + (uint32_t)(key & place_mask);
@@ -184,11 +184,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
           s_ks[buf][16 * wave + lane] = r8.ks * a.scale;
           s_vs[buf][16 * wave + lane] = r8.vs;
         }
-        float tall = r8.vs > kMaxScale ? 0.0f : fmaxf(r8.vs, 0.0f);   // (lanes from 16 on hold zero)
-        tall = fmaxf(tall, rotate16<8>(tall));
-        tall = fmaxf(tall, rotate16<4>(tall));
-        tall = fmaxf(tall, rotate16<2>(tall));
-        tall = fmaxf(tall, rotate16<1>(tall));
+        const float tall = max16(r8.vs > 0.0f && r8.vs <= kMaxScale ? r8.vs : 0.0f);
         if (lane == 0) s_tall[buf][wave] = tall;
       }
     };
@@ -332,7 +328,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      // O^T += V^T P^T.
+      // O^T += V^T P^T, ahead of the other workgroup's softmax: a product takes one
+      // issue of its sixteen cycles.
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int g = 0; g < kNG; ++g)
 #pragma unroll
@@ -347,6 +345,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
         __builtin_amdgcn_sched_group_barrier(kSchedMatrix, kRT, 1);
       }
       __builtin_amdgcn_sched_group_barrier(kSchedMatrix, AHEAD * kRT, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(0);
     };
 
     // Infinities and NaN among values that some row must not see (a weight of
@@ -427,33 +427,29 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
       }
     };
 
+    uint32_t page = page_of(step0);             // of the tile requested next
     if constexpr (I8) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        set[i].page = page_of(step0 + i);
-        if (step0 + i < step1) fetch(step0 + i, set[i].page, 0, set[i]);
-        set[i].page = page_of(step0 + 2 + i);
-      }
-      auto one = [&](int step, int buf, Codes& r8) {
-        put(buf, r8);
+      auto one = [&](int step, int buf) {
+        put(buf, codes);
         __syncthreads();                        // the tile is in LDS; the other stage is free
-        if (step + 2 < step1) fetch(step + 2, r8.page, 0, r8);
-        r8.page = page_of(step + 4);
+        if (step + 1 < step1) fetch(step + 1, page, 0, codes);
+        page = page_of(step + 2);
         if (step * kKeys < see_any) compute(step, buf);
       };
+      if (step0 < step1) fetch(step0, page, 0, codes);
+      page = page_of(step0 + 1);
       for (int step = step0; step < step1; step += 2) {
-        one(step, 0, set[0]);
-        if (step + 1 < step1) one(step + 1, 1, set[1]);
+        one(step, 0);
+        if (step + 1 < step1) one(step + 1, 1);
       }
     } else {
-      uint32_t page = page_of(step0);
-      if (step0 < step1) fetch(step0, page, step0 & 1, set[0]);
+      if (step0 < step1) fetch(step0, page, step0 & 1, codes);
       page = page_of(step0 + 1);
       for (int step = step0; step < step1; ++step) {
         const int buf = step & 1;
         __syncthreads();                        // the tile is in LDS; the other stage is free
         if (step + 1 < step1) {
-          fetch(step + 1, page, buf ^ 1, set[0]);
+          fetch(step + 1, page, buf ^ 1, codes);
           page = page_of(step + 2);
         }
         if (step * kKeys + kKeys > tile_see_all) note_odd(step, buf);
