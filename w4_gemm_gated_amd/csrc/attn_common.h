@@ -16,11 +16,11 @@ struct AttnK {
   const void *kc, *vc;
   const float *ks, *vs;
   half_t* out;
-  float* part;          // partial results, one for each piece of a split row tile
+  float* part;          // partial results of row tiles that workgroups share
   uint32_t* counters;   // zero before and after
   int32_t batch, total_q, q_heads, kv_heads, group, max_kv, page_log2, num_pages;
   int32_t part_bytes;
-  int32_t cus, min_piece;   // compute units planned for; fewest keys of a piece
+  int32_t cus;          // compute units planned for
   int32_t rows_from, rows_to;   // sequences with more rows than the one and no more than the other are this launch's
   float scale;                  // |scale| * log2(e)
   int32_t negate;               // the scale is negative: queries enter with the other sign
@@ -49,13 +49,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base,
   return make_rsrc((const void*)((uint64_t)uniform((uint32_t)(p >> 32)) << 32 | uniform((uint32_t)p)), uniform(bytes));
 }
 
-// ------------------------------------------------------------- the schedule
+// ------------------------------------------------------------- the sequences
 //
-// An item of work is a row tile of a kv head and its keys, or a piece of them:
-// pieces of one call have the same length, which follows from the total work
-// and from how many items the GPU should get.  The lengths are on the device, so
-// every workgroup finds its item by itself, with a scan over the sequences (64 a
-// step).
+// The lengths are on the device, so every workgroup finds its work by itself, with
+// a scan over the sequences (64 a step).
 
 // Sum over the lanes up to and with this one, in the vector unit.
 template <int CTRL, int ROWS>
@@ -104,73 +101,6 @@ __device__ __forceinline__ Seq sequence(const AttnK& a, int b) {
   return s;
 }
 
-// The length of a piece in keys, a multiple of STEP: the work (in tiles times 64
-// keys) over `target` items, or kWhole for no pieces.
-constexpr int kWhole = 1 << 30;
-template <int STEP>
-__device__ __forceinline__ int piece_keys(const AttnK& a, uint32_t work, uint32_t target) {
-  // (a float's quotient, rounded up past its error: no 64-bit division)
-  const float q = (float)work * (float)a.kv_heads / (float)target;
-  const uint32_t per = uniform((uint32_t)fminf(q * (1.0f + 0x1p-20f) + 1.0f, 0x1p25f));
-  const uint32_t keys = max((min(per, (uint32_t)kWhole / 64) * 64 + STEP - 1) / STEP * STEP, (uint32_t)a.min_piece);
-  return (int)min(keys, (uint32_t)kWhole);
-}
-// What the sequences add up to: work, row tiles, and the most work of a tile.
-struct Load {
-  uint32_t work, tiles, longest;
-};
-template <int R>
-__device__ __forceinline__ Load load_of(const AttnK& a, const Seq& s0, int lane) {
-  Load l = {0, 0, 0};
-  for (int b0 = 0; b0 < a.batch; b0 += kWave) {
-    const Seq s = b0 == 0 ? s0 : sequence<R>(a, b0 + lane);
-    const uint32_t keys = (uint32_t)((s.kv + 63) / 64);
-    l.work += (uint32_t)s.tiles * keys;
-    l.tiles += (uint32_t)s.tiles;
-    l.longest = max(l.longest, s.tiles > 0 ? keys : 0u);
-  }
-  l.work = wave_sum(l.work);
-  l.tiles = wave_sum(l.tiles);
-  l.longest = wave_max(l.longest);
-  return l;
-}
-
-__device__ __forceinline__ int pieces_of(int kv, int piece) { return kv > piece ? (kv + piece - 1) / piece : 1; }
-
-// Item `index` of a kv head: sequence, row tile (the last, which sees the most
-// keys, first) and piece.  `slot` numbers the pieces of split row tiles: this
-// row tile's first.
-struct Item {
-  int b, q0, n, kv, rt, piece, slot;
-};
-template <int R>
-__device__ __forceinline__ bool find(const AttnK& a, const Seq& s0, int piece, uint32_t index, int lane, Item* it) {
-  uint32_t before = 0, slots = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kWave) {
-    const Seq s = b0 == 0 ? s0 : sequence<R>(a, b0 + lane);
-    const int np = pieces_of(s.kv, piece);
-    const uint32_t mine = (uint32_t)s.tiles * (uint32_t)np, split = np > 1 ? mine : 0;
-    const uint32_t upto = before + wave_scan(mine), slot_upto = slots + wave_scan(split);
-    const uint64_t past = __ballot(upto > index);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      const int tiles = __builtin_amdgcn_readlane(s.tiles, l), n = __builtin_amdgcn_readlane(np, l);
-      const int at = (int)(index - (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), l));
-      it->b = b0 + l;
-      it->q0 = __builtin_amdgcn_readlane(s.q0, l);
-      it->n = __builtin_amdgcn_readlane(s.n, l);
-      it->kv = __builtin_amdgcn_readlane(s.kv, l);
-      it->piece = tiles == 1 ? at : uniform(at / tiles);
-      it->rt = tiles - 1 - (at - it->piece * tiles);
-      it->slot = __builtin_amdgcn_readlane((int)(slot_upto - split), l) + it->rt * n;
-      return true;
-    }
-    before = (uint32_t)__builtin_amdgcn_readlane((int)upto, kWave - 1);
-    slots = (uint32_t)__builtin_amdgcn_readlane((int)slot_upto, kWave - 1);
-  }
-  return false;
-}
-
 // -------------------------------------------------------------- small pieces
 
 // Over the four lanes (c, 0..3) that hold row c: swaps of 16- and 32-lane halves
@@ -189,16 +119,6 @@ __device__ __forceinline__ float row_max4(float x) {
 }
 __device__ __forceinline__ float row_sum4(float x) {
   return over_row(x, [](float a, float b) { return a + b; });
-}
-
-// The largest of 16 lanes' values, none of them negative or NaN (whose bits are
-// ordered as the numbers are), by rotations in the vector unit.
-__device__ __forceinline__ float max16(float x) {
-  uint32_t v = float_bits(x);
-  v = max_from<0x128, 0xF>(v);   // 8, 4, 2 and 1 lanes on
-  v = max_from<0x124, 0xF>(v);
-  v = max_from<0x122, 0xF>(v);
-  return bits_float(max_from<0x121, 0xF>(v));
 }
 
 // Codes become fp16 values exactly: a code's byte with its sign bit flipped, under

@@ -723,7 +723,6 @@ hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* stream) 
     k.rows_to = INT32_MAX;
     k.part = (float*)((char*)a.workspace + p.tile_part);
     k.part_bytes = (int32_t)p.tile_part_bytes;
-    k.min_piece = 256;   // shorter ones cost more in their partial sums than they save
     const hipError_t e = launch_attention_tiles(k, a.kv.dim, i8, p.tile_grid, st);
     if (e != hipSuccess || !p.both) return e;
   }

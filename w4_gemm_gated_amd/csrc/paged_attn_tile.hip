@@ -22,15 +22,22 @@
 // instructions, nearly the same time: two workgroups per CU let one's softmax
 // run under the other's products.
 //
-// Row tiles are cut into pieces (attn_common.h) where there are too few for the
-// GPU; workgroups of a piece read the same keys.  Items are numbered with the kv head fastest and a sequence's last row tile, which
+// Row tiles are cut into pieces of their keys where there are too few for the GPU.
+// Items are numbered with the kv head fastest and a sequence's last row tile, which
 // sees the most keys, first: workgroups are dealt to the eight XCDs in turn, so
-// those that run at a time on one XCD walk the same head's keys together and
-// its L2 serves all but the first of them.  (Equal shares of the keys for all
-// workgroups were measured on 2048 tokens over 8192 keys: the workgroups of a
-// head stood at different keys, 4 MB of them, and 2.7 GB instead of 0.08 came
-// from beyond the L2: 633 us instead of 419 then.)  Pieces leave their sums in the workspace; the last of a row
-// tile's to arrive joins them in order.
+// those that run at a time on one XCD walk the same head's keys together and its
+// L2 serves all but the first of them.  (Equal shares of the keys for all
+// workgroups were measured on 2048 tokens over 8192 keys: the workgroups of a head
+// stood at different keys, 4 MB of them, and 2.7 GB instead of 0.08 came from
+// beyond the L2: 633 us instead of 419 then.)  Pieces leave their sums in the
+// workspace; the last of a row tile's to arrive joins them in order.
+//
+// Measured (32 query heads on 8 kv heads): 8 x 2048 tokens over 4096 keys in
+// 960 us at head dimension 128 and 570 us at 64 (858 and 723 TFLOP/s; a large
+// library product reaches 1104), 1130 and 805 us over an 8-bit cache; one chunk
+// of 700 tokens over 2571 keys in 52, 31, 59 and 45 us.  Counted at the first of
+// these sizes, vector and matrix instructions together fill 83 (128) and 97 % (64)
+// of the cycles.
 #include "attn_common.h"
 
 namespace spear {
@@ -47,6 +54,78 @@ constexpr int kSchedMatrix = 0x8, kSchedLdsRead = 0x100;   // instruction classe
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __fp16 fp16x4_t __attribute__((__vector_size__(4 * sizeof(__fp16))));
 typedef __attribute__((address_space(3))) fp16x4_t lds_fp16x4_t;
+
+// An item of work is a row tile of a kv head and its keys, or a piece of them:
+// pieces of one call have the same length in keys, a multiple of a tile's, that of
+// the work (in row tiles times 64 keys) over `target` items, but no shorter than
+// kMinPiece: those cost more in their partial sums than they save.
+constexpr int kWhole = 1 << 30, kMinPiece = 256;
+__device__ __forceinline__ int piece_keys(const AttnK& a, uint32_t work, uint32_t target) {
+  // (a float's quotient, rounded up past its error: no 64-bit division)
+  const float q = (float)work * (float)a.kv_heads / (float)target;
+  const uint32_t per = uniform((uint32_t)fminf(q * (1.0f + 0x1p-20f) + 1.0f, 0x1p25f));
+  return (int)max(min(per, (uint32_t)(kWhole / kKeys)) * kKeys, (uint32_t)kMinPiece);
+}
+// What the sequences add up to: work and row tiles.
+struct Load {
+  uint32_t work, tiles;
+};
+__device__ __forceinline__ Load load_of(const AttnK& a, const Seq& s0, int lane) {
+  Load l = {0, 0};
+  for (int b0 = 0; b0 < a.batch; b0 += kWave) {
+    const Seq s = b0 == 0 ? s0 : sequence<kRows>(a, b0 + lane);
+    l.work += (uint32_t)s.tiles * (uint32_t)((s.kv + kKeys - 1) / kKeys);
+    l.tiles += (uint32_t)s.tiles;
+  }
+  l.work = wave_sum(l.work);
+  l.tiles = wave_sum(l.tiles);
+  return l;
+}
+
+__device__ __forceinline__ int pieces_of(int kv, int piece) { return kv > piece ? (kv + piece - 1) / piece : 1; }
+
+// Item `index` of a kv head: sequence, row tile (the last, which sees the most
+// keys, first) and piece.  `slot` numbers the pieces of split row tiles: this
+// row tile's first.
+struct Item {
+  int b, q0, n, kv, rt, piece, slot;
+};
+__device__ __forceinline__ bool find(const AttnK& a, const Seq& s0, int piece, uint32_t index, int lane, Item* it) {
+  uint32_t before = 0, slots = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kWave) {
+    const Seq s = b0 == 0 ? s0 : sequence<kRows>(a, b0 + lane);
+    const int np = pieces_of(s.kv, piece);
+    const uint32_t mine = (uint32_t)s.tiles * (uint32_t)np, split = np > 1 ? mine : 0;
+    const uint32_t upto = before + wave_scan(mine), slot_upto = slots + wave_scan(split);
+    const uint64_t past = __ballot(upto > index);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      const int tiles = __builtin_amdgcn_readlane(s.tiles, l), n = __builtin_amdgcn_readlane(np, l);
+      const int at = (int)(index - (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), l));
+      it->b = b0 + l;
+      it->q0 = __builtin_amdgcn_readlane(s.q0, l);
+      it->n = __builtin_amdgcn_readlane(s.n, l);
+      it->kv = __builtin_amdgcn_readlane(s.kv, l);
+      it->piece = tiles == 1 ? at : uniform(at / tiles);
+      it->rt = tiles - 1 - (at - it->piece * tiles);
+      it->slot = __builtin_amdgcn_readlane((int)(slot_upto - split), l) + it->rt * n;
+      return true;
+    }
+    before = (uint32_t)__builtin_amdgcn_readlane((int)upto, kWave - 1);
+    slots = (uint32_t)__builtin_amdgcn_readlane((int)slot_upto, kWave - 1);
+  }
+  return false;
+}
+
+// The largest of 16 lanes' values, none of them negative or NaN (whose bits are
+// ordered as the numbers are), by rotations in the vector unit.
+__device__ __forceinline__ float max16(float x) {
+  uint32_t v = float_bits(x);
+  v = max_from<0x128, 0xF>(v);   // 8, 4, 2 and 1 lanes on
+  v = max_from<0x124, 0xF>(v);
+  v = max_from<0x122, 0xF>(v);
+  return bits_float(max_from<0x121, 0xF>(v));
+}
 
 template <int D, bool I8>
 __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
@@ -70,10 +149,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
 
   const Seq seq0 = sequence<kRows>(a, lane);
   // Two workgroups run on a CU; no pieces if the row tiles alone are near to that.
-  const Load load = load_of<kRows>(a, seq0, lane);
+  const Load load = load_of(a, seq0, lane);
   const uint32_t held = 2 * (uint32_t)a.cus;
   const int piece = (uint64_t)load.tiles * (uint32_t)a.kv_heads * 4 >= (uint64_t)held * 3
-                        ? kWhole : piece_keys<kKeys>(a, load.work, held);
+                        ? kWhole : piece_keys(a, load.work, held);
 
   const int place_mask = (1 << a.page_log2) - 1;
   const uint32_t page_rows = (uint32_t)a.kv_heads << a.page_log2;
@@ -81,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
 
   for (uint32_t index = blockIdx.x / (uint32_t)a.kv_heads;; index += gridDim.x / (uint32_t)a.kv_heads) {
     Item u;
-    if (!find<kRows>(a, seq0, piece, uniform(index), lane, &u)) break;
+    if (!find(a, seq0, piece, uniform(index), lane, &u)) break;
     const int rows = u.n * a.group, r0 = u.rt * kRows;
     const int rows_here = min(kRows, rows - r0);
     const int pos0 = u.kv - u.n;
