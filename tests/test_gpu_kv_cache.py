@@ -117,6 +117,51 @@ def test_gather_ragged(dtype, lens, heads, dim, page):
                 assert np.array_equal(bits(x[cu[b] + i]), bits(want)), (b, i)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.int8])
+@pytest.mark.parametrize("heads,dim,page", [(9, 128, 16), (17, 64, 64)])
+def test_large_outputs(dtype, heads, dim, page):
+    """Outputs past 256 MiB (a thread takes two rows there): many sequences of odd
+    lengths, some empty, and rows of no sequence at the end; the same bits as the
+    definition in fp32 torch operations, row by row."""
+    rng = np.random.default_rng(dim + heads)
+    lens = rng.integers(0, 1400, size=90).tolist()
+    lens[4] = lens[5] = lens[89] = 0
+    total, rows = sum(lens), sum(lens) + 37
+    rows += max(0, (1 << 28) // (heads * dim * 4) + 3 - rows)
+    note(f"large gather {dtype} heads {heads} dim {dim} rows {rows} of which {total} cached")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(dim)
+    need = [-(-n // page) for n in lens]
+    pages = sum(need) + 1
+    order = torch.randperm(pages, generator=g, device=DEV)
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32, device=DEV)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n].int()
+        at += n
+    shape = (pages, heads, page, dim)
+    if dtype is torch.int8:
+        caches = [torch.randint(-127, 128, shape, generator=g, device=DEV).to(torch.int8) for _ in range(2)]
+        scales = [torch.rand(shape[:3], generator=g, device=DEV) for _ in range(2)]
+    else:
+        caches = [torch.randn(shape, generator=g, device=DEV).half() for _ in range(2)]
+        scales = [None, None]
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device=DEV)
+    out = sp.spear_kv_gather(*caches, table, cu, rows, k_scale=scales[0], v_scale=scales[1])
+    row = torch.arange(total, device=DEV)
+    b = torch.bucketize(row, cu[1:].long(), right=True)
+    i = row - cu.long()[b]
+    place = table[b, i // page].long()
+    for got, cache, scale in zip(out, caches, scales):
+        assert torch.count_nonzero(got[total:]).item() == 0
+        for r in range(0, total, 16384):
+            p, o = place[r:r + 16384], (i % page)[r:r + 16384]
+            want = cache[p, :, o]
+            if scale is not None:
+                want = (want.float() * scale[p, :, o][..., None]).half()
+            assert torch.equal(got[r:r + 16384][:want.shape[0]], want)
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 2^32 bytes (and 2^31 values): its last pages are
     written and read back."""

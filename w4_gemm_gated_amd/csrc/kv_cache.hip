@@ -6,12 +6,12 @@
 // (16 bytes of fp16, 8 of codes) of the keys and of the values, so every
 // fp16 access is 16 bytes wide and a head's row is one contiguous run of
 // head_dim / 8 lanes; the keys' and the values' loads are in flight together.  A
-// workgroup takes 16 (head_dim 128) or 32 tokens of one head: neighbours in a
-// page, so that it touches whole lines of codes and scales (with all heads of two
-// tokens instead, a line of scales went to all eight XCDs: 205 MB fetched for
-// 169, and 10,000 tokens of 8 heads of 64 took 45 us instead of 37).
+// workgroup takes 16 (head_dim 128) or 32 tokens of one head, or twice as many:
+// neighbours in a page, so that it touches whole lines of codes and scales (with
+// all heads of two tokens instead, a line of scales went to all eight XCDs: 205
+// MB fetched for 169, and 10,000 tokens of 8 heads of 64 took 45 us instead of 37).
 // Measured with 8 heads of 128: 24 sequences, 80,000 tokens, read back from 8 bits
-// in 106 us (498 MB read and written, 4.7 TB/s; a plain copy of 2 GiB reaches
+// in 102 us (498 MB read and written, 4.9 TB/s; a plain copy of 2 GiB reaches
 // 4.9); 6,800 tokens quantised, written and read back in 21 us (85 MB); a decode
 // step's 48 tokens in 2.7 us of the 7.5 that a launch takes.
 #include "serve_internal.h"
@@ -119,6 +119,9 @@ struct GatherK {
   int32_t batch, rows, heads, page_log2, num_pages;
 };
 
+template <bool I8> struct KvVec { typedef half8_t type; };
+template <> struct KvVec<true> { typedef u32x2_t type; };
+
 __device__ __forceinline__ half8_t dequantise(const u32x2_t& w, float s) {
   half8_t h;
 #pragma unroll
@@ -128,36 +131,70 @@ __device__ __forceinline__ half8_t dequantise(const u32x2_t& w, float s) {
 
 // A workgroup's rows belong to few sequences: its first row's is counted by the
 // whole wave (the rising entries of cu not above it), and a thread steps on
-// from there.
-template <int LANES, bool I8>
+// from there.  A thread takes ROWS rows, whose loads are in flight together.
+template <int LANES, bool I8, int ROWS>
 __global__ void __launch_bounds__(kThreads) kv_gather_kernel(GatherK a) {
+  typedef typename KvVec<I8>::type code_t;
+  constexpr int STEP = kThreads / LANES;
   const int head = (int)(blockIdx.x % (uint32_t)a.heads), c = (int)threadIdx.x % LANES;
-  const int64_t first = (int64_t)(blockIdx.x / (uint32_t)a.heads) * (kThreads / LANES);
-  const int64_t row = first + (int)threadIdx.x / LANES;
+  const int64_t first = (int64_t)(blockIdx.x / (uint32_t)a.heads) * (STEP * ROWS);
+  const int64_t row0 = first + (int)threadIdx.x / LANES;
   int b = -1;
   for (int i = 0; i <= a.batch; i += kWave) {
     const int j = i + (int)threadIdx.x % kWave;
     b += __popcll(__ballot(j <= a.batch && a.cu[j] <= first));
   }
-  if (row >= a.rows) return;
-  while (b < a.batch && a.cu[b + 1] <= row) ++b;
-  half8_t kx = zero_half8(), vx = zero_half8();
-  if (b >= 0 && b < a.batch) {
-    const int i = (int)row - a.cu[b];
-    const int64_t entry = min((int64_t)(i >> a.page_log2), a.table_stride - 1);
-    const uint32_t page = min((uint32_t)a.table[b * a.table_stride + entry], (uint32_t)a.num_pages - 1);
-    const int64_t at = (((int64_t)page * a.heads + head) << a.page_log2) + (i & ((1 << a.page_log2) - 1));
-    if constexpr (I8) {
-      kx = dequantise(((const u32x2_t*)a.kc)[at * LANES + c], a.ks[at]);
-      vx = dequantise(((const u32x2_t*)a.vc)[at * LANES + c], a.vs[at]);
-    } else {
-      kx = ((const half8_t*)a.kc)[at * LANES + c];
-      vx = ((const half8_t*)a.vc)[at * LANES + c];
+  int64_t at[ROWS];   // place in the cache; -1: a row of no sequence
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const int64_t row = row0 + r * STEP;
+    while (b < a.batch && a.cu[b + 1] <= row) ++b;
+    at[r] = -1;
+    if (b >= 0 && b < a.batch && row < a.rows) {
+      const int i = (int)row - a.cu[b];
+      const int64_t entry = min((int64_t)(i >> a.page_log2), a.table_stride - 1);
+      const uint32_t page = min((uint32_t)a.table[b * a.table_stride + entry], (uint32_t)a.num_pages - 1);
+      at[r] = (((int64_t)page * a.heads + head) << a.page_log2) + (i & ((1 << a.page_log2) - 1));
     }
   }
-  const int64_t u = (row * a.heads + head) * LANES + c;
-  __builtin_nontemporal_store(kx, &a.ko[u]);   // written once, not read here
-  __builtin_nontemporal_store(vx, &a.vo[u]);
+  code_t kw[ROWS], vw[ROWS];
+  float ks[ROWS], vs[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    kw[r] = vw[r] = code_t{};
+    ks[r] = vs[r] = 0.0f;
+    if (at[r] >= 0) {
+      kw[r] = ((const code_t*)a.kc)[at[r] * LANES + c];
+      vw[r] = ((const code_t*)a.vc)[at[r] * LANES + c];
+      if constexpr (I8) {
+        ks[r] = a.ks[at[r]];
+        vs[r] = a.vs[at[r]];
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const int64_t row = row0 + r * STEP;
+    if (row >= a.rows) break;
+    const int64_t u = (row * a.heads + head) * LANES + c;
+    // (written once, not read here)
+    if constexpr (I8) {
+      __builtin_nontemporal_store(dequantise(kw[r], ks[r]), &a.ko[u]);
+      __builtin_nontemporal_store(dequantise(vw[r], vs[r]), &a.vo[u]);
+    } else {
+      __builtin_nontemporal_store(kw[r], &a.ko[u]);
+      __builtin_nontemporal_store(vw[r], &a.vo[u]);
+    }
+  }
+}
+
+template <int LANES, bool I8>
+hipError_t launch_gather(const GatherK& k, bool two, hipStream_t st) {
+  const int64_t rows = kThreads / LANES * (two ? 2 : 1);   // of a workgroup
+  const dim3 grid((unsigned)(ceil_div((int64_t)k.rows, rows) * k.heads)), block(kThreads);
+  if (two) kv_gather_kernel<LANES, I8, 2><<<grid, block, 0, st>>>(k);
+  else kv_gather_kernel<LANES, I8, 1><<<grid, block, 0, st>>>(k);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -190,17 +227,13 @@ hipError_t launch_kv_gather(const KvGatherArgs& a, void* stream) {
   k.ko = (half8_t*)a.k_out; k.vo = (half8_t*)a.v_out;
   k.batch = a.batch; k.rows = a.rows; k.heads = a.kv.heads;
   k.page_log2 = a.kv.page_log2; k.num_pages = a.kv.num_pages;
-  const dim3 grid((unsigned)(ceil_div((int64_t)a.rows, kThreads / (a.kv.dim / 8)) * a.kv.heads)), block(kThreads);
+  // Two rows a thread where the outputs pass the 256 MiB that the card caches
+  // (328 MB: 102 us, 110 with one; 61 MB: 38.4, 36.8 with one).
+  const bool two = (int64_t)a.rows * a.kv.heads * a.kv.dim * 4 > (int64_t)256 << 20;
   const hipStream_t st = (hipStream_t)stream;
   const bool i8 = a.kv.dtype == SPEAR_KV_INT8;
-  if (a.kv.dim == 64) {
-    if (i8) kv_gather_kernel<8, true><<<grid, block, 0, st>>>(k);
-    else kv_gather_kernel<8, false><<<grid, block, 0, st>>>(k);
-  } else {
-    if (i8) kv_gather_kernel<16, true><<<grid, block, 0, st>>>(k);
-    else kv_gather_kernel<16, false><<<grid, block, 0, st>>>(k);
-  }
-  return hipGetLastError();
+  if (a.kv.dim == 64) return i8 ? launch_gather<8, true>(k, two, st) : launch_gather<8, false>(k, two, st);
+  return i8 ? launch_gather<16, true>(k, two, st) : launch_gather<16, false>(k, two, st);
 }
 
 }  // namespace spear
