@@ -11,7 +11,9 @@
 // them, and ties go to the lowest index whatever the order of the workgroups.
 // The last workgroup of a sequence to arrive takes the maximum over the
 // others' and writes the token.  Measured: 64 sequences of 128,001 entries in
-// 23 us (98 MB, 4.3 TB/s with the start and the exchange), 2 of 32,000 in 7.4 us.
+// 19.2 us (98 MB, 5.1 TB/s with the start and the exchange; 23 with the noise
+// requested after the count and vectors past a share's end read one by one), 2 of
+// 32,000 in 7.4 us.
 //
 // A residual that is zero everywhere (p <= q at every entry although a token
 // was refused: only rounding makes it so) is rare; the last workgroup then
@@ -44,40 +46,50 @@ struct Best {
   }
 };
 
-// Best key of the entries [beg, end) of one row.  MODE 0: w = p; 1: w = p - q;
-// 2: w = p - [j = x].
+// Where a thread's vector i of the round at r0 lies, kept within the share.
+__device__ __forceinline__ int place(int r0, int i, int end) {
+  return min(r0 + 4 * ((int)threadIdx.x + i * kThreads), end - 4);
+}
+
+// The noise of a share's first round (of at least four entries).
+struct Ahead {
+  f4u_t e[kUnroll];
+  __device__ __forceinline__ void load(const float* __restrict__ noise, int beg, int end) {
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) e[i] = *(const f4u_t*)(noise + place(beg, i, end));
+  }
+};
+
+// Best key of the entries [beg, end) of one row, `ahead` the first noise if it is
+// there already.  MODE 0: w = p; 1: w = p - q; 2: w = p - [j = x].  Vectors past
+// the end are read within it and count nothing, so that the last round's loads
+// are in flight together as every other's.
 template <int MODE>
 __device__ __forceinline__ uint64_t scan(const float* __restrict__ p, const float* __restrict__ q,
-                                         const float* __restrict__ e, int x, int beg, int end) {
+                                         const float* __restrict__ e, int x, int beg, int end, const Ahead* ahead) {
   Best best;
-  int j0 = beg + 4 * (int)threadIdx.x;
-  for (; j0 + 4 * kThreads * (kUnroll - 1) + 3 < end; j0 += kStep) {
+  auto weight = [x](float p, float q, int j) { return MODE == 0 ? p : MODE == 1 ? p - q : j == x ? p - 1.0f : p; };
+  for (int r0 = beg; r0 + 3 < end; r0 += kStep) {
     f4u_t pv[kUnroll], qv[kUnroll], ev[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int j = j0 + i * 4 * kThreads;
+      const int j = place(r0, i, end);
       pv[i] = *(const f4u_t*)(p + j);
       if (MODE == 1) qv[i] = *(const f4u_t*)(q + j);
-      ev[i] = *(const f4u_t*)(e + j);
+      if (ahead && r0 == beg) ev[i] = ahead->e[i];
+      else ev[i] = *(const f4u_t*)(e + j);
     }
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i)
+    for (int i = 0; i < kUnroll; ++i) {
+      const int j = r0 + 4 * ((int)threadIdx.x + i * kThreads);
+      if (r0 + kStep > end && j + 3 >= end) pv[i] = f4u_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int j = j0 + i * 4 * kThreads + k;
-        const float w = MODE == 0 ? pv[i][k] : MODE == 1 ? pv[i][k] - qv[i][k] : j == x ? pv[i][k] - 1.0f : pv[i][k];
-        best.see(w, ev[i][k], j);
-      }
+      for (int k = 0; k < 4; ++k) best.see(weight(pv[i][k], MODE == 1 ? qv[i][k] : 0.0f, j + k), ev[i][k], j + k);
+    }
   }
-  for (; j0 < end; j0 += 4 * kThreads)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int j = j0 + k;
-      if (j < end) {
-        const float w = MODE == 0 ? p[j] : MODE == 1 ? p[j] - q[j] : j == x ? p[j] - 1.0f : p[j];
-        best.see(w, e[j], j);
-      }
-    }
+  // The last one to three entries.
+  const int j = end - (end - beg) % 4 + (int)threadIdx.x;
+  if (j < end) best.see(weight(p[j], MODE == 1 ? q[j] : 0.0f, j), e[j], j);
   return best.key();
 }
 
@@ -104,6 +116,14 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
   const float* draft = a.draft ? a.draft + b * a.draft_bs : nullptr;
   const int32_t* drafted = a.drafted + (int64_t)b * K;
 
+  const int share = (int)((((int64_t)a.vocab + a.splits - 1) / a.splits + 3) / 4 * 4);
+  const int beg = (int)min((int64_t)part * share, (int64_t)a.vocab);
+  const int end = (int)min((int64_t)beg + share, (int64_t)a.vocab);
+  const float* e = a.noise + (int64_t)b * a.vocab;
+  // (does not depend on the kept tokens, so it comes in while those are counted)
+  Ahead ahead;
+  if (beg + 3 < end) ahead.load(e, beg, end);
+
   // Kept tokens: lanes take one drafted token each, the first refusal counts.
   // (The token, its random number and the sequence's length are requested
   // together, whether the length needs them or not.)
@@ -125,15 +145,11 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
   if (kept < 0) kept = n;
 
   // The race over this workgroup's share.
-  const int share = (int)((((int64_t)a.vocab + a.splits - 1) / a.splits + 3) / 4 * 4);
-  const int beg = (int)min((int64_t)part * share, (int64_t)a.vocab);
-  const int end = (int)min((int64_t)beg + share, (int64_t)a.vocab);
   const float* p = target + kept * a.target_rs;
-  const float* e = a.noise + (int64_t)b * a.vocab;
   uint64_t best;
-  if (kept == n) best = scan<0>(p, nullptr, e, -1, beg, end);
-  else if (draft) best = scan<1>(p, draft + kept * a.draft_rs, e, -1, beg, end);
-  else best = scan<2>(p, nullptr, e, drafted[kept], beg, end);
+  if (kept == n) best = scan<0>(p, nullptr, e, -1, beg, end, &ahead);
+  else if (draft) best = scan<1>(p, draft + kept * a.draft_rs, e, -1, beg, end, &ahead);
+  else best = scan<2>(p, nullptr, e, drafted[kept], beg, end, &ahead);
   best = block_max(best, lds);
 
   if (a.splits > 1) {
@@ -151,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
     best = block_max(best, lds);
     if (threadIdx.x == 0) st_dev_u32(&a.counters[b], 0u);
   }
-  if (best == 0 && kept < n) best = block_max(scan<0>(p, nullptr, e, -1, 0, a.vocab), lds);
+  if (best == 0 && kept < n) best = block_max(scan<0>(p, nullptr, e, -1, 0, a.vocab, nullptr), lds);
   const int token = best ? (int)~(uint32_t)best : -1;
   if (threadIdx.x == 0) a.accepted[b] = kept;
   for (int i = threadIdx.x; i <= K; i += kThreads)
