@@ -65,9 +65,9 @@ typedef struct spear_kv_desc {
  *            nothing (-1 for padding).  Two tokens with the same slot race.
  *   k_scale, v_scale  fp32, written beside the codes (SPEAR_KV_INT8; may be
  *            NULL for SPEAR_KV_FP16).
- * tokens = 0 does nothing.
+ * tokens = 0 does nothing; tokens * kv_heads may be up to 2^27.
  * Errors: NULL_POINTER, INVALID_SHAPE (sizes, strides not multiples of 8),
- *         UNSUPPORTED (head_dim, page_size), INVALID_ARGUMENT (dtype),
+ *         UNSUPPORTED (head_dim, page_size, size), INVALID_ARGUMENT (dtype),
  *         MISALIGNED, HIP.
  */
 spear_status_t spear_kv_append(const spear_kv_desc_t* kv, int32_t tokens, const void* k, int64_t k_token_stride,
@@ -83,7 +83,7 @@ spear_status_t spear_kv_append(const spear_kv_desc_t* kv, int32_t tokens, const 
  *            cu_kv[b] .. cu_kv[b + 1] - 1 of the outputs with its first tokens.
  *   k_out, v_out  fp16 [rows][kv_heads][head_dim], contiguous, 16-byte
  *            aligned; rows at and past cu_kv[batch] are set to zero.  An 8-bit
- *            cache gives fp16(code * s).
+ *            cache gives fp16(code * s).  rows * kv_heads may be up to 2^28.
  * Errors: as spear_kv_append.
  */
 spear_status_t spear_kv_gather(const spear_kv_desc_t* kv, int32_t batch, int32_t rows, const int32_t* block_table,

@@ -62,6 +62,7 @@ def test_append_checks(lib, buf):
     assert append(lib, p, k=False) == NULL and append(lib, p, slots=False) == NULL and append(lib, p, cache=False) == NULL
     assert append(lib, p, kv(dtype=1), ks=False) == NULL
     assert append(lib, p, off=8) == MISALIGNED
+    assert append(lib, p, kv(heads=1024), tokens=(1 << 17) + 1) == UNSUPPORTED     # more than a launch's threads
 
 
 def test_gather_checks(lib, buf):
@@ -76,6 +77,7 @@ def test_gather_checks(lib, buf):
     assert gather(rows=0, table=None, cu=None, c=None, o=None) == OK
     assert gather(table=None) == NULL and gather(cu=None) == NULL and gather(c=None) == NULL and gather(o=None) == NULL
     assert gather(kv(dtype=1), s=None) == NULL
+    assert gather(kv(heads=1024), rows=(1 << 18) + 1) == UNSUPPORTED
     assert gather(o=p + 2) == MISALIGNED and gather(cu=p + 2) == MISALIGNED and gather(c=p + 8) == MISALIGNED
 
 

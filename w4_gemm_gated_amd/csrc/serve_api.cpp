@@ -119,6 +119,8 @@ spear_status_t spear_kv_append(const spear_kv_desc_t* kv, int32_t tokens, const 
   if (tokens < 0 || !row_strides(k_token_stride, k_head_stride) || !row_strides(v_token_stride, v_head_stride))
     return SPEAR_ERR_INVALID_SHAPE;
   if (tokens == 0) return SPEAR_OK;
+  // (a launch holds fewer than 2^32 threads; a workgroup of 256 takes 16 rows at least)
+  if ((int64_t)tokens * a.kv.heads > (int64_t)1 << 27) return SPEAR_ERR_UNSUPPORTED;
   if (!k || !v || !slots) return SPEAR_ERR_NULL_POINTER;
   st = check_cache(a.kv, k_cache, v_cache, k_scale, v_scale);
   if (st != SPEAR_OK) return st;
@@ -140,6 +142,7 @@ spear_status_t spear_kv_gather(const spear_kv_desc_t* kv, int32_t batch, int32_t
   if (st != SPEAR_OK) return st;
   if (batch < 0 || rows < 0 || table_stride < 1) return SPEAR_ERR_INVALID_SHAPE;
   if (rows == 0) return SPEAR_OK;
+  if ((int64_t)rows * a.kv.heads > (int64_t)1 << 28) return SPEAR_ERR_UNSUPPORTED;   // as above, 32 rows each
   if (!block_table || !cu_kv || !k_out || !v_out) return SPEAR_ERR_NULL_POINTER;
   st = check_cache(a.kv, k_cache, v_cache, k_scale, v_scale);
   if (st != SPEAR_OK) return st;
