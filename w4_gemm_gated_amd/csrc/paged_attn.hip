@@ -64,6 +64,11 @@ struct Shares {
   }
 };
 
+// A row tile counts this many steps more than it has where shares are cut, for
+// what its start and its result take (24 drafts of 500 .. 6000 keys 34.0 -> 32.4
+// us, 96 sequences of 64 .. 8192 in fp16 176 -> 171, 256 of 512 67 -> 64; with three
+// 31.9, 173, 66).  A share that begins among them begins with the next row tile.
+constexpr uint32_t kTileCost = 2;
 constexpr int kSeqs = 512;   // sequences kept in LDS; more are read again where needed
 
 // Steps of KS keys that a sequence's row tile takes.
@@ -222,9 +227,13 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
   const uint32_t rounds = (units + gridDim.x - 1) / gridDim.x;
   const bool whole_tiles = longest <= 8 ? units <= gridDim.x
                                         : even && units >= cus && (rounds == 1 || rounds * gridDim.x * 7 <= units * 8);
-  const uint32_t per_head = whole_tiles ? tiles : steps, total = per_head * (uint32_t)a.kv_heads;
+  // (few row tiles of like length share evenly by themselves: 8 of 4096 keys 31 us, 33
+  // with the cost)
+  const uint32_t cost = even && units < cus ? 0 : kTileCost;
+  const uint32_t per_head = whole_tiles ? tiles : steps + cost * tiles, total = per_head * (uint32_t)a.kv_heads;
   uint32_t groups = whole_tiles ? min(units, gridDim.x)
-                    : min(min(gridDim.x, units >= cus ? gridDim.x : even ? cus : 2 * cus), max(units, total / 4));
+                    : min(min(gridDim.x, units >= cus ? gridDim.x : even ? cus : 2 * cus),
+                          max(units, steps * (uint32_t)a.kv_heads / 4));
   if (blockIdx.x >= groups) return;
   const uint32_t each = uniform(total / groups);
   const Shares shares = {each, total - each * groups};
@@ -242,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
     uint32_t before = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kWave) {
       const Seq s = seq_of(b0 + lane);
-      const uint32_t mine = (uint32_t)s.tiles * (whole_tiles ? 1u : (uint32_t)steps_of<KS>(s));
+      const uint32_t mine = (uint32_t)s.tiles * (whole_tiles ? 1u : (uint32_t)steps_of<KS>(s) + cost);
       const uint32_t upto = before + wave_scan(mine);
       const uint64_t past = __ballot(upto > p);
       if (past) {
@@ -254,8 +263,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
         u.steps = max((kv + KS - 1) / KS, 1);
         const uint32_t off = p - (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), l);
         const uint32_t rt = whole_tiles ? off
-                            : __builtin_amdgcn_readlane(s.tiles, l) == 1 ? 0u : uniform(off / (uint32_t)u.steps);
-        u.step0 = whole_tiles ? 0 : (int)(off - rt * (uint32_t)u.steps);
+                            : __builtin_amdgcn_readlane(s.tiles, l) == 1 ? 0u : uniform(off / ((uint32_t)u.steps + cost));
+        u.step0 = whole_tiles ? 0 : (int)(off - rt * ((uint32_t)u.steps + cost));
         u.unit0 = at - (uint32_t)u.step0;
         u.r0 = (int)rt * R;
         break;
@@ -356,10 +365,16 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
     for (int n = 0; n < NS; ++n) page[n] = later_page[n];
   };
 
+  // The row tile after u, or `end`.
+  auto after = [&](const Part& u) { return whole_tiles ? u.unit0 + 1u : u.unit0 + (uint32_t)u.steps + cost; };
   Part u = find(shares.begin(blockIdx.x));
+  if (u.step0 >= u.steps) {
+    if (after(u) >= end) return;
+    u = find(after(u));
+  }
   begin(u);
   for (;;) {
-    const uint32_t next = u.unit0 + (whole_tiles ? 1u : (uint32_t)u.step1);
+    const uint32_t next = after(u);
     const bool more = next < end;
     const Part then = find(more ? next : u.unit0);
     const int see_all = u.see_all;
@@ -690,7 +705,7 @@ AttnPlan attn_plan(const spear_attention_desc_t& d, int cus) {
   // The kernels count work in 32 bits: steps of 128 keys of all row tiles here,
   // row tiles of a head times 64 keys in the other.
   const int64_t few = p.tiles ? (p.both ? d.batch : 0) : d.batch + rows / R;
-  p.fits = few * ceil_div(max_kv, 32 * kWaves) * H <= INT32_MAX &&
+  p.fits = few * (ceil_div(max_kv, 32 * kWaves) + kTileCost) * H <= INT32_MAX &&
            (p.tiles ? d.batch + rows / 128 : 0) * ceil_div(max_kv, 64) <= INT32_MAX / 2;
   // One share for each workgroup that the GPU holds at once; no more of them than
   // there can be steps.
