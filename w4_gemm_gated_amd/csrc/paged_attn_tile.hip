@@ -526,7 +526,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
       page = page_of(step0 + 1);
       for (int step = step0; step < step1; ++step) {
         const int buf = step & 1;
-        __syncthreads();                        // the tile is in LDS; the other stage is free
+        // Every wave waits for its own copies of this tile, also one that computed
+        // nothing since it asked for them (a barrier waits for no copies); then
+        // the tile is in LDS, and the other stage is free.
+        wait_vm_all();
+        __syncthreads();
         if (step + 1 < step1) {
           fetch(step + 1, page, buf ^ 1, codes);
           page = page_of(step + 2);
