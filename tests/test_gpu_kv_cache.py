@@ -233,3 +233,30 @@ def test_refusals():
         sp.spear_kv_gather(kc, vc, table, cu[:1], 3, ks, vs)
     with pytest.raises(sp.SpearError, match="INVALID_SHAPE"):
         sp.spear_kv_gather(kc, vc, table[:, :0].contiguous(), cu, 3, ks, vs)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.int8])
+@pytest.mark.parametrize("cu", [[5, 9, 0], [100, 60, 50], [2 ** 31 - 1, 3, 40], [-2 ** 31, -2 ** 31, 2 ** 31 - 1],
+                                [0, 40, 7], [0, -9, 30], [70, 70, 70]])
+def test_offsets_that_do_not_rise_stay_inside(dtype, cu):
+    """Rows that the offsets place before a sequence's first are zero; every other
+    row holds some token of the cache: nothing outside the tensors is read."""
+    note(f"gather {dtype} offsets {cu}")
+    heads, dim, page, rows, batch = 2, 64, 16, 64, len(cu) - 1
+    kc, vc, ks, vs = sp.spear_kv_cache(5, heads, dim, page, dtype, DEV)
+    for x, a in ((kc, 1), (vc, 2)):
+        x.fill_(a)                              # every place of the cache holds this
+    for x in (ks, vs):
+        if x is not None:
+            x.fill_(1.0)
+    # the table in the middle of a larger one, whose other entries name a page of other values
+    kc[4] = vc[4] = 99
+    wide = torch.full((batch + 6, 3), 4, dtype=torch.int32, device=DEV)
+    wide[3:3 + batch] = torch.arange(3 * batch, dtype=torch.int32, device=DEV).view(batch, 3) % 4
+    k, v = sp.spear_kv_gather(kc, vc, wide[3:3 + batch], torch.tensor(cu, dtype=torch.int32, device=DEV), rows, ks, vs)
+    torch.cuda.synchronize()
+    for x, a in ((k, 1), (v, 2)):
+        assert bool(((x == 0) | (x == a)).all())
+        assert bool((x.flatten(1) == x[:, :1, 0]).all())            # whole rows
+    if cu[0] > 0 and cu[1] > 0:                 # no row before the smallest offset belongs to a sequence
+        assert not k[:min(max(min(cu), 0), rows)].any()

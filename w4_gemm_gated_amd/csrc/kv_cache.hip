@@ -151,10 +151,11 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(GatherK a) {
     while (b < a.batch && a.cu[b + 1] <= row) ++b;
     at[r] = -1;
     if (b >= 0 && b < a.batch && row < a.rows) {
-      const int i = (int)row - a.cu[b];
-      const int64_t entry = min((int64_t)(i >> a.page_log2), a.table_stride - 1);
-      const uint32_t page = min((uint32_t)a.table[b * a.table_stride + entry], (uint32_t)a.num_pages - 1);
-      at[r] = (((int64_t)page * a.heads + head) << a.page_log2) + (i & ((1 << a.page_log2) - 1));
+      const int64_t i = row - a.cu[b], entry = table_entry(row, a.cu[b], a.page_log2, a.table_stride);
+      if (entry >= 0) {
+        const uint32_t page = min((uint32_t)a.table[b * a.table_stride + entry], (uint32_t)a.num_pages - 1);
+        at[r] = (((int64_t)page * a.heads + head) << a.page_log2) + (i & ((1 << a.page_log2) - 1));
+      }
     }
   }
   code_t kw[ROWS], vw[ROWS];

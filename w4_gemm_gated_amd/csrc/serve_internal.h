@@ -28,6 +28,15 @@ struct KvAppendArgs {
 };
 hipError_t launch_kv_append(const KvAppendArgs& a, void* stream);
 
+// Entry of a sequence's block table row for output row `row` of a sequence whose
+// first row is `first`: within the table whatever the offsets hold, -1 for a row
+// before the first (offsets that do not rise give such rows).
+constexpr int64_t table_entry(int64_t row, int64_t first, int page_log2, int64_t table_stride) {
+  if (row < first) return -1;
+  const int64_t entry = (row - first) >> page_log2;
+  return entry < table_stride ? entry : table_stride - 1;
+}
+
 struct KvGatherArgs {
   KvShape kv;
   int32_t batch, rows;
