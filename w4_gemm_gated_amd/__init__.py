@@ -173,8 +173,11 @@ def spear_schedule_ec_costs(extra_us, weights, slack_us):
 
 
 # Zero-filled workspaces, one per (device, stream); every call leaves its
-# workspace zero-filled, so they are reused as they are.
+# workspace zero-filled, so they are reused as they are.  One that a larger call
+# replaces stays alive: a graph captured with it holds its address.  (Sizes are
+# powers of two, so all replaced ones together are smaller than the present one.)
 _workspaces = {}
+_replaced_workspaces = []
 
 
 def _workspace(nbytes, device):
@@ -184,7 +187,14 @@ def _workspace(nbytes, device):
     key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
+        if torch.cuda.is_current_stream_capturing():
+            # Its zero fill would be recorded, not run: other calls on the stream, and
+            # other graphs replayed before this one, would find it uncleared.
+            raise RuntimeError(f"the stream under capture has no workspace of {nbytes} bytes yet: make a call of this "
+                               "size on that stream before the capture, or give one with workspace=")
+        if ws is not None:
+            _replaced_workspaces.append(ws)
+        ws = torch.zeros(max(1 << (nbytes - 1).bit_length(), 1 << 20), dtype=torch.uint8, device=dev)
         _workspaces[key] = ws
     return ws
 
@@ -212,7 +222,9 @@ def spear_w4ec_linear(X, Wq, scales, A, B, w_g, gate_bias, skip_tau=0.0, variant
     [K, r]; B fp16 [r, N]; w_g fp16 [K].  A, B, w_g may be None (rank 0).
     `plan` may come from spear_dispatch_plan for the same shape; `workspace`
     (uint8, zero-filled before first use) defaults to a cached one for the
-    current stream.
+    current stream; under graph capture it has to be there already, from a call on
+    that stream (torch.cuda.graph captures on a stream of its own unless given one),
+    and the graph's replays must not run beside other calls on it.
     """
     _need(X, "X", torch.float16, 2)
     _need(Wq, "Wq", torch.uint8, 1)

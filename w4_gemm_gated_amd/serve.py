@@ -199,7 +199,8 @@ def spear_paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q
     [B + 1]: rows of sequence b; kv_lens int32 [B]: its cached tokens, the new
     ones among them; block_table int32 [B, max_pages]; max_q: the longest
     sequence's new tokens; scale defaults to 1 / sqrt(head_dim).  `workspace`
-    (uint8) defaults to the cached one of the current stream.
+    (uint8, zero-filled before first use) defaults to the cached one of the current
+    stream, as spear_w4ec_linear's, also under graph capture.
     """
     kv, dev, at = _kv_desc(k_cache, v_cache, k_scale, v_scale)
     qt, qh = _rows(q, "q", torch.float16, dev)
@@ -241,7 +242,8 @@ def spear_verify_draft(target, draft, drafted, u, noise, num_drafts=None, accept
     target fp32 [B, K + 1, V] and draft fp32 [B, K, V]: probabilities (last
     dimension contiguous), draft None where each drafted token was certain;
     drafted int32 [B, K]; u fp32 [B, K] uniform in [0, 1); noise fp32 [B, V] from
-    Exp(1); num_drafts int32 [B] or None (K each).
+    Exp(1); num_drafts int32 [B] or None (K each); `workspace` as in
+    spear_paged_attention.
     """
     if not isinstance(target, torch.Tensor) or not target.is_cuda:
         raise ValueError("target must be a GPU tensor")
