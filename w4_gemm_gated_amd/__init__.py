@@ -53,7 +53,15 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
 
+def _on_current(device):
+    """The library launches on the current device; tensors of another are refused."""
+    if device.index is not None and device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, but the current device is cuda:{torch.cuda.current_device()}: "
+                         "make the call under torch.cuda.device(..)")
+
+
 def _stream(device):
+    _on_current(device)
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 

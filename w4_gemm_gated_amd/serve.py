@@ -97,7 +97,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(device):
-    return _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+    index = device.index
+    if index != torch.cuda.current_device():
+        _pkg._on_current(device)                # refuses
+    return _raw_stream(index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
 
 
 # What follows from a call's sizes alone is made once for them: the descriptor
