@@ -80,7 +80,7 @@ spear_status_t spear_kv_append(const spear_kv_desc_t* kv, int32_t tokens, const 
 /*
  * spear_kv_gather -- read whole sequences back in fp16.
  *   block_table  int32 [batch][table_stride], entries of a sequence's pages in
- *            order; entries past its last page are not read.
+ *            order; entries past its last page are not read (batch 0: may be NULL).
  *   cu_kv    int32 [batch + 1], rising from 0: sequence b fills rows
  *            cu_kv[b] .. cu_kv[b + 1] - 1 of the outputs with its first tokens.
  *   k_out, v_out  fp16 [rows][kv_heads][head_dim], contiguous, 16-byte

@@ -260,3 +260,15 @@ def test_offsets_that_do_not_rise_stay_inside(dtype, cu):
         assert bool((x.flatten(1) == x[:, :1, 0]).all())            # whole rows
     if cu[0] > 0 and cu[1] > 0:                 # no row before the smallest offset belongs to a sequence
         assert not k[:min(max(min(cu), 0), rows)].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.int8])
+@pytest.mark.parametrize("pages", [0, 3])
+def test_gather_of_no_sequences_gives_zeros(dtype, pages):
+    note(f"gather of no sequences {dtype}")
+    kc, vc, ks, vs = sp.spear_kv_cache(2, 3, 64, 16, dtype, DEV)
+    out = [torch.full((70, 3, 64), 9.0, dtype=torch.float16, device=DEV) for _ in range(2)]
+    table = torch.zeros(0, pages, dtype=torch.int32, device=DEV)
+    sp.spear_kv_gather(kc, vc, table, torch.zeros(1, dtype=torch.int32, device=DEV), 70, ks, vs, *out)
+    torch.cuda.synchronize()
+    assert not out[0].any() and not out[1].any()

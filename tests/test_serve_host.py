@@ -166,3 +166,15 @@ def test_verify_checks(lib, buf):
     for o in ({"target": p + 2}, {"draft": p + 1}, {"noise": p + 2}, {"tok": p + 2}, {"ws": p + 8}):
         assert call(**o) == MISALIGNED
     assert call(bytes_=(1 << 20) + 8) == SMALL
+
+
+def test_gather_of_no_sequences_needs_no_table(lib, buf):
+    p = buf[1]
+    d = kv()
+
+    def gather(batch, table, stride, out, cu=p):
+        return lib.spear_kv_gather(ctypes.byref(d), batch, 1, table, stride, cu, p, p, p, p, out, out, None)
+    # (the outputs' alignment is looked at after the table)
+    assert gather(0, None, 4, p + 2) == MISALIGNED and gather(0, None, 0, p + 2) == MISALIGNED
+    assert gather(1, None, 4, p + 2) == NULL and gather(1, p, 0, p) == SHAPE
+    assert gather(0, None, 0, p, cu=None) == NULL

@@ -140,10 +140,10 @@ spear_status_t spear_kv_gather(const spear_kv_desc_t* kv, int32_t batch, int32_t
   KvGatherArgs a;
   spear_status_t st = check_kv(*kv, &a.kv);
   if (st != SPEAR_OK) return st;
-  if (batch < 0 || rows < 0 || table_stride < 1) return SPEAR_ERR_INVALID_SHAPE;
+  if (batch < 0 || rows < 0 || (batch > 0 && table_stride < 1)) return SPEAR_ERR_INVALID_SHAPE;
   if (rows == 0) return SPEAR_OK;
   if ((int64_t)rows * a.kv.heads > (int64_t)1 << 28) return SPEAR_ERR_UNSUPPORTED;   // as above, 32 rows each
-  if (!block_table || !cu_kv || !k_out || !v_out) return SPEAR_ERR_NULL_POINTER;
+  if ((batch > 0 && !block_table) || !cu_kv || !k_out || !v_out) return SPEAR_ERR_NULL_POINTER;   // no table of none
   st = check_cache(a.kv, k_cache, v_cache, k_scale, v_scale);
   if (st != SPEAR_OK) return st;
   if (!aligned(block_table, 4) || !aligned(cu_kv, 4) || !aligned(k_out, 16) || !aligned(v_out, 16))
