@@ -144,9 +144,9 @@ spear_status_t spear_paged_attention(const spear_attention_desc_t* desc, const v
 
 /* One verification call. */
 typedef struct spear_verify_desc {
-  int32_t batch;       /* sequences; 0 is a no-op */
-  int32_t max_drafts;  /* K >= 0 drafted tokens at most per sequence */
-  int32_t vocab;       /* V >= 1 */
+  int32_t batch;       /* sequences; 0 is a no-op; below 2^24 */
+  int32_t max_drafts;  /* K >= 0 drafted tokens at most per sequence; up to 2^20 */
+  int32_t vocab;       /* V >= 1; up to 2^30 */
   int32_t device_cus;  /* as in spear_attention_desc_t */
 } spear_verify_desc_t;
 
@@ -154,7 +154,8 @@ typedef struct spear_verify_desc {
  * spear_verify_workspace_bytes -- device workspace of a call (host only): one
  * of spear_w4ec_linear's kind, zero-filled before its first use; the call
  * returns the counters of its header to zero.
- * Errors: NULL_POINTER, INVALID_SHAPE, HIP.
+ * Errors: NULL_POINTER, INVALID_SHAPE, INVALID_ARGUMENT (device_cus),
+ *         UNSUPPORTED (sizes), HIP.
  */
 spear_status_t spear_verify_workspace_bytes(const spear_verify_desc_t* desc, size_t* bytes);
 
@@ -178,7 +179,8 @@ spear_status_t spear_verify_workspace_bytes(const spear_verify_desc_t* desc, siz
  *   num_drafts  int32 [batch], 0 to K each (clamped); NULL: K for all.
  *   accepted output int32 [batch]: a.  tokens output int32 [batch][K + 1]: the
  *            kept tokens, the drawn one, then -1.
- * Errors: NULL_POINTER, INVALID_SHAPE, MISALIGNED, WORKSPACE_TOO_SMALL, HIP.
+ * Errors: NULL_POINTER, INVALID_SHAPE, INVALID_ARGUMENT, UNSUPPORTED,
+ *         MISALIGNED, WORKSPACE_TOO_SMALL, HIP.
  */
 spear_status_t spear_verify_draft(const spear_verify_desc_t* desc, const float* target, int64_t target_batch_stride,
                                   int64_t target_row_stride, const float* draft, int64_t draft_batch_stride,

@@ -178,3 +178,12 @@ def test_gather_of_no_sequences_needs_no_table(lib, buf):
     assert gather(0, None, 4, p + 2) == MISALIGNED and gather(0, None, 0, p + 2) == MISALIGNED
     assert gather(1, None, 4, p + 2) == NULL and gather(1, p, 0, p) == SHAPE
     assert gather(0, None, 0, p, cu=None) == NULL
+
+
+def test_verification_takes_no_more_sequences_than_a_launch_holds(lib, buf):
+    n = ctypes.c_size_t(0)
+
+    def size(batch):
+        return lib.spear_verify_workspace_bytes(ctypes.byref(_binding.VerifyDesc(batch, 1, 100, 256)), ctypes.byref(n))
+    assert size(1 << 24) == UNSUPPORTED             # 2^24 workgroups of 256: 2^32 threads
+    assert size((1 << 24) - 1) == OK and n.value == 0

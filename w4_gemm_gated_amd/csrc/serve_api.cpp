@@ -96,7 +96,8 @@ spear_status_t plan_attention(const spear_attention_desc_t& d, AttnPlan* p) {
 spear_status_t check_verify(const spear_verify_desc_t& d) {
   if (d.batch < 0 || d.max_drafts < 0 || d.vocab < 1) return SPEAR_ERR_INVALID_SHAPE;
   if (d.device_cus < 0) return SPEAR_ERR_INVALID_ARGUMENT;
-  if (d.vocab > (1 << 30) || d.max_drafts > (1 << 20) || d.batch > (1 << 24)) return SPEAR_ERR_UNSUPPORTED;
+  // (a launch holds fewer than 2^32 threads; a sequence takes a workgroup of 256 at least)
+  if (d.vocab > (1 << 30) || d.max_drafts > (1 << 20) || d.batch >= (1 << 24)) return SPEAR_ERR_UNSUPPORTED;
   return SPEAR_OK;
 }
 
