@@ -144,3 +144,25 @@ def test_refusals():
         sp.spear_verify_draft(*big, workspace=torch.zeros(64, dtype=torch.uint8, device=DEV))
     a, t = sp.spear_verify_draft(target[:0], draft[:0], drafted[:0], u[:0], noise[:0])
     assert a.shape == (0,) and t.shape == (0, 4)
+
+
+@pytest.mark.parametrize("lost", [False, True])
+@pytest.mark.parametrize("V", [5, 63, 4097, 9001, 33002])
+def test_draft_entries_below_zero_count_where_they_are(V, lost):
+    """A draft row that is no distribution (entries below zero, as a clipped one may
+    hold) still draws by p - q, and only from the vocabulary, also where the target
+    is NaN."""
+    note(f"draft entries below zero, V {V}, target NaN there: {lost}")
+    rng = np.random.default_rng(V)
+    target, draft, drafted, u, noise = case(rng, 6, 2, V)
+    u[:] = 1.0                                    # (nothing is kept)
+    draft += np.float32(1e-3) + target[:, :2]
+    for b in range(6):
+        draft[b, :, V - 1 - b % 5] = -0.5         # the largest residual, near the end
+        draft[b, :, V // 2] = -0.01
+        if lost:
+            target[b, :, V - 1 - b % 5] = np.nan
+    drafted[:] = 0
+    got, want = run(target, draft, drafted, u, noise), ref.verify_draft(target, draft, drafted, u, noise)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+    assert (got[1] < V).all()

@@ -82,7 +82,10 @@ __device__ __forceinline__ uint64_t scan(const float* __restrict__ p, const floa
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       const int j = r0 + 4 * ((int)threadIdx.x + i * kThreads);
-      if (r0 + kStep > end && j + 3 >= end) pv[i] = f4u_t{0.0f, 0.0f, 0.0f, 0.0f};
+      if (r0 + kStep > end && j + 3 >= end) {
+        pv[i] = f4u_t{0.0f, 0.0f, 0.0f, 0.0f};
+        if (MODE == 1) qv[i] = pv[i];
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) best.see(weight(pv[i][k], MODE == 1 ? qv[i][k] : 0.0f, j + k), ev[i][k], j + k);
     }
