@@ -528,8 +528,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
         const int buf = step & 1;
         // Every wave waits for its own copies of this tile, also one that computed
         // nothing since it asked for them (a barrier waits for no copies); then
-        // the tile is in LDS, and the other stage is free.
-        wait_vm_all();
+        // the tile is in LDS, and the other stage is free.  (Written so that the
+        // compiler does not see the wait: told of it, it waits for the next tile's
+        // copies before this tile's scores, 1020 instead of 960 us for 8 x 2048
+        // tokens over 4096 keys at head dimension 128.)
+        drain_vm();
         __syncthreads();
         if (step + 1 < step1) {
           fetch(step + 1, page, buf ^ 1, codes);
