@@ -49,6 +49,7 @@ constexpr int kKeys = 64;                   // of a tile
 constexpr int kNS = kKeys / 16;             // 16-key tiles
 constexpr int kNG = kKeys / 32;             // 32-key groups
 constexpr int kRT = kWaveRows / 16;
+constexpr float kLarge = 0x1p20f;           // references past this are large
 constexpr int kSchedMatrix = 0x8, kSchedLdsRead = 0x100;   // instruction classes of the issue order
 
 typedef __attribute__((address_space(3))) void lds_void_t;
@@ -193,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
 
     float4_t acc[kRT][NJ];
     float mref[kRT], l[kRT];
+    uint64_t large = 0;   // lanes with a large reference
 #pragma unroll
     for (int x = 0; x < kRT; ++x) {
       mref[x] = kNone;
@@ -368,7 +370,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
       }
 #pragma unroll
       for (int x = 0; x < kRT; ++x) move |= top[x] > mref[x] + kHead;
-      if (__ballot(move)) {
+      // A reference is a rounded product, the weights' argument an exact one less it:
+      // at scores past 2^24 they differ by whole numbers, past 2^27 by more than
+      // fp16's range leaves room for.  So where a reference is large (rarely) the
+      // scores are rounded as their maximum was.
+      float by = a.scale;
+      if (__ballot(move) | large) {
 #pragma unroll
         for (int x = 0; x < kRT; ++x) {
           const float to = top[x] > mref[x] + kHead ? top[x] - kStart : mref[x];
@@ -377,6 +384,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
           l[x] *= f;
 #pragma unroll
           for (int j = 0; j < NJ; ++j) acc[x][j] *= f;
+          if constexpr (!I8) large |= __ballot(fabsf(to) > kLarge && to != kNone);
+        }
+        if (!I8 && large) {
+          by = 1.0f;
+#pragma unroll
+          for (int x = 0; x < kRT; ++x)
+#pragma unroll
+            for (int n = 0; n < kNS; ++n) st[x][n] *= a.scale;
         }
       }
       half8_t pf[kRT][kNG];
@@ -387,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float s = st[x][n][i];
-            float p = __builtin_amdgcn_exp2f(I8 ? s - mref[x] : __builtin_fmaf(s, a.scale, -mref[x]));
+            float p = __builtin_amdgcn_exp2f(I8 ? s - mref[x] : __builtin_fmaf(s, by, -mref[x]));
             l[x] += p;
             if constexpr (I8) p *= vs[n][i];
             pf[x][n / 2][4 * (n % 2) + i] = (half_t)p;
