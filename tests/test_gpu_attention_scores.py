@@ -52,3 +52,24 @@ def test_equal_large_scores_give_the_mean(int8, dim, score, q_lens, lens):
     keys(c, int8, [3])
     got = run(c, scale=score / 31.5)
     assert worst(c, got, lambda at: np.ones(len(at))) <= 1
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_lens,lens", BATCHES)
+def test_a_step_of_sixteen_at_large_scores(int8, dim, q_lens, lens):
+    """Scores (in powers of two) of 1500 * 2^17 for the first 128 keys and 16 more, the
+    next number in fp32, for the others: these weigh 2^16 times as much."""
+    note(f"neighbouring scores int8 {int8} dim {dim} q {q_lens} kv {lens}")
+    c = make(np.random.default_rng(4), q_lens, lens, 1, 4, dim, 16, int8)
+    c["q"][:] = 0
+    c["q"][:, :, 0] = 12 if int8 else 1
+    c["q"][:, :, 1] = 2.0 ** -13
+    keys(c, int8, [125 if int8 else 1500])
+    for b, length in enumerate(lens):
+        for i in range(128, length):
+            c["k"][c["table"][b, i // 16], :, i % 16, 1] = 1
+    scale = np.float32(2.0 ** 17) / np.float32(1.44269504088896341)
+    assert scale * np.float32(1.44269504088896341) == 2.0 ** 17
+    got = run(c, scale=float(scale))
+    assert worst(c, got, lambda at: np.where(at < 128, 1.0, 2.0 ** 16)) <= 1

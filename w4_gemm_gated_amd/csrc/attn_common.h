@@ -34,7 +34,8 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kNone = -1e30f;      // reference of a row that has seen no key
-constexpr float kHead = 14.0f;       // a maximum this far above the reference moves it
+constexpr float kHead = 14.0f;       // a maximum more than this above the reference moves it (by their
+                                     // difference: a sum would be rounded up at large scores)
 constexpr float kStart = 6.0f;       // .. to this far below the maximum
 constexpr float kMaxScale = 1e30f;   // scales above this do not enter the reference
 

@@ -464,12 +464,12 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
           }
           top[x] += e;
         }
-        move |= top[x] > mref[x] + kHead;
+        move |= top[x] - mref[x] > kHead;
       }
       if (__ballot(move)) {
 #pragma unroll
         for (int x = 0; x < RT; ++x) {
-          const float to = top[x] > mref[x] + kHead ? top[x] - kStart : mref[x];
+          const float to = top[x] - mref[x] > kHead ? top[x] - kStart : mref[x];
           const float f = __builtin_amdgcn_exp2f(mref[x] - to);
           mref[x] = to;
           l[x] *= f;

@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
         for (int x = 0; x < kRT; ++x) top[x] *= a.scale;
       }
 #pragma unroll
-      for (int x = 0; x < kRT; ++x) move |= top[x] > mref[x] + kHead;
+      for (int x = 0; x < kRT; ++x) move |= top[x] - mref[x] > kHead;
       // A reference is a rounded product, the weights' argument an exact one less it:
       // at scores past 2^24 they differ by whole numbers, past 2^27 by more than
       // fp16's range leaves room for.  So where a reference is large (rarely) the
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
       if (__ballot(move) | large) {
 #pragma unroll
         for (int x = 0; x < kRT; ++x) {
-          const float to = top[x] > mref[x] + kHead ? top[x] - kStart : mref[x];
+          const float to = top[x] - mref[x] > kHead ? top[x] - kStart : mref[x];
           const float f = __builtin_amdgcn_exp2f(mref[x] - to);
           mref[x] = to;
           l[x] *= f;
