@@ -73,3 +73,17 @@ def test_a_step_of_sixteen_at_large_scores(int8, dim, q_lens, lens):
     assert scale * np.float32(1.44269504088896341) == 2.0 ** 17
     got = run(c, scale=float(scale))
     assert worst(c, got, lambda at: np.where(at < 128, 1.0, 2.0 ** 16)) <= 1
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("score", [-1e9, -1e31, -1e33])
+@pytest.mark.parametrize("q_lens,lens", BATCHES)
+def test_equal_scores_far_below_zero_give_the_mean(int8, dim, score, q_lens, lens):
+    note(f"scores of {score:g} int8 {int8} dim {dim} q {q_lens} kv {lens}")
+    c = make(np.random.default_rng(5), q_lens, lens, 1, 4, dim, 16, int8)
+    c["q"][:] = 0
+    c["q"][:, :, 0] = 1050
+    keys(c, int8, [-3])
+    got = run(c, scale=-score / 3150)
+    assert worst(c, got, lambda at: np.ones(len(at))) <= 1

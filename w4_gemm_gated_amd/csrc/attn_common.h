@@ -33,7 +33,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr float kNone = -1e30f;      // reference of a row that has seen no key
+constexpr float kNone = -0x1.fffffep127f;   // reference of a row that has seen no key: below every finite score
 constexpr float kHead = 14.0f;       // a maximum more than this above the reference moves it (by their
                                      // difference: a sum would be rounded up at large scores)
 constexpr float kStart = 6.0f;       // .. to this far below the maximum
