@@ -29,10 +29,11 @@
  * back without a finite value.
  *
  * Memory safety against device data the host cannot check: lengths and offsets
- * are clamped to the tensors' bounds (with offsets that do not rise, a row that
- * comes before its sequence's first is read back as zeros), page numbers outside
- * [0, num_pages) are read as the last page, slots outside the cache are not
- * written.
+ * are clamped to the tensors' bounds, page numbers outside [0, num_pages) are
+ * read as the last page, slots outside the cache are not written.  With offsets
+ * that do not rise, a row that comes before its sequence's first is read back as
+ * zeros, and an attention call so large that the rows they repeat could pass its
+ * 32-bit counts computes nothing.
  */
 #ifndef SPEAR_SERVE_H
 #define SPEAR_SERVE_H

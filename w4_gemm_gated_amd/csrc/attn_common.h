@@ -24,6 +24,7 @@ struct AttnK {
   int32_t rows_from, rows_to;   // sequences with more rows than the one and no more than the other are this launch's
   float scale;                  // |scale| * log2(e)
   int32_t negate;               // the scale is negative: queries enter with the other sign
+  int32_t check_order;          // do nothing unless the offsets rise
 };
 
 hipError_t launch_attention_tiles(const AttnK& k, int dim, bool i8, int grid, hipStream_t st);
@@ -100,6 +101,13 @@ __device__ __forceinline__ Seq sequence(const AttnK& a, int b) {
     s.tiles = rows > a.rows_from && rows <= a.rows_to ? (rows + R - 1) / R : 0;
   }
   return s;
+}
+
+// Whether the offsets rise (the same in all workgroups).
+__device__ __forceinline__ bool offsets_rise(const AttnK& a, int lane) {
+  bool falls = false;
+  for (int b = lane; b < a.batch; b += kWave) falls |= a.cu[b + 1] < a.cu[b];
+  return !__ballot(falls);
 }
 
 // -------------------------------------------------------------- small pieces

@@ -196,6 +196,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) attn_kernel(AttnK a
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane % 16, t = lane / 16;
 
+  if (a.check_order && !offsets_rise(a, lane)) return;
+
   // This workgroup's share.  Whole row tiles where those come out even on the
   // workgroups: sequences of like length (64 of 2k, 512 row tiles: 112 us, 123 cut
   // into 768 shares), or all so short that a join would cost more than it saves.
@@ -707,6 +709,9 @@ AttnPlan attn_plan(const spear_attention_desc_t& d, int cus) {
   const int64_t few = p.tiles ? (p.both ? d.batch : 0) : d.batch + rows / R;
   p.fits = few * (ceil_div(max_kv, 32 * kWaves) + kTileCost) * H <= INT32_MAX &&
            (p.tiles ? d.batch + rows / 128 : 0) * ceil_div(max_kv, 64) <= INT32_MAX / 2;
+  // (in a batch of both kinds a sequence of few rows is one row tile)
+  p.check_few = !p.both && !counts_hold(d.batch, rows, R, max_kv, 32 * kWaves, kTileCost, H, INT32_MAX);
+  p.check_tiles = !counts_hold(d.batch, rows, 128, max_kv, 64, 0, 1, INT32_MAX / 2);
   // One share for each workgroup that the GPU holds at once; no more of them than
   // there can be steps.
   const int64_t held = (int64_t)(p.row_tiles == 1 ? 3 : 2) * p.cus;
@@ -744,6 +749,7 @@ hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* stream) 
     k.rows_to = INT32_MAX;
     k.part = (float*)((char*)a.workspace + p.tile_part);
     k.part_bytes = (int32_t)p.tile_part_bytes;
+    k.check_order = p.check_tiles;
     const hipError_t e = launch_attention_tiles(k, a.kv.dim, i8, p.tile_grid, st);
     if (e != hipSuccess || !p.both) return e;
   }
@@ -751,6 +757,7 @@ hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* stream) 
   k.rows_to = p.both ? p.few_rows : INT32_MAX;
   k.part = (float*)((char*)a.workspace + p.part);
   k.part_bytes = (int32_t)p.part_bytes;
+  k.check_order = p.check_few;
   if (a.kv.dim == 64) {
     if (i8) return two ? launch<64, true, 2>(k, p, st) : launch<64, true, 1>(k, p, st);
     return two ? launch<64, false, 2>(k, p, st) : launch<64, false, 1>(k, p, st);

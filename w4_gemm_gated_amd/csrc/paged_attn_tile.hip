@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tile_kernel(AttnK a) {
   // reads), rows 0 .. 15 one unit (the plain ones).
   auto swizzle = [](int row) { return (UPR == 16 ? (row & 7) << 1 : (row & 6)) | ((row >> 3) & 1); };
 
+  if (a.check_order && !offsets_rise(a, lane)) return;
   const Seq seq0 = sequence<kRows>(a, lane);
   // Two workgroups run on a CU; no pieces if the row tiles alone are near to that.
   const Load load = load_of(a, seq0, lane);

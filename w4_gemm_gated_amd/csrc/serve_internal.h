@@ -49,6 +49,15 @@ struct KvGatherArgs {
 };
 hipError_t launch_kv_gather(const KvGatherArgs& a, void* stream);
 
+// Whether an attention kernel's 32-bit counts hold for any offsets at all: with
+// ones that do not rise, each of the sequences can have all rows.  `extra` steps
+// count for each row tile beside those of its keys; `most` is the count's bound.
+constexpr bool counts_hold(int64_t batch, int64_t rows, int64_t tile_rows, int64_t max_kv, int64_t step_keys,
+                           int64_t extra, int64_t heads, int64_t most) {
+  const double tiles = (double)((rows + tile_rows - 1) / tile_rows), steps = (double)((max_kv + step_keys - 1) / step_keys);
+  return (double)batch * tiles * (steps + (double)extra) * (double)heads <= (double)most;
+}
+
 // Launch shape of an attention call.
 struct AttnPlan {
   bool tiles;         // sequences of many rows go to the kernel of 128-row tiles ..
@@ -57,7 +66,8 @@ struct AttnPlan {
   int few_rows;       // 16 * row_tiles
   int grid, tile_grid;   // workgroups of the latter and of the former
   int cus;
-  bool fits;          // the work can be counted in 32 bits
+  bool fits;          // the work of rising offsets can be counted in 32 bits
+  bool check_few, check_tiles;   // that of any others need not: the kernel looks whether they rise
   size_t part, part_bytes;            // partial results in the workspace
   size_t tile_part, tile_part_bytes;
   size_t bytes;       // workspace
