@@ -26,7 +26,7 @@ inline int64_t ec_cols(int64_t rank) { return round_up(rank + 1, 16); }
 // Row stride (floats) of the stored P: rank padded to the 32-k granule.
 inline int64_t p_stride(int64_t rank) { return round_up(rank, 32); }
 
-// Every workspace starts with a fixed 256 KiB header: cross-workgroup
+// Every workspace starts with a fixed 1 MiB header: cross-workgroup
 // counters of the EC projection in [0, 32 KiB) and of the GEMM kernels in
 // [32 KiB, 64 KiB), which every call returns to zero (except the GEMM call
 // epoch, which every fused call advances), and the fused variant's hand-off

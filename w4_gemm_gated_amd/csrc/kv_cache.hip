@@ -12,7 +12,7 @@
 // MB fetched for 169, and 10,000 tokens of 8 heads of 64 took 45 us instead of 37).
 // Measured with 8 heads of 128: 24 sequences, 80,000 tokens, read back from 8 bits
 // in 102 us (498 MB read and written, 4.9 TB/s; a plain copy of 2 GiB reaches
-// 4.9); 6,800 tokens quantised, written and read back in 21 us (85 MB); a decode
+// 4.9) and from fp16 in 117 (656 MB, 5.6 TB/s); 34,000 from fp16 in 45 us; 6,800 tokens quantised, written and read back in 21 us (85 MB); a decode
 // step's 48 tokens in 2.7 us of the 7.5 that a launch takes.
 #include "serve_internal.h"
 #include "device_common.h"
@@ -229,7 +229,7 @@ hipError_t launch_kv_gather(const KvGatherArgs& a, void* stream) {
   k.batch = a.batch; k.rows = a.rows; k.heads = a.kv.heads;
   k.page_log2 = a.kv.page_log2; k.num_pages = a.kv.num_pages;
   // Two rows a thread where the outputs pass the 256 MiB that the card caches
-  // (328 MB: 102 us, 110 with one; 61 MB: 38.4, 36.8 with one).
+  // (from 8 bits 328 MB: 102 us, 110 with one; 61 MB: 38.4, 36.8 with one).
   const bool two = (int64_t)a.rows * a.kv.heads * a.kv.dim * 4 > (int64_t)256 << 20;
   const hipStream_t st = (hipStream_t)stream;
   const bool i8 = a.kv.dtype == SPEAR_KV_INT8;

@@ -42,9 +42,12 @@
 //
 // Memory bounds it.  Measured (8 kv heads of 128; reading pages and computing
 // nothing reaches 6.0 TB/s): 64 sequences of 4096 keys over 8 bits 100 us (5.5
-// TB/s), of 2048 in fp16 107 us (5.0); 96 of 64 .. 8192 over 8 bits 88 us (4.7);
+// TB/s), of 2048 in fp16 107 us (5.0); 96 of 64 .. 8192 over 8 bits 88 us (4.7),
+// in fp16 170; 24 of 500 .. 6000 with drafts 32 us over 8 bits, 68 in fp16;
 // two of 54,000 and 60,000 in fp16 95 us (4.9); a few short ones 12 us, of
-// which the launch and the chain length - table - keys take 8.
+// which the launch and the chain length - table - keys take 8.  In fp16 at head
+// dimension 128 19 (16 rows) and 59 (32 rows) registers are kept in memory; without
+// the rare code for infinite and NaN values it would be 9 and none.
 #include <algorithm>
 
 #include "attn_common.h"

@@ -4,8 +4,8 @@
 // that share a kv head, S^T = K Q^T and O^T = V^T P^T, so that P goes from one
 // product's result registers into the other's operand without leaving its lane.
 // Here the matrix cores bound the work: a workgroup takes 128 rows, 32 for each of
-// its four waves, and all waves share a tile of 64 keys in LDS (two stages:
-// the next tile is copied in while this one is used).
+// its four waves, and all waves share a tile of 64 keys in LDS (two stages: the
+// next tile is requested before this one is used).
 //
 //   - fp16 tiles go straight from memory to LDS; 16-byte units are permuted
 //     within their row by the row's number on the way (the lane's source
@@ -14,6 +14,10 @@
 //   - K fragments are 16-byte reads of a row; V^T fragments are transposing
 //     reads (within 16 lanes, lane 4e + q gives the address of row e's four
 //     values at 4q, and lane i receives column i of the four rows).
+//   - in fp16 the request runs ahead by less than a tile: the compiler takes a read
+//     of one stage to alias the copies into the other, and waits for these before
+//     the tile's first keys (64) or first values (128) are read.  The other
+//     workgroup of the CU covers that wait.
 //   - the softmax reference moves rarely, the 8-bit scales enter the scores and
 //     the weights, and infinities in values that some row must not see are kept
 //     out, all as described in paged_attn.hip.
@@ -33,11 +37,13 @@
 // workspace; the last of a row tile's to arrive joins them in order.
 //
 // Measured (32 query heads on 8 kv heads): 8 x 2048 tokens over 4096 keys in
-// 960 us at head dimension 128 and 570 us at 64 (858 and 723 TFLOP/s; a large
-// library product reaches 1104), 1130 and 805 us over an 8-bit cache; one chunk
-// of 700 tokens over 2571 keys in 52, 31, 59 and 45 us.  Counted at the first of
-// these sizes, vector and matrix instructions together fill 83 (128) and 97 % (64)
-// of the cycles.
+// 942 us at head dimension 128 and 599 us at 64 (876 and 689 TFLOP/s; a large
+// library product reaches 1104), 1125 and 758 us over an 8-bit cache; one chunk
+// of 700 tokens over 2571 keys in 49, 31, 57 and 40 us.  Counted at the first of
+// these sizes in fp16, vector and matrix instructions together fill 90 % (128) and
+// all (64) of the cycles.  At 128 the code for infinite and NaN values, inlined but
+// rarely run, costs registers: 187 are kept in memory around the loop in fp16, none
+// within it (without that code none at all; four over 8 bits).
 #include "attn_common.h"
 
 namespace spear {
