@@ -87,3 +87,22 @@ def test_equal_scores_far_below_zero_give_the_mean(int8, dim, score, q_lens, len
     keys(c, int8, [-3])
     got = run(c, scale=-score / 3150)
     assert worst(c, got, lambda at: np.ones(len(at))) <= 1
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("score", [1.0, 2.4e8, 5e8])
+@pytest.mark.parametrize("power", [-36, -30, -24, -18, -10, 9])
+@pytest.mark.parametrize("q_lens,lens", BATCHES[1:4])
+def test_scales_of_values_beside_large_scores(dim, score, power, q_lens, lens):
+    """The exponent of the values' scales cannot be held beside a large score; the
+    result is the values' mean all the same (or zero where fp16 holds no such value)."""
+    note(f"scores of {score:g}, scales of 2^{power}, dim {dim} q {q_lens} kv {lens}")
+    c = make(np.random.default_rng(6), q_lens, lens, 1, 4, dim, 16, True)
+    c["q"][:] = 0
+    c["q"][:, :, 0] = 10.5
+    keys(c, True, [3])
+    c["v_scale"][np.isfinite(c["v_scale"])] = 2.0 ** power
+    got = run(c, scale=score / 31.5)
+    v = c["v"]
+    c["v"] = v.astype(np.float64) * 2.0 ** power
+    assert worst(c, got, lambda at: np.ones(len(at))) <= 1

@@ -184,10 +184,13 @@ __device__ __forceinline__ int opaque(int x) {
 }
 
 // Of an 8-bit cache's values: a power of two above their scales, as its exponent.
-// It enters the reference, so that weights times scales keep to fp16's range
-// (with a bound for values that vanish in an fp16 result anyway).
+// It enters the reference, so that weights times scales keep to fp16's range.
+// Bounded below, for two reasons.  A score past 2^27 rounds its sum with the exponent
+// to a multiple of 16, 32, ..: an exponent above -16 is then off by what the range
+// still holds.  And it loses nothing: the largest weight times a scale of 2^-35 is a
+// normal fp16 number, while the values of scales from 2^-32 down vanish in fp16.
 __device__ __forceinline__ float scale_exponent(float largest) {
-  return fmaxf((float)((int)(float_bits(largest) >> 23) - 126), -40.0f);
+  return fmaxf((float)((int)(float_bits(largest) >> 23) - 126), -15.0f);
 }
 
 // Queries of a row as a B operand; a negative scale's sign goes here.
