@@ -7,7 +7,13 @@
  *   - attention of new tokens over that cache: one token a sequence (decode),
  *     a few drafted ones, or a prompt's chunk, in one ragged batch;
  *   - verification of drafted tokens against the target's probabilities from
- *     random numbers that the caller gives.
+ *     random numbers that the caller gives;
+ *   - a step's plan: which requests get the pages that their new tokens need,
+ *     and the block tables, offsets and slots that follow;
+ *   - low-rank adapters of many requests at once, added beside a shared
+ *     projection;
+ *   - the draw of next tokens with temperature, top-k, top-p and min-p, and the
+ *     distribution that it draws from.
  *
  * The conventions of spear_w4ec.h hold: tensors are device pointers owned by
  * the caller and borrowed until the work enqueued on `stream` (a hipStream_t,
@@ -188,6 +194,62 @@ spear_status_t spear_verify_draft(const spear_verify_desc_t* desc, const float* 
                                   int64_t draft_row_stride, const int32_t* drafted, const float* u,
                                   const float* noise, const int32_t* num_drafts, int32_t* accepted,
                                   int32_t* tokens, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One step's plan. */
+typedef struct spear_kv_plan_desc {
+  int32_t batch;       /* sequences; 0 to 2^20 */
+  int32_t rows;        /* entries of the row outputs: the most new tokens of the step; 0 to 2^30 */
+  int32_t max_pages;   /* entries of a block table row; >= 1, max_pages * page_size up to 2^30 */
+  int32_t page_size;   /* a power of two, 16 to 1024 */
+  int32_t free_slots;  /* entries of the stack of free pages; >= 0 */
+} spear_kv_plan_desc_t;
+
+/*
+ * spear_kv_plan_workspace_bytes -- device workspace of a call (host only): one
+ * of spear_w4ec_linear's kind, zero-filled before its first use; the call
+ * returns the counter that it uses to zero.
+ * Errors: NULL_POINTER, INVALID_SHAPE, UNSUPPORTED.
+ */
+spear_status_t spear_kv_plan_workspace_bytes(const spear_kv_plan_desc_t* desc, size_t* bytes);
+
+/*
+ * spear_kv_plan -- pages, block tables, offsets and slots of a step's new
+ * tokens.  Sequence b has lens[b] cached tokens in held[b] pages and asks for
+ * new_tokens[b] more.  With want = ceil((lens + new_tokens) / page_size):
+ *   - pages past want are laid on the stack of free pages, sequence by
+ *     sequence, entry by entry (a sequence that has ended has lens = new_tokens
+ *     = 0 and gives back all);
+ *   - pages that are missing are taken from the stack's top, sequence by
+ *     sequence, entry by entry, after all have been laid on it;
+ *   - sequences are served in order as long as the pages and the rows last: from
+ *     the first that does not fit on, none gets anything (n = 0);
+ *   - a sequence whose want passes max_pages, whose pages do not cover its cached
+ *     tokens, or with a value below zero gets nothing and keeps what it has, and
+ *     the others are served as if it were not there.
+ * Outputs, n being the new tokens that a sequence is given:
+ *   cu_q      int32 [batch + 1], the running sum of n from 0.
+ *   kv_lens   int32 [batch], lens + n.
+ *   slots     int64 [rows], positions and sequence int32 [rows]: slot in the
+ *             cache, position and sequence of each new token; rows at and past
+ *             cu_q[batch] hold -1.
+ *   held_out  int32 [batch], free_out int32 [1]: pages held and pages free after
+ *             the step.
+ *   block_table  int32 [batch][table_stride], in and out: entries of pages
+ *             taken are written, no others.
+ *   free_pages   int32 [free_slots], in and out: the stack, its top at
+ *             free_count[0] - 1; only entries of pages laid on it are written.
+ * kv_lens may be lens, held_out may be held and free_out may be free_count: they
+ * are written when everything has been read.  Other buffers must not overlap.
+ * free_count is clamped to [0, free_slots]; pages that the stack has no room for
+ * are lost.
+ * Errors: NULL_POINTER, INVALID_SHAPE, UNSUPPORTED, MISALIGNED,
+ *         WORKSPACE_TOO_SMALL, HIP.
+ */
+spear_status_t spear_kv_plan(const spear_kv_plan_desc_t* desc, const int32_t* lens, const int32_t* new_tokens,
+                             const int32_t* held, int32_t* block_table, int64_t table_stride, int32_t* free_pages,
+                             const int32_t* free_count, int32_t* cu_q, int32_t* kv_lens, int64_t* slots,
+                             int32_t* positions, int32_t* sequence, int32_t* held_out, int32_t* free_out,
+                             void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,49 @@
+"""Oracle of what a serving step does around the layers and the cache: its pages,
+block tables and slots.  Plain loops over sequences and tokens; nothing is shared
+with the HIP path."""
+import numpy as np
+
+
+def kv_plan(lens, new_tokens, held, table, free_pages, free_count, rows, page):
+    """(cu_q, kv_lens, slots, positions, sequence, held, free_count, table, free_pages)
+    after the step, by the definition: one sequence and one page at a time."""
+    B, max_pages = table.shape
+    table, free_pages = table.copy(), free_pages.copy()
+    stack = [int(x) for x in free_pages[:min(max(int(free_count), 0), len(free_pages))]]
+    old = len(stack)
+    want, valid = [], []
+    for b in range(B):
+        want.append(-(-(int(lens[b]) + int(new_tokens[b])) // page))
+        valid.append(lens[b] >= 0 and new_tokens[b] >= 0 and 0 <= held[b] <= max_pages and want[b] <= max_pages
+                     and int(held[b]) * page >= lens[b])
+    now = [int(h) for h in held]
+    for b in range(B):
+        if valid[b]:
+            stack += [int(x) for x in table[b, want[b]:now[b]]]
+            now[b] = min(now[b], max(want[b], 0))
+    laid = list(stack)
+    n, full = [0] * B, False
+    for b in range(B):
+        if not valid[b] or full:
+            continue
+        need = want[b] - now[b]
+        if need > len(stack) or sum(n) + int(new_tokens[b]) > rows:
+            full = True
+            continue
+        for e in range(now[b], want[b]):
+            table[b, e] = stack.pop()
+        now[b], n[b] = want[b], int(new_tokens[b])
+    stack = stack[:len(free_pages)]
+    for i in range(old, len(stack)):
+        free_pages[i] = laid[i]
+    cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    slots = np.full(rows, -1, np.int64)
+    positions, sequence = np.full(rows, -1, np.int32), np.full(rows, -1, np.int32)
+    for b in range(B):
+        for i in range(n[b]):
+            r, p = int(cu[b]) + i, int(lens[b]) + i
+            positions[r], sequence[r] = p, b
+            slots[r] = int(table[b, p // page]) * page + p % page
+    kv_lens = (np.asarray(lens, np.int64) + n).astype(np.int32)
+    return (cu, kv_lens, slots, positions, sequence, np.asarray(now, np.int32), np.asarray([len(stack)], np.int32), table,
+            free_pages)

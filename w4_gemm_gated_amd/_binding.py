@@ -59,6 +59,8 @@ SERVE_EXPORTS = (
     "spear_paged_attention",
     "spear_verify_workspace_bytes",
     "spear_verify_draft",
+    "spear_kv_plan_workspace_bytes",
+    "spear_kv_plan",
 )
 
 
@@ -109,6 +111,11 @@ class AttentionDesc(ctypes.Structure):
 class VerifyDesc(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("max_drafts", ctypes.c_int32), ("vocab", ctypes.c_int32),
                 ("device_cus", ctypes.c_int32)]
+
+
+class KvPlanDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("free_slots", ctypes.c_int32)]
 
 
 class SpearError(RuntimeError):
@@ -191,6 +198,11 @@ def load(path=None):
     lib.spear_verify_draft.restype = ctypes.c_int
     lib.spear_verify_draft.argtypes = [ctypes.POINTER(VerifyDesc), vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, vp, vp,
                                        vp, sz, vp]
+    lib.spear_kv_plan_workspace_bytes.restype = ctypes.c_int
+    lib.spear_kv_plan_workspace_bytes.argtypes = [ctypes.POINTER(KvPlanDesc), ctypes.POINTER(sz)]
+    lib.spear_kv_plan.restype = ctypes.c_int
+    lib.spear_kv_plan.argtypes = [ctypes.POINTER(KvPlanDesc), vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                  vp, sz, vp]
     if path == LIB_PATH:
         _lib = lib
     return lib

@@ -1,0 +1,268 @@
+// A step's plan: which sequences get their new tokens' pages, and the block
+// tables, offsets, slots and positions that follow.
+//
+// Everything comes from running sums over the sequences: of the pages laid on the
+// stack of free ones, of the pages wanted, and of the new tokens.  A sequence is
+// served while the last two stay within what there is, so those that are served
+// come before all that are not, and the offsets of the latter are the totals.
+// The sums take a few microseconds of latency and no bandwidth, so every
+// workgroup forms all of them by itself (no second launch, no exchange) and then
+// fills as many rows as it has threads: it marks the rows at which its sequences
+// begin, a running maximum finds every row's own, and the row looks up its page, in
+// the table or, if it is a new one, on the stack.  A new page's first row is always
+// a new one: its thread writes the entry of the block table.
+//
+// The stack is read below its old top and written above it, and a taken page that was
+// laid on it in the same call is read from the block table that it left: no
+// workgroup reads what another writes.  Only state that is updated in place
+// is written by the last workgroup to arrive.
+#include "serve_internal.h"
+#include "device_common.h"
+
+namespace spear {
+namespace {
+
+// What sequence b asks for and gives back.
+struct Wish {
+  int32_t lens, held;
+  int32_t ask, need, freed;   // new tokens, pages missing and pages past what it needs
+  bool valid;
+};
+
+__device__ __forceinline__ Wish wish_of(const KvPlanArgs& a, int b) {
+  Wish w = {0, 0, 0, 0, 0, false};
+  if (b >= a.batch) return w;
+  w.lens = a.lens[b];
+  w.held = a.held[b];
+  const int32_t ask = a.ask[b];
+  const int64_t page = (int64_t)1 << a.page_log2;
+  const int64_t want = ((int64_t)w.lens + ask + page - 1) >> a.page_log2;
+  w.valid = w.lens >= 0 && ask >= 0 && w.held >= 0 && w.held <= a.max_pages && want <= a.max_pages &&
+            w.held * page >= w.lens;
+  if (w.valid) {
+    w.ask = ask;
+    w.need = max((int)want - w.held, 0);
+    w.freed = max(w.held - (int)want, 0);
+  }
+  return w;
+}
+
+// Running sums (inclusive) of two values over the workgroup, and their totals.
+struct Two {
+  int64_t x, y;
+};
+template <int THREADS>
+__device__ __forceinline__ Two running(Two v, Two* waves, Two* total) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+#pragma unroll
+  for (int o = 1; o < kWave; o *= 2) {
+    const int64_t x = __shfl_up(v.x, o), y = __shfl_up(v.y, o);
+    if (lane >= o) {
+      v.x += x;
+      v.y += y;
+    }
+  }
+  __syncthreads();
+  if (lane == kWave - 1) waves[wave] = v;
+  __syncthreads();
+  Two sum = {0, 0};
+#pragma unroll
+  for (int i = 0; i < THREADS / kWave; ++i) {
+    if (i == wave) {
+      v.x += sum.x;
+      v.y += sum.y;
+    }
+    sum.x += waves[i].x;
+    sum.y += waves[i].y;
+  }
+  *total = sum;
+  return v;
+}
+
+template <int THREADS>
+__device__ __forceinline__ int running_max(int v, int* waves) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+#pragma unroll
+  for (int o = 1; o < kWave; o *= 2) {
+    const int x = __shfl_up(v, o);
+    if (lane >= o) v = max(v, x);
+  }
+  __syncthreads();
+  if (lane == kWave - 1) waves[wave] = v;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < THREADS / kWave; ++i)
+    if (i < wave) v = max(v, waves[i]);
+  return v;
+}
+
+// A sequence with rows in this workgroup's range, kept at the place of the first.
+struct Begin {
+  int32_t seq, pos, held;   // pos: the first such row's position
+  int64_t take;             // pages taken before its own
+};
+
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) kv_plan_kernel(KvPlanArgs a) {
+  __shared__ Two waves[THREADS / kWave];
+  __shared__ int max_waves[THREADS / kWave];
+  __shared__ Begin begin[THREADS];
+  __shared__ int marked[THREADS];
+  __shared__ int64_t freed_to[THREADS];       // running sum of freed pages in one chunk of sequences
+  __shared__ int32_t freed_page[THREADS];     // pages taken here that were laid on the stack in this call
+  __shared__ unsigned long long given_rows, given_pages, lowest, highest;
+  __shared__ uint32_t arrived;
+  const int tid = threadIdx.x;
+  const int chunks = (a.batch + THREADS - 1) / THREADS;
+  const int64_t row0 = (int64_t)blockIdx.x * THREADS;
+
+  marked[tid] = -1;
+  if (tid == 0) {
+    given_rows = given_pages = 0;
+    lowest = ~0ull;
+    highest = 0;
+  }
+  const int64_t old = min(max(*a.free_count, 0), a.free_slots);
+  // Pages laid on the stack, all of them before any is taken.
+  Wish w = wish_of(a, tid);
+  Two sum;
+  int64_t freed = 0;
+  for (int c = 0; c < chunks; ++c) {
+    if (c > 0) w = wish_of(a, c * THREADS + tid);
+    running<THREADS>({w.freed, 0}, waves, &sum);
+    freed += sum.x;
+  }
+  const int64_t top = old + freed;
+  // (the running sums' barriers come after the clearing above)
+
+  // Who is served, and the first row of each sequence in the range.
+  const bool writes_state = !a.in_place && blockIdx.x == 0;
+  auto serve = [&](bool rows_too, bool state) {
+    int64_t rows_before = 0, pages_before = 0;
+    for (int c = 0; c < chunks; ++c) {
+      const int b = c * THREADS + tid;
+      if (chunks > 1) w = wish_of(a, b);
+      const Two v = running<THREADS>({w.ask, w.need}, waves, &sum);
+      const int64_t rows_to = rows_before + v.x, pages_to = pages_before + v.y;
+      const bool given = w.valid && rows_to <= a.rows && pages_to <= top;
+      if (given) {
+        atomicMax(&given_rows, (unsigned long long)rows_to);
+        atomicMax(&given_pages, (unsigned long long)pages_to);
+      }
+      __syncthreads();
+      const int64_t first = min(rows_to - w.ask, (int64_t)given_rows);
+      const int32_t n = given ? w.ask : 0;
+      if (rows_too && n > 0 && first < row0 + THREADS && first + n > row0) {
+        const int at = (int)max(first - row0, (int64_t)0);
+        begin[at] = {b, w.lens + (int)(row0 + at - first), w.held, pages_to - w.need};
+        marked[at] = at;
+      }
+      if (state && b < a.batch) {
+        a.cu_q[b] = (int32_t)first;
+        a.kv_lens[b] = w.lens + n;
+        a.held_out[b] = w.held - w.freed + (given ? w.need : 0);
+      }
+      rows_before += sum.x;
+      pages_before += sum.y;
+    }
+    if (state && tid == 0) {
+      a.cu_q[a.batch] = (int32_t)given_rows;
+      *a.free_out = (int32_t)min(top - (int64_t)given_pages, (int64_t)a.free_slots);
+    }
+  };
+  serve(true, writes_state);
+  __syncthreads();
+  const int64_t total_rows = (int64_t)given_rows, total_pages = (int64_t)given_pages;
+
+  // This thread's row.
+  const int64_t row = row0 + tid;
+  const int own = running_max<THREADS>(marked[tid], max_waves);
+  const bool used = row < total_rows && own >= 0;
+  Begin s = {0, 0, 0, 0};
+  int pos = -1;
+  int32_t page = 0;
+  int64_t from = -1;        // place on the stack of a page that is taken
+  if (used) {
+    s = begin[own];
+    pos = s.pos + (tid - own);
+    const int entry = pos >> a.page_log2;
+    if (entry < s.held) {
+      page = a.table[s.seq * a.table_stride + entry];
+    } else {
+      from = top - 1 - (s.take + (entry - s.held));
+      if (from < old) page = a.free_pages[from];
+    }
+  }
+  if (freed > 0) {
+    // Pages laid on the stack in this call: their places are found by the running
+    // sum of the sequences that gave them.
+    const bool mine = from >= old;
+    if (mine) {
+      atomicMin(&lowest, (unsigned long long)(from - old));
+      atomicMax(&highest, (unsigned long long)(from - old) + 1);
+    }
+    __syncthreads();
+    const int64_t lo = (int64_t)lowest, hi = (int64_t)highest;     // (fewer than THREADS: every page has a row here)
+    const int64_t stay = min(top - total_pages, (int64_t)a.free_slots) - old;   // of those laid on it, these remain
+    int64_t before = 0;
+    for (int c = 0; c < chunks; ++c) {
+      if (chunks > 1) w = wish_of(a, c * THREADS + tid);
+      const Two v = running<THREADS>({w.freed, 0}, waves, &sum);
+      freed_to[tid] = before + v.x;
+      __syncthreads();
+      auto find = [&](int64_t i) {       // page i of those laid on the stack, which this chunk gave
+        int at = 0;
+#pragma unroll
+        for (int step = THREADS / 2; step > 0; step /= 2)
+          if (freed_to[at + step - 1] <= i) at += step;
+        const int b = c * THREADS + at;
+        const Wish g = wish_of(a, b);
+        return a.table[b * a.table_stride + (g.held - (int)(freed_to[at] - i))];
+      };
+      const int64_t end = before + sum.x;
+      if (lo + tid < hi && lo + tid >= before && lo + tid < end) freed_page[tid] = find(lo + tid);
+      for (int64_t i = row0 + tid; i < stay; i += (int64_t)gridDim.x * THREADS)
+        if (i >= before && i < end) a.free_pages[old + i] = find(i);
+      before = end;
+      __syncthreads();
+    }
+    if (mine) page = freed_page[from - old - lo];
+  }
+  if (row < a.rows) {
+    const int in_page = pos & ((1 << a.page_log2) - 1);
+    if (from >= 0 && in_page == 0) a.table[s.seq * a.table_stride + (pos >> a.page_log2)] = page;
+    a.slots[row] = used ? ((int64_t)page << a.page_log2) + in_page : -1;
+    a.positions[row] = pos;
+    a.sequence[row] = used ? s.seq : -1;
+  }
+
+  if (!a.in_place) return;
+  if (gridDim.x > 1) {
+    // (every wave's reads of the state have come back: what follows from them has been written)
+    __syncthreads();
+    if (tid == 0) {
+      drain_vm();
+      arrived = add_dev_u32(a.counter, 1u);
+    }
+    __syncthreads();
+    if (arrived != gridDim.x - 1) return;
+    if (tid == 0) st_dev_u32(a.counter, 0u);
+  }
+  __syncthreads();
+  serve(false, true);
+}
+
+}  // namespace
+
+// Few sequences go with small workgroups: more of them share the rows, and their
+// sums are shorter.
+int kv_plan_threads(int batch) { return batch <= 256 ? 256 : 1024; }
+
+hipError_t launch_kv_plan(const KvPlanArgs& a, void* stream) {
+  const unsigned grid = (unsigned)(a.rows > 0 ? ceil_div(a.rows, a.threads) : 1);
+  if (a.threads == 256) kv_plan_kernel<256><<<dim3(grid), dim3(256), 0, (hipStream_t)stream>>>(a);
+  else kv_plan_kernel<1024><<<dim3(grid), dim3(1024), 0, (hipStream_t)stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace spear

@@ -3,7 +3,6 @@
 // device memory or synchronizes; every check runs before anything is enqueued.
 #include <hip/hip_runtime_api.h>
 
-#include <atomic>
 #include <cmath>
 
 #include "serve_internal.h"
@@ -11,32 +10,6 @@
 using namespace spear;
 
 namespace {
-
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
-spear_status_t hip_status(hipError_t e) { return e == hipSuccess ? SPEAR_OK : SPEAR_ERR_HIP; }
-
-// CUs to plan for: the caller's number, or the current device's (looked up once).
-spear_status_t cus_of(int32_t asked, int* out) {
-  constexpr int kMaxDevices = 64;
-  static std::atomic<int> cache[kMaxDevices];
-  if (asked < 0) return SPEAR_ERR_INVALID_ARGUMENT;
-  if (asked > 0) {
-    *out = asked < 4096 ? asked : 4096;
-    return SPEAR_OK;
-  }
-  int dev = 0, cus = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return SPEAR_ERR_HIP;
-  const bool kept = dev >= 0 && dev < kMaxDevices;
-  if (kept && (cus = cache[dev].load(std::memory_order_relaxed)) > 0) {
-    *out = cus;
-    return SPEAR_OK;
-  }
-  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
-    return SPEAR_ERR_HIP;
-  if (kept) cache[dev].store(cus, std::memory_order_relaxed);
-  *out = cus;
-  return SPEAR_OK;
-}
 
 // Sizes whose products the kernels index with are bounded here: a head's rows
 // of the cache and the tensors' elements stay below 2^62.

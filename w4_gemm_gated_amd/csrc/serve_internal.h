@@ -1,6 +1,7 @@
 // Internal interfaces of the serving operators (paged key/value cache, paged
-// attention, draft verification): launch arguments shared by serve_api.cpp and
-// the kernels.  Not installed; not part of the ABI.
+// attention, draft verification, and what a step does around them): launch
+// arguments shared by serve_api.cpp, step_api.cpp and the kernels.  Not
+// installed; not part of the ABI.
 #pragma once
 
 #include <stddef.h>
@@ -8,10 +9,38 @@
 
 #include <hip/hip_runtime_api.h>
 
+#include <atomic>
+
 #include "../../include/spear_serve.h"
 #include "internal.h"
 
 namespace spear {
+
+inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
+inline spear_status_t hip_status(hipError_t e) { return e == hipSuccess ? SPEAR_OK : SPEAR_ERR_HIP; }
+
+// CUs to plan for: the caller's number, or the current device's (looked up once).
+inline spear_status_t cus_of(int32_t asked, int* out) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> cache[kMaxDevices];
+  if (asked < 0) return SPEAR_ERR_INVALID_ARGUMENT;
+  if (asked > 0) {
+    *out = asked < 4096 ? asked : 4096;
+    return SPEAR_OK;
+  }
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return SPEAR_ERR_HIP;
+  const bool kept = dev >= 0 && dev < kMaxDevices;
+  if (kept && (cus = cache[dev].load(std::memory_order_relaxed)) > 0) {
+    *out = cus;
+    return SPEAR_OK;
+  }
+  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
+    return SPEAR_ERR_HIP;
+  if (kept) cache[dev].store(cus, std::memory_order_relaxed);
+  *out = cus;
+  return SPEAR_OK;
+}
 
 struct KvShape {
   int32_t dtype, num_pages, heads, dim, page_log2;
@@ -103,5 +132,22 @@ struct VerifyArgs {
   uint64_t* part;       // [batch][splits]
 };
 hipError_t launch_verify(const VerifyArgs& a, void* stream);
+
+// A step's plan: workgroups of `threads` threads, each for that many rows.
+struct KvPlanArgs {
+  int32_t batch, rows, max_pages, page_log2, free_slots, threads;
+  const int32_t *lens, *ask, *held;
+  int32_t* table;
+  int64_t table_stride;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t *cu_q, *kv_lens;
+  int64_t* slots;
+  int32_t *positions, *sequence, *held_out, *free_out;
+  bool in_place;        // a state output is its input: the last workgroup writes them all
+  uint32_t* counter;    // zero before and after
+};
+int kv_plan_threads(int batch);
+hipError_t launch_kv_plan(const KvPlanArgs& a, void* stream);
 
 }  // namespace spear
