@@ -251,6 +251,60 @@ spear_status_t spear_kv_plan(const spear_kv_plan_desc_t* desc, const int32_t* le
                              int32_t* positions, int32_t* sequence, int32_t* held_out, int32_t* free_out,
                              void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * spear_adapter_plan -- the rows of a batch by adapter: made once for a step and
+ * read by the spear_adapter_add calls of all its projections.
+ *   cu_q     int32 [batch + 1], rising from 0 to at most `rows`: rows of sequence b.
+ *   adapter  int32 [batch]: its adapter; one outside [0, adapters) means none.
+ *   plan     output, spear_adapter_plan_bytes bytes, 16-byte aligned; its content is
+ *            the library's own.  Offsets that do not rise within the rows give a
+ *            plan of no rows.
+ * adapters 1 to 4096, batch up to 2^20, rows up to 2^24.
+ * Errors: NULL_POINTER, INVALID_SHAPE, UNSUPPORTED, MISALIGNED,
+ *         WORKSPACE_TOO_SMALL (the plan), HIP.
+ */
+spear_status_t spear_adapter_plan_bytes(int32_t batch, int32_t adapters, int32_t rows, size_t* bytes);
+spear_status_t spear_adapter_plan(int32_t batch, int32_t adapters, int32_t rows, const int32_t* cu_q,
+                                  const int32_t* adapter, int32_t* plan, size_t plan_bytes, void* stream);
+
+/* One projection's adapters. */
+typedef struct spear_adapter_desc {
+  int32_t batch, adapters, rows;   /* as the plan was made with */
+  int32_t K, N;        /* of the projection; K a multiple of 8, K and N up to 2^24 */
+  int32_t rank;        /* a multiple of 8 up to 256 (smaller adapters are padded with zeros) */
+  int32_t device_cus;  /* as in spear_attention_desc_t */
+} spear_adapter_desc_t;
+
+/*
+ * spear_adapter_workspace_bytes -- device workspace of a call (host only): one of
+ * spear_w4ec_linear's kind, zero-filled before its first use; the call returns the
+ * counters of its header to zero.
+ * Errors: NULL_POINTER, INVALID_SHAPE, UNSUPPORTED, INVALID_ARGUMENT (device_cus), HIP.
+ */
+spear_status_t spear_adapter_workspace_bytes(const spear_adapter_desc_t* desc, size_t* bytes);
+
+/*
+ * spear_adapter_add -- add each row's adapter to a projection's output, in place:
+ *     Y[m] += scale[a] * (X[m] . A[a]^T) . B[a]^T
+ * for the rows of sequences that have an adapter a; other rows of Y are left as
+ * they are.
+ *   X        fp16 [rows][K], 16-byte aligned, row stride in elements (a multiple of 8).
+ *   A        fp16 [adapters][rank][K], B fp16 [adapters][N][rank], contiguous,
+ *            16-byte aligned (the layout of the adapters' own linear layers).
+ *   scale    fp32 [adapters], or NULL for 1.
+ *   plan     from spear_adapter_plan with the same batch, adapters and rows.
+ *   Y        fp16 [rows][N], row stride in elements (at least N): a part of a joint
+ *            projection's output may be given.  Must not overlap X.
+ * Sums are held in fp32 and the products of X and A enter the second product to 2^-22
+ * of the row's largest; Y is rounded once.  The result does not depend on
+ * scheduling.
+ * Errors: NULL_POINTER, INVALID_SHAPE, INVALID_ARGUMENT, UNSUPPORTED,
+ *         MISALIGNED, WORKSPACE_TOO_SMALL, HIP.
+ */
+spear_status_t spear_adapter_add(const spear_adapter_desc_t* desc, const void* X, int64_t x_stride, const void* A,
+                                 const void* B, const float* scale, const int32_t* plan, size_t plan_bytes, void* Y,
+                                 int64_t y_stride, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

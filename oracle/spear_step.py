@@ -1,6 +1,6 @@
 """Oracle of what a serving step does around the layers and the cache: its pages,
-block tables and slots.  Plain loops over sequences and tokens; nothing is shared
-with the HIP path."""
+block tables and slots, and the adapters of its requests, in 64 bits.  Plain loops
+over sequences and tokens; nothing is shared with the HIP path."""
 import numpy as np
 
 
@@ -47,3 +47,26 @@ def kv_plan(lens, new_tokens, held, table, free_pages, free_count, rows, page):
     kv_lens = (np.asarray(lens, np.int64) + n).astype(np.int32)
     return (cu, kv_lens, slots, positions, sequence, np.asarray(now, np.int32), np.asarray([len(stack)], np.int32), table,
             free_pages)
+
+
+def adapter_add(Y, X, A, B, cu, adapter, scale=None):
+    """(out, slack) float64 [rows, N]: Y + scale[a] (X A[a]^T) B[a]^T for the rows of
+    sequences with an adapter; slack bounds the error of an implementation that holds
+    sums in fp32 and H = X A^T to 2^-22 of its row's largest, before its last rounding:
+    K roundings of 2^-24 of each sum of H, 2 rank + 4 of the second product's."""
+    out = Y.astype(np.float64)
+    slack = np.zeros_like(out)
+    K, rank = X.shape[1], A.shape[1]
+    for b, a in enumerate(adapter):
+        if not 0 <= a < len(A):
+            continue
+        at = slice(int(cu[b]), int(cu[b + 1]))
+        x, wa, wb = X[at].astype(np.float64), A[a].astype(np.float64), B[a].astype(np.float64)
+        s = 1.0 if scale is None else float(scale[a])
+        h = x @ wa.T
+        out[at] += s * (h @ wb.T)
+        h_err = K * 2.0 ** -24 * (np.abs(x) @ np.abs(wa).T)
+        if h.size:
+            h_err += 2.0 ** -22 * np.abs(h).max(1, keepdims=True)
+        slack[at] = abs(s) * (h_err @ np.abs(wb).T + (2 * rank + 4) * 2.0 ** -24 * (np.abs(h) @ np.abs(wb).T))
+    return out, slack

@@ -63,3 +63,25 @@ def test_pages_are_neither_lost_nor_shared(seed):
     assert cu[-1] <= rows and np.all(now * page >= kv)
     got = slots[slots >= 0]
     assert len(got) == cu[-1] and len(set(got.tolist())) == len(got)
+
+
+def test_adapters_by_hand():
+    """One row with each adapter and one without: rank 1 products in whole numbers."""
+    X = np.array([[1, 2], [3, 4], [5, 6]], np.float16)
+    A = np.array([[[1, 0]], [[1, 1]]], np.float16)              # picks x0; x0 + x1
+    B = np.array([[[1], [10]], [[2], [0]]], np.float16)
+    Y = np.ones((3, 2), np.float16)
+    out, slack = ref.adapter_add(Y, X, A, B, [0, 1, 2, 3], [1, -1, 0], [0.5, 3.0])
+    assert out.tolist() == [[1 + 3 * 3 * 2, 1], [1, 1], [1 + 0.5 * 5, 1 + 0.5 * 50]]
+    assert (slack[1] == 0).all() and (slack[[0, 2], [0, 1]] > 0).all()
+
+
+def test_adapters_merge_into_the_weight():
+    """A batch of one adapter is the product with W + s B A."""
+    rng = np.random.default_rng(0)
+    X, A, B = (rng.normal(size=s).astype(np.float16) for s in ((6, 40), (2, 8, 40), (2, 24, 8)))
+    W = rng.normal(size=(24, 40))
+    Y = X.astype(np.float64) @ W.T
+    out, _ = ref.adapter_add(Y, X, A, B, [0, 2, 6], [1, 1], [0.0, 0.25])
+    merged = W + 0.25 * B[1].astype(np.float64) @ A[1].astype(np.float64)
+    assert np.allclose(out, X.astype(np.float64) @ merged.T, rtol=1e-12, atol=1e-12)

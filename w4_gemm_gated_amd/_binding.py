@@ -61,6 +61,10 @@ SERVE_EXPORTS = (
     "spear_verify_draft",
     "spear_kv_plan_workspace_bytes",
     "spear_kv_plan",
+    "spear_adapter_plan_bytes",
+    "spear_adapter_plan",
+    "spear_adapter_workspace_bytes",
+    "spear_adapter_add",
 )
 
 
@@ -116,6 +120,11 @@ class VerifyDesc(ctypes.Structure):
 class KvPlanDesc(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("free_slots", ctypes.c_int32)]
+
+
+class AdapterDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("adapters", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("rank", ctypes.c_int32), ("device_cus", ctypes.c_int32)]
 
 
 class SpearError(RuntimeError):
@@ -203,6 +212,14 @@ def load(path=None):
     lib.spear_kv_plan.restype = ctypes.c_int
     lib.spear_kv_plan.argtypes = [ctypes.POINTER(KvPlanDesc), vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                   vp, sz, vp]
+    lib.spear_adapter_plan_bytes.restype = ctypes.c_int
+    lib.spear_adapter_plan_bytes.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
+    lib.spear_adapter_plan.restype = ctypes.c_int
+    lib.spear_adapter_plan.argtypes = [i32, i32, i32, vp, vp, vp, sz, vp]
+    lib.spear_adapter_workspace_bytes.restype = ctypes.c_int
+    lib.spear_adapter_workspace_bytes.argtypes = [ctypes.POINTER(AdapterDesc), ctypes.POINTER(sz)]
+    lib.spear_adapter_add.restype = ctypes.c_int
+    lib.spear_adapter_add.argtypes = [ctypes.POINTER(AdapterDesc), vp, i64, vp, vp, vp, vp, sz, vp, i64, vp, sz, vp]
     if path == LIB_PATH:
         _lib = lib
     return lib

@@ -150,4 +150,38 @@ struct KvPlanArgs {
 int kv_plan_threads(int batch);
 hipError_t launch_kv_plan(const KvPlanArgs& a, void* stream);
 
+// Adapters of many requests.
+constexpr int kMaxAdapters = 4096;   // counted in LDS by the plan
+constexpr int kAdapterTile = 64;     // rows of one adapter that a workgroup takes
+constexpr int kAdapterColumns = 256; // columns of the output that one takes
+struct AdapterPlanArgs {
+  int32_t batch, adapters, rows, most_tiles;
+  const int32_t *cu, *adapter;
+  int32_t* plan;
+};
+hipError_t launch_adapter_plan(const AdapterPlanArgs& a, void* stream);
+int64_t adapter_most_tiles(int64_t rows, int64_t batch, int64_t adapters);
+size_t adapter_plan_size(int64_t rows, int64_t batch, int64_t adapters);
+
+// Launch shape and workspace (offsets in bytes) of an adapter call.
+struct AdapterShape {
+  int tiles, rank_pad, slices, slice_k;
+  size_t H, factor, part, bytes;
+};
+AdapterShape adapter_shape(const spear_adapter_desc_t& d, int cus);
+struct AdapterArgs {
+  int32_t rows, adapters, K, N, rank, rank_pad, most_tiles, slices, slice_k, chunks;
+  const void *X, *A, *B;
+  const float* scale;      // [adapters], or null: 1
+  const int32_t* plan;
+  void* Y;
+  int64_t x_stride, y_stride;
+  bool y_vectors;          // Y's rows are 16-byte aligned
+  uint32_t* counters;      // [tiles], zero before and after
+  char* part;              // fp32 [tiles][slices][64][rank]
+  void* H;                 // fp16 [tiles][64][2][rank_pad]
+  float* factor;           // [tiles][64]
+};
+hipError_t launch_adapter(const AdapterArgs& a, void* stream);
+
 }  // namespace spear

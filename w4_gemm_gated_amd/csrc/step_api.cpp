@@ -28,6 +28,24 @@ spear_status_t check_workspace(const void* workspace, size_t have, size_t need) 
   return workspace && !aligned(workspace, 16) ? SPEAR_ERR_MISALIGNED : SPEAR_OK;
 }
 
+spear_status_t check_batch(int32_t batch, int32_t adapters, int32_t rows) {
+  if (batch < 0 || rows < 0 || adapters < 1) return SPEAR_ERR_INVALID_SHAPE;
+  if (adapters > kMaxAdapters || batch > (1 << 20) || rows > (1 << 24)) return SPEAR_ERR_UNSUPPORTED;
+  return SPEAR_OK;
+}
+
+spear_status_t check_adapter(const spear_adapter_desc_t& d) {
+  const spear_status_t st = check_batch(d.batch, d.adapters, d.rows);
+  if (st != SPEAR_OK) return st;
+  if (d.K < 8 || d.K % 8 != 0 || d.N < 1 || d.rank < 8 || d.rank % 8 != 0) return SPEAR_ERR_INVALID_SHAPE;
+  if (d.rank > SPEAR_MAX_RANK || d.K > (1 << 24) || d.N > (1 << 24)) return SPEAR_ERR_UNSUPPORTED;
+  if (d.device_cus < 0) return SPEAR_ERR_INVALID_ARGUMENT;
+  // (a launch holds fewer than 2^32 threads: 256 for every tile and 256 columns)
+  if (adapter_most_tiles(d.rows, d.batch, d.adapters) * ceil_div(d.N, kAdapterColumns) >= (1 << 24))
+    return SPEAR_ERR_UNSUPPORTED;
+  return SPEAR_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -72,6 +90,70 @@ spear_status_t spear_kv_plan(const spear_kv_plan_desc_t* desc, const int32_t* le
   a.in_place = kv_lens == lens || held_out == held || free_out == free_count;
   a.counter = (uint32_t*)workspace;   // the header's first counter
   return hip_status(launch_kv_plan(a, stream));
+}
+
+spear_status_t spear_adapter_plan_bytes(int32_t batch, int32_t adapters, int32_t rows, size_t* bytes) {
+  if (!bytes) return SPEAR_ERR_NULL_POINTER;
+  const spear_status_t st = check_batch(batch, adapters, rows);
+  if (st == SPEAR_OK) *bytes = adapter_plan_size(rows, batch, adapters);
+  return st;
+}
+
+spear_status_t spear_adapter_plan(int32_t batch, int32_t adapters, int32_t rows, const int32_t* cu_q,
+                                  const int32_t* adapter, int32_t* plan, size_t plan_bytes, void* stream) {
+  const spear_status_t st = check_batch(batch, adapters, rows);
+  if (st != SPEAR_OK) return st;
+  if (!plan || (batch > 0 && (!cu_q || !adapter))) return SPEAR_ERR_NULL_POINTER;
+  if (plan_bytes < adapter_plan_size(rows, batch, adapters)) return SPEAR_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(cu_q, 4) || !aligned(adapter, 4) || !aligned(plan, 16)) return SPEAR_ERR_MISALIGNED;
+  AdapterPlanArgs a;
+  a.batch = batch; a.adapters = adapters; a.rows = rows;
+  a.most_tiles = (int32_t)adapter_most_tiles(rows, batch, adapters);
+  a.cu = cu_q; a.adapter = adapter; a.plan = plan;
+  return hip_status(launch_adapter_plan(a, stream));
+}
+
+spear_status_t spear_adapter_workspace_bytes(const spear_adapter_desc_t* desc, size_t* bytes) {
+  if (!desc || !bytes) return SPEAR_ERR_NULL_POINTER;
+  spear_status_t st = check_adapter(*desc);
+  if (st != SPEAR_OK) return st;
+  int cus = 0;
+  st = cus_of(desc->device_cus, &cus);
+  if (st == SPEAR_OK) *bytes = desc->rows == 0 || desc->batch == 0 ? 0 : adapter_shape(*desc, cus).bytes;
+  return st;
+}
+
+spear_status_t spear_adapter_add(const spear_adapter_desc_t* desc, const void* X, int64_t x_stride, const void* A,
+                                 const void* B, const float* scale, const int32_t* plan, size_t plan_bytes, void* Y,
+                                 int64_t y_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!desc) return SPEAR_ERR_NULL_POINTER;
+  spear_status_t st = check_adapter(*desc);
+  if (st != SPEAR_OK) return st;
+  const int64_t most = (int64_t)1 << 31;
+  if (x_stride < 0 || x_stride % 8 != 0 || x_stride > most || y_stride < desc->N || y_stride > most)
+    return SPEAR_ERR_INVALID_SHAPE;
+  if (desc->rows == 0 || desc->batch == 0) return SPEAR_OK;
+  if (!X || !A || !B || !plan || !Y) return SPEAR_ERR_NULL_POINTER;
+  if (!aligned(X, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(scale, 4) || !aligned(plan, 16) || !aligned(Y, 2))
+    return SPEAR_ERR_MISALIGNED;
+  if (plan_bytes < adapter_plan_size(desc->rows, desc->batch, desc->adapters)) return SPEAR_ERR_WORKSPACE_TOO_SMALL;
+  int cus = 0;
+  st = cus_of(desc->device_cus, &cus);
+  if (st != SPEAR_OK) return st;
+  const AdapterShape s = adapter_shape(*desc, cus);
+  st = check_workspace(workspace, workspace_bytes, s.bytes);
+  if (st != SPEAR_OK) return st;
+  AdapterArgs a;
+  a.rows = desc->rows; a.adapters = desc->adapters; a.K = desc->K; a.N = desc->N; a.rank = desc->rank;
+  a.rank_pad = s.rank_pad; a.most_tiles = s.tiles; a.slices = s.slices; a.slice_k = s.slice_k;
+  a.chunks = (int32_t)ceil_div(desc->N, kAdapterColumns);
+  a.X = X; a.A = A; a.B = B; a.scale = scale; a.plan = plan; a.Y = Y;
+  a.x_stride = x_stride; a.y_stride = y_stride;
+  a.y_vectors = aligned(Y, 16) && y_stride % 8 == 0;
+  char* ws = (char*)workspace;
+  a.counters = (uint32_t*)ws;   // the header's first counters
+  a.part = ws + s.part; a.H = ws + s.H; a.factor = (float*)(ws + s.factor);
+  return hip_status(launch_adapter(a, stream));
 }
 
 }  // extern "C"

@@ -1,16 +1,19 @@
 """What a serving step does around the W4 layers and the paged cache: its pages,
-block tables and slots planned on the GPU.
+block tables and slots planned on the GPU, and the low-rank adapters of its
+requests added beside a shared projection.
 
 Python names mirror the C ABI in include/spear_serve.h, which states the
 definitions; only arguments are marshalled here, as in serve.py.
 """
+import ctypes
+
 import torch
 
 from . import _binding
-from ._binding import KvPlanDesc
-from .serve import _dense, _p, _plan, _scratch, _stream
+from ._binding import AdapterDesc, KvPlanDesc
+from .serve import _check, _dense, _p, _plan, _scratch, _stream
 
-__all__ = ["spear_kv_plan"]
+__all__ = ["spear_kv_plan", "spear_adapter_plan", "spear_adapter_add"]
 
 
 def _out(t, name, shape, dtype, device):
@@ -85,3 +88,83 @@ def spear_kv_plan(lens, new_tokens, held, block_table, free_pages, free_count, r
                            free_out.data_ptr(), *ws, stream)
     _binding.check(st, "spear_kv_plan")
     return cu_q, kv_lens, slots, positions, sequence, held_out, free_out
+
+
+class AdapterPlan:
+    """The rows of a batch by adapter: what spear_adapter_plan makes for a step and
+    spear_adapter_add reads."""
+    __slots__ = ("data", "batch", "adapters", "rows")
+
+    def __init__(self, data, batch, adapters, rows):
+        self.data, self.batch, self.adapters, self.rows = data, batch, adapters, rows
+
+
+def spear_adapter_plan(cu_q, adapter, adapters, rows, plan=None):
+    """The plan of a step's adapters: sequence b has rows cu_q[b] .. cu_q[b + 1] - 1 and
+    adapter adapter[b] (outside [0, adapters): none).
+
+    cu_q int32 [B + 1], rising from 0 to at most rows; adapter int32 [B].  `plan`: one
+    of the same sizes to be filled again (a captured graph's).
+    """
+    dev = _gpu(cu_q, "cu_q")
+    _dense(cu_q, "cu_q", torch.int32, 1, dev)
+    _dense(adapter, "adapter", torch.int32, 1, dev)
+    B, adapters, rows = adapter.shape[0], int(adapters), int(rows)
+    if cu_q.shape[0] != B + 1:
+        raise ValueError("cu_q must have one entry more than adapter")
+    lib, stream = _binding.load(), _stream(dev)
+    if plan is None:
+        n = ctypes.c_size_t(0)
+        _binding.check(lib.spear_adapter_plan_bytes(B, adapters, rows, ctypes.byref(n)), "spear_adapter_plan")
+        plan = AdapterPlan(torch.empty(n.value, dtype=torch.uint8, device=dev), B, adapters, rows)
+    elif not isinstance(plan, AdapterPlan):
+        raise TypeError("plan must come from spear_adapter_plan")
+    elif (plan.batch, plan.adapters, plan.rows) != (B, adapters, rows) or plan.data.device != dev:
+        raise ValueError("plan was made for other sizes")
+    st = lib.spear_adapter_plan(B, adapters, rows, cu_q.data_ptr(), adapter.data_ptr(), plan.data.data_ptr(),
+                                plan.data.numel(), stream)
+    _binding.check(st, "spear_adapter_plan")
+    return plan
+
+
+def spear_adapter_add(Y, X, A, B, plan, scale=None, workspace=None):
+    """Y fp16 [rows, N], updated in place and returned: each row of a sequence with
+    adapter a gets scale[a] * (X . A[a]^T) . B[a]^T more.
+
+    X fp16 [rows, K]; A fp16 [adapters, rank, K]; B fp16 [adapters, N, rank]; X's and
+    Y's last dimension contiguous (Y may be a part of a joint projection's output);
+    scale fp32 [adapters] or None (1); plan from spear_adapter_plan; `workspace` as in
+    spear_paged_attention.
+    """
+    dev = _gpu(Y, "Y")
+    f16 = torch.float16
+    _check(Y, "Y", f16, 2, dev)
+    _check(X, "X", f16, 2, dev)
+    _dense(A, "A", f16, 3, dev)
+    _dense(B, "B", f16, 3, dev)
+    if not isinstance(plan, AdapterPlan):
+        raise TypeError("plan must come from spear_adapter_plan")
+    if plan.data.device != dev:
+        raise ValueError(f"plan must be on {dev}")
+    n, rank, K = A.shape
+    rows, N = Y.shape
+    if B.shape != (n, N, rank) or X.shape != (rows, K) or plan.adapters != n or plan.rows != rows:
+        raise ValueError("need Y [rows, N], X [rows, K], A [adapters, rank, K], B [adapters, N, rank] and a plan of "
+                         "these rows and adapters")
+    for t, name in ((X, "X"), (Y, "Y")):
+        if t.stride(1) != 1 and t.shape[1] > 1:
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+    if scale is not None:
+        _dense(scale, "scale", torch.float32, 1, dev)
+        if scale.shape[0] != n:
+            raise ValueError("scale must be [adapters]")
+    lib, stream = _binding.load(), _stream(dev)
+    d = _plan(("adapter", dev.index, plan.batch, n, rows, K, N, rank), lambda: (
+        AdapterDesc(plan.batch, n, rows, K, N, rank, 0), lib.spear_adapter_workspace_bytes, "spear_adapter_add"))
+    ws = _space(workspace, d[2], dev, stream)
+    # (the strides of a single row say nothing)
+    xs, ys = (K, N) if rows == 1 else (X.stride(0), Y.stride(0))
+    st = lib.spear_adapter_add(d[1], X.data_ptr(), xs, A.data_ptr(), B.data_ptr(), _p(scale), plan.data.data_ptr(),
+                               plan.data.numel(), Y.data_ptr(), ys, *ws, stream)
+    _binding.check(st, "spear_adapter_add")
+    return Y
