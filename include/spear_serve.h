@@ -305,6 +305,66 @@ spear_status_t spear_adapter_add(const spear_adapter_desc_t* desc, const void* X
                                  const void* B, const float* scale, const int32_t* plan, size_t plan_bytes, void* Y,
                                  int64_t y_stride, void* workspace, size_t workspace_bytes, void* stream);
 
+typedef enum spear_logits_dtype {
+  SPEAR_LOGITS_FP16 = 0,
+  SPEAR_LOGITS_FP32 = 1
+} spear_logits_dtype_t;
+
+/* One sampling call. */
+typedef struct spear_sample_desc {
+  int32_t batch;       /* draws; 0 is a no-op; up to 2^20 */
+  int32_t vocab;       /* V; 1 to 2^22 */
+  int32_t num_rows;    /* rows of the logits; >= 0 */
+  int32_t dtype;       /* spear_logits_dtype_t */
+  float temperature;   /* the settings of all draws where no array of them is given */
+  int32_t top_k;
+  float top_p;
+  float min_p;
+} spear_sample_desc_t;
+
+/*
+ * spear_sample_workspace_bytes -- device workspace of a call (host only): one of
+ * spear_w4ec_linear's kind, zero-filled before its first use; the call returns the
+ * counters of its header to zero.
+ * Errors: NULL_POINTER, INVALID_SHAPE, INVALID_ARGUMENT (dtype), UNSUPPORTED.
+ */
+spear_status_t spear_sample_workspace_bytes(const spear_sample_desc_t* desc, size_t* bytes);
+
+/*
+ * spear_sample -- draw one token from each of `batch` rows of logits l, and give the
+ * distributions that they are drawn from.  Tokens stand in falling order of l, equal
+ * ones by rising index; with the weights w(j) = exp((l(j) - max l) / temperature):
+ *   - top-k leaves the first k (k <= 0: all);
+ *   - top-p leaves the shortest run of first tokens that holds p of the total weight of
+ *     those that top-k left, one at least (p >= 1: all; p <= 0: one);
+ *   - min-p leaves those with w(j) >= m (m <= 0: all; above 1 as 1).
+ * A temperature of 0 (or below, or NaN) leaves the first token alone.  Logits of
+ * -infinity or NaN and weights below 2^-126 count as 0 and are never drawn;
+ * +infinity shares the draw with its equals alone.
+ *   tokens   int32 [batch] or NULL: the winner of an exponential race among the tokens
+ *            left, the largest w(j) / noise[b][j] (fp32, ties to the lowest j); the
+ *            first token where it is left alone; -1 for a row that has none.
+ *   probs    fp32 [batch][V], contiguous, or NULL: w(j) / (sum of those left), 0 for
+ *            the others (spear_verify_draft's target and draft rows).
+ *   logits   fp16 or fp32 [num_rows][V], the last dimension contiguous, row stride
+ *            in elements.
+ *   rows     int32 [batch]: the row of each draw, or NULL: draw b takes row b (batch
+ *            at most num_rows); one outside the logits has no token.
+ *   noise    fp32 [batch][V] drawn from Exp(1), contiguous; may be NULL where no
+ *            tokens are asked for or the settings leave one token to every row.
+ *   temperature, top_p, min_p  fp32 [batch], top_k int32 [batch], each NULL for the
+ *            descriptor's value.
+ * Which tokens are left is decided in 64 bits (weights enter the sums to 2^-34 of
+ * themselves); the weights of the race and of the probabilities are fp32.  The result
+ * does not depend on scheduling.
+ * Errors: NULL_POINTER, INVALID_SHAPE, INVALID_ARGUMENT, UNSUPPORTED,
+ *         MISALIGNED, WORKSPACE_TOO_SMALL, HIP.
+ */
+spear_status_t spear_sample(const spear_sample_desc_t* desc, const void* logits, int64_t row_stride,
+                            const int32_t* rows, const float* noise, const float* temperature,
+                            const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,
+                            float* probs, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

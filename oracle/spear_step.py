@@ -1,6 +1,7 @@
 """Oracle of what a serving step does around the layers and the cache: its pages,
-block tables and slots, and the adapters of its requests, in 64 bits.  Plain loops
-over sequences and tokens; nothing is shared with the HIP path."""
+block tables and slots, the adapters of its requests, and the draw of its next
+tokens, in 64 bits.  Plain loops over sequences and tokens; nothing is shared with the
+HIP path."""
 import numpy as np
 
 
@@ -70,3 +71,48 @@ def adapter_add(Y, X, A, B, cu, adapter, scale=None):
             h_err += 2.0 ** -22 * np.abs(h).max(1, keepdims=True)
         slack[at] = abs(s) * (h_err @ np.abs(wb).T + (2 * rank + 4) * 2.0 ** -24 * (np.abs(h) @ np.abs(wb).T))
     return out, slack
+
+
+def kept_tokens(logits, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, nudge=0.0):
+    """(tokens, weights) that the rules leave of one row, in falling order; weights in
+    64 bits relative to the largest.  `nudge`: relative change of top-p's mass, to ask
+    how near its cut is to the next."""
+    l = np.asarray(logits, np.float64)
+    l = np.where(np.isnan(l), -np.inf, l)
+    order = np.argsort(-l, kind="stable")
+    order = order[l[order] > -np.inf]
+    if not len(order) or not temperature > 0 or top_k == 1 or top_p <= 0:
+        return order[:1], np.ones(min(len(order), 1))
+    z = l[order]
+    with np.errstate(all="ignore"):
+        w = np.exp((z - z[0]) / float(temperature))
+    w = np.where(z == z[0], 1.0, w)                     # (infinite ones too)
+    w = np.where(w >= 2.0 ** -126, w, 0.0)
+    n = len(w) if top_k <= 0 else min(top_k, len(w))
+    n = min(n, int((w > 0).sum()))
+    if top_p < 1:
+        target = float(top_p) * w[:n].sum() * (1 + nudge)
+        n = max(1, int((np.concatenate([[0.0], np.cumsum(w[:n])[:-1]]) < target).sum()))
+    if min_p > 0:
+        n = min(n, int((w[:n] >= min(float(min_p), 1.0)).sum()))
+    return order[:n], w[:n]
+
+
+def sample(logits, noise, *rules, nudge=0.0):
+    """(token, scores, probabilities) of one row: the race in float32 as the definition
+    states; scores by token (-1: not drawn), None without noise."""
+    at, w = kept_tokens(logits, *rules, nudge=nudge)
+    probs = np.zeros(len(logits))
+    if not len(at):
+        return -1, None, probs
+    probs[at] = w / w.sum()
+    if len(at) == 1 and noise is None:
+        return int(at[0]), None, probs
+    if noise is None:
+        return None, None, probs
+    scores = np.full(len(logits), -1.0, np.float32)
+    with np.errstate(all="ignore"):
+        s = w.astype(np.float32) / noise[at].astype(np.float32)
+    scores[at] = np.where((s >= 0) & (w > 0), s, np.float32(-1))
+    best = scores.max()
+    return (int(np.argmax(scores)) if best >= 0 else -1), scores, probs

@@ -85,3 +85,28 @@ def test_adapters_merge_into_the_weight():
     out, _ = ref.adapter_add(Y, X, A, B, [0, 2, 6], [1, 1], [0.0, 0.25])
     merged = W + 0.25 * B[1].astype(np.float64) @ A[1].astype(np.float64)
     assert np.allclose(out, X.astype(np.float64) @ merged.T, rtol=1e-12, atol=1e-12)
+
+
+def test_rules_by_hand():
+    """Weights 8, 4, 2, 1, 1 at temperature 1, among a masked token and a NaN."""
+    l = np.log(np.array([2.0, 8, 1, 4, 1])).tolist() + [-np.inf, np.nan]
+    keep = lambda *r: ref.kept_tokens(l, *r)[0].tolist()  # noqa: E731
+    assert keep() == [1, 3, 0, 2, 4]
+    assert keep(1.0, 4) == [1, 3, 0, 2] and keep(1.0, 1) == [1] and keep(1.0, 99) == [1, 3, 0, 2, 4]
+    assert keep(1.0, 0, 0.4) == [1] and keep(1.0, 0, 0.51) == [1, 3] and keep(1.0, 0, 0.76) == [1, 3, 0]
+    assert keep(1.0, 2, 0.66) == [1] and keep(1.0, 2, 0.67) == [1, 3]       # of 12
+    assert keep(1.0, 0, 1.0, 0.24) == [1, 3, 0] and keep(1.0, 0, 1.0, 2.0) == [1]
+    assert keep(0.0) == keep(-1.0) == keep(float("nan")) == keep(1.0, 0, 0.0) == [1]
+    assert np.allclose(ref.sample(l, None, 0.5, 2)[2], [0, 0.8, 0, 0.2, 0, 0, 0])        # 64 to 16
+    assert ref.sample([-np.inf, np.nan], None)[0] == -1
+    assert ref.kept_tokens([1.0, np.inf, 2.0, np.inf])[0].tolist() == [1, 3]
+
+
+def test_the_race_draws_from_the_distribution():
+    """Frequencies of 20000 draws within five standard deviations."""
+    rng = np.random.default_rng(1)
+    l = np.array([0.3, -1.0, 1.2, 0.0, 2.0])
+    want = ref.sample(l, None, 0.8, 4)[2]
+    n = 20000
+    got = np.bincount([ref.sample(l, rng.exponential(size=5).astype(np.float32), 0.8, 4)[0] for _ in range(n)], minlength=5)
+    assert (np.abs(got / n - want) <= 5 * np.sqrt(want * (1 - want) / n)).all() and got[1] == 0

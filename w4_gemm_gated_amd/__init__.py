@@ -44,6 +44,7 @@ __all__ = [
     "spear_kv_plan",
     "spear_adapter_plan",
     "spear_adapter_add",
+    "spear_sample",
 ]
 
 
@@ -386,4 +387,4 @@ def spear_debug_mfma_rate(shape, waves_per_simd, iterations, sink):
 
 from .serve import (  # noqa: E402,F401
     spear_kv_cache, spear_kv_append, spear_kv_gather, spear_paged_attention, spear_verify_draft)
-from .step import spear_kv_plan, spear_adapter_plan, spear_adapter_add  # noqa: E402,F401
+from .step import spear_kv_plan, spear_adapter_plan, spear_adapter_add, spear_sample  # noqa: E402,F401

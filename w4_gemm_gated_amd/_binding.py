@@ -65,6 +65,8 @@ SERVE_EXPORTS = (
     "spear_adapter_plan",
     "spear_adapter_workspace_bytes",
     "spear_adapter_add",
+    "spear_sample_workspace_bytes",
+    "spear_sample",
 )
 
 
@@ -125,6 +127,12 @@ class KvPlanDesc(ctypes.Structure):
 class AdapterDesc(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("adapters", ctypes.c_int32), ("rows", ctypes.c_int32),
                 ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("rank", ctypes.c_int32), ("device_cus", ctypes.c_int32)]
+
+
+class SampleDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("vocab", ctypes.c_int32), ("num_rows", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("temperature", ctypes.c_float), ("top_k", ctypes.c_int32),
+                ("top_p", ctypes.c_float), ("min_p", ctypes.c_float)]
 
 
 class SpearError(RuntimeError):
@@ -220,6 +228,10 @@ def load(path=None):
     lib.spear_adapter_workspace_bytes.argtypes = [ctypes.POINTER(AdapterDesc), ctypes.POINTER(sz)]
     lib.spear_adapter_add.restype = ctypes.c_int
     lib.spear_adapter_add.argtypes = [ctypes.POINTER(AdapterDesc), vp, i64, vp, vp, vp, vp, sz, vp, i64, vp, sz, vp]
+    lib.spear_sample_workspace_bytes.restype = ctypes.c_int
+    lib.spear_sample_workspace_bytes.argtypes = [ctypes.POINTER(SampleDesc), ctypes.POINTER(sz)]
+    lib.spear_sample.restype = ctypes.c_int
+    lib.spear_sample.argtypes = [ctypes.POINTER(SampleDesc), vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     if path == LIB_PATH:
         _lib = lib
     return lib

@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "plan.cpp", "sched.cpp", "pack.hip", "ec_project.hip", "gemm.hip", "skinny.hip", "util.hip", "noalloc.hip", "ec_init.hip",
-           "serve_api.cpp", "kv_cache.hip", "paged_attn.hip", "paged_attn_tile.hip", "verify.hip", "step_api.cpp", "kv_plan.hip", "adapter.hip"]
+           "serve_api.cpp", "kv_cache.hip", "paged_attn.hip", "paged_attn_tile.hip", "verify.hip", "step_api.cpp", "kv_plan.hip", "adapter.hip", "sample.hip"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

@@ -184,4 +184,39 @@ struct AdapterArgs {
 };
 hipError_t launch_adapter(const AdapterArgs& a, void* stream);
 
+// The draw of next tokens.
+constexpr int kSampleShare = 8192;      // tokens of the vocabulary that a workgroup takes
+constexpr int kSampleList = 4096;       // tokens of the bins that are cut, gathered for the row's last workgroup
+constexpr int kSampleInfoBytes = 256;
+struct ShareInfo {
+  unsigned long long best;              // the largest (logit, token); then of (score, token)
+  unsigned long long number;            // a double: the place of its first bin; then the mass of what is kept
+  unsigned long long used;              // bins written
+};
+struct SampleShape {
+  int shares, group;                    // workgroups of a row, rows of a launch
+  size_t info, share, list, hist, bytes;
+};
+SampleShape sample_shape(const spear_sample_desc_t& d);
+struct SampleArgs {
+  int32_t batch, vocab, shares, num_rows;
+  int32_t first;                        // the group's first draw: row `first` + b where no rows are given
+  bool f16, only_first;                 // only_first: every row keeps its first token alone
+  const void* logits;
+  int64_t stride;
+  const int32_t* rows;
+  const float* noise;
+  const float *temperature, *top_p, *min_p;
+  const int32_t* top_k;
+  float one_temperature, one_top_p, one_min_p;
+  int32_t one_top_k;
+  int32_t* tokens;
+  float* probs;
+  uint32_t* counters;                   // [batch], zero before and after
+  void* info;
+  ShareInfo* share;                     // [batch][shares]
+  unsigned long long *list, *hist;      // [batch][kSampleList], [batch][shares][bins]
+};
+hipError_t launch_sample(const SampleArgs& a, void* stream);
+
 }  // namespace spear

@@ -46,6 +46,13 @@ spear_status_t check_adapter(const spear_adapter_desc_t& d) {
   return SPEAR_OK;
 }
 
+spear_status_t check_sample(const spear_sample_desc_t& d) {
+  if (d.batch < 0 || d.vocab < 1 || d.num_rows < 0) return SPEAR_ERR_INVALID_SHAPE;
+  if (d.dtype != SPEAR_LOGITS_FP16 && d.dtype != SPEAR_LOGITS_FP32) return SPEAR_ERR_INVALID_ARGUMENT;
+  if (d.batch > (1 << 20) || d.vocab > (1 << 22)) return SPEAR_ERR_UNSUPPORTED;
+  return SPEAR_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -154,6 +161,59 @@ spear_status_t spear_adapter_add(const spear_adapter_desc_t* desc, const void* X
   a.counters = (uint32_t*)ws;   // the header's first counters
   a.part = ws + s.part; a.H = ws + s.H; a.factor = (float*)(ws + s.factor);
   return hip_status(launch_adapter(a, stream));
+}
+
+spear_status_t spear_sample_workspace_bytes(const spear_sample_desc_t* desc, size_t* bytes) {
+  if (!desc || !bytes) return SPEAR_ERR_NULL_POINTER;
+  const spear_status_t st = check_sample(*desc);
+  if (st == SPEAR_OK) *bytes = desc->batch == 0 ? 0 : sample_shape(*desc).bytes;
+  return st;
+}
+
+spear_status_t spear_sample(const spear_sample_desc_t* desc, const void* logits, int64_t row_stride,
+                            const int32_t* rows, const float* noise, const float* temperature,
+                            const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,
+                            float* probs, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!desc) return SPEAR_ERR_NULL_POINTER;
+  spear_status_t st = check_sample(*desc);
+  if (st != SPEAR_OK) return st;
+  if (row_stride < 0 || row_stride > (int64_t)1 << 31 || (!rows && desc->batch > desc->num_rows))
+    return SPEAR_ERR_INVALID_SHAPE;
+  if (desc->batch == 0 || (!tokens && !probs)) return SPEAR_OK;
+  const bool one = (!temperature && !(desc->temperature > 0.0f)) || (!top_k && desc->top_k == 1) ||
+                   (!top_p && desc->top_p <= 0.0f);
+  if ((desc->num_rows > 0 && !logits) || (tokens && !noise && !one)) return SPEAR_ERR_NULL_POINTER;
+  const bool f16 = desc->dtype == SPEAR_LOGITS_FP16;
+  if (!aligned(logits, f16 ? 2 : 4) || !aligned(rows, 4) || !aligned(noise, 4) || !aligned(temperature, 4) ||
+      !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(tokens, 4) || !aligned(probs, 4))
+    return SPEAR_ERR_MISALIGNED;
+  const SampleShape s = sample_shape(*desc);
+  st = check_workspace(workspace, workspace_bytes, s.bytes);
+  if (st != SPEAR_OK) return st;
+  char* ws = (char*)workspace;
+  SampleArgs a;
+  a.vocab = desc->vocab; a.shares = s.shares; a.num_rows = desc->num_rows;
+  a.f16 = f16; a.only_first = one;
+  a.logits = logits; a.stride = row_stride;
+  a.one_temperature = desc->temperature; a.one_top_k = desc->top_k; a.one_top_p = desc->top_p; a.one_min_p = desc->min_p;
+  a.counters = (uint32_t*)ws;   // the header's first counters
+  a.info = ws + s.info; a.share = (ShareInfo*)(ws + s.share);
+  a.list = (unsigned long long*)(ws + s.list); a.hist = (unsigned long long*)(ws + s.hist);
+  for (int32_t at = 0; at < desc->batch; at += s.group) {
+    a.batch = desc->batch - at < s.group ? desc->batch - at : s.group;
+    a.first = at;
+    a.rows = rows ? rows + at : nullptr;
+    a.noise = noise ? noise + (int64_t)at * desc->vocab : nullptr;
+    a.temperature = temperature ? temperature + at : nullptr;
+    a.top_k = top_k ? top_k + at : nullptr;
+    a.top_p = top_p ? top_p + at : nullptr;
+    a.min_p = min_p ? min_p + at : nullptr;
+    a.tokens = tokens ? tokens + at : nullptr;
+    a.probs = probs ? probs + (int64_t)at * desc->vocab : nullptr;
+    st = hip_status(launch_sample(a, stream));
+    if (st != SPEAR_OK) return st;
+  }
+  return SPEAR_OK;
 }
 
 }  // extern "C"

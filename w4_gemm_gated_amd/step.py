@@ -1,6 +1,6 @@
 """What a serving step does around the W4 layers and the paged cache: its pages,
-block tables and slots planned on the GPU, and the low-rank adapters of its
-requests added beside a shared projection.
+block tables and slots planned on the GPU, the low-rank adapters of its requests
+added beside a shared projection, and the draw of its next tokens.
 
 Python names mirror the C ABI in include/spear_serve.h, which states the
 definitions; only arguments are marshalled here, as in serve.py.
@@ -10,10 +10,10 @@ import ctypes
 import torch
 
 from . import _binding
-from ._binding import AdapterDesc, KvPlanDesc
+from ._binding import AdapterDesc, KvPlanDesc, SampleDesc
 from .serve import _check, _dense, _p, _plan, _scratch, _stream
 
-__all__ = ["spear_kv_plan", "spear_adapter_plan", "spear_adapter_add"]
+__all__ = ["spear_kv_plan", "spear_adapter_plan", "spear_adapter_add", "spear_sample"]
 
 
 def _out(t, name, shape, dtype, device):
@@ -168,3 +168,68 @@ def spear_adapter_add(Y, X, A, B, plan, scale=None, workspace=None):
                                plan.data.numel(), Y.data_ptr(), ys, *ws, stream)
     _binding.check(st, "spear_adapter_add")
     return Y
+
+
+_LOGITS = {torch.float16: 0, torch.float32: 1}
+
+
+def _setting(x, name, dtype, batch, device):
+    """(address, value for all): an array of a value for each draw, or one for all."""
+    if not isinstance(x, torch.Tensor):
+        return None, x
+    _dense(x, name, dtype, 1, device)
+    if x.shape[0] != batch:
+        raise ValueError(f"{name} must have an entry for each draw")
+    return x.data_ptr(), 0
+
+
+def spear_sample(logits, noise=None, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, rows=None, probs=False,
+                 tokens=None, workspace=None):
+    """(tokens int32 [B], probs fp32 [B, V]): one token drawn for each row of the
+    logits, and the distribution that it is drawn from.
+
+    logits fp16 or fp32 [R, V] (last dimension contiguous); rows int32 [B]: the row of
+    each draw, or None: all in order; noise fp32 [B, V] from Exp(1): None if no tokens
+    are wanted (tokens is then None, unless the settings below, given as numbers,
+    leave a single token).  Settings are numbers, or a tensor [B] with one for each
+    draw: temperature (0: the largest logit's token), top_k (int32; 0: off), top_p
+    (1: off), min_p (0: off).  probs: True, or the tensor to be filled, for the
+    distribution; else None is returned.  `workspace` as in spear_paged_attention.
+    """
+    dev = _gpu(logits, "logits")
+    dt = logits.dtype
+    if dt not in _LOGITS:
+        raise TypeError(f"logits must be torch.float16 or torch.float32, got {dt}")
+    _check(logits, "logits", dt, 2, dev)
+    R, V = logits.shape
+    if logits.stride(1) != 1 and V > 1:
+        raise ValueError("logits must be contiguous in its last dimension")
+    B = R
+    if rows is not None:
+        _dense(rows, "rows", torch.int32, 1, dev)
+        B = rows.shape[0]
+    if noise is not None:
+        _dense(noise, "noise", torch.float32, 2, dev)
+        if noise.shape != (B, V):
+            raise ValueError("noise must be [B, V]")
+    f32 = torch.float32
+    t_at, t = _setting(temperature, "temperature", f32, B, dev)
+    k_at, k = _setting(top_k, "top_k", torch.int32, B, dev)
+    p_at, p = _setting(top_p, "top_p", f32, B, dev)
+    m_at, m = _setting(min_p, "min_p", f32, B, dev)
+    t, k, p, m = float(t), min(max(int(k), 0), V), float(p), float(m)
+    one = (t_at is None and not t > 0) or (k_at is None and k == 1) or (p_at is None and p <= 0)
+    if noise is not None or one or tokens is not None:
+        tokens = _out(tokens, "tokens", (B,), torch.int32, dev)
+    if probs is True or isinstance(probs, torch.Tensor):
+        probs = _out(None if probs is True else probs, "probs", (B, V), f32, dev)
+    else:
+        probs = None
+    lib, stream = _binding.load(), _stream(dev)
+    d = _plan(("sample", B, V, R, dt, t, k, p, m), lambda: (
+        SampleDesc(B, V, R, _LOGITS[dt], t, k, p, m), lib.spear_sample_workspace_bytes, "spear_sample"))
+    ws = _space(workspace, d[2], dev, stream)
+    st = lib.spear_sample(d[1], logits.data_ptr(), V if R == 1 else logits.stride(0), _p(rows), _p(noise), t_at, k_at,
+                          p_at, m_at, _p(tokens), _p(probs), *ws, stream)
+    _binding.check(st, "spear_sample")
+    return tokens, probs
