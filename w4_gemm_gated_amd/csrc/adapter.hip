@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlanA
   __shared__ int32_t list_at[kMaxAdapters];
   __shared__ int64_t waves[kPlanThreads / kWave];
   __shared__ int32_t first_of[kPlanThreads], rows_of[kPlanThreads], place_of[kPlanThreads];
-  __shared__ int32_t bad;
+  __shared__ int32_t bad, longs;
   const int tid = threadIdx.x;
   for (int i = tid; i < a.adapters; i += kPlanThreads) count[i] = 0;
   if (tid == 0) bad = 0;
@@ -129,16 +129,18 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlanA
     constexpr int kShort = 16;
     if (n <= kShort)
       for (int i = 0; i < n; ++i) list[at + i] = from + i;
-    first_of[tid] = from;
-    rows_of[tid] = n;
-    place_of[tid] = at;
-    const int any = __syncthreads_or(n > kShort);
-    if (any)
-      for (int s = 0; s < kPlanThreads; ++s) {
-        const int m = rows_of[s];
-        if (m > kShort)
-          for (int i = tid; i < m; i += kPlanThreads) list[place_of[s] + i] = first_of[s] + i;
-      }
+    if (tid == 0) longs = 0;
+    __syncthreads();
+    if (n > kShort) {
+      const int s = atomicAdd(&longs, 1);
+      first_of[s] = from;
+      rows_of[s] = n;
+      place_of[s] = at;
+    }
+    __syncthreads();
+    const int many = longs;
+    for (int s = tid / kWave; s < many; s += kPlanThreads / kWave)       // a wave to each
+      for (int i = tid % kWave; i < rows_of[s]; i += kWave) list[place_of[s] + i] = first_of[s] + i;
     __syncthreads();
   }
 }

@@ -4,20 +4,20 @@
 // The rules keep a prefix of the tokens in falling order of their logits, so what
 // has to be found is where that order is cut: no sort of the vocabulary is needed,
 // only the counts and sums of weights above a value.  A row's vocabulary is shared by
-// workgroups of kShare tokens each, in two launches (three for probabilities):
+// workgroups, in two launches (three for probabilities):
 //
 //   1. Every share finds its maximum and, for top-k and top-p, a histogram of its
-//      weights: bins of 1/16 in log2 of the weight, on one grid for the whole row
-//      (t = 16 logit / (T ln 2); bin floor(t)), so that shares need no common
+//      weights: 32 bins to a power of two, on one grid for the whole row
+//      (t = 32 logit / (T ln 2); bin floor(t)), so that shares need no common
 //      maximum first and the row is read once.  A bin holds its count and the sum of
 //      its weights' distances from the bin's upper edge in fixed point, both in one
 //      64-bit integer (one LDS atomic a token; integer sums have no order).  The
 //      row's last share to arrive adds the histograms, sums counts and weights from the
 //      top, and finds the bin in which each rule's cut lies.
 //   2. Tokens above that bin are drawn from at once (an exponential race: the largest
-//      weight / noise, ties to the lowest index), those in it (some hundreds) go
+//      weight / noise, ties to the lowest index), those in it (up to some hundreds) go
 //      to a list; noise is read for tokens that are kept, and for no others.  The last
-//      share to arrive cuts the list by a radix selection on (logit, index), ends the
+//      share to arrive sorts the list by (logit, index), cuts it by a running sum, ends the
 //      race, and sums what is kept.
 //   3. Probabilities are written.
 //
@@ -25,8 +25,9 @@
 // has a millionth of the total: weights enter the sums to 2^-34 of themselves, and
 // sums are held in 64 bits.
 //
-// A bin that holds more tokens than the list (equal logits, a very high temperature)
-// is cut by the same selection over the row itself, by one workgroup: slow, and right.
+// Longer lists are cut by a radix selection, and a bin that holds more tokens than the
+// list (equal logits, a very high temperature) by the same selection over the row
+// itself, by one workgroup: slow, and right.
 #include <algorithm>
 
 #include "serve_internal.h"
@@ -36,24 +37,26 @@ namespace spear {
 namespace {
 
 constexpr int kThreads = 512, kWaves = kThreads / kWave;
-constexpr int kEach = kSampleShare / kThreads;    // tokens of a thread
-constexpr int kBins = 2048;                       // 128 in log2 of the weight
+constexpr int kPer = 32;                          // bins in a power of two
+constexpr int kBins = 128 * kPer;
 constexpr int kBinsEach = kBins / kThreads;
-constexpr double kCut = -126.0 * 16.0;            // weights below 2^-126 of the largest are zero
-constexpr int kDefBits = 38;                      // fixed point of a bin's sum of distances
+constexpr double kCut = -126.0 * kPer;            // weights below 2^-126 of the largest are zero
+constexpr int kDefBits = 37;                      // fixed point of a bin's sum of distances
 constexpr int kFixBits = 40;                      // fixed point of weights in a selection
+constexpr int kRanked = kThreads;                 // tokens that are sorted by counting
 constexpr int kSubs = 2048;                       // sub-bins of a selection's step
+constexpr double kLn2 = 0.693147180559945309417;
 typedef float f4u_t __attribute__((ext_vector_type(4), aligned(4)));
 typedef _Float16 h8u_t __attribute__((ext_vector_type(8), aligned(2)));
 typedef unsigned long long u64;
 
 enum Kind : int32_t { kEmpty, kOne, kRace };      // no token, the first one, a race of several
 
-// What a row's first launch leaves for the others.  t: 16 log2 of a weight, on the
+// What a row's first launch leaves for the others.  t: kPer log2 of a weight, on the
 // row's grid; bins are counted from the one of the row's largest; masses are in units
 // of that bin's upper edge.
 struct RowInfo {
-  double c16, tm;            // t of a logit of 1, and of the row's largest
+  double scale, tm;          // t of a logit of 1, and of the row's largest
   double first, last;        // tokens of bins before `first` are kept, those of bins past `last` are not ..
   double bin_k;              // .. and top-k's cut lies in this bin (one of them, or past them; -1: no such cut)
   double lim;                // min-p: t - tm at least
@@ -61,6 +64,7 @@ struct RowInfo {
   double target;             // top-p's mass if that is known; else (with top-k) p
   u64 end;                   // second launch: key of the last token kept (0: all)
   double inv;                // 1 / mass of what is kept, in units of the largest weight
+  float low;                 // no token below this logit is kept or listed
   int32_t kind, token;       // token: the largest logit's
   int32_t left_k;            // tokens that top-k keeps of its bin
   int32_t by_k, by_p;        // which rules cut
@@ -79,14 +83,14 @@ __device__ __forceinline__ float logit_of(u64 key) {
 }
 __device__ __forceinline__ bool valid(float l) { return l > -INFINITY; }
 // (an infinite logit lies above all others, and equal ones share a place)
-__device__ __forceinline__ double t_of(float l, double c16) { return fmin((double)l * c16, 1e300); }
-
+__device__ __forceinline__ double t_of(float l, double scale) { return fmin((double)l * scale, 1e300); }
 // The bin of a t, from the one of the row's largest: whole numbers, exact wherever two
 // bins are near each other.
 __device__ __forceinline__ double bin_of(const RowInfo& o, double t) { return floor(o.tm) - floor(t); }
-// log2 of a weight in units of the upper edge of bin `bin`.
-__device__ __forceinline__ double below_edge(const RowInfo& o, double t, double bin) {
-  return ((t - floor(o.tm)) + (bin - 1.0)) * 0.0625;
+// A weight in units of the upper edge of bin `bin`, in fixed point.
+__device__ __forceinline__ u64 fixed_below(const RowInfo& o, double t, double bin) {
+  const double x = ((t - floor(o.tm)) + (bin - 1.0)) * (1.0 / kPer);
+  return (u64)(exp2(x) * (double)(1ull << kFixBits));
 }
 
 // The workgroup's maximum, bitwise and / or, and sum, in every thread.
@@ -131,31 +135,31 @@ __device__ __forceinline__ T block_run(T v, T* lds) {
 // A thread's tokens of a share: vectors of eight in turn.
 __device__ __forceinline__ int place(int beg, int i) { return beg + 8 * ((i / 8) * kThreads + (int)threadIdx.x) + i % 8; }
 
-template <bool F16>
+template <bool F16, int EACH>
 __device__ __forceinline__ void load_share(const void* row, int beg, int end, float* l) {
-  if (end - beg == kSampleShare) {
+  if (end - beg == EACH * kThreads) {
     const int at = beg + 8 * (int)threadIdx.x;
     if constexpr (F16) {
-      h8u_t v[kEach / 8];
+      h8u_t v[EACH / 8];
 #pragma unroll
-      for (int i = 0; i < kEach / 8; ++i) v[i] = *(const h8u_t*)((const half_t*)row + at + i * 8 * kThreads);
+      for (int i = 0; i < EACH / 8; ++i) v[i] = *(const h8u_t*)((const half_t*)row + at + i * 8 * kThreads);
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) l[i] = (float)v[i / 8][i % 8];
+      for (int i = 0; i < EACH; ++i) l[i] = (float)v[i / 8][i % 8];
     } else {
-      f4u_t v[kEach / 4];
+      f4u_t v[EACH / 4];
 #pragma unroll
-      for (int i = 0; i < kEach / 4; ++i) v[i] = *(const f4u_t*)((const float*)row + at + (i / 2) * 8 * kThreads + i % 2 * 4);
+      for (int i = 0; i < EACH / 4; ++i) v[i] = *(const f4u_t*)((const float*)row + at + (i / 2) * 8 * kThreads + i % 2 * 4);
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) l[i] = v[i / 4][i % 4];
+      for (int i = 0; i < EACH; ++i) l[i] = v[i / 4][i % 4];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
+    for (int i = 0; i < EACH; ++i) {
       const int j = min(place(beg, i), end - 1);
       l[i] = F16 ? (float)((const half_t*)row)[j] : ((const float*)row)[j];
     }
 #pragma unroll
-    for (int i = 0; i < kEach; ++i)
+    for (int i = 0; i < EACH; ++i)
       if (place(beg, i) >= end) l[i] = -INFINITY;
   }
 }
@@ -189,13 +193,9 @@ __device__ __forceinline__ void st64(u64* p, u64 v) { __hip_atomic_store(p, v, _
 
 // Whether this workgroup is the last of its row's; the counter is then zero again.
 __device__ __forceinline__ bool last_of_row(const SampleArgs& a, int b, uint32_t* arrived) {
-  if (a.shares == 1) {
-    drain_vm();
-    __syncthreads();
-    return true;
-  }
   drain_vm();
   __syncthreads();
+  if (a.shares == 1) return true;
   if (threadIdx.x == 0) *arrived = add_dev_u32(&a.counters[b], 1u);
   __syncthreads();
   if (*arrived != (uint32_t)a.shares - 1) return false;
@@ -205,32 +205,43 @@ __device__ __forceinline__ bool last_of_row(const SampleArgs& a, int b, uint32_t
 
 // -------------------------------------------------------------- first launch
 
-template <bool F16>
+// 2^(-i / kPer)
+__device__ const double kSteps[kPer] = {
+    1.0, 0.9785720620877001, 0.9576032806985737, 0.93708381705515,
+    0.9170040432046712, 0.8973545375015536, 0.8781260801866497, 0.859309649061239,
+    0.8408964152537145, 0.8228777390769825, 0.8052451659746271, 0.7879904225539432,
+    0.7711054127039704, 0.7545822137967114, 0.7384130729697497, 0.7225904034885233,
+    0.7071067811865476, 0.691954940981916, 0.6771277734684463, 0.6626183215798707,
+    0.6484197773255048, 0.6345254785958666, 0.620928906036742, 0.6076236799902345,
+    0.5946035575013605, 0.5818624293887887, 0.5693943173783458, 0.5571933712979462,
+    0.5452538663326288, 0.5335702003384118, 0.5221368912137069, 0.5109485743270583};
+
+template <bool F16, int EACH>
 __global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
-  __shared__ u64 hist[kBins];
-  __shared__ uint32_t counts[kBins];
+  // One share's bins; then the row's: the mass and the tokens up to and with each bin.
+  __shared__ __attribute__((aligned(16))) u64 hist[kBins];
+  __shared__ uint32_t count_to[kBins];
   __shared__ u64 red[kWaves];
   __shared__ double redd[kWaves];
   __shared__ uint32_t redc[kWaves];
+  __shared__ int share_off[kThreads], share_used[kThreads];
   __shared__ uint32_t arrived;
-  __shared__ double found_mass;     // of a search over the bins
-  __shared__ int found, found_count, found_in;
-  __shared__ double total_mass;
-  __shared__ uint32_t total_count;
   const int b = blockIdx.x / a.shares, share = blockIdx.x % a.shares, tid = threadIdx.x;
   const Rules r = rules_of(a, b);
   const void* row = row_of(a, b);
   const bool bins = !r.one && (r.k > 0 || r.p < 1.0f);
-  const int beg = share * kSampleShare, end = min(beg + kSampleShare, a.vocab);
-  float l[kEach];
+  const int beg = share * EACH * kThreads, end = min(beg + EACH * kThreads, a.vocab);
+  float l[EACH];
   u64 best = 0;
   uint32_t least = ~0u;
+  if (row) load_share<F16, EACH>(row, beg, end, l);
+  if (bins)
+    for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
   if (row) {
-    load_share<F16>(row, beg, end, l);
     float top = -INFINITY, low = INFINITY;
     int at = 0;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
+    for (int i = 0; i < EACH; ++i) {
       if (l[i] > top) {
         top = l[i];
         at = place(beg, i);
@@ -243,28 +254,25 @@ __global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
     }
   }
   best = block_max(best, red);
-  const double c16 = fmax(16.0 / ((double)r.t * 0.693147180559945309417), 1e-300);
+  const double scale = fmax((double)kPer / ((double)r.t * kLn2), 1e-300);
   ShareInfo* mine = a.share + (int64_t)b * a.shares + share;
-  u64* bins_out = a.hist + ((int64_t)b * a.shares + share) * kBins;
   if (bins && best != 0) {
-    for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
     least = block_all(least, redc, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
-    const double q = floor(t_of(logit_of(best), c16));
+    const double q = floor(t_of(logit_of(best), scale));
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const double t = t_of(l[i], c16), f = floor(t), rel = q - f;
+    for (int i = 0; i < EACH; ++i) {
+      const double t = t_of(l[i], scale), f = floor(t), rel = q - f;
       if (valid(l[i]) && rel < kBins) {
-        // 1 - 2^((t - f - 1) / 16): the first term in 64 bits, the rest is below 2^-10
-        const double u = (1.0 - (t - f)) * (0.693147180559945309417 / 16.0);
-        const float s = (float)u;
-        const float h = s * s * (0.5f - s * (1.0f / 6.0f - s * (1.0f / 24.0f - s * (1.0f / 120.0f))));
-        const double d = u - (double)h;
-        const u64 fixed = (u64)__double_as_longlong(__builtin_fma(d, (double)(1ull << kDefBits), 0x1p52));
-        atomicAdd(&hist[(int)rel], fixed - 0x4330000000000000ull + (1ull << 48));
+        // The weight's distance from the bin's upper edge, 1 - e^-u: u in 64 bits, the rest is below 2^-12.
+        const double u = (1.0 - (t - f)) * (kLn2 / kPer);
+        const float s = (float)u, h = s * s * (0.5f - s * (1.0f / 6.0f - s * (1.0f / 24.0f - s * (1.0f / 120.0f))));
+        const double d = __builtin_fma(u, (double)(1ull << kDefBits), -(double)(h * (float)(1ull << kDefBits)));
+        atomicAdd(&hist[(int)rel], ((u64)(1u << 16) << 32) | (uint32_t)d);
       }
     }
-    const double span = q - floor(t_of(logit_of((u64)least << 32), c16)) + 1.0;
+    const double span = q - floor(t_of(logit_of((u64)least << 32), scale)) + 1.0;
     const int used = span < kBins ? (int)span : kBins;
+    u64* bins_out = a.hist + ((int64_t)b * a.shares + share) * kBins;
     __syncthreads();
     for (int i = tid; i < used; i += kThreads) st64(&bins_out[i], hist[i]);
     if (tid == 0) {
@@ -276,21 +284,25 @@ __global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
   if (!last_of_row(a, b, &arrived)) return;
 
   // The row: its largest, ..
-  ShareInfo* all = a.share + (int64_t)b * a.shares;
+  static_assert((1 << 22) / (2 * kSampleLeast) <= kThreads, "a thread for every share");
+  u64 number = 0, used = 0;
   best = 0;
-  for (int s = tid; s < a.shares; s += kThreads) {
-    const u64 v = ld64(&all[s].best);
-    best = best > v ? best : v;
+  if (tid < a.shares) {
+    const ShareInfo* from = a.share + (int64_t)b * a.shares + tid;
+    best = ld64(&from->best);
+    number = ld64(&from->number);
+    used = ld64(&from->used);
   }
+  const bool any = best != 0;
   best = block_max(best, red);
   RowInfo* info = (RowInfo*)((char*)a.info + (int64_t)b * kSampleInfoBytes);
   static_assert(sizeof(RowInfo) <= kSampleInfoBytes, "room for it");
   RowInfo o;
-  o.c16 = c16;
-  o.tm = best ? t_of(logit_of(best), c16) : 0.0;
+  o.scale = scale;
+  o.tm = best ? t_of(logit_of(best), scale) : 0.0;
   o.first = INFINITY;
   o.last = o.bin_k = -1.0;
-  o.lim = fmax(r.m > 0.0f ? 16.0 * log2((double)r.m) : kCut, kCut);
+  o.lim = fmax(r.m > 0.0f ? (double)kPer * log2((double)r.m) : kCut, kCut);
   o.before = o.before_k = o.target = 0.0;
   o.end = 0;
   o.inv = 1.0;
@@ -298,111 +310,91 @@ __global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
   o.token = best ? (int)~(uint32_t)best : -1;
   o.left_k = o.by_k = o.by_p = o.heavy = 0;
   o.listed = 0;
+  double low = o.tm + o.lim;
   if (o.kind != kRace && a.tokens && tid == 0) a.tokens[b] = o.token;
   if (o.kind == kRace && bins) {
-    // .. its bins (a thread's are neighbours), ..
-    const double q = floor(o.tm);
-    uint32_t n[kBinsEach];
-    u64 def[kBinsEach];
-#pragma unroll
-    for (int i = 0; i < kBinsEach; ++i) n[i] = 0, def[i] = 0;
-    for (int s = 0; s < a.shares; ++s) {
-      if (ld64(&all[s].best) == 0) continue;
-      const double behind = q - __longlong_as_double((long long)ld64(&all[s].number));
-      if (!(behind < kBins)) continue;
-      const int off = (int)behind, used = (int)ld64(&all[s].used);
-      const u64* from = a.hist + ((int64_t)b * a.shares + s) * kBins;
-#pragma unroll
-      for (int i = 0; i < kBinsEach; ++i) {
-        const int at = tid * kBinsEach + i - off;
-        if (at >= 0 && at < used) {
-          const u64 v = ld64(&from[at]);
-          n[i] += (uint32_t)(v >> 48);
-          def[i] += v & ((1ull << 48) - 1);
-        }
-      }
+    // .. its bins, ..
+    const double q = floor(o.tm), behind = q - __longlong_as_double((long long)number);
+    const bool near = any && behind < kBins;
+    if (tid < a.shares) {
+      share_off[tid] = near ? (int)behind : 0;
+      share_used[tid] = near ? (int)used : 0;
     }
+    const int rows = (int)block_max((u64)(near ? min((int)behind + (int)used, kBins) : 0), red);   // bins of the row
+    const u64* from = a.hist + (int64_t)b * a.shares * kBins;
+    constexpr int kTogether = 8;      // shares whose loads are in flight together
+    for (int bin = tid; bin < kBins; bin += kThreads) {
+      uint32_t n = 0;
+      u64 def = 0;
+      if (bin < rows)
+        for (int s0 = 0; s0 < a.shares; s0 += kTogether) {
+          u64 v[kTogether];
+#pragma unroll
+          for (int s = 0; s < kTogether; ++s) {
+            const int of = min(s0 + s, a.shares - 1), at = bin - share_off[of];
+            v[s] = s0 + s < a.shares && at >= 0 && at < share_used[of] ? ld64(&from[(int64_t)of * kBins + at]) : 0;
+          }
+#pragma unroll
+          for (int s = 0; s < kTogether; ++s) {
+            n += (uint32_t)(v[s] >> 48);
+            def += v[s] & ((1ull << 48) - 1);
+          }
+        }
+      const double edge = kSteps[bin % kPer] * __longlong_as_double((long long)(1023 - bin / kPer) << 52);
+      hist[bin] = (u64)__double_as_longlong(edge * ((double)n - (double)def * (1.0 / (double)(1ull << kDefBits))));
+      count_to[bin] = n;
+    }
+    __syncthreads();
     // .. and their running sums.
-    double mass[kBinsEach], mass_to = 0.0;
-    uint32_t count_to = 0;
+    double mass[kBinsEach], mass_own = 0.0;
+    uint32_t n[kBinsEach], n_own = 0;
 #pragma unroll
     for (int i = 0; i < kBinsEach; ++i) {
-      const int at = tid * kBinsEach + i;
-      const double edge = ldexp(exp2(-(double)(at % 16) / 16.0), -(at / 16));
-      mass[i] = edge * ((double)n[i] - (double)def[i] * (1.0 / (double)(1ull << kDefBits)));
-      mass_to += mass[i];
-      count_to += n[i];
+      mass[i] = __longlong_as_double((long long)hist[tid * kBinsEach + i]);
+      n[i] = count_to[tid * kBinsEach + i];
+      mass_own += mass[i];
+      n_own += n[i];
     }
-    const double own_mass = mass_to;
-    const uint32_t own_count = count_to;
-    mass_to = block_run(mass_to, redd);
-    count_to = block_run(count_to, redc);
-    __syncthreads();
-    if (tid == kThreads - 1) {
-      total_mass = mass_to;
-      total_count = count_to;
-    }
+    double mass_at = block_run(mass_own, redd) - mass_own;
+    uint32_t n_at = block_run(n_own, redc) - n_own;
 #pragma unroll
-    for (int i = 0; i < kBinsEach; ++i) counts[tid * kBinsEach + i] = n[i];
+    for (int i = 0; i < kBinsEach; ++i) {
+      mass_at += mass[i];
+      n_at += n[i];
+      hist[tid * kBinsEach + i] = (u64)__double_as_longlong(mass_at);
+      count_to[tid * kBinsEach + i] = n_at;
+    }
     __syncthreads();
-    const double total = total_mass;
-    const bool by_k = r.k > 0 && (uint32_t)r.k < total_count;
-    // The first bin in which the count reaches k, or the mass a target (the last of any
-    // tokens if it never does): its place, what lies before it and in it.
+    auto mass_to = [&](int bin) { return bin < 0 ? 0.0 : __longlong_as_double((long long)hist[bin]); };
+    auto tokens_to = [&](int bin) { return bin < 0 ? 0u : count_to[bin]; };
+    // The first bin up to which there are k tokens, or a mass (the last bin if there are
+    // none): every thread looks for itself.
     auto search = [&](bool by_count, double target) {
-      __syncthreads();
-      if (tid == 0) found = kBins;
-      __syncthreads();
-      int reaches = kBins, lowest = -1;
-      double before = mass_to - own_mass;
-      uint32_t count = count_to - own_count;
+      int at = 0;
 #pragma unroll
-      for (int i = 0; i < kBinsEach; ++i) {
-        before += mass[i];
-        count += n[i];
-        if (n[i] > 0) lowest = tid * kBinsEach + i;
-        if (n[i] > 0 && reaches == kBins && (by_count ? count >= (uint32_t)r.k : before >= target))
-          reaches = tid * kBinsEach + i;
-      }
-      if (reaches < kBins) atomicMin(&found, reaches);
-      const int bin_end = (int)block_max((u64)(lowest + 1), red) - 1;
-      const int bin = found < kBins ? found : bin_end;
-      before = mass_to - own_mass;
-      count = count_to - own_count;
-#pragma unroll
-      for (int i = 0; i < kBinsEach; ++i) {
-        if (tid * kBinsEach + i == bin) {
-          found_count = (int)count;
-          found_mass = before;
-          found_in = (int)n[i];
-        }
-        before += mass[i];
-        count += n[i];
-      }
-      __syncthreads();
-      return bin;
+      for (int step = kBins / 2; step > 0; step /= 2)
+        if (by_count ? count_to[at + step - 1] < (uint32_t)r.k : mass_to(at + step - 1) < target) at += step;
+      return at;
     };
+    const bool by_k = r.k > 0 && (uint32_t)r.k < tokens_to(kBins - 1);
+    const double total = mass_to(kBins - 1);
     int bin_k = kBins, first = kBins, last = kBins;
     double low_sum = total, high_sum = total;
     if (by_k) {
       bin_k = search(true, 0.0);
-      o.left_k = r.k - found_count;
-      o.before_k = found_mass;
-      o.before = found_mass;
-      low_sum = found_mass;
-      // (the bin's own mass is at most its count at the upper edge)
-      high_sum = found_mass + found_in * ldexp(exp2(-(double)(bin_k % 16) / 16.0), -(bin_k / 16));
+      o.left_k = r.k - (int)tokens_to(bin_k - 1);
+      o.before_k = o.before = low_sum = mass_to(bin_k - 1);
+      high_sum = mass_to(bin_k);
       first = last = bin_k;
     }
     if (r.p < 1.0f) {
       // Bins in which top-p's cut can lie: rounding, and what top-k keeps of its own bin, leave a range.
       constexpr double kNear = 0x1p-30;
       const int hi = search(false, (double)r.p * low_sum * (1.0 - kNear));
-      const double before = found_mass;
       const int lo = search(false, (double)r.p * high_sum * (1.0 + kNear));
       if (hi <= first) {
         first = hi;
-        o.before = before;
+        o.before = mass_to(hi - 1);
       }
       last = min(last, lo);
       o.target = by_k ? (double)r.p : (double)r.p * total;
@@ -412,24 +404,28 @@ __global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
     if (first < kBins) {
       o.first = first;
       o.last = last;
-      if (by_k) o.bin_k = bin_k;
-      // How many they are.
-      u64 listed = 0;
-      for (int i = tid; i < kBins; i += kThreads)
-        if ((i >= first && i <= last) || (by_k && i == bin_k)) listed += counts[i];
-      listed = block_add(listed, red);
+      uint32_t listed = tokens_to(last) - tokens_to(first - 1);
+      if (by_k) {
+        o.bin_k = bin_k;
+        if (bin_k > last) listed += tokens_to(bin_k) - tokens_to(bin_k - 1);
+      }
       o.heavy = listed > kSampleList;
+      low = q - max(last, by_k ? bin_k : 0);
     }
   }
+  // (rounded down by more than the division and the rounding to fp32 can raise it)
+  const double at = low / scale;
+  o.low = fmax(at - fabs(at) * 0x1p-20, -3.4e38);
+  if (!(o.low > -3.0e38f)) o.low = -INFINITY;
   if (tid == 0) *info = o;
 }
 
 // ------------------------------------------------------------- second launch
 
-// 2^(x / 16) for x <= 0, as fp32: the exponent's whole part apart, so that the rest is
-// exact to a few 2^-24.
-__device__ __forceinline__ float weight_of(double x16) {
-  const double x = x16 * 0.0625, n = rint(x);
+// The weight of a t that lies `behind` (<= 0) the row's largest, as fp32: the exponent's
+// whole part apart, so that the rest is exact to a few 2^-24.
+__device__ __forceinline__ float weight_of(double behind) {
+  const double x = behind * (1.0 / kPer), n = rint(x);
   return ldexpf(__builtin_amdgcn_exp2f((float)(x - n)), (int)n);
 }
 
@@ -440,13 +436,8 @@ __device__ __forceinline__ u64 race_key(float w, float noise, int j) {
   return w > 0.0f && s >= 0.0f ? ((u64)float_bits(s) << 32) | (uint32_t)~j : 0ull;
 }
 
-// A weight in units of the upper edge of a bin, in fixed point.
-__device__ __forceinline__ u64 fixed_below(const RowInfo& o, double t, double bin) {
-  return (u64)(exp2(below_edge(o, t, bin)) * (double)(1ull << kFixBits));
-}
-
 struct Scratch {
-  u64 list[kSampleList];
+  __attribute__((aligned(16))) u64 list[kSampleList];
   uint32_t counts[kSubs];
   u64 sums[kSubs];
   u64 red[kWaves];
@@ -481,7 +472,7 @@ __device__ u64 select(const SampleArgs& a, const RowInfo& o, const void* row, Sc
   const int tid = threadIdx.x;
   u64 mask = 0, value = 0;      // tokens left: key & mask == value
   auto here = [&](u64 k) {
-    const double bin = bin_of(o, t_of(logit_of(k), o.c16));
+    const double bin = bin_of(o, t_of(logit_of(k), o.scale));
     return bin >= first && bin <= last && (k & mask) == value;
   };
   for (;;) {
@@ -508,7 +499,7 @@ __device__ u64 select(const SampleArgs& a, const RowInfo& o, const void* row, Sc
         const int sub = kSubs - 1 - (int)((k >> shift) & (kSubs - 1));     // the largest first
         atomicAdd(&s.counts[sub], 1u);
         if (!by_count)
-          atomicAdd(&s.sums[sub], fixed_below(o, t_of(logit_of(k), o.c16), first));
+          atomicAdd(&s.sums[sub], fixed_below(o, t_of(logit_of(k), o.scale), first));
       }
     });
     __syncthreads();
@@ -555,51 +546,158 @@ __device__ u64 select(const SampleArgs& a, const RowInfo& o, const void* row, Sc
   }
 }
 
+// The cuts among the n <= kRanked tokens of the list, all of them at once: every token's
+// place in the order by counting those before it (two threads to a token where they
+// are few), the masses before it by a running sum in that order.
+struct Cut {
+  u64 end;          // key of the last token kept (~0: none of these)
+  u64 best, sum;    // the race among those kept, and their mass in fixed point
+};
+__device__ __forceinline__ Cut cut_ranked(const SampleArgs& a, const RowInfo& o, int b, Scratch& s, int n) {
+  const int tid = threadIdx.x;
+  u64* sorted = s.sums;
+  const int parts = n <= kThreads / 2 ? 2 : 1, own = tid % (kThreads / parts), part = tid / (kThreads / parts);
+  const u64 key = own < n ? s.list[own] : 0;
+  const float* noise = a.noise ? a.noise + (int64_t)b * a.vocab : nullptr;
+  float e = 0.0f;
+  if (noise && own < n && part == 0) e = noise[(int)~(uint32_t)key];
+  if (tid < n) s.counts[tid] = 0;
+  if (tid == 0 && n % 2) s.list[n] = 0;      // (read in pairs)
+  __syncthreads();
+  if (own < n) {
+    const int pairs = (n + 1) / 2, half = (pairs + parts - 1) / parts;
+    uint32_t before = 0;
+    for (int j = part * half; j < min((part + 1) * half, pairs); ++j) {
+      const u64 x = s.list[2 * j], y = s.list[2 * j + 1];
+      before += (x > key ? 1u : 0u) + (y > key ? 1u : 0u);
+    }
+    atomicAdd(&s.counts[own], before);
+  }
+  __syncthreads();
+  float* sorted_noise = (float*)(sorted + kRanked);
+  if (own < n && part == 0) {
+    const uint32_t at = s.counts[own];
+    sorted[at] = key;
+    sorted_noise[at] = e;
+  }
+  __syncthreads();
+  const bool here = tid < n;
+  const u64 k = here ? sorted[tid] : 0;
+  const double t = here ? t_of(logit_of(k), o.scale) : 0.0, bin = here ? bin_of(o, t) : INFINITY;
+  const u64 mass = here ? fixed_below(o, t, o.first) : 0;
+  bool kept = here && bin <= o.last;
+  double target = o.target;
+  if (o.by_k) {
+    const int ahead = __syncthreads_count(here && bin < o.bin_k);
+    const bool of_k = here && (bin < o.bin_k || tid - ahead < o.left_k);
+    kept &= of_k;
+    if (o.by_p)
+      target *= o.before_k +
+                ldexp((double)block_add(of_k && bin == o.bin_k ? mass : 0, s.red), -kFixBits) * exp2(-o.first * (1.0 / kPer));
+  }
+  if (o.by_p) {
+    const u64 to = block_run(mass, s.red);
+    kept &= o.before + ldexp((double)(to - mass), -kFixBits) * exp2(-o.first * (1.0 / kPer)) < target;
+  }
+  const int many = __syncthreads_count(kept);
+  Cut c;
+  c.end = many > 0 ? sorted[many - 1] : ~0ull;
+  c.best = c.sum = 0;
+  if (kept && t - o.tm >= o.lim) {
+    const float w = weight_of(t - o.tm);
+    c.sum = (u64)((double)w * 0x1p40);
+    if (noise) c.best = race_key(w, sorted_noise[tid], (int)~(uint32_t)k);
+  }
+  return c;
+}
+
+// The same for any number of tokens, by selections.
 template <bool F16>
+__device__ Cut cut_selected(const SampleArgs& a, const RowInfo& o, const void* row, int b, Scratch& s) {
+  Cut c = {0, 0, 0};
+  double target = o.target;
+  if (o.by_k) {
+    c.end = select<F16>(a, o, row, s, o.bin_k, o.bin_k, true, (uint32_t)o.left_k, 0);
+    if (o.by_p) {
+      // What top-k left of its bin, and with it top-p's mass.
+      u64 part = 0;
+      each<F16>(a, o, row, s, [&](u64 k) {
+        const double t = t_of(logit_of(k), o.scale);
+        if (bin_of(o, t) == o.bin_k && k >= c.end) part += fixed_below(o, t, o.bin_k);
+      });
+      part = block_add(part, s.red);
+      target *= o.before_k + ldexp((double)part, -kFixBits) * exp2(-o.bin_k * (1.0 / kPer));
+    }
+  }
+  if (o.by_p) {
+    const double left = (target - o.before) * exp2(o.first * (1.0 / kPer));     // in units of the bins' upper edge
+    const u64 mass = left > 0.0 ? (u64)fmin(ceil(left * (double)(1ull << kFixBits)), 0x1p62) : 1;
+    const u64 by_p = select<F16>(a, o, row, s, o.first, o.last, false, 0, mass);
+    c.end = c.end > by_p ? c.end : by_p;
+  }
+  each<F16>(a, o, row, s, [&](u64 k) {
+    const double t = t_of(logit_of(k), o.scale);
+    if (k >= c.end && bin_of(o, t) >= o.first && t - o.tm >= o.lim) {
+      const float w = weight_of(t - o.tm);
+      const int j = (int)~(uint32_t)k;
+      c.sum += (u64)((double)w * 0x1p40);     // (a sum in fixed point has no order, as the list has none)
+      if (a.noise) {
+        const u64 v = race_key(w, a.noise[(int64_t)b * a.vocab + j], j);
+        c.best = c.best > v ? c.best : v;
+      }
+    }
+  });
+  return c;
+}
+
+template <bool F16, int EACH>
 __global__ void __launch_bounds__(kThreads) sample_race_kernel(SampleArgs a) {
   __shared__ Scratch s;
   const int b = blockIdx.x / a.shares, share = blockIdx.x % a.shares, tid = threadIdx.x;
+  const void* row = row_of(a, b);
+  const int beg = share * EACH * kThreads, end = min(beg + EACH * kThreads, a.vocab);
+  float l[EACH];
+  if (row) load_share<F16, EACH>(row, beg, end, l);     // (requested before the row's kind is known)
   RowInfo* info = (RowInfo*)((char*)a.info + (int64_t)b * kSampleInfoBytes);
   const RowInfo o = *info;
   if (o.kind != kRace) return;
-  const void* row = row_of(a, b);
-  const int beg = share * kSampleShare, end = min(beg + kSampleShare, a.vocab);
-  float l[kEach];
-  load_share<F16>(row, beg, end, l);
   if (tid == 0) s.listed = 0;
   __syncthreads();
   // Noise is read where a token is kept: elsewhere the load is out of its buffer.
   const __amdgpu_buffer_rsrc_t noise =
       make_rsrc(a.noise ? a.noise + (int64_t)b * a.vocab : nullptr, a.noise ? (uint32_t)a.vocab * 4u : 0u);
-  float e[kEach];
-  uint32_t kept = 0;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const double t = t_of(l[i], o.c16);
-    const double bin = bin_of(o, t);
-    const bool sure = valid(l[i]) && bin < o.first && t - o.tm >= o.lim;
-    kept |= (uint32_t)sure << i;
-    const bool listed = !o.heavy && valid(l[i]) && ((bin >= o.first && bin <= o.last) || bin == o.bin_k);
-    if (listed) {
-      const uint32_t at = atomicAdd(&s.listed, 1u);
-      if (at < kSampleList) s.list[at] = key_of(l[i], place(beg, i));
-    }
-    const uint32_t off = sure && a.noise ? 4u * (uint32_t)place(beg, i) : kOutOfRange;
-    e[i] = bits_float(__builtin_amdgcn_raw_buffer_load_b32(noise, off, 0, 0));
-  }
   u64 best = 0;
   double sum = 0.0;
-  if (__any(kept != 0)) {
+  bool some = false;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (kept >> i & 1) {
-        const float w = weight_of(t_of(l[i], o.c16) - o.tm);
-        sum += (double)w;
-        if (a.noise) {
-          const u64 k = race_key(w, e[i], place(beg, i));
-          best = best > k ? best : k;
-        }
+  for (int i = 0; i < EACH; ++i) some |= l[i] >= o.low;
+  if (__any(some)) {
+    float e[EACH];
+    uint32_t kept = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const double t = t_of(l[i], o.scale), bin = bin_of(o, t);
+      const bool sure = valid(l[i]) && bin < o.first && t - o.tm >= o.lim;
+      kept |= (uint32_t)sure << i;
+      if (!o.heavy && valid(l[i]) && ((bin >= o.first && bin <= o.last) || bin == o.bin_k)) {
+        const uint32_t at = atomicAdd(&s.listed, 1u);
+        if (at < kSampleList) s.list[at] = key_of(l[i], place(beg, i));
       }
+      const uint32_t off = sure && a.noise ? 4u * (uint32_t)place(beg, i) : kOutOfRange;
+      e[i] = bits_float(__builtin_amdgcn_raw_buffer_load_b32(noise, off, 0, 0));
+    }
+    if (__any(kept != 0)) {
+#pragma unroll
+      for (int i = 0; i < EACH; ++i)
+        if (kept >> i & 1) {
+          const float w = weight_of(t_of(l[i], o.scale) - o.tm);
+          sum += (double)w;
+          if (a.noise) {
+            const u64 k = race_key(w, e[i], place(beg, i));
+            best = best > k ? best : k;
+          }
+        }
+    }
   }
   best = block_max(best, s.red);
   sum = block_all(sum, s.redd, [](double x, double y) { return x + y; });
@@ -607,7 +705,6 @@ __global__ void __launch_bounds__(kThreads) sample_race_kernel(SampleArgs a) {
   ShareInfo* mine = a.share + (int64_t)b * a.shares + share;
   u64* list = a.list + (int64_t)b * kSampleList;
   if (a.shares > 1 && listed > 0) {
-    __syncthreads();
     if (tid == 0) s.found_count = add_dev_u32(&info->listed, listed);
     __syncthreads();
     for (uint32_t i = tid; i < listed; i += kThreads)
@@ -619,58 +716,30 @@ __global__ void __launch_bounds__(kThreads) sample_race_kernel(SampleArgs a) {
   }
   if (!last_of_row(a, b, &s.arrived)) return;
 
-  ShareInfo* all = a.share + (int64_t)b * a.shares;
   best = 0;
   sum = 0.0;
-  for (int i = tid; i < a.shares; i += kThreads) {
-    const u64 v = ld64(&all[i].best);
-    best = best > v ? best : v;
+  uint32_t n = 0;
+  const bool cuts = o.by_k || o.by_p;
+  if (cuts && a.shares > 1) n = ld_dev_u32(&info->listed);
+  if (tid < a.shares) {
+    const ShareInfo* from = a.share + (int64_t)b * a.shares + tid;
+    best = ld64(&from->best);
+    sum = __longlong_as_double((long long)ld64(&from->number));
   }
-  for (int i = 0; i < a.shares; ++i) sum += __longlong_as_double((long long)ld64(&all[i].number));   // (in order)
+  if (cuts && a.shares > 1) {
+    n = min(n, (uint32_t)kSampleList);
+    for (uint32_t i = tid; i < n; i += kThreads) s.list[i] = ld64(&list[i]);
+    if (tid == 0) s.listed = n;
+  }
+  sum = block_all(sum, s.redd, [](double x, double y) { return x + y; });     // (always in the same order)
   u64 last = 0;
-  if (o.by_k || o.by_p) {
-    if (a.shares > 1) {
-      const uint32_t n = min(ld_dev_u32(&info->listed), (uint32_t)kSampleList);
-      for (uint32_t i = tid; i < n; i += kThreads) s.list[i] = ld64(&list[i]);
-      if (tid == 0) s.listed = n;
-    }
+  if (cuts) {
     __syncthreads();
-    double target = o.target;
-    if (o.by_k) {
-      last = select<F16>(a, o, row, s, o.bin_k, o.bin_k, true, (uint32_t)o.left_k, 0);
-      if (o.by_p) {
-        // What top-k left of its bin, and with it top-p's mass.
-        u64 part = 0;
-        each<F16>(a, o, row, s, [&](u64 k) {
-          const double t = t_of(logit_of(k), o.c16);
-          if (bin_of(o, t) == o.bin_k && k >= last) part += fixed_below(o, t, o.bin_k);
-        });
-        part = block_add(part, s.red);
-        target *= o.before_k + ldexp((double)part, -kFixBits) * exp2(-o.bin_k * 0.0625);
-      }
-    }
-    if (o.by_p) {
-      const double left = (target - o.before) * exp2(o.first * 0.0625);     // in units of the bins' upper edge
-      const u64 mass = left > 0.0 ? (u64)fmin(ceil(left * (double)(1ull << kFixBits)), 0x1p62) : 1;
-      const u64 by_p = select<F16>(a, o, row, s, o.first, o.last, false, 0, mass);
-      last = last > by_p ? last : by_p;
-    }
-    // The tokens of these bins that are kept.
-    u64 more = 0, more_sum = 0;
-    each<F16>(a, o, row, s, [&](u64 k) {
-      const double t = t_of(logit_of(k), o.c16);
-      if (k >= last && bin_of(o, t) >= o.first && t - o.tm >= o.lim) {
-        const float w = weight_of(t - o.tm);
-        const int j = (int)~(uint32_t)k;
-        more_sum += (u64)((double)w * 0x1p40);     // (a sum in fixed point has no order, as the list has none)
-        if (a.noise) {
-          const u64 v = race_key(w, a.noise[(int64_t)b * a.vocab + j], j);
-          more = more > v ? more : v;
-        }
-      }
-    });
-    best = best > more ? best : more;
-    sum += ldexp((double)block_add(more_sum, s.red), -40);
+    n = s.listed;
+    const Cut c = !o.heavy && n <= kRanked ? cut_ranked(a, o, b, s, (int)n) : cut_selected<F16>(a, o, row, b, s);
+    last = c.end;
+    best = best > c.best ? best : c.best;
+    sum += ldexp((double)block_add(c.sum, s.red), -40);
   }
   best = block_max(best, s.red);
   if (tid == 0) {
@@ -682,52 +751,63 @@ __global__ void __launch_bounds__(kThreads) sample_race_kernel(SampleArgs a) {
 
 // -------------------------------------------------------------- third launch
 
-template <bool F16>
+template <bool F16, int EACH>
 __global__ void __launch_bounds__(kThreads) sample_probs_kernel(SampleArgs a) {
   const int b = blockIdx.x / a.shares, share = blockIdx.x % a.shares;
+  const void* row = row_of(a, b);
+  const int beg = share * EACH * kThreads, end = min(beg + EACH * kThreads, a.vocab);
+  float l[EACH], p[EACH];
+  if (row) load_share<F16, EACH>(row, beg, end, l);
   const RowInfo o = *(const RowInfo*)((const char*)a.info + (int64_t)b * kSampleInfoBytes);
-  const int beg = share * kSampleShare, end = min(beg + kSampleShare, a.vocab);
-  float l[kEach];
-  if (o.kind == kRace) load_share<F16>(row_of(a, b), beg, end, l);
-  const float inv = (float)o.inv;
-  float p[kEach];
+  bool some = false;
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int j = place(beg, i);
-    if (o.kind == kRace) {
-      const double x = t_of(l[i], o.c16) - o.tm;
-      p[i] = valid(l[i]) && x >= o.lim && key_of(l[i], j) >= o.end ? weight_of(x) * inv : 0.0f;
-    } else {
-      p[i] = j == o.token ? 1.0f : 0.0f;
+  for (int i = 0; i < EACH; ++i) {
+    if (o.kind == kRace) some |= l[i] >= o.low;
+    p[i] = o.kind == kOne && place(beg, i) == o.token ? 1.0f : 0.0f;
+  }
+  if (__any(some)) {
+    const float inv = (float)o.inv;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const double behind = t_of(l[i], o.scale) - o.tm;
+      if (valid(l[i]) && behind >= o.lim && key_of(l[i], place(beg, i)) >= o.end) p[i] = weight_of(behind) * inv;
     }
   }
   float* out = a.probs + (int64_t)b * a.vocab;
-  if (end - beg == kSampleShare) {
+  if (end - beg == EACH * kThreads) {
 #pragma unroll
-    for (int i = 0; i < kEach; i += 4) *(f4u_t*)(out + place(beg, i)) = f4u_t{p[i], p[i + 1], p[i + 2], p[i + 3]};
+    for (int i = 0; i < EACH; i += 4) *(f4u_t*)(out + place(beg, i)) = f4u_t{p[i], p[i + 1], p[i + 2], p[i + 3]};
   } else {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i)
+    for (int i = 0; i < EACH; ++i)
       if (place(beg, i) < end) out[place(beg, i)] = p[i];
   }
 }
 
-template <bool F16>
+template <bool F16, int EACH>
 hipError_t launch(const SampleArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)(a.batch * a.shares)), block(kThreads);
-  sample_bins_kernel<F16><<<grid, block, 0, s>>>(a);
-  if (!a.only_first) sample_race_kernel<F16><<<grid, block, 0, s>>>(a);
-  if (a.probs) sample_probs_kernel<F16><<<grid, block, 0, s>>>(a);
+  sample_bins_kernel<F16, EACH><<<grid, block, 0, s>>>(a);
+  if (!a.only_first) sample_race_kernel<F16, EACH><<<grid, block, 0, s>>>(a);
+  if (a.probs) sample_probs_kernel<F16, EACH><<<grid, block, 0, s>>>(a);
   return hipGetLastError();
+}
+
+template <bool F16>
+hipError_t launch_share(const SampleArgs& a, hipStream_t s) {
+  return a.share_tokens == 8 * kThreads ? launch<F16, 8>(a, s) : launch<F16, 16>(a, s);
 }
 
 }  // namespace
 
-// Rows of one group: as many as the header has counters for, and shares whose
-// histograms take no more than 64 MiB.
+// Shares of 8192 tokens (4096 where the batch has few), as many of a row as a
+// workgroup has threads; rows of one group: as many as the header has counters for, and
+// shares whose bins take no more than 128 MiB.
 SampleShape sample_shape(const spear_sample_desc_t& d) {
   SampleShape s;
-  s.shares = (int)ceil_div(d.vocab, kSampleShare);
+  const int64_t large = kSampleLeast * 2;
+  s.share_tokens = (int)(d.batch * ceil_div(d.vocab, kSampleLeast) <= 512 ? kSampleLeast : large);
+  s.shares = (int)ceil_div(d.vocab, s.share_tokens);
   s.group = (int)std::max<int64_t>(1, std::min<int64_t>(d.batch, std::min<int64_t>(kMaxEcTiles, 4096 / s.shares)));
   size_t at = kSyncHeaderBytes;
   const size_t shares = (size_t)s.group * s.shares;
@@ -744,7 +824,7 @@ SampleShape sample_shape(const spear_sample_desc_t& d) {
 }
 
 hipError_t launch_sample(const SampleArgs& a, void* stream) {
-  return a.f16 ? launch<true>(a, (hipStream_t)stream) : launch<false>(a, (hipStream_t)stream);
+  return a.f16 ? launch_share<true>(a, (hipStream_t)stream) : launch_share<false>(a, (hipStream_t)stream);
 }
 
 }  // namespace spear

@@ -185,8 +185,8 @@ struct AdapterArgs {
 hipError_t launch_adapter(const AdapterArgs& a, void* stream);
 
 // The draw of next tokens.
-constexpr int kSampleShare = 8192;      // tokens of the vocabulary that a workgroup takes
-constexpr int kSampleList = 4096;       // tokens of the bins that are cut, gathered for the row's last workgroup
+constexpr int kSampleLeast = 4096;      // tokens of the vocabulary that a workgroup takes, or twice as many
+constexpr int kSampleList = 4094;       // tokens of the bins that are cut, gathered for the row's last workgroup
 constexpr int kSampleInfoBytes = 256;
 struct ShareInfo {
   unsigned long long best;              // the largest (logit, token); then of (score, token)
@@ -194,12 +194,12 @@ struct ShareInfo {
   unsigned long long used;              // bins written
 };
 struct SampleShape {
-  int shares, group;                    // workgroups of a row, rows of a launch
+  int share_tokens, shares, group;      // tokens of a workgroup, workgroups of a row, rows of a launch
   size_t info, share, list, hist, bytes;
 };
 SampleShape sample_shape(const spear_sample_desc_t& d);
 struct SampleArgs {
-  int32_t batch, vocab, shares, num_rows;
+  int32_t batch, vocab, share_tokens, shares, num_rows;
   int32_t first;                        // the group's first draw: row `first` + b where no rows are given
   bool f16, only_first;                 // only_first: every row keeps its first token alone
   const void* logits;

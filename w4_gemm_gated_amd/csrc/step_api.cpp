@@ -192,7 +192,7 @@ spear_status_t spear_sample(const spear_sample_desc_t* desc, const void* logits,
   if (st != SPEAR_OK) return st;
   char* ws = (char*)workspace;
   SampleArgs a;
-  a.vocab = desc->vocab; a.shares = s.shares; a.num_rows = desc->num_rows;
+  a.vocab = desc->vocab; a.share_tokens = s.share_tokens; a.shares = s.shares; a.num_rows = desc->num_rows;
   a.f16 = f16; a.only_first = one;
   a.logits = logits; a.stride = row_stride;
   a.one_temperature = desc->temperature; a.one_top_k = desc->top_k; a.one_top_p = desc->top_p; a.one_min_p = desc->min_p;
