@@ -191,7 +191,8 @@ constexpr int kSampleInfoBytes = 256;
 struct ShareInfo {
   unsigned long long best;              // the largest (logit, token); then of (score, token)
   unsigned long long number;            // a double: the place of its first bin; then the mass of what is kept
-  unsigned long long used;              // bins written
+  unsigned long long mass;              // a double: of all its tokens
+  unsigned long long used;              // tokens and bins written
 };
 struct SampleShape {
   int share_tokens, shares, group;      // tokens of a workgroup, workgroups of a row, rows of a launch
