@@ -3,23 +3,26 @@
 //
 // The rules keep a prefix of the tokens in falling order of their logits, so what
 // has to be found is where that order is cut: no sort of the vocabulary is needed,
-// only the counts and sums of weights above a value.  A row's vocabulary is shared by
-// workgroups, in two launches (three for probabilities):
+// only the counts and sums of weights above a value.  Launches:
 //
-//   1. Every share finds its maximum and, for top-k and top-p, a histogram of its
-//      weights: 32 bins to a power of two, on one grid for the whole row
-//      (t = 32 logit / (T ln 2); bin floor(t)), so that shares need no common
-//      maximum first and the row is read once.  A bin holds its count and the sum of
-//      its weights' distances from the bin's upper edge in fixed point, both in one
-//      64-bit integer (one LDS atomic a token; integer sums have no order).  The
-//      row's last share to arrive adds the histograms, sums counts and weights from the
-//      top, and finds the bin in which each rule's cut lies.
-//   2. Tokens above that bin are drawn from at once (an exponential race: the largest
-//      weight / noise, ties to the lowest index), those in it (up to some hundreds) go
-//      to a list; noise is read for tokens that are kept, and for no others.  The last
-//      share to arrive sorts the list by (logit, index), cuts it by a running sum, ends the
-//      race, and sums what is kept.
-//   3. Probabilities are written.
+//   bins   A workgroup a share of a row: its maximum and, for top-k and top-p, a
+//          histogram of its weights: 32 bins to a power of two, on one grid for the
+//          whole row (t = 32 logit / (T ln 2); bin floor(t)), so that shares need no
+//          common maximum first and the row is read once.  A bin holds its count and
+//          the sum of its weights' distances from the bin's upper edge in fixed point,
+//          both in one 64-bit integer (one LDS atomic a token; integer sums have no
+//          order).
+//   cuts   A workgroup a row: adds the shares' bins from the top until they hold what
+//          the rules ask for, finds the bin in which each rule's cut lies, and turns the
+//          limits on t into limits on the logit, which cost the next launches one
+//          comparison a token.
+//   race   A workgroup a part of a row: tokens above that bin are drawn from at once (an
+//          exponential race: the largest weight / noise, ties to the lowest index),
+//          those in it (up to some hundreds) go to a list; noise is read where tokens are
+//          kept or listed, and nowhere else.
+//   end    A workgroup a row: sorts the list by (logit, index), cuts it by a running
+//          sum, ends the race, and sums what is kept.
+//   probs  Probabilities, if they are asked for.
 //
 // The sums decide which token is the last one, and in a flat distribution that token
 // has a millionth of the total: weights enter the sums to 2^-34 of themselves, and
@@ -39,12 +42,11 @@ namespace {
 constexpr int kThreads = 512, kWaves = kThreads / kWave;
 constexpr int kPer = 32;                          // bins in a power of two
 constexpr int kBins = 128 * kPer;
-constexpr int kBinsEach = kBins / kThreads;
 constexpr double kCut = -126.0 * kPer;            // weights below 2^-126 of the largest are zero
 constexpr int kDefBits = 37;                      // fixed point of a bin's sum of distances
 constexpr int kFixBits = 40;                      // fixed point of weights in a selection
-constexpr int kRanked = kThreads;                 // tokens that are sorted by counting
-constexpr int kStaged = 2 * kRanked;              // tokens of the list that a share gathers in LDS
+constexpr int kRanked = kThreads / 2;             // tokens that are sorted by counting
+constexpr int kStaged = 1024;                 // tokens of the list that a share gathers in LDS
 constexpr int kSubs = 1024, kSubBits = 10;        // sub-bins of a selection's step
 constexpr double kLn2 = 0.693147180559945309417;
 typedef float f4_t __attribute__((ext_vector_type(4)));
@@ -93,10 +95,33 @@ __device__ __forceinline__ double t_of(float l, double scale) { return fmin((dou
 // The bin of a logit, from the one of the row's largest: whole numbers, exact wherever
 // two bins are near each other.
 __device__ __forceinline__ double bin_of(const RowInfo& o, float l) { return o.q - floor(t_of(l, o.scale)); }
-// A weight in units of the upper edge of bin `bin`, in fixed point.
-__device__ __forceinline__ u64 fixed_below(const RowInfo& o, float l, int bin) {
-  const double x = ((t_of(l, o.scale) - o.q) + (bin - 1.0)) * (1.0 / kPer);
-  return (u64)(exp2(x) * (double)(1ull << kFixBits));
+// 2^(-i / kPer)
+__device__ const double kSteps[kPer] = {
+    1.0, 0.9785720620877001, 0.9576032806985737, 0.93708381705515,
+    0.9170040432046712, 0.8973545375015536, 0.8781260801866497, 0.859309649061239,
+    0.8408964152537145, 0.8228777390769825, 0.8052451659746271, 0.7879904225539432,
+    0.7711054127039704, 0.7545822137967114, 0.7384130729697497, 0.7225904034885233,
+    0.7071067811865476, 0.691954940981916, 0.6771277734684463, 0.6626183215798707,
+    0.6484197773255048, 0.6345254785958666, 0.620928906036742, 0.6076236799902345,
+    0.5946035575013605, 0.5818624293887887, 0.5693943173783458, 0.5571933712979462,
+    0.5452538663326288, 0.5335702003384118, 0.5221368912137069, 0.5109485743270583};
+
+// The weight at the upper edge of a bin.  (`steps`: kSteps in LDS, a round trip to memory less.)
+__device__ __forceinline__ double edge_of(const double* steps, int bin) {
+  return steps[bin % kPer] * __longlong_as_double((long long)(1023 - bin / kPer) << 52);
+}
+// The distance of a weight from its bin's upper edge, 1 - e^-u with u = ln 2 / kPer below
+// `in` = t - floor(t), times 2^kDefBits: u in 64 bits, the rest is below 2^-12.
+__device__ __forceinline__ double distance(double in) {
+  const double u = (1.0 - in) * (kLn2 / kPer);
+  const float s = (float)u, h = s * s * (0.5f - s * (1.0f / 6.0f - s * (1.0f / 24.0f)));
+  return __builtin_fma(u, (double)(1ull << kDefBits), -(double)(h * (float)(1ull << kDefBits)));
+}
+// A weight in units of the upper edge of bin `bin`, its own or one above it, in fixed point.
+__device__ __forceinline__ u64 fixed_below(const RowInfo& o, const double* steps, float l, int bin) {
+  const double t = t_of(l, o.scale), f = floor(t);
+  const double w = (double)(1ull << kFixBits) - distance(t - f) * (double)(1 << (kFixBits - kDefBits));
+  return (u64)(w * edge_of(steps, min((int)(o.q - f) - bin, kBins - 1)));
 }
 // The weight relative to the row's largest, as fp32: the exponent's whole part apart, so
 // that the rest is exact to a few 2^-24.  (The difference of the logits first: that of
@@ -241,141 +266,58 @@ __device__ __forceinline__ Rules rules_of(const SampleArgs& a, int b) {
   return r;
 }
 
+__device__ __forceinline__ double scale_of(const Rules& r) { return fmax((double)kPer / ((double)r.t * kLn2), 1e-300); }
+
 __device__ __forceinline__ const void* row_of(const SampleArgs& a, int b) {
   const int64_t r = a.rows ? a.rows[b] : a.first + b;
   if (r < 0 || r >= a.num_rows) return nullptr;
   return (const char*)a.logits + r * a.stride * (a.f16 ? 2 : 4);
 }
 
-__device__ __forceinline__ u64 ld64(const u64* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-__device__ __forceinline__ void st64(u64* p, u64 v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-
-// Whether this workgroup is the last of its row's; the counter is then zero again.
-__device__ __forceinline__ bool last_of_row(const SampleArgs& a, int b, uint32_t* arrived) {
-  drain_vm();
-  __syncthreads();
-  if (a.shares == 1) return true;
-  if (threadIdx.x == 0) *arrived = add_dev_u32(&a.counters[b], 1u);
-  __syncthreads();
-  if (*arrived != (uint32_t)a.shares - 1) return false;
-  if (threadIdx.x == 0) st_dev_u32(&a.counters[b], 0u);
-  return true;
-}
-
 // -------------------------------------------------------------- first launch
 
-// 2^(-i / kPer)
-__device__ const double kSteps[kPer] = {
-    1.0, 0.9785720620877001, 0.9576032806985737, 0.93708381705515,
-    0.9170040432046712, 0.8973545375015536, 0.8781260801866497, 0.859309649061239,
-    0.8408964152537145, 0.8228777390769825, 0.8052451659746271, 0.7879904225539432,
-    0.7711054127039704, 0.7545822137967114, 0.7384130729697497, 0.7225904034885233,
-    0.7071067811865476, 0.691954940981916, 0.6771277734684463, 0.6626183215798707,
-    0.6484197773255048, 0.6345254785958666, 0.620928906036742, 0.6076236799902345,
-    0.5946035575013605, 0.5818624293887887, 0.5693943173783458, 0.5571933712979462,
-    0.5452538663326288, 0.5335702003384118, 0.5221368912137069, 0.5109485743270583};
-
-// The weight at the upper edge of a bin, and a bin's mass.
-__device__ __forceinline__ double edge_of(int bin) {
-  return kSteps[bin % kPer] * __longlong_as_double((long long)(1023 - bin / kPer) << 52);
-}
-__device__ __forceinline__ double mass_of(int bin, uint32_t n, u64 def) {
-  return edge_of(bin) * ((double)n - (double)def * (1.0 / (double)(1ull << kDefBits)));
+// (`step`: kSteps of the bin, the same for all of a thread's)
+static_assert(kThreads % kPer == 0, "a thread's bins have one place in their powers of two");
+__device__ __forceinline__ double mass_of(int bin, double step, uint32_t n, u64 def) {
+  return step * __longlong_as_double((long long)(1023 - bin / kPer) << 52) * ((double)n - (double)def * (1.0 / (double)(1ull << kDefBits)));
 }
 constexpr double kNear = 0x1p-30;     // a mass this near to a target may lie on either side of it
 
-template <bool F16, int EACH>
-__global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
-  // One share's bins; then the row's: the mass up to and with each bin.
-  __shared__ __attribute__((aligned(16))) u64 hist[kBins];
-  __shared__ u64 red[kWaves];
-  __shared__ double redd[kWaves];
-  __shared__ uint32_t redc[kWaves];
-  __shared__ short share_off[kThreads], share_used[kThreads];
-  __shared__ uint32_t arrived, tokens_all, found_before;
-  __shared__ int found;
-  __shared__ float limits[6];
-  const int b = blockIdx.x / a.shares, share = blockIdx.x % a.shares, tid = threadIdx.x;
-  const Rules r = rules_of(a, b);
-  const void* row = row_of(a, b);
-  const bool bins = !r.one && (r.k > 0 || r.p < 1.0f);
-  const int beg = share * EACH * kThreads, end = min(beg + EACH * kThreads, a.vocab);
-  float l[EACH];
-  u64 best = 0;
-  uint32_t least = ~0u;
-  if (row) load_share<F16, EACH>(row, beg, end, a.vocab, l);
-  if (bins)
-    for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-  if (row) {
-    float top = -INFINITY, low = INFINITY;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-      if (l[i] > top) {
-        top = l[i];
-        at = place(beg, i);
-      }
-      if (valid(l[i])) low = fminf(low, l[i]);
-    }
-    if (valid(top)) {
-      best = key_of(top, at);
-      least = rising(low);
-    }
-  }
-  best = block_max(best, red);
-  const double scale = fmax((double)kPer / ((double)r.t * kLn2), 1e-300);
-  ShareInfo* mine = a.share + (int64_t)b * a.shares + share;
-  if (bins && best != 0) {
-    least = block_all(least, redc, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
-    const double q = floor(t_of(logit_of(best), scale));
-#pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-      const double t = t_of(l[i], scale), f = floor(t), rel = q - f;
-      if (valid(l[i]) && rel < kBins) {
-        // The weight's distance from the bin's upper edge, 1 - e^-u: u in 64 bits, the rest is below 2^-12.
-        const double u = (1.0 - (t - f)) * (kLn2 / kPer);
-        const float s = (float)u, h = s * s * (0.5f - s * (1.0f / 6.0f - s * (1.0f / 24.0f - s * (1.0f / 120.0f))));
-        const double d = __builtin_fma(u, (double)(1ull << kDefBits), -(double)(h * (float)(1ull << kDefBits)));
-        atomicAdd(&hist[(int)rel], ((u64)(1u << 16) << 32) | (uint32_t)d);
-      }
-    }
-    const double span = q - floor(t_of(logit_of((u64)least << 32), scale)) + 1.0;
-    const int used = span < kBins ? (int)span : kBins;
-    u64* bins_out = a.hist + ((int64_t)b * a.shares + share) * kBins;
-    __syncthreads();
-    // The bins, and their sums: those of the row come from the shares' own.
-    double mass = 0.0;
-    uint32_t n = 0;
-    for (int i = tid; i < used; i += kThreads) {
-      const u64 v = hist[i];
-      st64(&bins_out[i], v);
-      mass += mass_of(i, (uint32_t)(v >> 48), v & ((1ull << 48) - 1));
-      n += (uint32_t)(v >> 48);
-    }
-    mass = block_all(mass, redd, [](double x, double y) { return x + y; });
-    n = block_all(n, redc, [](uint32_t x, uint32_t y) { return x + y; });
-    if (tid == 0) {
-      st64(&mine->number, (u64)__double_as_longlong(q));
-      st64(&mine->mass, (u64)__double_as_longlong(mass));
-      st64(&mine->used, (u64)n << 32 | (u64)used);
-    }
-  }
-  if (tid == 0) st64(&mine->best, best);
-  if (!last_of_row(a, b, &arrived)) return;
+struct BinsScratch {
+  u64 hist[kBins];
+  u64 red[kWaves];
+  double redd[kWaves];
+  uint32_t redc[kWaves];
+};
+struct CutScratch {
+  double mass_to[kBins];        // the row's mass up to and with each bin
+  double steps[kPer];
+  double redd[kWaves];
+  uint32_t redc[kWaves];
+  short share_off[kSampleShares], share_used[kSampleShares];
+  uint32_t tokens_all, found_before;
+  int found;
+  float limits[6];
+};
 
+// From a row's shares, when all of them are there: its largest, and the bins in which
+// the cuts lie.
+__device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rules& r, double scale, double step,
+                                          CutScratch& s) {
+  const int tid = threadIdx.x;
+  const bool bins = !r.one && (r.k > 0 || r.p < 1.0f);
   // The row: its largest, ..
-  static_assert((1 << 22) / (2 * kSampleLeast) <= kThreads, "a thread for every share");
-  u64 number = 0, used = 0, mass_bits = 0;
-  best = 0;
-  if (tid < a.shares) {
-    const ShareInfo* from = a.share + (int64_t)b * a.shares + tid;
-    best = ld64(&from->best);
-    number = ld64(&from->number);
-    used = ld64(&from->used);
-    mass_bits = ld64(&from->mass);
+  // (every wave for itself: a share a lane, or several)
+  const ShareInfo* shares = a.share + (int64_t)b * a.shares;
+  const int lane = tid % kWave;
+  ShareInfo mine = shares[min(lane, a.shares - 1)];
+  u64 best = mine.best;
+  for (int i = lane + kWave; i < a.shares; i += kWave) best = best > shares[i].best ? best : shares[i].best;
+#pragma unroll
+  for (int o = kWave / 2; o > 0; o /= 2) {
+    const u64 v = __shfl_xor(best, o);
+    best = best > v ? best : v;
   }
-  const bool any = best != 0;
-  best = block_max(best, red);
   RowInfo* info = (RowInfo*)((char*)a.info + (int64_t)b * kSampleInfoBytes);
   static_assert(sizeof(RowInfo) <= kSampleInfoBytes, "room for it");
   const float largest = logit_of(best);
@@ -401,66 +343,77 @@ __global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
   }
   if (bins) {
     // .. the shares' places and sums, ..
-    const double behind = o.q - __longlong_as_double((long long)number);
-    const bool near = any && behind < kBins;
-    const int off = near ? (int)behind : 0, have = near ? (int)(uint32_t)used : 0;
-    if (tid < a.shares) {
-      share_off[tid] = (short)off;
-      share_used[tid] = (short)have;
+    double total = 0.0;
+    uint32_t tokens = 0;
+    int rows = 0;        // bins of the row
+    for (int i = lane; i < a.shares; i += kWave) {
+      if (i >= kWave) mine = shares[i];
+      const double behind = o.q - __longlong_as_double((long long)mine.number);
+      const bool near = mine.best != 0 && behind < kBins;
+      const int off = near ? (int)behind : 0, have = near ? (int)(uint32_t)mine.used : 0;
+      s.share_off[i] = (short)off;
+      s.share_used[i] = (short)have;
+      total += near ? __longlong_as_double((long long)mine.mass) * edge_of(s.steps, off) : 0.0;
+      tokens += near ? (uint32_t)(mine.used >> 32) : 0u;
+      rows = max(rows, min(off + have, kBins));
     }
-    const double part = near ? __longlong_as_double((long long)mass_bits) * edge_of(off) : 0.0;
-    const double total = block_all(part, redd, [](double x, double y) { return x + y; });
-    const uint32_t tokens = block_all(near ? (uint32_t)(used >> 32) : 0u, redc, [](uint32_t x, uint32_t y) { return x + y; });
-    const int rows = (int)block_max((u64)min(off + have, kBins), red);   // bins of the row
+#pragma unroll
+    for (int o = kWave / 2; o > 0; o /= 2) {
+      total += __shfl_xor(total, o);
+      tokens += __shfl_xor(tokens, o);
+      rows = max(rows, __shfl_xor(rows, o));
+    }
+    __syncthreads();
     const bool by_k = r.k > 0 && (uint32_t)r.k < tokens;
-    // .. and its bins from the top, a thread each, until they hold all that the rules ask for.
+    // .. and its bins from the top, one to a thread, until they hold all that the rules ask
+    // for (one CU reads them: bins that need not be read are time saved).
     const double ask = r.p < 1.0f ? (double)r.p * total * (1.0 + kNear) : 0.0;
     const u64* from = a.hist + (int64_t)b * a.shares * kBins;
     constexpr int kTogether = 8;      // shares whose loads are in flight together
     double mass_before = 0.0;
     uint32_t tokens_before = 0;
-    int turns = 0;
+    int bins_read = 0;
     do {
-      const int bin = turns * kThreads + tid;
+      const int bin = bins_read + tid;
       uint32_t n = 0;
       u64 def = 0;
-      for (int s0 = 0; s0 < a.shares; s0 += kTogether) {
+      for (int i0 = 0; i0 < a.shares; i0 += kTogether) {
         u64 v[kTogether];
 #pragma unroll
-        for (int s = 0; s < kTogether; ++s) {
-          const int of = min(s0 + s, a.shares - 1), at = bin - share_off[of];
-          v[s] = s0 + s < a.shares && at >= 0 && at < share_used[of] ? ld64(&from[(int64_t)of * kBins + at]) : 0;
+        for (int i = 0; i < kTogether; ++i) {
+          const int of = min(i0 + i, a.shares - 1), at = bin - s.share_off[of];
+          v[i] = i0 + i < a.shares && at >= 0 && at < s.share_used[of] ? from[(int64_t)of * kBins + at] : 0;
         }
 #pragma unroll
-        for (int s = 0; s < kTogether; ++s) {
-          n += (uint32_t)(v[s] >> 48);
-          def += v[s] & ((1ull << 48) - 1);
+        for (int i = 0; i < kTogether; ++i) {
+          n += (uint32_t)(v[i] >> 48);
+          def += v[i] & ((1ull << 48) - 1);
         }
       }
-      double mass_to = mass_of(bin, n, def);
+      double mass_to = mass_of(bin, step, n, def);
       uint32_t tokens_to = n;
-      block_run(mass_to, tokens_to, redd, redc);
+      block_run(mass_to, tokens_to, s.redd, s.redc);
       mass_to += mass_before;
       tokens_to += tokens_before;
-      hist[bin] = (u64)__double_as_longlong(mass_to);
+      s.mass_to[bin] = mass_to;
       if (by_k && tokens_to >= (uint32_t)r.k && tokens_to - n < (uint32_t)r.k) {
-        found = bin;
-        found_before = tokens_to - n;
+        s.found = bin;
+        s.found_before = tokens_to - n;
       }
-      if (tid == kThreads - 1) tokens_all = tokens_to;
+      if (tid == kThreads - 1) s.tokens_all = tokens_to;
       __syncthreads();
-      ++turns;
-      mass_before = __longlong_as_double((long long)hist[turns * kThreads - 1]);
-      tokens_before = tokens_all;
+      bins_read += kThreads;
+      mass_before = s.mass_to[bins_read - 1];
+      tokens_before = s.tokens_all;
       __syncthreads();
       // (uniform: all threads have the same sums)
-    } while (turns < kBinsEach && turns * kThreads < rows && (by_k ? tokens_before < (uint32_t)r.k : mass_before < ask));
-    auto mass_up_to = [&](int bin) { return bin < 0 ? 0.0 : __longlong_as_double((long long)hist[bin]); };
+    } while (bins_read < rows && (by_k ? tokens_before < (uint32_t)r.k : mass_before < ask));
+    auto mass_up_to = [&](int bin) { return bin < 0 ? 0.0 : s.mass_to[bin]; };
     int bin_k = kBins, first = kBins, last = kBins;
     double low_sum = total, high_sum = total;
     if (by_k) {
-      bin_k = found;
-      o.left_k = r.k - (int)found_before;
+      bin_k = s.found;
+      o.left_k = r.k - (int)s.found_before;
       o.before_k = o.before = low_sum = mass_up_to(bin_k - 1);
       high_sum = mass_up_to(bin_k);
       first = last = bin_k;
@@ -470,17 +423,17 @@ __global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
       // (As many bins as hold less than a mass up to and with them, and the next one.)
       const double low = (double)r.p * low_sum * (1.0 - kNear), high = (double)r.p * high_sum * (1.0 + kNear);
       int hi = 0, lo = 0;
-      for (int i = 0; i < turns; ++i) {
-        const double m = mass_up_to(i * kThreads + tid);
+      for (int i = 0; i < bins_read; i += kThreads) {
+        const double m = mass_up_to(i + tid);
         hi += __syncthreads_count(m < low);
         lo += __syncthreads_count(m < high);
       }
-      hi = min(hi, turns * kThreads - 1);
+      hi = min(hi, bins_read - 1);
       if (hi <= first) {
         first = hi;
         o.before = mass_up_to(hi - 1);
       }
-      last = min(last, min(lo, turns * kThreads - 1));
+      last = min(last, min(lo, bins_read - 1));
       o.target = by_k ? (double)r.p : (double)r.p * total;
     }
     o.by_k = by_k;
@@ -488,7 +441,7 @@ __global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
     if (first < kBins) {
       o.first = first;
       o.last = last;
-      o.edge = edge_of(first);
+      o.edge = edge_of(s.steps, first);
       if (by_k) o.bin_k = bin_k;
     }
   }
@@ -516,18 +469,95 @@ __global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
       none = o.bin_k <= o.last;
     }
     if (tid == 5) t = o.q - o.bin_k + 1.0;
-    limits[tid] = none ? __builtin_nanf("") : logit_from(t, scale);
+    s.limits[tid] = none ? __builtin_nanf("") : logit_from(t, scale);
   }
   __syncthreads();
   if (tid == 0) {
-    o.least = limits[0];
-    o.sure = limits[1];
-    o.from = limits[2];
-    o.to = limits[3];
-    o.from_k = limits[4];
-    o.to_k = limits[5];
+    o.least = s.limits[0];
+    o.sure = s.limits[1];
+    o.from = s.limits[2];
+    o.to = s.limits[3];
+    o.from_k = s.limits[4];
+    o.to_k = s.limits[5];
     *info = o;
   }
+}
+
+template <bool F16, int EACH>
+__global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
+  __shared__ BinsScratch s;
+  const int b = blockIdx.x / a.shares, share = blockIdx.x % a.shares, tid = threadIdx.x;
+  const Rules r = rules_of(a, b);
+  const void* row = row_of(a, b);
+  const bool bins = !r.one && (r.k > 0 || r.p < 1.0f);
+  const int beg = share * EACH * kThreads, end = min(beg + EACH * kThreads, a.vocab);
+  const double step = kSteps[tid % kPer];
+  float l[EACH];
+  u64 best = 0;
+  uint32_t least = ~0u;
+  if (row) load_share<F16, EACH>(row, beg, end, a.vocab, l);
+  if (bins)
+    for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
+  if (row) {
+    float top = -INFINITY, low = INFINITY;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      if (l[i] > top) {
+        top = l[i];
+        at = place(beg, i);
+      }
+      if (valid(l[i])) low = fminf(low, l[i]);
+    }
+    if (valid(top)) {
+      best = key_of(top, at);
+      least = rising(low);
+    }
+  }
+  best = block_max(best, s.red);
+  const double scale = scale_of(r);
+  ShareInfo* mine = a.share + (int64_t)b * a.shares + share;
+  if (bins && best != 0) {
+    least = block_all(least, s.redc, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
+    const double q = floor(t_of(logit_of(best), scale));
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const double t = t_of(l[i], scale), f = floor(t), rel = q - f;
+      if (valid(l[i]) && rel < kBins) {
+        atomicAdd(&s.hist[(int)rel], ((u64)(1u << 16) << 32) | (uint32_t)distance(t - f));
+      }
+    }
+    const double span = q - floor(t_of(logit_of((u64)least << 32), scale)) + 1.0;
+    const int used = span < kBins ? (int)span : kBins;
+    u64* bins_out = a.hist + ((int64_t)b * a.shares + share) * kBins;
+    __syncthreads();
+    // The bins, and their sums: those of the row come from the shares' own.
+    double mass = 0.0;
+    uint32_t n = 0;
+    for (int i = tid; i < used; i += kThreads) {
+      const u64 v = s.hist[i];
+      bins_out[i] = v;
+      mass += mass_of(i, step, (uint32_t)(v >> 48), v & ((1ull << 48) - 1));
+      n += (uint32_t)(v >> 48);
+    }
+    block_run(mass, n, s.redd, s.redc);
+    if (tid == kThreads - 1) {
+      mine->number = (u64)__double_as_longlong(q);
+      mine->mass = (u64)__double_as_longlong(mass);
+      mine->used = (u64)n << 32 | (u64)used;
+    }
+  }
+  if (tid == 0) mine->best = best;
+}
+
+__global__ void __launch_bounds__(kThreads) sample_cuts_kernel(SampleArgs a) {
+  __shared__ CutScratch s;
+  const int b = blockIdx.x;
+  const Rules r = rules_of(a, b);
+  const double step = kSteps[threadIdx.x % kPer];
+  if (threadIdx.x < kPer) s.steps[threadIdx.x] = step;
+  __syncthreads();
+  find_cuts(a, b, r, scale_of(r), step, s);
 }
 
 // ------------------------------------------------------------- second launch
@@ -539,31 +569,60 @@ __device__ __forceinline__ u64 race_key(float w, float noise, int j) {
   return w > 0.0f && s >= 0.0f ? ((u64)float_bits(s) << 32) | (uint32_t)~j : 0ull;
 }
 
-struct Scratch {
+// What a share needs in LDS; and what the end of a row needs beside it.
+struct Staged {
   __attribute__((aligned(16))) u64 list[kStaged];     // a share's tokens; then the row's, if they are kRanked at most
+  float noise[kStaged];           // of these tokens
+  u64 red[kWaves];
+  double redd[kWaves];
+  uint32_t found_count, listed;
+};
+struct Scratch : Staged {
   u64 sums[kSubs];
   uint32_t counts[kSubs];
   u64 sorted_key[kRanked];
-  u64 red[kWaves];
+  double steps[kPer];
   uint32_t redc[kWaves];
-  double redd[kWaves];
   u64 found_sum;
-  uint32_t found_count, listed;
   int found;
-  uint32_t arrived;
 };
 
 // Every token of a row's list, or of the row itself if the list does not hold its n.
 template <bool F16, typename F>
 __device__ __forceinline__ void each(const SampleArgs& a, const void* row, const u64* list, uint32_t n, F f) {
   if (n <= kSampleList) {
-    for (uint32_t i = threadIdx.x; i < n; i += kThreads) f(ld64(&list[i]));
+#pragma unroll 1
+    for (uint32_t i = threadIdx.x; i < n; i += kThreads) f(list[i]);
   } else {
+#pragma unroll 1
     for (int j = threadIdx.x; j < a.vocab; j += kThreads) {
       const float l = F16 ? (float)((const half_t*)row)[j] : ((const float*)row)[j];
       if (valid(l)) f(key_of(l, j));
     }
   }
+}
+
+// A wave's own sorting: the place of each of its first n lanes' keys, largest first
+// (other lanes keep theirs), values moved to their places, and running sums.
+__device__ __forceinline__ u64 read_lane(u64 v, int lane) {
+  return (u64)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+__device__ __forceinline__ int place_in_wave(u64 key, int n) {
+  const int lane = threadIdx.x % kWave;
+  int at = 0;
+  for (int j = 0; j < n; ++j) at += read_lane(key, j) > key;
+  return lane < n ? at : lane;
+}
+__device__ __forceinline__ uint32_t push(uint32_t v, int to) { return (uint32_t)__builtin_amdgcn_ds_permute(4 * to, (int)v); }
+__device__ __forceinline__ u64 push(u64 v, int to) { return (u64)push((uint32_t)(v >> 32), to) << 32 | push((uint32_t)v, to); }
+__device__ __forceinline__ u64 wave_run(u64 v) {
+#pragma unroll
+  for (int o = 1; o < kWave; o *= 2) {
+    const u64 x = __shfl_up(v, o);
+    if (threadIdx.x % kWave >= o) v += x;
+  }
+  return v;
 }
 
 // Of the tokens of bins `first` to `last`, in falling order: the key of the one at which
@@ -603,7 +662,7 @@ __device__ u64 select(const SampleArgs& a, const RowInfo& o, const void* row, co
         const int sub = kSubs - 1 - (int)((k >> shift) & (kSubs - 1));     // the largest first
         atomicAdd(&s.counts[sub], 1u);
         if (!by_count)
-          atomicAdd(&s.sums[sub], fixed_below(o, logit_of(k), first));
+          atomicAdd(&s.sums[sub], fixed_below(o, s.steps, logit_of(k), first));
       }
     });
     __syncthreads();
@@ -643,37 +702,88 @@ __device__ u64 select(const SampleArgs& a, const RowInfo& o, const void* row, co
       count -= s.found_count;
       mass -= s.found_sum;
     }
+    const uint32_t left = s.counts[sub];
     mask = ~((1ull << shift) - 1);
     value = (all & ~((2ull << top) - 1)) | ((u64)(kSubs - 1 - sub) << shift);
     if (top < kSubBits - 1) value = (all & ~(u64)(kSubs - 1)) | (u64)(kSubs - 1 - sub);
     __syncthreads();
+    if (left <= kWave) {
+      // Few are left: every wave sorts them for itself.
+      if (tid == 0) s.found_count = 0;
+      __syncthreads();
+      each<F16>(a, row, list, listed, [&](u64 k) {
+        if (here(k)) s.sorted_key[atomicAdd(&s.found_count, 1u)] = k;
+      });
+      __syncthreads();
+      const int lane = tid % kWave, n = (int)s.found_count;
+      u64 key = lane < n ? s.sorted_key[lane] : 0;
+      key = push(key, place_in_wave(key, n));
+      u64 before = lane < n && !by_count ? fixed_below(o, s.steps, logit_of(key), first) : 0;
+      const u64 own = before;
+      before = wave_run(before) - own;
+      const bool in = lane < n && (by_count ? (uint32_t)lane < count : before < mass);
+      return read_lane(key, max(__popcll(__ballot(in)) - 1, 0));
+    }
   }
 }
 
-// The cuts among the n <= kRanked tokens of the list, all of them at once: every token's
-// place in the order by counting those before it (two threads to a token where they
-// are few), the masses before it by a running sum in that order.
 struct Cut {
   u64 end;          // key of the last token kept (~0: none of these)
   u64 best, sum;    // the race among those kept, and their mass in fixed point
 };
-__device__ __forceinline__ Cut cut_ranked(const SampleArgs& a, const RowInfo& o, int b, Scratch& s, int n) {
+
+// The cuts among a list of no more tokens than a wave has lanes: every wave for itself,
+// without a barrier.
+__device__ __forceinline__ Cut cut_in_wave(const SampleArgs& a, const RowInfo& o, const double* steps, int n, u64 key,
+                                           float noise) {
+  const int lane = threadIdx.x % kWave;
+  const bool here = lane < n;
+  const int to = place_in_wave(key, n);
+  key = push(here ? key : 0, to);
+  noise = bits_float(push(float_bits(noise), to));
+  const float l = logit_of(key);
+  const int bin = here ? (int)bin_of(o, l) : kBins;
+  const u64 mass = here ? fixed_below(o, steps, l, o.first) : 0;
+  bool kept = here && bin <= o.last;
+  double target = o.target;
+  const double unit = o.edge * (1.0 / (double)(1ull << kFixBits));
+  if (o.by_k) {
+    const int ahead = __popcll(__ballot(here && bin < o.bin_k));
+    const bool of_k = here && (bin < o.bin_k || lane - ahead < o.left_k);
+    kept &= of_k;
+    if (o.by_p)
+      target *= o.before_k + (double)read_lane(wave_run(of_k && bin == o.bin_k ? mass : 0), kWave - 1) * unit;
+  }
+  if (o.by_p) kept &= o.before + (double)(wave_run(mass) - mass) * unit < target;
+  const int many = __popcll(__ballot(kept));
+  Cut c;
+  c.end = many > 0 ? read_lane(key, many - 1) : ~0ull;
+  c.best = c.sum = 0;
+  if (kept && l >= o.least) {
+    const float w = weight_of(o, l);
+    c.sum = (u64)((double)w * 0x1p40);
+    if (a.noise) c.best = race_key(w, noise, (int)~(uint32_t)key);
+  }
+  return c;
+}
+
+// The cuts among the n <= kRanked tokens of the list: every token's place in the order by
+// counting those before it, the masses before it by a running sum in that order.
+__device__ __forceinline__ Cut cut_ranked(const SampleArgs& a, const RowInfo& o, Scratch& s, int n) {
   const int tid = threadIdx.x;
   u64* sorted = s.sums;
   float* sorted_noise = (float*)(sorted + kRanked);
   static_assert(kSubs >= kRanked + kRanked / 2, "room for both");
-  const int parts = n <= kThreads / 2 ? 2 : 1, own = tid % (kThreads / parts), part = tid / (kThreads / parts);
+  const int own = tid % kRanked, part = tid / kRanked;       // two threads to a token
   const u64 key = own < n ? s.list[own] : 0;
-  const float* noise = a.noise ? a.noise + (int64_t)b * a.vocab : nullptr;
-  float e = 0.0f;
-  if (noise && own < n && part == 0) e = noise[(int)~(uint32_t)key];
+  const float e = own < n ? s.noise[own] : 0.0f;
   const float own_l = logit_of(key);
-  const u64 own_mass = own < n && part == 0 ? fixed_below(o, own_l, o.first) : 0;
+  const u64 own_mass = own < n && part == 0 ? fixed_below(o, s.steps, own_l, o.first) : 0;
   if (tid < n) s.counts[tid] = 0;
   if (tid == 0 && n % 2) s.list[n] = 0;      // (read in pairs)
   __syncthreads();
   if (own < n) {
-    const int pairs = (n + 1) / 2, half = (pairs + parts - 1) / parts, to = min((part + 1) * half, pairs);
+    const int pairs = (n + 1) / 2, half = (pairs + 1) / 2, to = min((part + 1) * half, pairs);
     uint32_t before = 0;
 #pragma unroll 4
     for (int j = part * half; j < to; ++j) {
@@ -714,7 +824,7 @@ __device__ __forceinline__ Cut cut_ranked(const SampleArgs& a, const RowInfo& o,
   if (kept && l >= o.least) {
     const float w = weight_of(o, l);
     c.sum = (u64)((double)w * 0x1p40);
-    if (noise) c.best = race_key(w, sorted_noise[tid], (int)~(uint32_t)k);
+    if (a.noise) c.best = race_key(w, sorted_noise[tid], (int)~(uint32_t)k);
   }
   return c;
 }
@@ -725,23 +835,24 @@ __device__ Cut cut_selected(const SampleArgs& a, const RowInfo& o, const void* r
                             uint32_t listed, Scratch& s) {
   Cut c = {0, 0, 0};
   double target = o.target;
-  if (o.by_k) {
-    c.end = select<F16>(a, o, row, list, listed, s, o.bin_k, o.bin_k, true, (uint32_t)o.left_k, 0);
-    if (o.by_p) {
+#pragma unroll 1
+  for (int rule = 0; rule < 2; ++rule) {       // top-k, then top-p
+    const bool by_count = rule == 0;
+    if (!(by_count ? o.by_k : o.by_p)) continue;
+    const double left = (target - o.before) / o.edge;     // top-p's mass in units of the bins' upper edge
+    const u64 mass = left > 0.0 ? (u64)fmin(ceil(left * (double)(1ull << kFixBits)), 0x1p62) : 1;
+    const u64 end = select<F16>(a, o, row, list, listed, s, by_count ? o.bin_k : o.first, by_count ? o.bin_k : o.last,
+                                by_count, (uint32_t)o.left_k, mass);
+    c.end = c.end > end ? c.end : end;
+    if (by_count && o.by_p) {
       // What top-k left of its bin, and with it top-p's mass.
       u64 part = 0;
       each<F16>(a, row, list, listed, [&](u64 k) {
-        if (bin_of(o, logit_of(k)) == o.bin_k && k >= c.end) part += fixed_below(o, logit_of(k), o.bin_k);
+        if (bin_of(o, logit_of(k)) == o.bin_k && k >= c.end) part += fixed_below(o, s.steps, logit_of(k), o.bin_k);
       });
       part = block_add(part, s.red);
-      target *= o.before_k + ldexp((double)part, -kFixBits) * edge_of(o.bin_k);
+      target *= o.before_k + ldexp((double)part, -kFixBits) * edge_of(s.steps, o.bin_k);
     }
-  }
-  if (o.by_p) {
-    const double left = (target - o.before) / o.edge;     // in units of the bins' upper edge
-    const u64 mass = left > 0.0 ? (u64)fmin(ceil(left * (double)(1ull << kFixBits)), 0x1p62) : 1;
-    const u64 by_p = select<F16>(a, o, row, list, listed, s, o.first, o.last, false, 0, mass);
-    c.end = c.end > by_p ? c.end : by_p;
   }
   each<F16>(a, row, list, listed, [&](u64 k) {
     const float l = logit_of(k);
@@ -758,12 +869,86 @@ __device__ Cut cut_selected(const SampleArgs& a, const RowInfo& o, const void* r
   return c;
 }
 
-template <bool F16, int EACH>
+// From a row's shares, when all of them are there: the list cut, and the race's end.
+template <bool F16>
+__device__ __forceinline__ void end_race(const SampleArgs& a, int b, const void* row, const RowInfo& o, RowInfo* info,
+                                         Scratch& s) {
+  const int tid = threadIdx.x;
+  const u64* list = a.list + (int64_t)b * kSampleList;
+  const float* list_noise = a.list_noise + (int64_t)b * kSampleList;
+  const bool cuts = o.by_k || o.by_p;
+  const int lane = tid % kWave;
+  // (every wave for itself: the list's first tokens, with their number, and the shares)
+  uint32_t n = 0;
+  u64 key = 0;
+  float e = 0.0f;
+  if (cuts) {
+    n = info->listed;
+    key = list[lane];
+    e = list_noise[lane];
+  }
+  u64 best = 0;
+  double sum = 0.0;
+  for (int i = lane; i < a.parts; i += kWave) {
+    const PartInfo from = a.part[(int64_t)b * a.parts + i];
+    best = best > from.best ? best : from.best;
+    sum += from.mass;
+  }
+  Cut c = {0, 0, 0};
+  bool split = false;       // whether c is each thread's part, or each wave's whole
+  if (cuts) {
+    if (n <= kWave) {
+      c = cut_in_wave(a, o, s.steps, (int)n, key, e);
+    } else if (n <= kRanked) {
+      if (tid < (int)n) {
+        s.list[tid] = list[tid];
+        s.noise[tid] = list_noise[tid];
+      }
+      __syncthreads();
+      c = cut_ranked(a, o, s, (int)n);
+      split = true;
+    } else {
+      c = cut_selected<F16>(a, o, row, b, list, n, s);
+      split = true;
+    }
+  }
+  best = best > c.best ? best : c.best;
+#pragma unroll
+  for (int x = kWave / 2; x > 0; x /= 2) {        // (sums always in the same order)
+    const u64 v = __shfl_xor(best, x);
+    best = best > v ? best : v;
+    sum += __shfl_xor(sum, x);
+    c.sum += __shfl_xor(c.sum, x);
+  }
+  if (split) {
+    __syncthreads();
+    if (lane == 0) {
+      s.red[tid / kWave] = best;
+      s.sums[tid / kWave] = c.sum;
+    }
+    __syncthreads();
+    c.sum = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      best = best > s.red[i] ? best : s.red[i];
+      c.sum += s.sums[i];
+    }
+  }
+  sum += ldexp((double)c.sum, -40);
+  if (tid == 0) {
+    if (a.tokens) a.tokens[b] = best ? (int)~(uint32_t)best : -1;
+    info->end = c.end;
+    info->inv = 1.0 / sum;
+  }
+}
+
+template <bool F16>
 __global__ void __launch_bounds__(kThreads) sample_race_kernel(SampleArgs a) {
-  __shared__ Scratch s;
-  const int b = blockIdx.x / a.shares, share = blockIdx.x % a.shares, tid = threadIdx.x;
+  constexpr int EACH = kSampleLeast / kThreads;
+  __shared__ Staged s;
+  const int b = blockIdx.x / a.parts, part = blockIdx.x % a.parts, tid = threadIdx.x;
   const void* row = row_of(a, b);
-  const int beg = share * EACH * kThreads, end = min(beg + EACH * kThreads, a.vocab);
+  const int beg = part * EACH * kThreads, end = min(beg + EACH * kThreads, a.vocab);
   float l[EACH];
   if (row) load_share<F16, EACH>(row, beg, end, a.vocab, l);     // (requested before the row's kind is known)
   RowInfo* info = (RowInfo*)((char*)a.info + (int64_t)b * kSampleInfoBytes);
@@ -772,7 +957,8 @@ __global__ void __launch_bounds__(kThreads) sample_race_kernel(SampleArgs a) {
   if (tid == 0) s.listed = 0;
   __syncthreads();
   u64* list = a.list + (int64_t)b * kSampleList;
-  // Noise is read where a token is kept: elsewhere the load is out of its buffer.
+  float* list_noise = a.list_noise + (int64_t)b * kSampleList;
+  // Noise is read where a token is kept or listed: elsewhere the load is out of its buffer.
   const __amdgpu_buffer_rsrc_t noise =
       make_rsrc(a.noise ? a.noise + (int64_t)b * a.vocab : nullptr, a.noise ? (uint32_t)a.vocab * 4u : 0u);
   u64 best = 0;
@@ -783,12 +969,12 @@ __global__ void __launch_bounds__(kThreads) sample_race_kernel(SampleArgs a) {
     kept |= (uint32_t)(l[i] >= o.sure) << i;
     cut |= (uint32_t)((l[i] >= o.from && !(l[i] >= o.to)) || (l[i] >= o.from_k && !(l[i] >= o.to_k))) << i;
   }
-  if (__any(kept != 0)) {
+  if (__any((kept | cut) != 0)) {
     float e[EACH];
 #pragma unroll
     for (int i = 0; i < EACH; i += 4) {
       const int at = place(beg, i);
-      const bool some = (kept >> i & 15) && a.noise;
+      const bool some = ((kept | cut) >> i & 15) && a.noise;
       const f4_t v = __builtin_bit_cast(f4_t, __builtin_amdgcn_raw_buffer_load_b128(
           noise, some && at + 4 <= end ? 4u * (uint32_t)at : kOutOfRange, 0, 0));
 #pragma unroll
@@ -799,88 +985,65 @@ __global__ void __launch_bounds__(kThreads) sample_race_kernel(SampleArgs a) {
           if (at + j < end) e[i + j] = a.noise[(int64_t)b * a.vocab + at + j];
       }
     }
+    if (__any(kept != 0)) {
 #pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-      const float w = kept >> i & 1 ? weight_of(o, l[i]) : 0.0f;
-      sum += (double)w;
-      const u64 k = a.noise ? race_key(w, e[i], place(beg, i)) : 0;
-      best = best > k ? best : k;
-    }
-  }
-  if (cut != 0) {
-#pragma unroll
-    for (int i = 0; i < EACH; ++i)
-      if (cut >> i & 1) {
-        const u64 k = key_of(l[i], place(beg, i));
-        const uint32_t at = atomicAdd(&s.listed, 1u);
-        if (at < kStaged) {
-          s.list[at] = k;
-        } else {
-          const uint32_t to = add_dev_u32(&info->listed, 1u);
-          if (to < kSampleList) st64(&list[to], k);
-        }
+      for (int i = 0; i < EACH; ++i) {
+        const float w = kept >> i & 1 ? weight_of(o, l[i]) : 0.0f;
+        sum += (double)w;
+        const u64 k = a.noise ? race_key(w, e[i], place(beg, i)) : 0;
+        best = best > k ? best : k;
       }
+    }
+    if (cut != 0) {
+#pragma unroll
+      for (int i = 0; i < EACH; ++i)
+        if (cut >> i & 1) {
+          const u64 k = key_of(l[i], place(beg, i));
+          const uint32_t at = atomicAdd(&s.listed, 1u);
+          if (at < kStaged) {
+            s.list[at] = k;
+            s.noise[at] = e[i];
+          } else {
+            const uint32_t to = add_dev_u32(&info->listed, 1u);
+            if (to < kSampleList) list[to] = k;      // (a list this long is cut without its noise)
+          }
+        }
+    }
   }
   best = block_max(best, s.red);
   sum = block_all(sum, s.redd, [](double x, double y) { return x + y; });
   const uint32_t staged = min(s.listed, (uint32_t)kStaged);
-  ShareInfo* mine = a.share + (int64_t)b * a.shares + share;
   if (staged > 0) {
     if (tid == 0) s.found_count = add_dev_u32(&info->listed, staged);
     __syncthreads();
     for (uint32_t i = tid; i < staged; i += kThreads)
-      if (s.found_count + i < kSampleList) st64(&list[s.found_count + i], s.list[i]);
+      if (s.found_count + i < kSampleList) {
+        list[s.found_count + i] = s.list[i];
+        list_noise[s.found_count + i] = s.noise[i];
+      }
   }
-  if (tid == 0) {
-    st64(&mine->best, best);
-    st64(&mine->number, (u64)__double_as_longlong(sum));
-  }
-  if (!last_of_row(a, b, &s.arrived)) return;
+  if (tid == 0) a.part[(int64_t)b * a.parts + part] = {best, sum};
+}
 
-  best = 0;
-  sum = 0.0;
-  const bool cuts = o.by_k || o.by_p;
-  uint32_t n = 0;
-  u64 key = 0;
-  if (cuts) {
-    n = ld_dev_u32(&info->listed);
-    key = ld64(&list[tid]);           // (with the count: which of them are tokens is known then)
-  }
-  if (tid < a.shares) {
-    const ShareInfo* from = a.share + (int64_t)b * a.shares + tid;
-    best = ld64(&from->best);
-    sum = __longlong_as_double((long long)ld64(&from->number));
-  }
-  sum = block_all(sum, s.redd, [](double x, double y) { return x + y; });     // (always in the same order)
-  u64 last = 0;
-  if (cuts) {
-    Cut c;
-    if (n <= kRanked) {
-      if (tid < (int)n) s.list[tid] = key;
-      __syncthreads();
-      c = cut_ranked(a, o, b, s, (int)n);
-    } else {
-      c = cut_selected<F16>(a, o, row, b, list, n, s);
-    }
-    last = c.end;
-    best = best > c.best ? best : c.best;
-    sum += ldexp((double)block_add(c.sum, s.red), -40);
-  }
-  best = block_max(best, s.red);
-  if (tid == 0) {
-    if (a.tokens) a.tokens[b] = best ? (int)~(uint32_t)best : -1;
-    info->end = last;
-    info->inv = 1.0 / sum;
-  }
+template <bool F16>
+__global__ void __launch_bounds__(kThreads) sample_end_kernel(SampleArgs a) {
+  __shared__ Scratch s;
+  const int b = blockIdx.x;
+  RowInfo* info = (RowInfo*)((char*)a.info + (int64_t)b * kSampleInfoBytes);
+  const RowInfo o = *info;
+  if (threadIdx.x < kPer) s.steps[threadIdx.x] = kSteps[threadIdx.x];
+  __syncthreads();
+  if (o.kind == kRace) end_race<F16>(a, b, row_of(a, b), o, info, s);
 }
 
 // -------------------------------------------------------------- third launch
 
-template <bool F16, int EACH>
+template <bool F16>
 __global__ void __launch_bounds__(kThreads) sample_probs_kernel(SampleArgs a) {
-  const int b = blockIdx.x / a.shares, share = blockIdx.x % a.shares;
+  constexpr int EACH = kSampleLeast / kThreads;
+  const int b = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
   const void* row = row_of(a, b);
-  const int beg = share * EACH * kThreads, end = min(beg + EACH * kThreads, a.vocab);
+  const int beg = part * EACH * kThreads, end = min(beg + EACH * kThreads, a.vocab);
   float l[EACH], p[EACH];
   if (row) load_share<F16, EACH>(row, beg, end, a.vocab, l);
   const RowInfo o = *(const RowInfo*)((const char*)a.info + (int64_t)b * kSampleInfoBytes);
@@ -914,28 +1077,43 @@ __global__ void __launch_bounds__(kThreads) sample_probs_kernel(SampleArgs a) {
 
 template <bool F16, int EACH>
 hipError_t launch(const SampleArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.batch * a.shares)), block(kThreads);
+  const dim3 grid((unsigned)(a.batch * a.shares)), parts((unsigned)(a.batch * a.parts)), rows((unsigned)a.batch),
+      block(kThreads);
   sample_bins_kernel<F16, EACH><<<grid, block, 0, s>>>(a);
-  if (!a.only_first) sample_race_kernel<F16, EACH><<<grid, block, 0, s>>>(a);
-  if (a.probs) sample_probs_kernel<F16, EACH><<<grid, block, 0, s>>>(a);
+  sample_cuts_kernel<<<rows, dim3(kThreads), 0, s>>>(a);
+  if (!a.only_first) {
+    sample_race_kernel<F16><<<parts, block, 0, s>>>(a);
+    sample_end_kernel<F16><<<rows, block, 0, s>>>(a);
+  }
+  if (a.probs) sample_probs_kernel<F16><<<parts, block, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <bool F16>
 hipError_t launch_share(const SampleArgs& a, hipStream_t s) {
-  return a.share_tokens == 8 * kThreads ? launch<F16, 8>(a, s) : launch<F16, 16>(a, s);
+  return a.share_tokens == 8 * kThreads    ? launch<F16, 8>(a, s)
+         : a.share_tokens == 16 * kThreads ? launch<F16, 16>(a, s)
+                                           : launch<F16, 32>(a, s);
 }
 
 }  // namespace
 
-// Shares of 8192 tokens (4096 where the batch has few), as many of a row as a
-// workgroup has threads; rows of one group: as many as the header has counters for, and
-// shares whose bins take no more than 128 MiB.
+// Shares of 4096, 8192 or 16384 tokens: the first launch takes what the fullest CU has to
+// do (0.36 us per 1024 tokens), and the workgroup that sums a row's bins 0.35 us per
+// share.  Rows of one group: shares whose bins take no more than 128 MiB.
 SampleShape sample_shape(const spear_sample_desc_t& d) {
   SampleShape s;
-  const int64_t large = kSampleLeast * 2;
-  s.share_tokens = (int)(d.batch * ceil_div(d.vocab, kSampleLeast) <= 512 ? kSampleLeast : large);
-  s.shares = (int)ceil_div(d.vocab, s.share_tokens);
+  constexpr int kCus = 256;
+  double least = 0.0;
+  for (int tokens = kSampleLeast; tokens <= 4 * kSampleLeast; tokens *= 2) {
+    const int64_t shares = ceil_div(d.vocab, tokens);
+    const double us = 0.36 * (double)(ceil_div(d.batch * shares, kCus) * (tokens / 1024)) + 0.35 * (double)shares;
+    if (shares <= kSampleShares && (least == 0.0 || us < least)) {
+      least = us;
+      s.share_tokens = tokens;
+      s.shares = (int)shares;
+    }
+  }
   s.group = (int)std::max<int64_t>(1, std::min<int64_t>(d.batch, std::min<int64_t>(kMaxEcTiles, 4096 / s.shares)));
   size_t at = kSyncHeaderBytes;
   const size_t shares = (size_t)s.group * s.shares;
@@ -943,10 +1121,15 @@ SampleShape sample_shape(const spear_sample_desc_t& d) {
   at += (size_t)s.group * kSampleInfoBytes;
   s.share = at;
   at += shares * sizeof(ShareInfo);
+  s.parts = (int)ceil_div(d.vocab, kSampleLeast);
+  s.part = at;
+  at += (size_t)s.group * s.parts * sizeof(PartInfo);
   s.list = at;
   at += (size_t)s.group * kSampleList * 8;
   s.hist = at;
   at += shares * kBins * 8;
+  s.list_noise = at;
+  at += (size_t)s.group * kSampleList * 4;
   s.bytes = at;
   return s;
 }

@@ -185,22 +185,28 @@ struct AdapterArgs {
 hipError_t launch_adapter(const AdapterArgs& a, void* stream);
 
 // The draw of next tokens.
-constexpr int kSampleLeast = 4096;      // tokens of the vocabulary that a workgroup takes, or twice as many
-constexpr int kSampleList = 4094;       // tokens of the bins that are cut, gathered for the row's last workgroup
+constexpr int kSampleLeast = 4096;      // tokens of the vocabulary that a workgroup takes, two or four times as many for bins
+constexpr int kSampleShares = 512;      // most workgroups of a row's bins
+constexpr int kSampleList = 4094;       // tokens of the bins that are cut, gathered for the row's end
 constexpr int kSampleInfoBytes = 256;
 struct ShareInfo {
-  unsigned long long best;              // the largest (logit, token); then of (score, token)
-  unsigned long long number;            // a double: the place of its first bin; then the mass of what is kept
+  unsigned long long best;              // the largest (logit, token)
+  unsigned long long number;            // a double: the place of its first bin
   unsigned long long mass;              // a double: of all its tokens
   unsigned long long used;              // tokens and bins written
 };
+struct PartInfo {
+  unsigned long long best;              // the largest (score, token)
+  double mass;                          // of what is kept
+};
 struct SampleShape {
-  int share_tokens, shares, group;      // tokens of a workgroup, workgroups of a row, rows of a launch
-  size_t info, share, list, hist, bytes;
+  int share_tokens, shares;             // tokens of a workgroup of the bins, their workgroups of a row
+  int parts, group;                     // workgroups of a row after that, rows of a launch
+  size_t info, share, part, list, hist, list_noise, bytes;
 };
 SampleShape sample_shape(const spear_sample_desc_t& d);
 struct SampleArgs {
-  int32_t batch, vocab, share_tokens, shares, num_rows;
+  int32_t batch, vocab, share_tokens, shares, parts, num_rows;
   int32_t first;                        // the group's first draw: row `first` + b where no rows are given
   bool f16, only_first;                 // only_first: every row keeps its first token alone
   const void* logits;
@@ -213,10 +219,11 @@ struct SampleArgs {
   int32_t one_top_k;
   int32_t* tokens;
   float* probs;
-  uint32_t* counters;                   // [batch], zero before and after
   void* info;
   ShareInfo* share;                     // [batch][shares]
+  PartInfo* part;                       // [batch][parts]
   unsigned long long *list, *hist;      // [batch][kSampleList], [batch][shares][bins]
+  float* list_noise;                    // [batch][kSampleList]
 };
 hipError_t launch_sample(const SampleArgs& a, void* stream);
 

@@ -46,6 +46,7 @@ spear_status_t check_adapter(const spear_adapter_desc_t& d) {
   return SPEAR_OK;
 }
 
+static_assert((1 << 22) / (4 * kSampleLeast) <= kSampleShares, "room for every share");
 spear_status_t check_sample(const spear_sample_desc_t& d) {
   if (d.batch < 0 || d.vocab < 1 || d.num_rows < 0) return SPEAR_ERR_INVALID_SHAPE;
   if (d.dtype != SPEAR_LOGITS_FP16 && d.dtype != SPEAR_LOGITS_FP32) return SPEAR_ERR_INVALID_ARGUMENT;
@@ -192,13 +193,14 @@ spear_status_t spear_sample(const spear_sample_desc_t* desc, const void* logits,
   if (st != SPEAR_OK) return st;
   char* ws = (char*)workspace;
   SampleArgs a;
-  a.vocab = desc->vocab; a.share_tokens = s.share_tokens; a.shares = s.shares; a.num_rows = desc->num_rows;
+  a.vocab = desc->vocab; a.share_tokens = s.share_tokens; a.shares = s.shares; a.parts = s.parts;
+  a.num_rows = desc->num_rows;
   a.f16 = f16; a.only_first = one;
   a.logits = logits; a.stride = row_stride;
   a.one_temperature = desc->temperature; a.one_top_k = desc->top_k; a.one_top_p = desc->top_p; a.one_min_p = desc->min_p;
-  a.counters = (uint32_t*)ws;   // the header's first counters
-  a.info = ws + s.info; a.share = (ShareInfo*)(ws + s.share);
+  a.info = ws + s.info; a.share = (ShareInfo*)(ws + s.share); a.part = (PartInfo*)(ws + s.part);
   a.list = (unsigned long long*)(ws + s.list); a.hist = (unsigned long long*)(ws + s.hist);
+  a.list_noise = (float*)(ws + s.list_noise);
   for (int32_t at = 0; at < desc->batch; at += s.group) {
     a.batch = desc->batch - at < s.group ? desc->batch - at : s.group;
     a.first = at;
