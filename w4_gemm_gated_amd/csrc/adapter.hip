@@ -30,6 +30,7 @@ namespace spear {
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / kWave;
+constexpr int kShrinkThreads = 512, kShrinkWaves = kShrinkThreads / kWave;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanHead = 8;      // words: tiles
 constexpr int kUnit = kAdapterColumns / kWaves;   // columns of Y that a wave computes
@@ -156,8 +157,7 @@ struct Tile {
 };
 
 // Ranks [rank0, rank0 + 16 RB) of one slice of K for a tile of up to 16 SUB rows: the
-// four waves take 32-k blocks in turn (together whole lines of X and A), and add
-// their sums through LDS.
+// waves take 64 k in turn (whole lines of X and A), and add their sums through LDS.
 template <int RB, int SUB>
 __device__ __forceinline__ void shrink(const AdapterArgs& a, const Tile& t, const int32_t* list, int rank0, int k_lo,
                                        int k_hi, f4_t* red, __amdgpu_buffer_rsrc_t part) {
@@ -177,59 +177,70 @@ __device__ __forceinline__ void shrink(const AdapterArgs& a, const Tile& t, cons
   for (int j = 0; j < SUB; ++j)
 #pragma unroll
     for (int i = 0; i < RB; ++i) acc[j][i] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  constexpr int kAhead = SUB * RB >= 8 ? 2 : 4;    // blocks whose loads are in flight together
-  constexpr int kTurn = 32 * kWaves;
-  int k = k_lo + 32 * wave;
-  for (; k + (kAhead - 1) * kTurn + 32 <= k_hi; k += kAhead * kTurn) {
-    half8_t xv[kAhead][SUB], wv[kAhead][RB];
+  constexpr int kTurn = 64 * kShrinkWaves;
+  constexpr int kAhead = SUB * RB >= 8 ? 1 : 2;    // turns whose loads are in flight together
+  int k = k_lo + 64 * wave;
+  for (; k + (kAhead - 1) * kTurn + 64 <= k_hi; k += kAhead * kTurn) {
+    half8_t xv[2 * kAhead][SUB], wv[2 * kAhead][RB];
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n) {
+    for (int n = 0; n < 2 * kAhead; ++n) {
+      const int at = k + n / 2 * kTurn + n % 2 * 32;
 #pragma unroll
-      for (int j = 0; j < SUB; ++j) xv[n][j] = load_half8(x[j] + k + n * kTurn);
+      for (int i = 0; i < RB; ++i) wv[n][i] = load_half8(w[i] + at);
 #pragma unroll
-      for (int i = 0; i < RB; ++i) wv[n][i] = load_half8(w[i] + k + n * kTurn);
+      for (int j = 0; j < SUB; ++j) xv[n][j] = load_half8(x[j] + at);
     }
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n)
+    for (int n = 0; n < 2 * kAhead; ++n)
 #pragma unroll
       for (int j = 0; j < SUB; ++j)
 #pragma unroll
         for (int i = 0; i < RB; ++i) acc[j][i] = mfma16x16x32(wv[n][i], xv[n][j], acc[j][i]);
   }
-  for (; k < k_hi; k += kTurn) {
-    const bool in = k + 8 * oct < k_hi;            // (K and the slices are multiples of 8)
-    const int at = in ? k : k_hi - 8 - 8 * oct;
-    half8_t xv[SUB], wv[RB];
+#pragma unroll 1
+  for (; k < k_hi; k += kTurn)
+#pragma unroll 1
+    for (int at = k; at < min(k + 64, k_hi); at += 32) {
+      const bool in = at + 8 * oct < k_hi;            // (K and the slices are multiples of 8)
+      const int from = in ? at : k_hi - 8 - 8 * oct;
+      half8_t xv[SUB], wv[RB];
 #pragma unroll
-    for (int j = 0; j < SUB; ++j) xv[j] = load_half8(x[j] + at);
+      for (int i = 0; i < RB; ++i) wv[i] = load_half8(w[i] + from);
 #pragma unroll
-    for (int i = 0; i < RB; ++i) wv[i] = load_half8(w[i] + at);
+      for (int j = 0; j < SUB; ++j) xv[j] = load_half8(x[j] + from);
 #pragma unroll
-    for (int j = 0; j < SUB; ++j) xv[j] = in ? xv[j] : zero_half8();
+      for (int i = 0; i < RB; ++i) wv[i] = in ? wv[i] : zero_half8();
 #pragma unroll
-    for (int i = 0; i < RB; ++i) wv[i] = in ? wv[i] : zero_half8();
+      for (int j = 0; j < SUB; ++j) xv[j] = in ? xv[j] : zero_half8();
 #pragma unroll
-    for (int j = 0; j < SUB; ++j)
+      for (int j = 0; j < SUB; ++j)
 #pragma unroll
-      for (int i = 0; i < RB; ++i) acc[j][i] = mfma16x16x32(wv[i], xv[j], acc[j][i]);
+        for (int i = 0; i < RB; ++i) acc[j][i] = mfma16x16x32(wv[i], xv[j], acc[j][i]);
+    }
+  // The upper four waves' sums to the lower four, theirs to all.
+  constexpr int kHalf = kShrinkWaves / 2, kUnits = SUB * RB;
+#pragma unroll
+  for (int turn = 0; turn < 2; ++turn) {
+    __syncthreads();
+    if (turn == 0 ? wave >= kHalf : wave < kHalf)
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) red[((wave % kHalf) * kUnits + u) * kWave + lane] = acc[u / RB][u % RB];
+    __syncthreads();
+    if (turn == 0 && wave < kHalf)
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) acc[u / RB][u % RB] += red[(wave * kUnits + u) * kWave + lane];
   }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < SUB; ++j)
-#pragma unroll
-    for (int i = 0; i < RB; ++i) red[(wave * SUB * RB + j * RB + i) * kWave + lane] = acc[j][i];
-  __syncthreads();
-  for (int u = wave; u < SUB * RB; u += kWaves) {
+  for (int u = wave; u < kUnits; u += kShrinkWaves) {
     f4_t sum = red[u * kWave + lane];
 #pragma unroll
-    for (int v = 1; v < kWaves; ++v) sum += red[(v * SUB * RB + u) * kWave + lane];
+    for (int v = 1; v < kHalf; ++v) sum += red[(v * kUnits + u) * kWave + lane];
     const int row = 16 * (u / RB) + c, rank = rank0 + 16 * (u % RB) + 4 * oct;
     if (row < t.rows && rank < a.rank) store_f4_dev(part, 4u * (uint32_t)(row * a.rank + rank), sum);
   }
 }
 
 template <int RB>
-__global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(AdapterArgs a) {
+__global__ void __launch_bounds__(kShrinkThreads) adapter_shrink_kernel(AdapterArgs a) {
   extern __shared__ f4_t lds[];
   __shared__ float factor[kAdapterTile];
   __shared__ uint32_t arrived;
@@ -258,7 +269,7 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(AdapterArgs a)
   float* h = (float*)lds;
   const __amdgpu_buffer_rsrc_t all = make_rsrc(parts, (uint32_t)(tile_bytes * a.slices));
   const int quads = a.rank / 4;
-  for (int u = tid; u < t.rows * quads; u += kThreads) {
+  for (int u = tid; u < t.rows * quads; u += kShrinkThreads) {
     f4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
     int s = 0;
     for (; s + 4 <= a.slices; s += 4) {
@@ -273,22 +284,23 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(AdapterArgs a)
   }
   __syncthreads();
   {
-    const int row = tid / 4;          // four lanes to a row
+    constexpr int kLanes = kShrinkThreads / kAdapterTile;     // lanes to a row
+    const int row = tid / kLanes;
     float most = 0.0f;
     if (row < t.rows)
-      for (int i = tid % 4; i < a.rank; i += 4) {
+      for (int i = tid % kLanes; i < a.rank; i += kLanes) {
         const float v = fabsf(h[row * a.rank + i]);
         most = v > most || v != v ? v : most;
       }
 #pragma unroll
-    for (int o = 1; o < 4; o *= 2) {
+    for (int o = 1; o < kLanes; o *= 2) {
       const float v = __shfl_xor(most, o);
       most = v > most || v != v ? v : most;
     }
     // The power of two at or below the row's largest (1 where that is zero, infinite or NaN).
     const uint32_t e = float_bits(most) >> 23;
     const float p = e == 0 ? (most > 0.0f ? 0x1p-126f : 1.0f) : e == 255 ? 1.0f : bits_float(e << 23);
-    if (tid % 4 == 0 && row < t.rows) {
+    if (tid % kLanes == 0 && row < t.rows) {
       factor[row] = p;
       a.factor[(int64_t)tile * kAdapterTile + row] = p * (a.scale ? a.scale[t.adapter] : 1.0f);
     }
@@ -296,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(AdapterArgs a)
   __syncthreads();
   const int octets = a.rank_pad / 8;
   half_t* out = (half_t*)a.H + (int64_t)tile * kAdapterTile * 2 * a.rank_pad;
-  for (int u = tid; u < t.rows * octets; u += kThreads) {
+  for (int u = tid; u < t.rows * octets; u += kShrinkThreads) {
     const int row = u / octets, o = u % octets;
     half8_t hi = zero_half8(), lo = zero_half8();
     if (8 * o < a.rank) {
@@ -317,9 +329,12 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(AdapterArgs a)
 // ------------------------------------------------------------ second product
 
 // A wave's unit of 64 columns: block j of four holds, in operand row i, column
-// 16 (i / 4) + 4 j + i % 4, so that a lane's results of the four blocks are sixteen
-// neighbouring columns of one token.  SB: 32-rank blocks of B; PACK (rank 8 or 16):
-// both halves of H share one block.
+// 32 (j / 2) + 8 (i / 4) + 4 (j % 2) + i % 4, so that a lane's results of two blocks are
+// eight neighbouring columns of one token, and a load of all lanes takes whole
+// 64-byte pieces of sixteen rows.  SB: 32-rank blocks of B; PACK (rank 8 or 16): both halves of H
+// share one block.
+//
+// What a group of 16 rows needs is requested while the group before it is computed.
 template <int SB, bool PACK>
 __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(AdapterArgs a) {
   const int tile = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
@@ -330,77 +345,100 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(AdapterArgs a)
   const int4 q = plan_tiles(a.plan)[tile];
   const Tile t = {min(max(q.x, 0), a.adapters - 1), min(max(q.y, 0), a.rows - 1), min(max(q.z, 1), kAdapterTile)};
   const int32_t* list = a.plan + kPlanHead + 4 * (int64_t)a.most_tiles;
+  const half_t* H = (const half_t*)a.H + (int64_t)tile * kAdapterTile * 2 * a.rank_pad;
+  const float* factors = a.factor + (int64_t)tile * kAdapterTile;
+  const bool whole = a.y_vectors && n0 + kUnit <= a.N;      // (else column by column)
+  const int groups = (t.rows + 15) / 16;
+  half_t* y[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int32_t token = min(max(list[t.first + min(16 * g + c, t.rows - 1)], 0), a.rows - 1);
+    y[g] = (half_t*)a.Y + (int64_t)token * a.y_stride + n0 + 8 * oct;
+  }
   half8_t b[4][SB];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int n = min(n0 + 16 * (c / 4) + 4 * j + c % 4, a.N - 1);    // (a column past the last is not stored)
+    const int n = min(n0 + 32 * (j / 2) + 8 * (c / 4) + 4 * (j % 2) + c % 4, a.N - 1);    // (a column past the last is not stored)
     const half_t* row = (const half_t*)a.B + ((int64_t)t.adapter * a.N + n) * a.rank;
 #pragma unroll
     for (int s = 0; s < SB; ++s) {
       const int o = PACK ? oct % (a.rank / 8) : 4 * s + oct;
       b[j][s] = load_half8(row + 8 * min(o, a.rank / 8 - 1));
-      if (PACK ? oct >= a.rank / 4 : o >= a.rank / 8) b[j][s] = zero_half8();
     }
   }
-  const half_t* H = (const half_t*)a.H + (int64_t)tile * kAdapterTile * 2 * a.rank_pad;
-  const int col = n0 + 16 * oct;
-  for (int i0 = 0; i0 < t.rows; i0 += 16) {
-    const int i = i0 + c;
-    const bool in = i < t.rows && col < a.N;
-    const int at = min(i, t.rows - 1);
-    const int32_t token = min(max(list[t.first + at], 0), a.rows - 1);
-    half_t* y = (half_t*)a.Y + (int64_t)token * a.y_stride + col;
-    const float factor = a.factor[(int64_t)tile * kAdapterTile + at];
+  constexpr int kH = PACK ? 1 : 2 * SB;
+  struct Group {
+    half8_t h[kH], old[2];
+    float factor;
+  };
+  auto request = [&](int g, Group& r) {
+    const int at = min(16 * g + c, t.rows - 1);
     const half_t* hr = H + (int64_t)at * 2 * a.rank_pad;
-    half8_t h[PACK ? 1 : 2 * SB];
     if constexpr (PACK) {
-      h[0] = load_half8(hr + 8 * min(oct, a.rank / 4 - 1));
+      r.h[0] = load_half8(hr + 8 * min(oct, a.rank / 4 - 1));
     } else {
 #pragma unroll
-      for (int s = 0; s < 2 * SB; ++s) h[s] = load_half8(hr + 32 * s + 8 * oct);
+      for (int s = 0; s < kH; ++s) r.h[s] = load_half8(hr + 32 * s + 8 * oct);
     }
-    const bool whole = a.y_vectors && col + 16 <= a.N;
-    half8_t old[2];
-    if (in && whole) {
-      old[0] = load_half8(y);
-      old[1] = load_half8(y + 8);
+    r.factor = factors[at];
+    if (whole) {
+      r.old[0] = load_half8(y[g]);
+      r.old[1] = load_half8(y[g] + 32);
     }
+  };
+  auto compute = [&](int g, Group& r) {
     f4_t acc[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       acc[j] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
       if constexpr (PACK) {
-        const half8_t hv = oct >= a.rank / 4 ? zero_half8() : h[0];
+        const half8_t hv = oct >= a.rank / 4 ? zero_half8() : r.h[0];
         acc[j] = mfma16x16x32(b[j][0], hv, acc[j]);
       } else {
 #pragma unroll
-        for (int s = 0; s < SB; ++s) acc[j] = mfma16x16x32(b[j][s], h[SB + s], acc[j]);
+        for (int s = 0; s < SB; ++s) acc[j] = mfma16x16x32(b[j][s], r.h[SB + s], acc[j]);
 #pragma unroll
-        for (int s = 0; s < SB; ++s) acc[j] = mfma16x16x32(b[j][s], h[s], acc[j]);
+        for (int s = 0; s < SB; ++s) acc[j] = mfma16x16x32(b[j][s], r.h[s], acc[j]);
       }
     }
-    if (!in) continue;
+    if (16 * g + c >= t.rows) return;
     if (whole) {
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        half8_t r;
+        half8_t o;
 #pragma unroll
-        for (int n = 0; n < 8; ++n) r[n] = (half_t)__builtin_fmaf(factor, acc[2 * v + n / 4][n % 4], (float)old[v][n]);
-        *(half8_t*)(y + 8 * v) = r;
+        for (int n = 0; n < 8; ++n) o[n] = (half_t)__builtin_fmaf(r.factor, acc[2 * v + n / 4][n % 4], (float)r.old[v][n]);
+        *(half8_t*)(y[g] + 32 * v) = o;
       }
     } else {
 #pragma unroll
-      for (int n = 0; n < 16; ++n)
-        if (col + n < a.N) y[n] = (half_t)__builtin_fmaf(factor, acc[n / 4][n % 4], (float)y[n]);
+      for (int n = 0; n < 16; ++n) {
+        const int at = 32 * (n / 8) + n % 8;
+        if (n0 + 8 * oct + at < a.N) y[g][at] = (half_t)__builtin_fmaf(r.factor, acc[n / 4][n % 4], (float)y[g][at]);
+      }
     }
+  };
+  Group ring[2];
+  request(0, ring[0]);
+  // (ranks past the last count nothing, whatever lies there)
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int s = 0; s < SB; ++s)
+      if (PACK ? oct >= a.rank / 4 : 4 * s + oct >= a.rank / 8) b[j][s] = zero_half8();
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    if (g >= groups) break;
+    if (g + 1 < groups) request(g + 1, ring[(g + 1) % 2]);
+    compute(g, ring[g % 2]);
   }
 }
 
 template <int RB>
 hipError_t shrink_launch(const AdapterArgs& a, hipStream_t s) {
-  const size_t red = (size_t)kWaves * 4 * RB * kWave * sizeof(f4_t), h = (size_t)kAdapterTile * a.rank * 4;
+  const size_t red = (size_t)kShrinkWaves / 2 * 4 * RB * kWave * sizeof(f4_t), h = (size_t)kAdapterTile * a.rank * 4;
   const size_t bytes = red > h ? red : h;
-  adapter_shrink_kernel<RB><<<dim3((unsigned)(a.most_tiles * a.slices)), dim3(kThreads), bytes, s>>>(a);
+  adapter_shrink_kernel<RB><<<dim3((unsigned)(a.most_tiles * a.slices)), dim3(kShrinkThreads), bytes, s>>>(a);
   return hipGetLastError();
 }
 
@@ -420,17 +458,27 @@ size_t adapter_plan_size(int64_t rows, int64_t batch, int64_t adapters) {
   return 4 * (size_t)(kPlanHead + 4 * adapter_most_tiles(rows, batch, adapters) + rows);
 }
 
-// Slices of K: 512 k (a wave's four blocks at once) while all tiles' together do not
-// fill the GPU four times; more tiles than counters are not sliced.
+// Slices of K by what a call is expected to take: a workgroup reads its rows of X and
+// its ranks of A at about 50 bytes a ns, workgroups past the CUs' number wait for a place,
+// and slices are joined in 2 us and the time in which one workgroup reads them.
 AdapterShape adapter_shape(const spear_adapter_desc_t& d, int cus) {
   AdapterShape s;
   s.tiles = (int)adapter_most_tiles(d.rows, d.batch, d.adapters);
   s.rank_pad = d.rank <= 16 ? d.rank : d.rank <= 32 ? 32 : d.rank <= 64 ? 64 : d.rank <= 128 ? 128 : 256;
-  const int64_t most = s.tiles > 0 ? std::max<int64_t>(1, 4 * (int64_t)cus / s.tiles) : 1;
-  int64_t slices = std::min(ceil_div(d.K, 512), most);
-  if (s.tiles > (int)kMaxEcTiles) slices = 1;
-  s.slice_k = (int)round_up(ceil_div(d.K, slices), 128);
-  s.slices = (int)ceil_div(d.K, s.slice_k);
+  const double rows = s.tiles > 0 ? (double)d.rows / s.tiles : 1.0;
+  double least = 0.0;
+  s.slices = 1;
+  s.slice_k = (int)round_up(d.K, 512);
+  for (int64_t n = 1; n <= ceil_div(d.K, 512) && s.tiles <= (int)kMaxEcTiles; n *= 2) {
+    const int64_t k = round_up(ceil_div(d.K, n), 512), slices = ceil_div(d.K, k);
+    const double read = (double)k * 2.0 * (rows + d.rank) / 50e3, waits = (double)ceil_div(s.tiles * slices, cus);
+    const double us = read * waits + (slices > 1 ? 2.0 + (double)slices * rows * d.rank * 4.0 / 40e3 : 0.0);
+    if (n == 1 || us < least) {
+      least = us;
+      s.slice_k = (int)k;
+      s.slices = (int)slices;
+    }
+  }
   size_t at = kSyncHeaderBytes;
   s.H = at;
   at += (size_t)s.tiles * kAdapterTile * 2 * s.rank_pad * 2;
