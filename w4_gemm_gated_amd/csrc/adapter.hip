@@ -269,18 +269,28 @@ __global__ void __launch_bounds__(kShrinkThreads) adapter_shrink_kernel(AdapterA
   float* h = (float*)lds;
   const __amdgpu_buffer_rsrc_t all = make_rsrc(parts, (uint32_t)(tile_bytes * a.slices));
   const int quads = a.rank / 4;
-  for (int u = tid; u < t.rows * quads; u += kShrinkThreads) {
-    f4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    int s = 0;
-    for (; s + 4 <= a.slices; s += 4) {
-      f4_t v[4];
+  // (two values of a thread and eight slices in flight together; loads past either end are
+  // out of the buffer and give zeros)
+  for (int u0 = tid; u0 < t.rows * quads; u0 += 2 * kShrinkThreads) {
+    f4_t sum[2] = {};
+    for (int s0 = 0; s0 < a.slices; s0 += 8) {
+      f4_t v[8][2];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) v[n] = buffer_load_f4_dev(all, (uint32_t)((s + n) * tile_bytes) + 16u * u);
+      for (int n = 0; n < 8; ++n)
 #pragma unroll
-      for (int n = 0; n < 4; ++n) sum += v[n];
+        for (int i = 0; i < 2; ++i) {
+          const int u = u0 + i * kShrinkThreads;
+          v[n][i] = buffer_load_f4_dev(all, s0 + n < a.slices && u < t.rows * quads
+                                                ? (uint32_t)((s0 + n) * tile_bytes) + 16u * u : kOutOfRange);
+        }
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sum[i] += v[n][i];
     }
-    for (; s < a.slices; ++s) sum += buffer_load_f4_dev(all, (uint32_t)(s * tile_bytes) + 16u * u);
-    *(f4_t*)(h + 4 * u) = sum;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (u0 + i * kShrinkThreads < t.rows * quads) *(f4_t*)(h + 4 * (u0 + i * kShrinkThreads)) = sum[i];
   }
   __syncthreads();
   {
@@ -334,27 +344,16 @@ __global__ void __launch_bounds__(kShrinkThreads) adapter_shrink_kernel(AdapterA
 // 64-byte pieces of sixteen rows.  SB: 32-rank blocks of B; PACK (rank 8 or 16): both halves of H
 // share one block.
 //
-// What a group of 16 rows needs is requested while the group before it is computed.
-template <int SB, bool PACK>
-__global__ void __launch_bounds__(kThreads) adapter_expand_kernel(AdapterArgs a) {
-  const int tile = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
-  if (tile >= min(a.plan[0], a.most_tiles)) return;
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, c = lane % 16, oct = lane / 16;
-  const int n0 = (chunk * kWaves + wave) * kUnit;
-  if (n0 >= a.N) return;
-  const int4 q = plan_tiles(a.plan)[tile];
-  const Tile t = {min(max(q.x, 0), a.adapters - 1), min(max(q.y, 0), a.rows - 1), min(max(q.z, 1), kAdapterTile)};
+// With more than 16 rows the four waves share the tile's H through LDS (read by each of
+// them from memory it cost 8 us of 32 at 2048 rows and rank 64: the vector caches, not
+// memory, were the bound), up to rank 128; Y, B and H are all requested at once.
+template <int SB, bool PACK, int SUB, bool LDS>
+__device__ __forceinline__ void expand(const AdapterArgs& a, const Tile& t, int tile, int n0, half_t* lds) {
+  constexpr int kH = PACK ? 1 : 2 * SB;
+  const int tid = threadIdx.x, lane = tid % kWave, c = lane % 16, oct = lane / 16;
   const int32_t* list = a.plan + kPlanHead + 4 * (int64_t)a.most_tiles;
   const half_t* H = (const half_t*)a.H + (int64_t)tile * kAdapterTile * 2 * a.rank_pad;
-  const float* factors = a.factor + (int64_t)tile * kAdapterTile;
-  const bool whole = a.y_vectors && n0 + kUnit <= a.N;      // (else column by column)
-  const int groups = (t.rows + 15) / 16;
-  half_t* y[4];
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int32_t token = min(max(list[t.first + min(16 * g + c, t.rows - 1)], 0), a.rows - 1);
-    y[g] = (half_t*)a.Y + (int64_t)token * a.y_stride + n0 + 8 * oct;
-  }
+  const bool some = n0 < a.N, whole = a.y_vectors && n0 + kUnit <= a.N;     // (else column by column)
   half8_t b[4][SB];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -366,60 +365,41 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(AdapterArgs a)
       b[j][s] = load_half8(row + 8 * min(o, a.rank / 8 - 1));
     }
   }
-  constexpr int kH = PACK ? 1 : 2 * SB;
-  struct Group {
-    half8_t h[kH], old[2];
-    float factor;
-  };
-  auto request = [&](int g, Group& r) {
+  // H's rows: 2 rank_pad halves, a place of eight more between them in LDS.
+  const int octets = a.rank_pad / 4, stride = 8 * octets + 8;
+  constexpr int kStage = LDS ? kAdapterTile * 8 * SB / kThreads : 1;      // 16-byte pieces of a thread
+  half8_t staged[kStage];
+  if constexpr (LDS)
+#pragma unroll
+    for (int i = 0; i < kStage; ++i) {
+      const int u = tid + i * kThreads;
+      staged[i] = load_half8(H + 8 * (int64_t)min(u, t.rows * octets - 1));
+    }
+  half_t* y[SUB];
+  half8_t old[SUB][2];
+  float factor[SUB];
+#pragma unroll
+  for (int g = 0; g < SUB; ++g) {
     const int at = min(16 * g + c, t.rows - 1);
-    const half_t* hr = H + (int64_t)at * 2 * a.rank_pad;
-    if constexpr (PACK) {
-      r.h[0] = load_half8(hr + 8 * min(oct, a.rank / 4 - 1));
-    } else {
+    const int32_t token = min(max(list[t.first + at], 0), a.rows - 1);
+    y[g] = (half_t*)a.Y + (int64_t)token * a.y_stride + n0 + 8 * oct;
+    factor[g] = a.factor[(int64_t)tile * kAdapterTile + at];
+  }
 #pragma unroll
-      for (int s = 0; s < kH; ++s) r.h[s] = load_half8(hr + 32 * s + 8 * oct);
-    }
-    r.factor = factors[at];
+  for (int g = 0; g < SUB; ++g)
     if (whole) {
-      r.old[0] = load_half8(y[g]);
-      r.old[1] = load_half8(y[g] + 32);
+      old[g][0] = load_half8(y[g]);
+      old[g][1] = load_half8(y[g] + 32);
     }
-  };
-  auto compute = [&](int g, Group& r) {
-    f4_t acc[4];
+  if constexpr (LDS) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      acc[j] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      if constexpr (PACK) {
-        const half8_t hv = oct >= a.rank / 4 ? zero_half8() : r.h[0];
-        acc[j] = mfma16x16x32(b[j][0], hv, acc[j]);
-      } else {
-#pragma unroll
-        for (int s = 0; s < SB; ++s) acc[j] = mfma16x16x32(b[j][s], r.h[SB + s], acc[j]);
-#pragma unroll
-        for (int s = 0; s < SB; ++s) acc[j] = mfma16x16x32(b[j][s], r.h[s], acc[j]);
-      }
+    for (int i = 0; i < kStage; ++i) {
+      const int u = tid + i * kThreads;
+      if (u < t.rows * octets) *(half8_t*)(lds + u / octets * stride + 8 * (u % octets)) = staged[i];
     }
-    if (16 * g + c >= t.rows) return;
-    if (whole) {
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        half8_t o;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) o[n] = (half_t)__builtin_fmaf(r.factor, acc[2 * v + n / 4][n % 4], (float)r.old[v][n]);
-        *(half8_t*)(y[g] + 32 * v) = o;
-      }
-    } else {
-#pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        const int at = 32 * (n / 8) + n % 8;
-        if (n0 + 8 * oct + at < a.N) y[g][at] = (half_t)__builtin_fmaf(r.factor, acc[n / 4][n % 4], (float)y[g][at]);
-      }
-    }
-  };
-  Group ring[2];
-  request(0, ring[0]);
+    __syncthreads();
+  }
+  if (!some) return;
   // (ranks past the last count nothing, whatever lies there)
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -427,11 +407,62 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(AdapterArgs a)
     for (int s = 0; s < SB; ++s)
       if (PACK ? oct >= a.rank / 4 : 4 * s + oct >= a.rank / 8) b[j][s] = zero_half8();
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    if (g >= groups) break;
-    if (g + 1 < groups) request(g + 1, ring[(g + 1) % 2]);
-    compute(g, ring[g % 2]);
+  for (int g = 0; g < SUB; ++g) {
+    if (16 * g >= t.rows) break;
+    const int at = min(16 * g + c, t.rows - 1);
+    const half_t* hr = LDS ? lds + at * stride : H + (int64_t)at * 8 * octets;
+    half8_t h[kH];
+    if constexpr (PACK) {
+      h[0] = load_half8(hr + 8 * min(oct, a.rank / 4 - 1));
+      if (oct >= a.rank / 4) h[0] = zero_half8();
+    } else {
+#pragma unroll
+      for (int s = 0; s < kH; ++s) h[s] = load_half8(hr + 32 * s + 8 * oct);
+    }
+    f4_t acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      acc[j] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (PACK) {
+        acc[j] = mfma16x16x32(b[j][0], h[0], acc[j]);
+      } else {
+#pragma unroll
+        for (int s = 0; s < SB; ++s) acc[j] = mfma16x16x32(b[j][s], h[SB + s], acc[j]);
+#pragma unroll
+        for (int s = 0; s < SB; ++s) acc[j] = mfma16x16x32(b[j][s], h[s], acc[j]);
+      }
+    }
+    if (16 * g + c >= t.rows) continue;
+    if (whole) {
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        half8_t o;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) o[n] = (half_t)__builtin_fmaf(factor[g], acc[2 * v + n / 4][n % 4], (float)old[g][v][n]);
+        *(half8_t*)(y[g] + 32 * v) = o;
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        const int col = 32 * (n / 8) + n % 8;
+        if (n0 + 8 * oct + col < a.N)
+          y[g][col] = (half_t)__builtin_fmaf(factor[g], acc[n / 4][n % 4], (float)y[g][col]);
+      }
+    }
   }
+}
+
+template <int SB, bool PACK>
+__global__ void __launch_bounds__(kThreads) adapter_expand_kernel(AdapterArgs a) {
+  constexpr bool kLds = SB <= 4;
+  __shared__ __attribute__((aligned(16))) half_t lds[kLds ? kAdapterTile * (64 * SB + 8) : 8];
+  const int tile = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks, wave = threadIdx.x / kWave;
+  if (tile >= min(a.plan[0], a.most_tiles)) return;
+  const int n0 = (chunk * kWaves + wave) * kUnit;
+  const int4 q = plan_tiles(a.plan)[tile];
+  const Tile t = {min(max(q.x, 0), a.adapters - 1), min(max(q.y, 0), a.rows - 1), min(max(q.z, 1), kAdapterTile)};
+  if (t.rows <= 16) expand<SB, PACK, 1, false>(a, t, tile, n0, lds);
+  else expand<SB, PACK, 4, kLds>(a, t, tile, n0, lds);
 }
 
 template <int RB>
