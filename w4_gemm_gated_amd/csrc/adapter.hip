@@ -155,12 +155,17 @@ __device__ __forceinline__ void store_f4_dev(__amdgpu_buffer_rsrc_t r, uint32_t 
 struct Tile {
   int adapter, first, rows;
 };
+__device__ __forceinline__ Tile tile_of(const AdapterArgs& a, int tile) {
+  const int4 q = plan_tiles(a.plan)[tile];
+  return {min(max(q.x, 0), a.adapters - 1), min(max(q.y, 0), a.rows - 1), min(max(q.z, 1), kAdapterTile)};
+}
 
 // Ranks [rank0, rank0 + 16 RB) of one slice of K for a tile of up to 16 SUB rows: the
 // waves take 64 k in turn (whole lines of X and A), and add their sums through LDS.
-template <int RB, int SUB>
+// keep(row, rank, four sums)
+template <int RB, int SUB, typename F>
 __device__ __forceinline__ void shrink(const AdapterArgs& a, const Tile& t, const int32_t* list, int rank0, int k_lo,
-                                       int k_hi, f4_t* red, __amdgpu_buffer_rsrc_t part) {
+                                       int k_hi, f4_t* red, F keep) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, c = lane % 16, oct = lane / 16;
   const half_t* x[SUB];
   const half_t* w[RB];
@@ -235,8 +240,51 @@ __device__ __forceinline__ void shrink(const AdapterArgs& a, const Tile& t, cons
 #pragma unroll
     for (int v = 1; v < kHalf; ++v) sum += red[(v * kUnits + u) * kWave + lane];
     const int row = 16 * (u / RB) + c, rank = rank0 + 16 * (u % RB) + 4 * oct;
-    if (row < t.rows && rank < a.rank) store_f4_dev(part, 4u * (uint32_t)(row * a.rank + rank), sum);
+    if (row < t.rows && rank < a.rank) keep(row, rank, sum);
   }
+}
+
+// H's rows (fp32, in LDS) as two fp16 numbers per value, and the factor of each row: the
+// power of two that they are relative to times the adapter's scale.
+template <int ROWS>
+__device__ __forceinline__ void to_halves(const AdapterArgs& a, const Tile& t, const float* h, float* factor, half_t* out,
+                                          int stride) {
+  constexpr int kLanes = kShrinkThreads / ROWS;     // to a row
+  static_assert(kLanes <= kWave, "a row's lanes are of one wave");
+  const int tid = threadIdx.x, row = tid / kLanes;
+  float most = 0.0f;
+  if (row < t.rows)
+    for (int i = tid % kLanes; i < a.rank; i += kLanes) {
+      const float v = fabsf(h[row * a.rank + i]);
+      most = v > most || v != v ? v : most;
+    }
+#pragma unroll
+  for (int o = 1; o < kLanes; o *= 2) {
+    const float v = __shfl_xor(most, o);
+    most = v > most || v != v ? v : most;
+  }
+  // The power of two at or below the row's largest (1 where that is zero, infinite or NaN).
+  const uint32_t e = float_bits(most) >> 23;
+  const float p = e == 0 ? (most > 0.0f ? 0x1p-126f : 1.0f) : e == 255 ? 1.0f : bits_float(e << 23);
+  if (row < t.rows) {
+    const float inv = 1.0f / p;
+    for (int o = tid % kLanes; o < a.rank_pad / 8; o += kLanes) {
+      half8_t hi = zero_half8(), lo = zero_half8();
+      if (8 * o < a.rank) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          float v = h[row * a.rank + 8 * o + n] * inv;
+          if (fabsf(v) > 65504.0f && fabsf(v) < INFINITY) v = copysignf(65504.0f, v);   // (beside an infinity or NaN)
+          hi[n] = (half_t)v;
+          lo[n] = fabsf(v) < INFINITY ? (half_t)(v - (float)hi[n]) : (half_t)0.0f;
+        }
+      }
+      *(half8_t*)(out + row * stride + 8 * o) = hi;
+      *(half8_t*)(out + row * stride + a.rank_pad + 8 * o) = lo;
+    }
+    if (tid % kLanes == 0) factor[row] = p * (a.scale ? a.scale[t.adapter] : 1.0f);
+  }
+  __syncthreads();
 }
 
 template <int RB>
@@ -246,16 +294,16 @@ __global__ void __launch_bounds__(kShrinkThreads) adapter_shrink_kernel(AdapterA
   __shared__ uint32_t arrived;
   const int tile = blockIdx.x / a.slices, slice = blockIdx.x % a.slices, tid = threadIdx.x;
   if (tile >= min(a.plan[0], a.most_tiles)) return;
-  const int4 q = plan_tiles(a.plan)[tile];
-  const Tile t = {min(max(q.x, 0), a.adapters - 1), min(max(q.y, 0), a.rows - 1), min(max(q.z, 1), kAdapterTile)};
+  const Tile t = tile_of(a, tile);
   const int32_t* list = a.plan + kPlanHead + 4 * (int64_t)a.most_tiles;
   const size_t tile_bytes = (size_t)kAdapterTile * a.rank * 4;
   char* parts = a.part + (size_t)tile * a.slices * tile_bytes;
   const __amdgpu_buffer_rsrc_t part = make_rsrc(parts + slice * tile_bytes, (uint32_t)tile_bytes);
   const int k_lo = slice * a.slice_k, k_hi = min(k_lo + a.slice_k, a.K);
   for (int rank0 = 0; rank0 < a.rank; rank0 += 16 * RB) {
-    if (t.rows <= 16) shrink<RB, 1>(a, t, list, rank0, k_lo, k_hi, lds, part);
-    else shrink<RB, 4>(a, t, list, rank0, k_lo, k_hi, lds, part);
+    auto keep = [&](int row, int rank, const f4_t& v) { store_f4_dev(part, 4u * (uint32_t)(row * a.rank + rank), v); };
+    if (t.rows <= 16) shrink<RB, 1>(a, t, list, rank0, k_lo, k_hi, lds, keep);
+    else shrink<RB, 4>(a, t, list, rank0, k_lo, k_hi, lds, keep);
   }
   drain_vm();
   __syncthreads();
@@ -293,47 +341,8 @@ __global__ void __launch_bounds__(kShrinkThreads) adapter_shrink_kernel(AdapterA
       if (u0 + i * kShrinkThreads < t.rows * quads) *(f4_t*)(h + 4 * (u0 + i * kShrinkThreads)) = sum[i];
   }
   __syncthreads();
-  {
-    constexpr int kLanes = kShrinkThreads / kAdapterTile;     // lanes to a row
-    const int row = tid / kLanes;
-    float most = 0.0f;
-    if (row < t.rows)
-      for (int i = tid % kLanes; i < a.rank; i += kLanes) {
-        const float v = fabsf(h[row * a.rank + i]);
-        most = v > most || v != v ? v : most;
-      }
-#pragma unroll
-    for (int o = 1; o < kLanes; o *= 2) {
-      const float v = __shfl_xor(most, o);
-      most = v > most || v != v ? v : most;
-    }
-    // The power of two at or below the row's largest (1 where that is zero, infinite or NaN).
-    const uint32_t e = float_bits(most) >> 23;
-    const float p = e == 0 ? (most > 0.0f ? 0x1p-126f : 1.0f) : e == 255 ? 1.0f : bits_float(e << 23);
-    if (tid % kLanes == 0 && row < t.rows) {
-      factor[row] = p;
-      a.factor[(int64_t)tile * kAdapterTile + row] = p * (a.scale ? a.scale[t.adapter] : 1.0f);
-    }
-  }
-  __syncthreads();
-  const int octets = a.rank_pad / 8;
-  half_t* out = (half_t*)a.H + (int64_t)tile * kAdapterTile * 2 * a.rank_pad;
-  for (int u = tid; u < t.rows * octets; u += kShrinkThreads) {
-    const int row = u / octets, o = u % octets;
-    half8_t hi = zero_half8(), lo = zero_half8();
-    if (8 * o < a.rank) {
-      const float inv = 1.0f / factor[row];
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        float v = h[row * a.rank + 8 * o + n] * inv;
-        if (fabsf(v) > 65504.0f && fabsf(v) < INFINITY) v = copysignf(65504.0f, v);   // (beside an infinity or NaN)
-        hi[n] = (half_t)v;
-        lo[n] = fabsf(v) < INFINITY ? (half_t)(v - (float)hi[n]) : (half_t)0.0f;
-      }
-    }
-    *(half8_t*)(out + (int64_t)row * 2 * a.rank_pad + 8 * o) = hi;
-    *(half8_t*)(out + (int64_t)row * 2 * a.rank_pad + a.rank_pad + 8 * o) = lo;
-  }
+  to_halves<kAdapterTile>(a, t, h, factor, (half_t*)a.H + (int64_t)tile * kAdapterTile * 2 * a.rank_pad, 2 * a.rank_pad);
+  if (tid < t.rows) a.factor[(int64_t)tile * kAdapterTile + tid] = factor[tid];
 }
 
 // ------------------------------------------------------------ second product
@@ -344,17 +353,16 @@ __global__ void __launch_bounds__(kShrinkThreads) adapter_shrink_kernel(AdapterA
 // 64-byte pieces of sixteen rows.  SB: 32-rank blocks of B; PACK (rank 8 or 16): both halves of H
 // share one block.
 //
-// With more than 16 rows the four waves share the tile's H through LDS (read by each of
-// them from memory it cost 8 us of 32 at 2048 rows and rank 64: the vector caches, not
-// memory, were the bound), up to rank 128; Y, B and H are all requested at once.
-template <int SB, bool PACK, int SUB, bool LDS>
-__device__ __forceinline__ void expand(const AdapterArgs& a, const Tile& t, int tile, int n0, half_t* lds) {
-  constexpr int kH = PACK ? 1 : 2 * SB;
-  const int tid = threadIdx.x, lane = tid % kWave, c = lane % 16, oct = lane / 16;
+template <int SB, int SUB>
+struct Operands {
+  half8_t b[4][SB], old[SUB][2];
+  half_t* y[SUB];
+};
+
+template <int SB, bool PACK, int SUB>
+__device__ __forceinline__ void request(const AdapterArgs& a, const Tile& t, int n0, Operands<SB, SUB>& r) {
+  const int lane = threadIdx.x % kWave, c = lane % 16, oct = lane / 16;
   const int32_t* list = a.plan + kPlanHead + 4 * (int64_t)a.most_tiles;
-  const half_t* H = (const half_t*)a.H + (int64_t)tile * kAdapterTile * 2 * a.rank_pad;
-  const bool some = n0 < a.N, whole = a.y_vectors && n0 + kUnit <= a.N;     // (else column by column)
-  half8_t b[4][SB];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int n = min(n0 + 32 * (j / 2) + 8 * (c / 4) + 4 * (j % 2) + c % 4, a.N - 1);    // (a column past the last is not stored)
@@ -362,55 +370,41 @@ __device__ __forceinline__ void expand(const AdapterArgs& a, const Tile& t, int 
 #pragma unroll
     for (int s = 0; s < SB; ++s) {
       const int o = PACK ? oct % (a.rank / 8) : 4 * s + oct;
-      b[j][s] = load_half8(row + 8 * min(o, a.rank / 8 - 1));
+      r.b[j][s] = load_half8(row + 8 * min(o, a.rank / 8 - 1));
     }
   }
-  // H's rows: 2 rank_pad halves, a place of eight more between them in LDS.
-  const int octets = a.rank_pad / 4, stride = 8 * octets + 8;
-  constexpr int kStage = LDS ? kAdapterTile * 8 * SB / kThreads : 1;      // 16-byte pieces of a thread
-  half8_t staged[kStage];
-  if constexpr (LDS)
-#pragma unroll
-    for (int i = 0; i < kStage; ++i) {
-      const int u = tid + i * kThreads;
-      staged[i] = load_half8(H + 8 * (int64_t)min(u, t.rows * octets - 1));
-    }
-  half_t* y[SUB];
-  half8_t old[SUB][2];
-  float factor[SUB];
 #pragma unroll
   for (int g = 0; g < SUB; ++g) {
-    const int at = min(16 * g + c, t.rows - 1);
-    const int32_t token = min(max(list[t.first + at], 0), a.rows - 1);
-    y[g] = (half_t*)a.Y + (int64_t)token * a.y_stride + n0 + 8 * oct;
-    factor[g] = a.factor[(int64_t)tile * kAdapterTile + at];
+    const int32_t token = min(max(list[t.first + min(16 * g + c, t.rows - 1)], 0), a.rows - 1);
+    r.y[g] = (half_t*)a.Y + (int64_t)token * a.y_stride + n0 + 8 * oct;
   }
+  if (a.y_vectors && n0 + kUnit <= a.N)      // (else column by column)
 #pragma unroll
-  for (int g = 0; g < SUB; ++g)
-    if (whole) {
-      old[g][0] = load_half8(y[g]);
-      old[g][1] = load_half8(y[g] + 32);
+    for (int g = 0; g < SUB; ++g) {
+      r.old[g][0] = load_half8(r.y[g]);
+      r.old[g][1] = load_half8(r.y[g] + 32);
     }
-  if constexpr (LDS) {
-#pragma unroll
-    for (int i = 0; i < kStage; ++i) {
-      const int u = tid + i * kThreads;
-      if (u < t.rows * octets) *(half8_t*)(lds + u / octets * stride + 8 * (u % octets)) = staged[i];
-    }
-    __syncthreads();
-  }
-  if (!some) return;
+}
+
+// The product of a unit, and Y with it.  H's rows are `stride` halves apart.
+template <int SB, bool PACK, int SUB>
+__device__ __forceinline__ void apply(const AdapterArgs& a, const Tile& t, int n0, Operands<SB, SUB>& r, const half_t* H,
+                                      int stride, const float* factor) {
+  constexpr int kH = PACK ? 1 : 2 * SB;
+  const int lane = threadIdx.x % kWave, c = lane % 16, oct = lane / 16;
+  const bool whole = a.y_vectors && n0 + kUnit <= a.N;
   // (ranks past the last count nothing, whatever lies there)
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int s = 0; s < SB; ++s)
-      if (PACK ? oct >= a.rank / 4 : 4 * s + oct >= a.rank / 8) b[j][s] = zero_half8();
+      if (PACK ? oct >= a.rank / 4 : 4 * s + oct >= a.rank / 8) r.b[j][s] = zero_half8();
 #pragma unroll
   for (int g = 0; g < SUB; ++g) {
     if (16 * g >= t.rows) break;
     const int at = min(16 * g + c, t.rows - 1);
-    const half_t* hr = LDS ? lds + at * stride : H + (int64_t)at * 8 * octets;
+    const half_t* hr = H + at * stride;
+    const float f = factor[at];
     half8_t h[kH];
     if constexpr (PACK) {
       h[0] = load_half8(hr + 8 * min(oct, a.rank / 4 - 1));
@@ -424,12 +418,12 @@ __device__ __forceinline__ void expand(const AdapterArgs& a, const Tile& t, int 
     for (int j = 0; j < 4; ++j) {
       acc[j] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
       if constexpr (PACK) {
-        acc[j] = mfma16x16x32(b[j][0], h[0], acc[j]);
+        acc[j] = mfma16x16x32(r.b[j][0], h[0], acc[j]);
       } else {
 #pragma unroll
-        for (int s = 0; s < SB; ++s) acc[j] = mfma16x16x32(b[j][s], h[SB + s], acc[j]);
+        for (int s = 0; s < SB; ++s) acc[j] = mfma16x16x32(r.b[j][s], h[SB + s], acc[j]);
 #pragma unroll
-        for (int s = 0; s < SB; ++s) acc[j] = mfma16x16x32(b[j][s], h[s], acc[j]);
+        for (int s = 0; s < SB; ++s) acc[j] = mfma16x16x32(r.b[j][s], h[s], acc[j]);
       }
     }
     if (16 * g + c >= t.rows) continue;
@@ -438,31 +432,87 @@ __device__ __forceinline__ void expand(const AdapterArgs& a, const Tile& t, int 
       for (int v = 0; v < 2; ++v) {
         half8_t o;
 #pragma unroll
-        for (int n = 0; n < 8; ++n) o[n] = (half_t)__builtin_fmaf(factor[g], acc[2 * v + n / 4][n % 4], (float)old[g][v][n]);
-        *(half8_t*)(y[g] + 32 * v) = o;
+        for (int n = 0; n < 8; ++n) o[n] = (half_t)__builtin_fmaf(f, acc[2 * v + n / 4][n % 4], (float)r.old[g][v][n]);
+        *(half8_t*)(r.y[g] + 32 * v) = o;
       }
     } else {
 #pragma unroll
       for (int n = 0; n < 16; ++n) {
         const int col = 32 * (n / 8) + n % 8;
         if (n0 + 8 * oct + col < a.N)
-          y[g][col] = (half_t)__builtin_fmaf(factor[g], acc[n / 4][n % 4], (float)y[g][col]);
+          r.y[g][col] = (half_t)__builtin_fmaf(f, acc[n / 4][n % 4], (float)r.y[g][col]);
       }
     }
   }
 }
 
+// With more than 16 rows the four waves share the tile's H through LDS (read by each of
+// them from memory it cost 8 us of 32 at 2048 rows and rank 64: the vector caches, not
+// memory, were the bound), up to rank 128; Y, B and H are all requested at once.
 template <int SB, bool PACK>
 __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(AdapterArgs a) {
   constexpr bool kLds = SB <= 4;
+  constexpr int kStage = kAdapterTile * 8 * SB / kThreads;      // 16-byte pieces of a thread
   __shared__ __attribute__((aligned(16))) half_t lds[kLds ? kAdapterTile * (64 * SB + 8) : 8];
-  const int tile = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks, wave = threadIdx.x / kWave;
+  const int tile = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks, tid = threadIdx.x, wave = tid / kWave;
   if (tile >= min(a.plan[0], a.most_tiles)) return;
   const int n0 = (chunk * kWaves + wave) * kUnit;
-  const int4 q = plan_tiles(a.plan)[tile];
-  const Tile t = {min(max(q.x, 0), a.adapters - 1), min(max(q.y, 0), a.rows - 1), min(max(q.z, 1), kAdapterTile)};
-  if (t.rows <= 16) expand<SB, PACK, 1, false>(a, t, tile, n0, lds);
-  else expand<SB, PACK, 4, kLds>(a, t, tile, n0, lds);
+  const Tile t = tile_of(a, tile);
+  // (a row: 2 rank_pad halves, and a place of eight more in LDS)
+  const int octets = a.rank_pad / 4, stride = 8 * octets + 8;
+  const half_t* H = (const half_t*)a.H + (int64_t)tile * kAdapterTile * 8 * octets;
+  const float* factor = a.factor + (int64_t)tile * kAdapterTile;
+  if (t.rows <= 16) {
+    if (n0 >= a.N) return;
+    Operands<SB, 1> r;
+    request<SB, PACK, 1>(a, t, n0, r);
+    apply<SB, PACK, 1>(a, t, n0, r, H, 8 * octets, factor);
+    return;
+  }
+  half8_t staged[kStage];
+  if constexpr (kLds)
+#pragma unroll
+    for (int i = 0; i < kStage; ++i) staged[i] = load_half8(H + 8 * (int64_t)min(tid + i * kThreads, t.rows * octets - 1));
+  Operands<SB, 4> r;
+  if (n0 < a.N) request<SB, PACK, 4>(a, t, n0, r);
+  if constexpr (kLds) {
+#pragma unroll
+    for (int i = 0; i < kStage; ++i) {
+      const int u = tid + i * kThreads;
+      if (u < t.rows * octets) *(half8_t*)(lds + u / octets * stride + 8 * (u % octets)) = staged[i];
+    }
+    __syncthreads();
+  }
+  if (n0 < a.N) apply<SB, PACK, 4>(a, t, n0, r, kLds ? lds : H, kLds ? stride : 8 * octets, factor);
+}
+
+// Both products in one launch, for few rows and a short K: every workgroup of a tile forms
+// its H by itself (from the XCD's L2, after the first) and applies it to its columns,
+// whose B and Y come in meanwhile.  Tiles of more rows go sixteen at a time.
+template <int RB, int SB, bool PACK>
+__global__ void __launch_bounds__(kShrinkThreads) adapter_fused_kernel(AdapterArgs a) {
+  constexpr int kStride = (PACK ? 32 : 64 * SB) + 8;
+  __shared__ f4_t red[kShrinkWaves / 2 * RB * kWave];
+  __shared__ float h[16 * 16 * RB];
+  __shared__ __attribute__((aligned(16))) half_t halves[16 * kStride];
+  __shared__ float factor[16];
+  const int tile = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks, wave = threadIdx.x / kWave;
+  if (tile >= min(a.plan[0], a.most_tiles)) return;
+  const Tile whole = tile_of(a, tile);
+  const int32_t* list = a.plan + kPlanHead + 4 * (int64_t)a.most_tiles;
+  const int n_end = min((chunk + 1) * a.chunk_columns, a.N), n0 = chunk * a.chunk_columns + wave * kUnit;
+  for (int row0 = 0; row0 < whole.rows; row0 += 16) {
+    const Tile t = {whole.adapter, whole.first + row0, min(whole.rows - row0, 16)};
+    Operands<SB, 1> r;
+    if (n0 < n_end) request<SB, PACK, 1>(a, t, n0, r);
+    shrink<RB, 1>(a, t, list, 0, 0, a.K, red, [&](int row, int rank, const f4_t& v) { *(f4_t*)(h + row * a.rank + rank) = v; });
+    __syncthreads();
+    to_halves<16>(a, t, h, factor, halves, kStride);
+    for (int n = n0; n < n_end; n += kShrinkWaves * kUnit) {
+      if (n > n0) request<SB, PACK, 1>(a, t, n, r);
+      apply<SB, PACK, 1>(a, t, n, r, halves, kStride, factor);
+    }
+  }
 }
 
 template <int RB>
@@ -489,27 +539,33 @@ size_t adapter_plan_size(int64_t rows, int64_t batch, int64_t adapters) {
   return 4 * (size_t)(kPlanHead + 4 * adapter_most_tiles(rows, batch, adapters) + rows);
 }
 
-// Slices of K by what a call is expected to take: a workgroup reads its rows of X and
-// its ranks of A at about 50 bytes a ns, workgroups past the CUs' number wait for a place,
-// and slices are joined in 2 us and the time in which one workgroup reads them.
+// The launch shape by what a call is expected to take.  A workgroup reads its rows of X
+// and its ranks of A at about 25 bytes a ns, and workgroups past the CUs' number wait for
+// a place.  Two launches: slices of K (at least 512, joined in 2 us and the time in which
+// one workgroup reads them), and 4 us more than one.  One launch: all of K in every
+// workgroup, for as many columns as leave no more workgroups than CUs.
 AdapterShape adapter_shape(const spear_adapter_desc_t& d, int cus) {
   AdapterShape s;
   s.tiles = (int)adapter_most_tiles(d.rows, d.batch, d.adapters);
   s.rank_pad = d.rank <= 16 ? d.rank : d.rank <= 32 ? 32 : d.rank <= 64 ? 64 : d.rank <= 128 ? 128 : 256;
   const double rows = s.tiles > 0 ? (double)d.rows / s.tiles : 1.0;
+  auto reads = [&](double k, int64_t workgroups) { return k * 2.0 * (rows + d.rank) / 25e3 * (double)ceil_div(workgroups, cus); };
   double least = 0.0;
   s.slices = 1;
   s.slice_k = (int)round_up(d.K, 512);
-  for (int64_t n = 1; n <= ceil_div(d.K, 512) && s.tiles <= (int)kMaxEcTiles; n *= 2) {
+  for (int64_t n = 1; n <= std::min<int64_t>(ceil_div(d.K, 512), 64) && s.tiles <= (int)kMaxEcTiles; ++n) {
     const int64_t k = round_up(ceil_div(d.K, n), 512), slices = ceil_div(d.K, k);
-    const double read = (double)k * 2.0 * (rows + d.rank) / 50e3, waits = (double)ceil_div(s.tiles * slices, cus);
-    const double us = read * waits + (slices > 1 ? 2.0 + (double)slices * rows * d.rank * 4.0 / 40e3 : 0.0);
+    const double us = reads((double)k, s.tiles * slices) + (slices > 1 ? 2.0 + (double)slices * rows * d.rank * 4.0 / 80e3 : 0.0);
     if (n == 1 || us < least) {
       least = us;
       s.slice_k = (int)k;
       s.slices = (int)slices;
     }
   }
+  const int64_t units = ceil_div(d.N, 2 * kAdapterColumns), fit = s.tiles > 0 ? std::max<int64_t>(1, cus / s.tiles) : 1;
+  const int64_t chunks = std::min(units, fit);
+  s.fused = d.rank <= 64 && rows <= 16.0 && reads((double)d.K, s.tiles * chunks) <= least + 4.0;
+  s.chunk_columns = s.fused ? (int)(2 * kAdapterColumns * ceil_div(units, chunks)) : kAdapterColumns;
   size_t at = kSyncHeaderBytes;
   s.H = at;
   at += (size_t)s.tiles * kAdapterTile * 2 * s.rank_pad * 2;
@@ -523,6 +579,13 @@ AdapterShape adapter_shape(const spear_adapter_desc_t& d, int cus) {
 
 hipError_t launch_adapter(const AdapterArgs& a, void* stream) {
   hipStream_t s = (hipStream_t)stream;
+  if (a.fused) {
+    const dim3 grid((unsigned)(a.most_tiles * (int64_t)a.chunks)), block(kShrinkThreads);
+    if (a.rank <= 16) adapter_fused_kernel<1, 1, true><<<grid, block, 0, s>>>(a);
+    else if (a.rank_pad == 32) adapter_fused_kernel<2, 1, false><<<grid, block, 0, s>>>(a);
+    else adapter_fused_kernel<4, 2, false><<<grid, block, 0, s>>>(a);
+    return hipGetLastError();
+  }
   const hipError_t e = a.rank <= 16 ? shrink_launch<1>(a, s) : a.rank <= 32 ? shrink_launch<2>(a, s) : shrink_launch<4>(a, s);
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)(a.most_tiles * (int64_t)a.chunks)), block(kThreads);
