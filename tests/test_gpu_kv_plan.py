@@ -77,6 +77,16 @@ def test_against_the_oracle(B, page, max_len, most_new, spare):
         check(s, rows, page)
 
 
+@pytest.mark.parametrize("B", [1023, 1026, 2047, 2048, 2049, 4100])
+def test_a_few_sequences_more_or_less_than_threads_hold(B):
+    rng = np.random.default_rng(B)
+    s = state(rng, B, 16, 90, 6, 0.7)
+    total = int(s[1].sum())
+    for rows in (total + 3, total * 3 // 4):
+        note(f"B {B} new {total} rows {rows}")
+        check(s, rows, 16)
+
+
 @pytest.mark.parametrize("seed", range(4))
 def test_sequences_that_cannot_be_served(seed):
     rng = np.random.default_rng(seed)

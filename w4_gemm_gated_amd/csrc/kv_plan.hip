@@ -5,7 +5,7 @@
 // stack of free ones, of the pages wanted, and of the new tokens.  A sequence is
 // served while the last two stay within what there is, so those that are served
 // come before all that are not, and the offsets of the latter are the totals.
-// The sums take a few microseconds of latency and no bandwidth, so every
+// The sums take a microsecond or two of latency and no bandwidth, so every
 // workgroup forms all of them by itself (no second launch, no exchange) and then
 // fills as many rows as it has threads: it marks the rows at which its sequences
 // begin, a running maximum finds every row's own, and the row looks up its page, in
@@ -47,33 +47,35 @@ __device__ __forceinline__ Wish wish_of(const KvPlanArgs& a, int b) {
   return w;
 }
 
-// Running sums (inclusive) of two values over the workgroup, and their totals.
-struct Two {
-  int64_t x, y;
+// Sums over the sequences up to one: pages given back, new tokens, pages missing.
+struct Sums {
+  int64_t freed, ask, need;
 };
+__device__ __forceinline__ void add(Sums& a, const Sums& b) {
+  a.freed += b.freed;
+  a.ask += b.ask;
+  a.need += b.need;
+}
+
+// Sums before each thread's values, and those of all threads.
 template <int THREADS>
-__device__ __forceinline__ Two running(Two v, Two* waves, Two* total) {
+__device__ __forceinline__ Sums running(const Sums& own, Sums* waves, Sums* total) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  Sums v = own;
 #pragma unroll
   for (int o = 1; o < kWave; o *= 2) {
-    const int64_t x = __shfl_up(v.x, o), y = __shfl_up(v.y, o);
-    if (lane >= o) {
-      v.x += x;
-      v.y += y;
-    }
+    const Sums x = {__shfl_up(v.freed, o), __shfl_up(v.ask, o), __shfl_up(v.need, o)};
+    if (lane >= o) add(v, x);
   }
   __syncthreads();
   if (lane == kWave - 1) waves[wave] = v;
   __syncthreads();
-  Two sum = {0, 0};
+  v = {v.freed - own.freed, v.ask - own.ask, v.need - own.need};
+  Sums sum = {0, 0, 0};
 #pragma unroll
   for (int i = 0; i < THREADS / kWave; ++i) {
-    if (i == wave) {
-      v.x += sum.x;
-      v.y += sum.y;
-    }
-    sum.x += waves[i].x;
-    sum.y += waves[i].y;
+    if (i == wave) add(v, sum);
+    add(sum, waves[i]);
   }
   *total = sum;
   return v;
@@ -102,18 +104,21 @@ struct Begin {
   int64_t take;             // pages taken before its own
 };
 
-template <int THREADS>
+// EACH: neighbouring sequences of a thread.
+template <int THREADS, int EACH>
 __global__ void __launch_bounds__(THREADS) kv_plan_kernel(KvPlanArgs a) {
-  __shared__ Two waves[THREADS / kWave];
+  constexpr int kChunk = THREADS * EACH;
+  __shared__ Sums waves[THREADS / kWave];
   __shared__ int max_waves[THREADS / kWave];
   __shared__ Begin begin[THREADS];
   __shared__ int marked[THREADS];
-  __shared__ int64_t freed_to[THREADS];       // running sum of freed pages in one chunk of sequences
+  __shared__ int64_t freed_to[kChunk];        // running sum of freed pages in one chunk of sequences
+  __shared__ int32_t held_of[kChunk];
   __shared__ int32_t freed_page[THREADS];     // pages taken here that were laid on the stack in this call
   __shared__ unsigned long long given_rows, given_pages, lowest, highest;
   __shared__ uint32_t arrived;
-  const int tid = threadIdx.x;
-  const int chunks = (a.batch + THREADS - 1) / THREADS;
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int chunks = (a.batch + kChunk - 1) / kChunk;
   const int64_t row0 = (int64_t)blockIdx.x * THREADS;
 
   marked[tid] = -1;
@@ -124,13 +129,20 @@ __global__ void __launch_bounds__(THREADS) kv_plan_kernel(KvPlanArgs a) {
   }
   const int64_t old = min(max(*a.free_count, 0), a.free_slots);
   // Pages laid on the stack, all of them before any is taken.
-  Wish w = wish_of(a, tid);
-  Two sum;
+  Wish w[EACH];
+  Sums sum = {0, 0, 0}, v = {0, 0, 0};
+  auto look = [&](int c) {
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) w[e] = wish_of(a, c * kChunk + tid * EACH + e);
+    Sums own = {0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) add(own, {w[e].freed, w[e].ask, w[e].need});
+    v = running<THREADS>(own, waves, &sum);
+  };
   int64_t freed = 0;
   for (int c = 0; c < chunks; ++c) {
-    if (c > 0) w = wish_of(a, c * THREADS + tid);
-    running<THREADS>({w.freed, 0}, waves, &sum);
-    freed += sum.x;
+    look(c);
+    freed += sum.freed;
   }
   const int64_t top = old + freed;
   // (the running sums' barriers come after the clearing above)
@@ -140,30 +152,48 @@ __global__ void __launch_bounds__(THREADS) kv_plan_kernel(KvPlanArgs a) {
   auto serve = [&](bool rows_too, bool state) {
     int64_t rows_before = 0, pages_before = 0;
     for (int c = 0; c < chunks; ++c) {
-      const int b = c * THREADS + tid;
-      if (chunks > 1) w = wish_of(a, b);
-      const Two v = running<THREADS>({w.ask, w.need}, waves, &sum);
-      const int64_t rows_to = rows_before + v.x, pages_to = pages_before + v.y;
-      const bool given = w.valid && rows_to <= a.rows && pages_to <= top;
-      if (given) {
-        atomicMax(&given_rows, (unsigned long long)rows_to);
-        atomicMax(&given_pages, (unsigned long long)pages_to);
+      if (chunks > 1) look(c);
+      int64_t rows_to = rows_before + v.ask, pages_to = pages_before + v.need;
+      int64_t rows_given = -1, pages_given = 0;
+#pragma unroll
+      for (int e = 0; e < EACH; ++e) {
+        rows_to += w[e].ask;
+        pages_to += w[e].need;
+        if (w[e].valid && rows_to <= a.rows && pages_to <= top) {
+          rows_given = rows_to;
+          pages_given = pages_to;
+        }
+      }
+      // (the sums rise: a wave's last served sequence has the largest)
+      const uint64_t some = __ballot(rows_given >= 0);
+      if (some != 0 && lane == 63 - __builtin_clzll(some)) {
+        atomicMax(&given_rows, (unsigned long long)rows_given);
+        atomicMax(&given_pages, (unsigned long long)pages_given);
       }
       __syncthreads();
-      const int64_t first = min(rows_to - w.ask, (int64_t)given_rows);
-      const int32_t n = given ? w.ask : 0;
-      if (rows_too && n > 0 && first < row0 + THREADS && first + n > row0) {
-        const int at = (int)max(first - row0, (int64_t)0);
-        begin[at] = {b, w.lens + (int)(row0 + at - first), w.held, pages_to - w.need};
-        marked[at] = at;
+      rows_to = rows_before + v.ask;
+      pages_to = pages_before + v.need;
+#pragma unroll
+      for (int e = 0; e < EACH; ++e) {
+        const int b = c * kChunk + tid * EACH + e;
+        const int64_t first = min(rows_to, (int64_t)given_rows);
+        rows_to += w[e].ask;
+        pages_to += w[e].need;
+        const bool given = w[e].valid && rows_to <= a.rows && pages_to <= top;
+        const int32_t n = given ? w[e].ask : 0;
+        if (rows_too && n > 0 && first < row0 + THREADS && first + n > row0) {
+          const int at = (int)max(first - row0, (int64_t)0);
+          begin[at] = {b, w[e].lens + (int)(row0 + at - first), w[e].held, pages_to - w[e].need};
+          marked[at] = at;
+        }
+        if (state && b < a.batch) {
+          a.cu_q[b] = (int32_t)first;
+          a.kv_lens[b] = w[e].lens + n;
+          a.held_out[b] = w[e].held - w[e].freed + (given ? w[e].need : 0);
+        }
       }
-      if (state && b < a.batch) {
-        a.cu_q[b] = (int32_t)first;
-        a.kv_lens[b] = w.lens + n;
-        a.held_out[b] = w.held - w.freed + (given ? w.need : 0);
-      }
-      rows_before += sum.x;
-      pages_before += sum.y;
+      rows_before += sum.ask;
+      pages_before += sum.need;
     }
     if (state && tid == 0) {
       a.cu_q[a.batch] = (int32_t)given_rows;
@@ -197,29 +227,31 @@ __global__ void __launch_bounds__(THREADS) kv_plan_kernel(KvPlanArgs a) {
     // Pages laid on the stack in this call: their places are found by the running
     // sum of the sequences that gave them.
     const bool mine = from >= old;
-    if (mine) {
-      atomicMin(&lowest, (unsigned long long)(from - old));
-      atomicMax(&highest, (unsigned long long)(from - old) + 1);
-    }
+    const uint64_t some = __ballot(mine);       // (`from` falls as the rows rise)
+    if (mine && lane == 63 - __builtin_clzll(some)) atomicMin(&lowest, (unsigned long long)(from - old));
+    if (mine && lane == __builtin_ctzll(some)) atomicMax(&highest, (unsigned long long)(from - old) + 1);
     __syncthreads();
-    const int64_t lo = (int64_t)lowest, hi = (int64_t)highest;     // (fewer than THREADS: every page has a row here)
+    const int64_t lo = (int64_t)lowest, hi = (int64_t)highest;     // (at most THREADS: every page has a row here)
     const int64_t stay = min(top - total_pages, (int64_t)a.free_slots) - old;   // of those laid on it, these remain
     int64_t before = 0;
     for (int c = 0; c < chunks; ++c) {
-      if (chunks > 1) w = wish_of(a, c * THREADS + tid);
-      const Two v = running<THREADS>({w.freed, 0}, waves, &sum);
-      freed_to[tid] = before + v.x;
+      if (chunks > 1) look(c);
+      int64_t to = before + v.freed;
+#pragma unroll
+      for (int e = 0; e < EACH; ++e) {
+        to += w[e].freed;
+        freed_to[tid * EACH + e] = to;
+        held_of[tid * EACH + e] = w[e].held;
+      }
       __syncthreads();
       auto find = [&](int64_t i) {       // page i of those laid on the stack, which this chunk gave
         int at = 0;
 #pragma unroll
-        for (int step = THREADS / 2; step > 0; step /= 2)
+        for (int step = kChunk / 2; step > 0; step /= 2)
           if (freed_to[at + step - 1] <= i) at += step;
-        const int b = c * THREADS + at;
-        const Wish g = wish_of(a, b);
-        return a.table[b * a.table_stride + (g.held - (int)(freed_to[at] - i))];
+        return a.table[(int64_t)(c * kChunk + at) * a.table_stride + (held_of[at] - (int)(freed_to[at] - i))];
       };
-      const int64_t end = before + sum.x;
+      const int64_t end = before + sum.freed;
       if (lo + tid < hi && lo + tid >= before && lo + tid < end) freed_page[tid] = find(lo + tid);
       for (int64_t i = row0 + tid; i < stay; i += (int64_t)gridDim.x * THREADS)
         if (i >= before && i < end) a.free_pages[old + i] = find(i);
@@ -255,13 +287,18 @@ __global__ void __launch_bounds__(THREADS) kv_plan_kernel(KvPlanArgs a) {
 }  // namespace
 
 // Few sequences go with small workgroups: more of them share the rows, and their
-// sums are shorter.
-int kv_plan_threads(int batch) { return batch <= 256 ? 256 : 1024; }
+// sums are shorter.  Up to 2048 sequences stay in registers from one sum to the next
+// (1500 of them with a prompt's chunk among them: 9 us; read again for every sum, by
+// 1024 threads of one each, 39).  96 sequences of a token each: 4 us, of which 2 are
+// those of any launch that reads memory twice in a row.
+int kv_plan_threads(int batch) { return batch <= 1024 ? 256 : 512; }
 
 hipError_t launch_kv_plan(const KvPlanArgs& a, void* stream) {
-  const unsigned grid = (unsigned)(a.rows > 0 ? ceil_div(a.rows, a.threads) : 1);
-  if (a.threads == 256) kv_plan_kernel<256><<<dim3(grid), dim3(256), 0, (hipStream_t)stream>>>(a);
-  else kv_plan_kernel<1024><<<dim3(grid), dim3(1024), 0, (hipStream_t)stream>>>(a);
+  const dim3 grid((unsigned)(a.rows > 0 ? ceil_div(a.rows, a.threads) : 1)), block((unsigned)a.threads);
+  hipStream_t s = (hipStream_t)stream;
+  if (a.batch <= 256) kv_plan_kernel<256, 1><<<grid, block, 0, s>>>(a);
+  else if (a.batch <= 1024) kv_plan_kernel<256, 4><<<grid, block, 0, s>>>(a);
+  else kv_plan_kernel<512, 4><<<grid, block, 0, s>>>(a);
   return hipGetLastError();
 }
 
