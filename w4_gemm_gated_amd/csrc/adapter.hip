@@ -31,7 +31,6 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / kWave;
 constexpr int kShrinkThreads = 512, kShrinkWaves = kShrinkThreads / kWave;
-constexpr int kPlanThreads = 1024;
 constexpr int kPlanHead = 8;      // words: tiles
 constexpr int kUnit = kAdapterColumns / kWaves;   // columns of Y that a wave computes
 typedef float f4_t __attribute__((ext_vector_type(4)));
@@ -41,6 +40,7 @@ __device__ __forceinline__ const int4* plan_tiles(const int32_t* plan) { return 
 
 // ------------------------------------------------------------------ the plan
 
+template <int THREADS>
 __device__ __forceinline__ int64_t sum_before(int64_t v, int64_t* waves, int64_t* total) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   int64_t run = v;
@@ -54,7 +54,7 @@ __device__ __forceinline__ int64_t sum_before(int64_t v, int64_t* waves, int64_t
   __syncthreads();
   int64_t before = 0, sum = 0;
 #pragma unroll
-  for (int i = 0; i < kPlanThreads / kWave; ++i) {
+  for (int i = 0; i < THREADS / kWave; ++i) {
     if (i < wave) before += waves[i];
     sum += waves[i];
   }
@@ -62,25 +62,41 @@ __device__ __forceinline__ int64_t sum_before(int64_t v, int64_t* waves, int64_t
   return before + run - v;
 }
 
-// One workgroup: rows per adapter, their running sums, then every sequence takes
-// its place among its adapter's rows.  (Which place it gets is a matter of order
-// of arrival; a row's result does not depend on it.)  Offsets that do not rise
-// within the rows give a plan of no tiles.
-__global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlanArgs a) {
-  __shared__ int32_t count[kMaxAdapters];      // rows, then the next free entry of the list
+// One workgroup: rows per adapter, their running sums, and every sequence's place among
+// its adapter's rows.  (Which place it gets is a matter of order of arrival; a row's
+// result does not depend on it.)  Offsets that do not rise within the rows give a plan
+// of no tiles.  A chain of round trips: 3 us at 64 sequences, 4.6 with 2048 rows; for
+// up to 256 sequences and adapters by 256 threads (1024, and the places given out in a
+// second round of atomics: 5.2 and 5.7).
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) adapter_plan_kernel(AdapterPlanArgs a) {
+  __shared__ int32_t count[kMaxAdapters];      // rows
   __shared__ int32_t tile_to[kMaxAdapters];    // running sum of tiles
   __shared__ int32_t list_at[kMaxAdapters];
-  __shared__ int64_t waves[kPlanThreads / kWave];
-  __shared__ int32_t first_of[kPlanThreads], rows_of[kPlanThreads], place_of[kPlanThreads];
+  __shared__ int64_t waves[THREADS / kWave];
+  __shared__ int32_t first_of[THREADS], rows_of[THREADS], place_of[THREADS];
   __shared__ int32_t bad, longs;
   const int tid = threadIdx.x;
-  for (int i = tid; i < a.adapters; i += kPlanThreads) count[i] = 0;
-  if (tid == 0) bad = 0;
+  for (int i = tid; i < a.adapters; i += THREADS) count[i] = 0;
+  if (tid == 0) bad = longs = 0;
+  // Sequence b: its rows, its adapter, its place among that one's rows.
+  int32_t from = 0, n = 0, of = 0, at = 0;
+  auto look = [&](int b) {       // false: its offsets are no plan's
+    n = 0;
+    if (b >= a.batch) return true;
+    from = a.cu[b];
+    const int32_t to = a.cu[b + 1];
+    of = a.adapter[b];
+    if (from < 0 || to < from || to > a.rows) return false;
+    if (of >= 0 && of < a.adapters) n = to - from;
+    return true;
+  };
+  bool rises = look(tid);        // (its loads come back while the counts are cleared)
   __syncthreads();
-  for (int b = tid; b < a.batch; b += kPlanThreads) {
-    const int32_t from = a.cu[b], to = a.cu[b + 1], of = a.adapter[b];
-    if (from < 0 || to < from || to > a.rows) bad = 1;
-    else if (of >= 0 && of < a.adapters && to > from) atomicAdd(&count[of], to - from);
+  for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
+    if (b0 > 0) rises = look(b0 + tid);
+    if (!rises) bad = 1;
+    if (n > 0) at = atomicAdd(&count[of], n);
   }
   __syncthreads();
   int32_t* list = a.plan + kPlanHead + 4 * (int64_t)a.most_tiles;
@@ -88,23 +104,21 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlanA
     if (tid == 0) a.plan[0] = 0;
     return;
   }
-  int64_t rows_before = 0, tiles_before = 0, sum;
-  for (int i0 = 0; i0 < a.adapters; i0 += kPlanThreads) {
+  int64_t before = 0, sum;       // rows and tiles, both under 2^25
+  for (int i0 = 0; i0 < a.adapters; i0 += THREADS) {
     const int i = i0 + tid;
-    const int32_t n = i < a.adapters ? count[i] : 0, tiles = (n + kAdapterTile - 1) / kAdapterTile;
-    const int64_t at = rows_before + sum_before(n, waves, &sum);
-    rows_before += sum;
-    const int64_t t = tiles_before + sum_before(tiles, waves, &sum);
-    tiles_before += sum;
+    const int32_t rows = i < a.adapters ? count[i] : 0, tiles = (rows + kAdapterTile - 1) / kAdapterTile;
+    const int64_t to = before + sum_before<THREADS>((int64_t)rows << 32 | tiles, waves, &sum);
+    before += sum;
     if (i < a.adapters) {
-      tile_to[i] = (int32_t)(t + tiles);
-      list_at[i] = (int32_t)at;
+      tile_to[i] = (int32_t)to + tiles;
+      list_at[i] = (int32_t)(to >> 32);
     }
   }
   __syncthreads();
-  const int tiles = (int)min(tiles_before, (int64_t)a.most_tiles);
+  const int tiles = min((int32_t)before, a.most_tiles);
   if (tid == 0) a.plan[0] = tiles;
-  for (int t = tid; t < tiles; t += kPlanThreads) {
+  for (int t = tid; t < tiles; t += THREADS) {
     int lo = 0, hi = a.adapters - 1;           // the first adapter whose tiles reach past t
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
@@ -114,34 +128,33 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlanA
     const int in = (t - (lo > 0 ? tile_to[lo - 1] : 0)) * kAdapterTile;
     ((int4*)(a.plan + kPlanHead))[t] = make_int4(lo, list_at[lo] + in, min(count[lo] - in, kAdapterTile), 0);
   }
-  __syncthreads();
-  for (int i = tid; i < a.adapters; i += kPlanThreads) count[i] = list_at[i];
-  __syncthreads();
-  for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
-    const int b = b0 + tid;
-    int32_t from = 0, n = 0, at = 0;
-    if (b < a.batch) {
-      const int32_t of = a.adapter[b];
-      from = a.cu[b];
-      n = of >= 0 && of < a.adapters ? a.cu[b + 1] - from : 0;
+  if (a.batch > THREADS) {       // the places were not kept: they are given out again
+    __syncthreads();
+    for (int i = tid; i < a.adapters; i += THREADS) count[i] = 0;
+    __syncthreads();
+  }
+  for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
+    if (a.batch > THREADS) {
+      look(b0 + tid);
       if (n > 0) at = atomicAdd(&count[of], n);
     }
-    // Short sequences are written by their thread, long ones by all.
+    const int place = n > 0 ? list_at[of] + at : 0;
+    // Short sequences are written by their thread, long ones by a wave each.
     constexpr int kShort = 16;
     if (n <= kShort)
-      for (int i = 0; i < n; ++i) list[at + i] = from + i;
-    if (tid == 0) longs = 0;
-    __syncthreads();
+      for (int i = 0; i < n; ++i) list[place + i] = from + i;
     if (n > kShort) {
       const int s = atomicAdd(&longs, 1);
       first_of[s] = from;
       rows_of[s] = n;
-      place_of[s] = at;
+      place_of[s] = place;
     }
     __syncthreads();
     const int many = longs;
-    for (int s = tid / kWave; s < many; s += kPlanThreads / kWave)       // a wave to each
+    for (int s = tid / kWave; s < many; s += THREADS / kWave)
       for (int i = tid % kWave; i < rows_of[s]; i += kWave) list[place_of[s] + i] = first_of[s] + i;
+    __syncthreads();
+    if (tid == 0) longs = 0;
     __syncthreads();
   }
 }
@@ -526,7 +539,8 @@ hipError_t shrink_launch(const AdapterArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_adapter_plan(const AdapterPlanArgs& a, void* stream) {
-  adapter_plan_kernel<<<dim3(1), dim3(kPlanThreads), 0, (hipStream_t)stream>>>(a);
+  if (a.batch <= 256 && a.adapters <= 256) adapter_plan_kernel<256><<<dim3(1), dim3(256), 0, (hipStream_t)stream>>>(a);
+  else adapter_plan_kernel<1024><<<dim3(1), dim3(1024), 0, (hipStream_t)stream>>>(a);
   return hipGetLastError();
 }
 
