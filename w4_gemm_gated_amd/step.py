@@ -6,6 +6,7 @@ Python names mirror the C ABI in include/spear_serve.h, which states the
 definitions; only arguments are marshalled here, as in serve.py.
 """
 import ctypes
+import functools
 
 import torch
 
@@ -41,6 +42,9 @@ def _space(workspace, nbytes, device, stream):
     return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
 
 
+_PLANNED = ("cu_q", "kv_lens", "positions", "sequence", "held_out", "free_out")
+
+
 def spear_kv_plan(lens, new_tokens, held, block_table, free_pages, free_count, rows, page_size=16, cu_q=None,
                   kv_lens=None, slots=None, positions=None, sequence=None, held_out=None, free_out=None,
                   workspace=None):
@@ -70,13 +74,17 @@ def spear_kv_plan(lens, new_tokens, held, block_table, free_pages, free_count, r
     rows = int(rows)
     if rows < 0:
         raise ValueError("rows must not be negative")
-    cu_q = _out(cu_q, "cu_q", (B + 1,), i32, dev)
-    kv_lens = _out(kv_lens, "kv_lens", (B,), i32, dev)
-    slots = _out(slots, "slots", (rows,), torch.int64, dev)
-    positions = _out(positions, "positions", (rows,), i32, dev)
-    sequence = _out(sequence, "sequence", (rows,), i32, dev)
-    held_out = _out(held_out, "held_out", (B,), i32, dev)
-    free_out = _out(free_out, "free_out", (1,), i32, dev)
+    if slots is None:
+        slots = torch.empty(rows, dtype=torch.int64, device=dev)
+    else:
+        _out(slots, "slots", (rows,), torch.int64, dev)
+    given = (cu_q, kv_lens, positions, sequence, held_out, free_out)
+    sizes = (B + 1, B, rows, rows, B, 1)
+    if cu_q is kv_lens is positions is sequence is held_out is free_out is None:     # (one allocation, a microsecond each)
+        given = torch.empty(sum(sizes), dtype=i32, device=dev).split_with_sizes(sizes)
+    else:
+        given = [_out(t, name, (n,), i32, dev) for t, name, n in zip(given, _PLANNED, sizes)]
+    cu_q, kv_lens, positions, sequence, held_out, free_out = given
     lib, stream = _binding.load(), _stream(dev)
     d = _plan(("kv_plan", B, rows, pages, int(page_size), free_pages.shape[0]), lambda: (
         KvPlanDesc(B, rows, pages, int(page_size), free_pages.shape[0]), lib.spear_kv_plan_workspace_bytes,
@@ -99,6 +107,13 @@ class AdapterPlan:
         self.data, self.batch, self.adapters, self.rows = data, batch, adapters, rows
 
 
+@functools.lru_cache(maxsize=4096)
+def _plan_bytes(batch, adapters, rows):
+    n = ctypes.c_size_t(0)
+    _binding.check(_binding.load().spear_adapter_plan_bytes(batch, adapters, rows, ctypes.byref(n)), "spear_adapter_plan")
+    return n.value
+
+
 def spear_adapter_plan(cu_q, adapter, adapters, rows, plan=None):
     """The plan of a step's adapters: sequence b has rows cu_q[b] .. cu_q[b + 1] - 1 and
     adapter adapter[b] (outside [0, adapters): none).
@@ -114,9 +129,7 @@ def spear_adapter_plan(cu_q, adapter, adapters, rows, plan=None):
         raise ValueError("cu_q must have one entry more than adapter")
     lib, stream = _binding.load(), _stream(dev)
     if plan is None:
-        n = ctypes.c_size_t(0)
-        _binding.check(lib.spear_adapter_plan_bytes(B, adapters, rows, ctypes.byref(n)), "spear_adapter_plan")
-        plan = AdapterPlan(torch.empty(n.value, dtype=torch.uint8, device=dev), B, adapters, rows)
+        plan = AdapterPlan(torch.empty(_plan_bytes(B, adapters, rows), dtype=torch.uint8, device=dev), B, adapters, rows)
     elif not isinstance(plan, AdapterPlan):
         raise TypeError("plan must come from spear_adapter_plan")
     elif (plan.batch, plan.adapters, plan.rows) != (B, adapters, rows) or plan.data.device != dev:
