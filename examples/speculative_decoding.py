@@ -7,7 +7,9 @@ the drafter is the same model with them switched off, which costs less a call an
 mostly agrees.  Each round the drafter proposes `drafts` tokens one at a time, the
 target scores all of them in one call (a chunk of new tokens over its cache),
 and the verification keeps those that leave the output distributed as the
-target's.  Rejected tokens stay in the cache's memory and are written over.
+target's.  Both draw from the same rules (temperature, top-p).  Rejected tokens stay
+in the cache's memory and are written over; pages that no sequence needs any more go
+back to the free ones with the next step's plan.
 
     python examples/speculative_decoding.py --rounds 8
 """
@@ -68,21 +70,23 @@ class Model:
 
 
 class Sequences:
-    """A batch's paged cache: every sequence owns its pages, taken at random."""
+    """A batch's paged cache: pages are taken from a stack of free ones in random order."""
 
     def __init__(self, batch, room, model, g, dtype=torch.int8):
-        pages = -(-room // PAGE)
-        self.cache = sp.spear_kv_cache(batch * pages, model.kv_heads, model.dim, PAGE, dtype)
-        order = torch.randperm(batch * pages, generator=g, device="cuda")
-        self.table = order.view(batch, pages).to(torch.int32).contiguous()
+        most = -(-room // PAGE)
+        self.cache = sp.spear_kv_cache(batch * most, model.kv_heads, model.dim, PAGE, dtype)
+        self.free_pages = torch.randperm(batch * most, generator=g, device="cuda").to(torch.int32)
+        self.free_count = torch.full((1,), batch * most, dtype=torch.int32, device="cuda")
+        self.table = torch.zeros(batch, most, dtype=torch.int32, device="cuda")
+        self.held = torch.zeros(batch, dtype=torch.int32, device="cuda")
         self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
 
     def slots(self, cu, rows):
-        """Where the last cu[b + 1] - cu[b] tokens of each sequence lie."""
-        row = torch.arange(rows, device="cuda")
-        b = torch.bucketize(row, cu[1:].long(), right=True)
-        at = self.lens.long()[b] - (cu[1:].long()[b] - row)
-        return self.table[b, at // PAGE].long() * PAGE + at % PAGE
+        """Where the last cu[b + 1] - cu[b] tokens of each sequence lie, on new pages as
+        far as it has none for them."""
+        new = cu[1:] - cu[:-1]
+        return sp.spear_kv_plan(self.lens - new, new, self.held, self.table, self.free_pages, self.free_count, rows,
+                                page_size=PAGE, held_out=self.held, free_out=self.free_count)[2]
 
 
 def offsets(n, batch):
@@ -90,7 +94,7 @@ def offsets(n, batch):
 
 
 def generate(batch=4, prompt=50, rounds=8, drafts=4, temperature=0.3, vocab=1000, hidden=512, q_heads=8, kv_heads=2,
-             dim=64, seed=0, dtype=torch.int8):
+             dim=64, seed=0, dtype=torch.int8, top_p=0.95):
     """Runs `rounds` rounds; returns the model, the target's sequences, each
     sequence's tokens (lists, the prompt first) and the kept drafts per round."""
     g = torch.Generator(device="cuda")
@@ -101,8 +105,10 @@ def generate(batch=4, prompt=50, rounds=8, drafts=4, temperature=0.3, vocab=1000
     text = torch.randint(vocab, (batch, prompt), generator=g, device="cuda")
     tokens = [row.tolist() for row in text]
 
-    def probabilities(logits):
-        return torch.softmax(logits.float() / temperature, -1)
+    def noise():
+        return torch.empty(batch, vocab, device="cuda").exponential_(generator=g)
+
+    rules = dict(temperature=temperature, top_p=top_p, probs=True)
 
     # The prompt, all but its last token, into both caches as one chunk.
     for seqs, ec in ((target, True), (draft, False)):
@@ -117,19 +123,18 @@ def generate(batch=4, prompt=50, rounds=8, drafts=4, temperature=0.3, vocab=1000
         new, p_draft = [last], []
         for _ in range(drafts):
             draft.lens += 1
-            p = probabilities(model(new[-1].long(), draft, one, 1, False))
+            drawn, p = sp.spear_sample(model(new[-1].long(), draft, one, 1, False), noise(), **rules)
             p_draft.append(p)
-            new.append((p / torch.empty_like(p).exponential_(generator=g)).argmax(-1).to(torch.int32))
+            new.append(drawn)
         draft.lens += 1                         # the last drafted token's keys, should it be kept
         model(new[-1].long(), draft, one, 1, False)
         new = torch.stack(new, 1)               # [batch, 1 + drafts]
         # The target, all of them at once.
         target.lens += drafts + 1
-        p_target = probabilities(model(new.reshape(-1).long(), target, chunk, drafts + 1, True))
+        _, p_target = sp.spear_sample(model(new.reshape(-1).long(), target, chunk, drafts + 1, True), **rules)
         accepted, out = sp.spear_verify_draft(
             p_target.view(batch, drafts + 1, vocab), torch.stack(p_draft, 1), new[:, 1:].contiguous(),
-            torch.rand(batch, drafts, generator=g, device="cuda"),
-            torch.empty(batch, vocab, device="cuda").exponential_(generator=g))
+            torch.rand(batch, drafts, generator=g, device="cuda"), noise())
         # What was refused leaves the caches: the lengths go back.
         target.lens -= drafts - accepted
         draft.lens.copy_(start + 1 + accepted)
