@@ -24,7 +24,7 @@
 #include <algorithm>
 
 #include "serve_internal.h"
-#include "device_common.h"
+#include "wave_ops.h"
 
 namespace spear {
 namespace {
@@ -43,12 +43,7 @@ __device__ __forceinline__ const int4* plan_tiles(const int32_t* plan) { return 
 template <int THREADS>
 __device__ __forceinline__ int64_t sum_before(int64_t v, int64_t* waves, int64_t* total) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  int64_t run = v;
-#pragma unroll
-  for (int o = 1; o < kWave; o *= 2) {
-    const int64_t x = __shfl_up(run, o);
-    if (lane >= o) run += x;
-  }
+  const int64_t run = wave_run(v);
   __syncthreads();
   if (lane == kWave - 1) waves[wave] = run;
   __syncthreads();

@@ -17,7 +17,7 @@
 // workgroup reads what another writes.  Only state that is updated in place
 // is written by the last workgroup to arrive.
 #include "serve_internal.h"
-#include "device_common.h"
+#include "wave_ops.h"
 
 namespace spear {
 namespace {
@@ -61,12 +61,7 @@ __device__ __forceinline__ void add(Sums& a, const Sums& b) {
 template <int THREADS>
 __device__ __forceinline__ Sums running(const Sums& own, Sums* waves, Sums* total) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  Sums v = own;
-#pragma unroll
-  for (int o = 1; o < kWave; o *= 2) {
-    const Sums x = {__shfl_up(v.freed, o), __shfl_up(v.ask, o), __shfl_up(v.need, o)};
-    if (lane >= o) add(v, x);
-  }
+  Sums v = {wave_run(own.freed), wave_run(own.ask), wave_run(own.need)};
   __syncthreads();
   if (lane == kWave - 1) waves[wave] = v;
   __syncthreads();
@@ -81,14 +76,11 @@ __device__ __forceinline__ Sums running(const Sums& own, Sums* waves, Sums* tota
   return v;
 }
 
+// .. and the running maximum of numbers from -1.
 template <int THREADS>
 __device__ __forceinline__ int running_max(int v, int* waves) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-#pragma unroll
-  for (int o = 1; o < kWave; o *= 2) {
-    const int x = __shfl_up(v, o);
-    if (lane >= o) v = max(v, x);
-  }
+  v = wave_run(v, -1, [](int a, int b) { return max(a, b); });
   __syncthreads();
   if (lane == kWave - 1) waves[wave] = v;
   __syncthreads();

@@ -34,7 +34,7 @@
 #include <algorithm>
 
 #include "serve_internal.h"
-#include "device_common.h"
+#include "wave_ops.h"
 
 namespace spear {
 namespace {
@@ -145,11 +145,11 @@ __device__ __forceinline__ float logit_from(double t, double scale) {
   return __builtin_nanf("");
 }
 
-// The workgroup's maximum, bitwise and / or, and sum, in every thread.
+// The workgroup's maximum, bitwise and / or, and sum, in every thread.  (`none`: what leaves
+// any value as it is.)
 template <typename T, typename F>
-__device__ __forceinline__ T block_all(T v, T* lds, F f) {
-#pragma unroll
-  for (int o = kWave / 2; o > 0; o /= 2) v = f(v, (T)__shfl_xor(v, o));
+__device__ __forceinline__ T block_all(T v, T none, T* lds, F f) {
+  v = wave_all(v, none, f);
   __syncthreads();
   if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = v;
   __syncthreads();
@@ -159,21 +159,17 @@ __device__ __forceinline__ T block_all(T v, T* lds, F f) {
   return v;
 }
 __device__ __forceinline__ u64 block_max(u64 v, u64* lds) {
-  return block_all(v, lds, [](u64 a, u64 b) { return a > b ? a : b; });
+  return block_all(v, (u64)0, lds, [](u64 a, u64 b) { return a > b ? a : b; });
 }
 __device__ __forceinline__ u64 block_add(u64 v, u64* lds) {
-  return block_all(v, lds, [](u64 a, u64 b) { return a + b; });
+  return block_all(v, (u64)0, lds, [](u64 a, u64 b) { return a + b; });
 }
 
 // Running sum (inclusive) over the workgroup.
 template <typename T>
 __device__ __forceinline__ T block_run(T v, T* lds) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-#pragma unroll
-  for (int o = 1; o < kWave; o *= 2) {
-    const T x = __shfl_up(v, o);
-    if (lane >= o) v += x;
-  }
+  v = wave_run(v);
   __syncthreads();
   if (lane == kWave - 1) lds[wave] = v;
   __syncthreads();
@@ -187,15 +183,8 @@ __device__ __forceinline__ T block_run(T v, T* lds) {
 // .. of two values at once.
 __device__ __forceinline__ void block_run(double& x, uint32_t& y, double* ldsx, uint32_t* ldsy) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-#pragma unroll
-  for (int o = 1; o < kWave; o *= 2) {
-    const double p = __shfl_up(x, o);
-    const uint32_t q = __shfl_up(y, o);
-    if (lane >= o) {
-      x += p;
-      y += q;
-    }
-  }
+  x = wave_run(x);
+  y = wave_run(y);
   __syncthreads();
   if (lane == kWave - 1) {
     ldsx[wave] = x;
@@ -313,11 +302,7 @@ __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rule
   ShareInfo mine = shares[min(lane, a.shares - 1)];
   u64 best = mine.best;
   for (int i = lane + kWave; i < a.shares; i += kWave) best = best > shares[i].best ? best : shares[i].best;
-#pragma unroll
-  for (int o = kWave / 2; o > 0; o /= 2) {
-    const u64 v = __shfl_xor(best, o);
-    best = best > v ? best : v;
-  }
+  best = wave_max(best, (u64)0);
   RowInfo* info = (RowInfo*)((char*)a.info + (int64_t)b * kSampleInfoBytes);
   static_assert(sizeof(RowInfo) <= kSampleInfoBytes, "room for it");
   const float largest = logit_of(best);
@@ -357,12 +342,9 @@ __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rule
       tokens += near ? (uint32_t)(mine.used >> 32) : 0u;
       rows = max(rows, min(off + have, kBins));
     }
-#pragma unroll
-    for (int o = kWave / 2; o > 0; o /= 2) {
-      total += __shfl_xor(total, o);
-      tokens += __shfl_xor(tokens, o);
-      rows = max(rows, __shfl_xor(rows, o));
-    }
+    total = wave_sum(total);
+    tokens = wave_sum(tokens);
+    rows = wave_max(rows, 0);
     __syncthreads();
     const bool by_k = r.k > 0 && (uint32_t)r.k < tokens;
     // .. and its bins from the top, one to a thread, until they hold all that the rules ask
@@ -514,11 +496,21 @@ __global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
       least = rising(low);
     }
   }
-  best = block_max(best, s.red);
+  best = wave_max(best, (u64)0);
+  least = wave_all(least, ~0u, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
+  if (tid % kWave == 0) {
+    s.red[tid / kWave] = best;
+    s.redc[tid / kWave] = least;
+  }
+  __syncthreads();      // (and the bins are cleared)
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    best = best > s.red[i] ? best : s.red[i];
+    least = least < s.redc[i] ? least : s.redc[i];
+  }
   const double scale = scale_of(r);
   ShareInfo* mine = a.share + (int64_t)b * a.shares + share;
   if (bins && best != 0) {
-    least = block_all(least, s.redc, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
     const double q = floor(t_of(logit_of(best), scale));
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
@@ -604,27 +596,14 @@ __device__ __forceinline__ void each(const SampleArgs& a, const void* row, const
 
 // A wave's own sorting: the place of each of its first n lanes' keys, largest first
 // (other lanes keep theirs), values moved to their places, and running sums.
-__device__ __forceinline__ u64 read_lane(u64 v, int lane) {
-  return (u64)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
-         (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
-}
 __device__ __forceinline__ int place_in_wave(u64 key, int n) {
   const int lane = threadIdx.x % kWave;
   int at = 0;
-  for (int j = 0; j < n; ++j) at += read_lane(key, j) > key;
+  for (int j = 0; j < n; ++j) at += of_lane(key, j) > key;
   return lane < n ? at : lane;
 }
 __device__ __forceinline__ uint32_t push(uint32_t v, int to) { return (uint32_t)__builtin_amdgcn_ds_permute(4 * to, (int)v); }
 __device__ __forceinline__ u64 push(u64 v, int to) { return (u64)push((uint32_t)(v >> 32), to) << 32 | push((uint32_t)v, to); }
-__device__ __forceinline__ u64 wave_run(u64 v) {
-#pragma unroll
-  for (int o = 1; o < kWave; o *= 2) {
-    const u64 x = __shfl_up(v, o);
-    if (threadIdx.x % kWave >= o) v += x;
-  }
-  return v;
-}
-
 // Of the tokens of bins `first` to `last`, in falling order: the key of the one at which
 // the count reaches `count`, or the mass (in units of the upper edge, fixed point)
 // `mass`; the last one if it never does.  Each step splits the tokens that are
@@ -646,8 +625,8 @@ __device__ u64 select(const SampleArgs& a, const RowInfo& o, const void* row, co
         any |= k;
       }
     });
-    all = block_all(all, s.red, [](u64 x, u64 y) { return x & y; });
-    any = block_all(any, s.red, [](u64 x, u64 y) { return x | y; });
+    all = block_all(all, ~0ull, s.red, [](u64 x, u64 y) { return x & y; });
+    any = block_all(any, 0ull, s.red, [](u64 x, u64 y) { return x | y; });
     if (all == ~0ull && any == 0) return ~0ull;      // none at all
     if (all == any) return all;                       // one
     const int top = 63 - __builtin_clzll(all ^ any), shift = max(top - (kSubBits - 1), 0);
@@ -722,7 +701,7 @@ __device__ u64 select(const SampleArgs& a, const RowInfo& o, const void* row, co
       const u64 own = before;
       before = wave_run(before) - own;
       const bool in = lane < n && (by_count ? (uint32_t)lane < count : before < mass);
-      return read_lane(key, max(__popcll(__ballot(in)) - 1, 0));
+      return of_lane(key, max(__popcll(__ballot(in)) - 1, 0));
     }
   }
 }
@@ -752,12 +731,12 @@ __device__ __forceinline__ Cut cut_in_wave(const SampleArgs& a, const RowInfo& o
     const bool of_k = here && (bin < o.bin_k || lane - ahead < o.left_k);
     kept &= of_k;
     if (o.by_p)
-      target *= o.before_k + (double)read_lane(wave_run(of_k && bin == o.bin_k ? mass : 0), kWave - 1) * unit;
+      target *= o.before_k + (double)of_lane(wave_run(of_k && bin == o.bin_k ? mass : 0), kWave - 1) * unit;
   }
   if (o.by_p) kept &= o.before + (double)(wave_run(mass) - mass) * unit < target;
   const int many = __popcll(__ballot(kept));
   Cut c;
-  c.end = many > 0 ? read_lane(key, many - 1) : ~0ull;
+  c.end = many > 0 ? of_lane(key, many - 1) : ~0ull;
   c.best = c.sum = 0;
   if (kept && l >= o.least) {
     const float w = weight_of(o, l);
@@ -913,13 +892,9 @@ __device__ __forceinline__ void end_race(const SampleArgs& a, int b, const void*
     }
   }
   best = best > c.best ? best : c.best;
-#pragma unroll
-  for (int x = kWave / 2; x > 0; x /= 2) {        // (sums always in the same order)
-    const u64 v = __shfl_xor(best, x);
-    best = best > v ? best : v;
-    sum += __shfl_xor(sum, x);
-    c.sum += __shfl_xor(c.sum, x);
-  }
+  best = wave_max(best, (u64)0);
+  sum = wave_sum(sum);
+  c.sum = wave_sum(c.sum);
   if (split) {
     __syncthreads();
     if (lane == 0) {
@@ -1010,11 +985,23 @@ __global__ void __launch_bounds__(kThreads) sample_race_kernel(SampleArgs a) {
         }
     }
   }
-  best = block_max(best, s.red);
-  sum = block_all(sum, s.redd, [](double x, double y) { return x + y; });
+  best = wave_max(best, (u64)0);
+  sum = wave_sum(sum);
+  if (tid % kWave == 0) {
+    s.red[tid / kWave] = best;
+    s.redd[tid / kWave] = sum;
+  }
+  __syncthreads();
   const uint32_t staged = min(s.listed, (uint32_t)kStaged);
+  if (tid == 0) {
+    if (staged > 0) s.found_count = add_dev_u32(&info->listed, staged);
+    for (int i = 1; i < kWaves; ++i) {
+      best = best > s.red[i] ? best : s.red[i];
+      sum += s.redd[i];
+    }
+    a.part[(int64_t)b * a.parts + part] = {best, sum};
+  }
   if (staged > 0) {
-    if (tid == 0) s.found_count = add_dev_u32(&info->listed, staged);
     __syncthreads();
     for (uint32_t i = tid; i < staged; i += kThreads)
       if (s.found_count + i < kSampleList) {
@@ -1022,7 +1009,6 @@ __global__ void __launch_bounds__(kThreads) sample_race_kernel(SampleArgs a) {
         list_noise[s.found_count + i] = s.noise[i];
       }
   }
-  if (tid == 0) a.part[(int64_t)b * a.parts + part] = {best, sum};
 }
 
 template <bool F16>
