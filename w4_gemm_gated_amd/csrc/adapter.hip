@@ -230,23 +230,32 @@ __device__ __forceinline__ void shrink(const AdapterArgs& a, const Tile& t, cons
 #pragma unroll
         for (int i = 0; i < RB; ++i) acc[j][i] = mfma16x16x32(wv[i], xv[j], acc[j][i]);
     }
-  // The upper four waves' sums to the lower four, theirs to all.
+  // The waves' sums, those of w and w + 4 first.  (Where there are many the upper four
+  // waves' go to the lower four before: LDS holds them in half the place.)
   constexpr int kHalf = kShrinkWaves / 2, kUnits = SUB * RB;
+  __syncthreads();
+  if constexpr (SUB > 1) {
+    if (wave >= kHalf)
 #pragma unroll
-  for (int turn = 0; turn < 2; ++turn) {
+      for (int u = 0; u < kUnits; ++u) red[((wave - kHalf) * kUnits + u) * kWave + lane] = acc[u / RB][u % RB];
     __syncthreads();
-    if (turn == 0 ? wave >= kHalf : wave < kHalf)
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u) red[((wave % kHalf) * kUnits + u) * kWave + lane] = acc[u / RB][u % RB];
-    __syncthreads();
-    if (turn == 0 && wave < kHalf)
+    if (wave < kHalf)
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) acc[u / RB][u % RB] += red[(wave * kUnits + u) * kWave + lane];
+    __syncthreads();
   }
-  for (int u = wave; u < kUnits; u += kShrinkWaves) {
-    f4_t sum = red[u * kWave + lane];
+  if (SUB == 1 || wave < kHalf)
 #pragma unroll
-    for (int v = 1; v < kHalf; ++v) sum += red[(v * kUnits + u) * kWave + lane];
+    for (int u = 0; u < kUnits; ++u) red[(wave * kUnits + u) * kWave + lane] = acc[u / RB][u % RB];
+  __syncthreads();
+  for (int u = wave; u < kUnits; u += kShrinkWaves) {
+    f4_t sum = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int v = 0; v < kHalf; ++v) {
+      f4_t two = red[(v * kUnits + u) * kWave + lane];
+      if constexpr (SUB == 1) two += red[((v + kHalf) * kUnits + u) * kWave + lane];
+      sum = v == 0 ? two : sum + two;
+    }
     const int row = 16 * (u / RB) + c, rank = rank0 + 16 * (u % RB) + 4 * oct;
     if (row < t.rows && rank < a.rank) keep(row, rank, sum);
   }
@@ -266,11 +275,7 @@ __device__ __forceinline__ void to_halves(const AdapterArgs& a, const Tile& t, c
       const float v = fabsf(h[row * a.rank + i]);
       most = v > most || v != v ? v : most;
     }
-#pragma unroll
-  for (int o = 1; o < kLanes; o *= 2) {
-    const float v = __shfl_xor(most, o);
-    most = v > most || v != v ? v : most;
-  }
+  most = lanes_all<kLanes>(most, [](float x, float v) { return v > x || v != v ? v : x; });
   // The power of two at or below the row's largest (1 where that is zero, infinite or NaN).
   const uint32_t e = float_bits(most) >> 23;
   const float p = e == 0 ? (most > 0.0f ? 0x1p-126f : 1.0f) : e == 255 ? 1.0f : bits_float(e << 23);
@@ -500,7 +505,7 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(AdapterArgs a)
 template <int RB, int SB, bool PACK>
 __global__ void __launch_bounds__(kShrinkThreads) adapter_fused_kernel(AdapterArgs a) {
   constexpr int kStride = (PACK ? 32 : 64 * SB) + 8;
-  __shared__ f4_t red[kShrinkWaves / 2 * RB * kWave];
+  __shared__ f4_t red[kShrinkWaves * RB * kWave];
   __shared__ float h[16 * 16 * RB];
   __shared__ __attribute__((aligned(16))) half_t halves[16 * kStride];
   __shared__ float factor[16];

@@ -40,6 +40,18 @@ __device__ __forceinline__ T wave_run(T v) {
   return wave_run(v, (T)0, [](T a, T b) { return a + b; });
 }
 
+// f over groups of 8, 16 or 32 neighbouring lanes, in each of them.
+template <int LANES, typename T, typename F>
+__device__ __forceinline__ T lanes_all(T v, F f) {
+  static_assert(LANES == 8 || LANES == 16 || LANES == 32, "within a half of the wave");
+  v = f(v, moved<0xB1, 0xF>(v, v));       // the lane one apart, two apart, ..
+  v = f(v, moved<0x4E, 0xF>(v, v));
+  v = f(v, moved<0x141, 0xF>(v, v));      // .. the other four of eight, the other eight of sixteen
+  if constexpr (LANES > 8) v = f(v, moved<0x140, 0xF>(v, v));
+  if constexpr (LANES > 16) v = f(v, (T)__shfl_xor(v, 16));
+  return v;
+}
+
 // A lane's value, in every lane.
 template <typename T>
 __device__ __forceinline__ T of_lane(T v, int lane) {
