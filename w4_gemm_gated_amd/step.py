@@ -20,7 +20,7 @@ __all__ = ["spear_kv_plan", "spear_adapter_plan", "spear_adapter_add", "spear_sa
 def _out(t, name, shape, dtype, device):
     """The caller's output tensor, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape if len(shape) > 1 else shape[0], dtype=dtype, device=device)
     _dense(t, name, dtype, len(shape), device)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
