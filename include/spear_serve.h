@@ -324,8 +324,8 @@ typedef struct spear_sample_desc {
 
 /*
  * spear_sample_workspace_bytes -- device workspace of a call (host only): one of
- * spear_w4ec_linear's kind, zero-filled before its first use; the call returns the
- * counters of its header to zero.
+ * spear_w4ec_linear's kind, zero-filled before its first use; the call leaves its header
+ * as it is.
  * Errors: NULL_POINTER, INVALID_SHAPE, INVALID_ARGUMENT (dtype), UNSUPPORTED.
  */
 spear_status_t spear_sample_workspace_bytes(const spear_sample_desc_t* desc, size_t* bytes);
@@ -354,7 +354,7 @@ spear_status_t spear_sample_workspace_bytes(const spear_sample_desc_t* desc, siz
  *            tokens are asked for or the settings leave one token to every row.
  *   temperature, top_p, min_p  fp32 [batch], top_k int32 [batch], each NULL for the
  *            descriptor's value.
- * Which tokens are left is decided in 64 bits (weights enter the sums to 2^-34 of
+ * Which tokens are left is decided in 64 bits (weights enter the sums to 2^-33 of
  * themselves); the weights of the race and of the probabilities are fp32.  The result
  * does not depend on scheduling.
  * Errors: NULL_POINTER, INVALID_SHAPE, INVALID_ARGUMENT, UNSUPPORTED,

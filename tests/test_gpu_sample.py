@@ -2,7 +2,7 @@
 
 Which tokens are left: equal to the oracle's, except that top-p's cut may fall one way
 or the other where the sum before it is within 2^-31 of its mass (weights enter the
-sums to 2^-34 of themselves, and a selection's to 2^-40 of a bin's edge).
+sums to 2^-33 of themselves, and a selection's to 2^-40 of a bin's edge).
 
 Probabilities: the weight is an fp32 power of two of an argument exact to 2^-25 (one
 step of the hardware's exponential: 2^-23), the sum's reciprocal and the product are

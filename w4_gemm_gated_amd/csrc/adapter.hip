@@ -2,14 +2,19 @@
 //
 //   Y[m] += s_a (X[m] . A_a^T) . B_a^T      a = the adapter of row m's sequence
 //
-// Three kernels.  The plan, made once for a step and used by all of its
-// projections, sorts the batch's rows by adapter and cuts each adapter's into tiles
-// of at most 64.  The first product (adapter_shrink_kernel) takes tiles x slices
-// of K, the last slice of a tile to arrive adds them in order; the second
-// (adapter_expand_kernel) takes tiles x columns and updates Y in place.  With one
-// token a request both are a chain of round trips over the adapters in use (each
-// read once, whatever the order of the requests); with a prompt's chunk the
-// second is bound by Y, read and written.
+// The plan, made once for a step and used by all of its projections, sorts the batch's
+// rows by adapter and cuts each adapter's into tiles of at most 64.  The first product
+// (adapter_shrink_kernel) takes tiles x slices of K, the last slice of a tile to arrive
+// adds them in order; the second (adapter_expand_kernel) takes tiles x columns and
+// updates Y in place.  With few rows and a short K one launch does both
+// (adapter_fused_kernel).
+//
+// With one token a request these are chains of round trips over the adapters in use
+// (each read once, whatever the order of the requests): 64 rows, 24 adapters of rank 16,
+// K = N = 2048 take 8 us a projection in one launch, 11.5 in two.  With a prompt's chunk
+// the second product is bound by Y, read and written: 2048 rows of rank 64 from 4096 to
+// 14336 columns take 28.5 us for it (117 MB of Y: 4.1 TB/s) and 16.5 for the first (140
+// workgroups at 30 bytes a ns, the rate of a CU, and 6 us for the exchange).
 //
 // Matrix operands need no staging: A [rank][K] and B [N][rank] are contiguous along
 // the summed index, so a lane's eight values are one 16-byte load from memory, as

@@ -25,8 +25,16 @@
 //   probs  Probabilities, if they are asked for.
 //
 // The sums decide which token is the last one, and in a flat distribution that token
-// has a millionth of the total: weights enter the sums to 2^-34 of themselves, and
-// sums are held in 64 bits.
+// has a millionth of the total: weights enter the sums to 2^-33 of themselves (five fp32
+// roundings of a term below 2^-12), and sums are held in 64 bits.
+//
+// What a call takes (replayed from a graph): 2 x 32000 tokens 18 us, a chain of four
+// launches of 3 to 6 us, whatever they do; 64 x 128001 fp16 logits under mixed rules 44:
+// 13 for the bins (15 vector instructions a token, some of them of 64 bits, and 4.5 us of
+// launch, loads and exchanges), 9 for the cuts (a row's bins are read by one CU), 13 for
+// the race (logits and the noise's lines at 3 TB/s), 9 for the ends; distributions of
+// 144 x 32000 tokens 42.  The launches' shapes follow from how fast one CU goes, which is
+// some 25 bytes a ns whatever the pattern.
 //
 // Longer lists are cut by a radix selection, and a bin that holds more tokens than the
 // list (equal logits, a very high temperature) by the same selection over the row
@@ -95,7 +103,7 @@ __device__ __forceinline__ double t_of(float l, double scale) { return fmin((dou
 // The bin of a logit, from the one of the row's largest: whole numbers, exact wherever
 // two bins are near each other.
 __device__ __forceinline__ double bin_of(const RowInfo& o, float l) { return o.q - floor(t_of(l, o.scale)); }
-// 2^(-i / kPer)
+// 2^(-i / kPer)  (correctly rounded)
 __device__ const double kSteps[kPer] = {
     1.0, 0.9785720620877001, 0.9576032806985737, 0.93708381705515,
     0.9170040432046712, 0.8973545375015536, 0.8781260801866497, 0.859309649061239,
