@@ -293,21 +293,20 @@ struct CutScratch {
   uint32_t redc[kWaves];
   short share_off[kSampleShares], share_used[kSampleShares];
   uint32_t tokens_all, found_before;
-  int found;
+  int found, hi, lo;
   float limits[6];
 };
 
 // From a row's shares, when all of them are there: its largest, and the bins in which
 // the cuts lie.
-__device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rules& r, double scale, double step,
-                                          CutScratch& s) {
+__device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rules& r, ShareInfo mine, double scale,
+                                          double step, CutScratch& s) {
   const int tid = threadIdx.x;
   const bool bins = !r.one && (r.k > 0 || r.p < 1.0f);
   // The row: its largest, ..
   // (every wave for itself: a share a lane, or several)
   const ShareInfo* shares = a.share + (int64_t)b * a.shares;
   const int lane = tid % kWave;
-  ShareInfo mine = shares[min(lane, a.shares - 1)];
   u64 best = mine.best;
   for (int i = lane + kWave; i < a.shares; i += kWave) best = best > shares[i].best ? best : shares[i].best;
   best = wave_max(best, (u64)0);
@@ -412,18 +411,20 @@ __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rule
       // Bins in which top-p's cut can lie: rounding, and what top-k keeps of its own bin, leave a range.
       // (As many bins as hold less than a mass up to and with them, and the next one.)
       const double low = (double)r.p * low_sum * (1.0 - kNear), high = (double)r.p * high_sum * (1.0 + kNear);
-      int hi = 0, lo = 0;
-      for (int i = 0; i < bins_read; i += kThreads) {
-        const double m = mass_up_to(i + tid);
-        hi += __syncthreads_count(m < low);
-        lo += __syncthreads_count(m < high);
+      if (tid == 0) s.hi = s.lo = bins_read - 1;
+      __syncthreads();
+      for (int i = tid; i < bins_read; i += kThreads) {        // (the masses rise)
+        const double m = mass_up_to(i), before = mass_up_to(i - 1);
+        if (m >= low && (before < low || i == 0)) s.hi = i;
+        if (m >= high && (before < high || i == 0)) s.lo = i;
       }
-      hi = min(hi, bins_read - 1);
+      __syncthreads();
+      const int hi = s.hi, lo = s.lo;
       if (hi <= first) {
         first = hi;
         o.before = mass_up_to(hi - 1);
       }
-      last = min(last, min(lo, bins_read - 1));
+      last = min(last, lo);
       o.target = by_k ? (double)r.p : (double)r.p * total;
     }
     o.by_k = by_k;
@@ -553,11 +554,12 @@ __global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
 __global__ void __launch_bounds__(kThreads) sample_cuts_kernel(SampleArgs a) {
   __shared__ CutScratch s;
   const int b = blockIdx.x;
+  const ShareInfo mine = a.share[(int64_t)b * a.shares + min((int)threadIdx.x % kWave, a.shares - 1)];
   const Rules r = rules_of(a, b);
   const double step = kSteps[threadIdx.x % kPer];
   if (threadIdx.x < kPer) s.steps[threadIdx.x] = step;
   __syncthreads();
-  find_cuts(a, b, r, scale_of(r), step, s);
+  find_cuts(a, b, r, mine, scale_of(r), step, s);
 }
 
 // ------------------------------------------------------------- second launch
@@ -858,29 +860,33 @@ __device__ Cut cut_selected(const SampleArgs& a, const RowInfo& o, const void* r
 
 // From a row's shares, when all of them are there: the list cut, and the race's end.
 template <bool F16>
-__device__ __forceinline__ void end_race(const SampleArgs& a, int b, const void* row, const RowInfo& o, RowInfo* info,
-                                         Scratch& s) {
+__device__ __forceinline__ void end_race(const SampleArgs& a, int b, Scratch& s) {
   const int tid = threadIdx.x;
+  RowInfo* info = (RowInfo*)((char*)a.info + (int64_t)b * kSampleInfoBytes);
   const u64* list = a.list + (int64_t)b * kSampleList;
   const float* list_noise = a.list_noise + (int64_t)b * kSampleList;
-  const bool cuts = o.by_k || o.by_p;
   const int lane = tid % kWave;
-  // (every wave for itself: the list's first tokens, with their number, and the shares)
-  uint32_t n = 0;
-  u64 key = 0;
-  float e = 0.0f;
-  if (cuts) {
-    n = info->listed;
-    key = list[lane];
-    e = list_noise[lane];
-  }
+  // The row, and what its list's first tokens and its parts are if it has any: all of it
+  // requested at once, every wave for itself.
+  const u64 key = list[lane];
+  const float e = list_noise[lane];
+  const PartInfo* parts = a.part + (int64_t)b * a.parts;
+  PartInfo from = parts[min(lane, a.parts - 1)];
+  const RowInfo o = *info;
+  if (tid < kPer) s.steps[tid] = kSteps[tid];
+  if (o.kind != kRace) return;
+  const bool cuts = o.by_k || o.by_p;
+  const uint32_t n = cuts ? o.listed : 0;
+  if (n <= kWave && tid >= kWave) return;         // one wave does what there is
   u64 best = 0;
   double sum = 0.0;
   for (int i = lane; i < a.parts; i += kWave) {
-    const PartInfo from = a.part[(int64_t)b * a.parts + i];
+    if (i >= kWave) from = parts[i];
     best = best > from.best ? best : from.best;
     sum += from.mass;
   }
+  if (n > kWave) __syncthreads();
+  else __builtin_amdgcn_wave_barrier();           // (a wave's LDS operations are in order)
   Cut c = {0, 0, 0};
   bool split = false;       // whether c is each thread's part, or each wave's whole
   if (cuts) {
@@ -895,7 +901,7 @@ __device__ __forceinline__ void end_race(const SampleArgs& a, int b, const void*
       c = cut_ranked(a, o, s, (int)n);
       split = true;
     } else {
-      c = cut_selected<F16>(a, o, row, b, list, n, s);
+      c = cut_selected<F16>(a, o, row_of(a, b), b, list, n, s);
       split = true;
     }
   }
@@ -1022,12 +1028,7 @@ __global__ void __launch_bounds__(kThreads) sample_race_kernel(SampleArgs a) {
 template <bool F16>
 __global__ void __launch_bounds__(kThreads) sample_end_kernel(SampleArgs a) {
   __shared__ Scratch s;
-  const int b = blockIdx.x;
-  RowInfo* info = (RowInfo*)((char*)a.info + (int64_t)b * kSampleInfoBytes);
-  const RowInfo o = *info;
-  if (threadIdx.x < kPer) s.steps[threadIdx.x] = kSteps[threadIdx.x];
-  __syncthreads();
-  if (o.kind == kRace) end_race<F16>(a, b, row_of(a, b), o, info, s);
+  end_race<F16>(a, blockIdx.x, s);
 }
 
 // -------------------------------------------------------------- third launch

@@ -81,7 +81,7 @@ def spear_kv_plan(lens, new_tokens, held, block_table, free_pages, free_count, r
     given = (cu_q, kv_lens, positions, sequence, held_out, free_out)
     sizes = (B + 1, B, rows, rows, B, 1)
     if cu_q is kv_lens is positions is sequence is held_out is free_out is None:     # (one allocation, a microsecond each)
-        given = torch.empty(sum(sizes), dtype=i32, device=dev).split_with_sizes(sizes)
+        given = torch.empty(sum(sizes), dtype=i32, device=dev).unsafe_split_with_sizes(sizes)
     else:
         given = [_out(t, name, (n,), i32, dev) for t, name, n in zip(given, _PLANNED, sizes)]
     cu_q, kv_lens, positions, sequence, held_out, free_out = given
