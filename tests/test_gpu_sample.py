@@ -133,6 +133,20 @@ def test_equal_logits(V, dtype):
     check(l, noise, rules)
 
 
+@pytest.mark.parametrize("V", [6517, 9000, 40000])
+def test_tokens_too_light_to_count(V):
+    """A few tokens so far above all others that these weigh nothing, with a top-k
+    that reaches into them; the others are many, and alone in most of the row."""
+    note(f"tokens that weigh nothing, V {V}")
+    rng = np.random.default_rng(V)
+    rules = [(0.05, 1000, 1.0, 1e-6), (0.05, 1000, 0.999, 0.9), (0.05, 1000, 0.01, 0.0), (0.05, 5, 0.5, 0.0),
+             (0.05, 2, 1.0, 0.0), (0.05, V - 1, 0.9, 0.0), (0.02, 300, 0.95, 0.0), (0.001, 100, 1.0, 0.0)]
+    for dtype in (np.float16, np.float32):
+        l = rng.normal(0, 0.1, size=(len(rules), V)).astype(dtype)
+        l[:, rng.permutation(min(V, 4096))[:4]] += np.array([6.3, 6.0, 3.9, 3.2], dtype)
+        check(l, rng.exponential(size=l.shape).astype(np.float32), rules)
+
+
 def test_flat_rows():
     """Distinct logits in a few bins: a selection over the row, step by step."""
     note("flat rows")

@@ -353,7 +353,7 @@ __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rule
     tokens = wave_sum(tokens);
     rows = wave_max(rows, 0);
     __syncthreads();
-    const bool by_k = r.k > 0 && (uint32_t)r.k < tokens;
+    bool by_k = r.k > 0 && (uint32_t)r.k < tokens;
     // .. and its bins from the top, one to a thread, until they hold all that the rules ask
     // for (one CU reads them: bins that need not be read are time saved).
     const double ask = r.p < 1.0f ? (double)r.p * total * (1.0 + kNear) : 0.0;
@@ -397,6 +397,8 @@ __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rule
       __syncthreads();
       // (uniform: all threads have the same sums)
     } while (bins_read < rows && (by_k ? tokens_before < (uint32_t)r.k : mass_before < ask));
+    // (a share whose own largest is far below the row's counts tokens that weigh nothing here)
+    by_k = by_k && tokens_before >= (uint32_t)r.k;
     auto mass_up_to = [&](int bin) { return bin < 0 ? 0.0 : s.mass_to[bin]; };
     int bin_k = kBins, first = kBins, last = kBins;
     double low_sum = total, high_sum = total;
