@@ -1096,15 +1096,15 @@ hipError_t launch_share(const SampleArgs& a, hipStream_t s) {
 }  // namespace
 
 // Shares of 4096, 8192 or 16384 tokens: the first launch takes what the fullest CU has to
-// do (0.36 us per 1024 tokens), and the workgroup that sums a row's bins 0.35 us per
-// share.  Rows of one group: shares whose bins take no more than 128 MiB.
+// do (0.36 us per 1024 tokens), and a row's bins, written by one and read by the next,
+// 0.45 us per share (144 x 32000 tokens: 41.5 us in shares of 4096, 39.8 of 8192).  Rows of one group: shares whose bins take no more than 128 MiB.
 SampleShape sample_shape(const spear_sample_desc_t& d) {
   SampleShape s;
   constexpr int kCus = 256;
   double least = 0.0;
   for (int tokens = kSampleLeast; tokens <= 4 * kSampleLeast; tokens *= 2) {
     const int64_t shares = ceil_div(d.vocab, tokens);
-    const double us = 0.36 * (double)(ceil_div(d.batch * shares, kCus) * (tokens / 1024)) + 0.35 * (double)shares;
+    const double us = 0.36 * (double)(ceil_div(d.batch * shares, kCus) * (tokens / 1024)) + 0.45 * (double)shares;
     if (shares <= kSampleShares && (least == 0.0 || us < least)) {
       least = us;
       s.share_tokens = tokens;
