@@ -29,11 +29,11 @@
 // roundings of a term below 2^-12), and sums are held in 64 bits.
 //
 // What a call takes (replayed from a graph): 2 x 32000 tokens 18 us, a chain of four
-// launches of 3 to 6 us, whatever they do; 64 x 128001 fp16 logits under mixed rules 44:
-// 13 for the bins (15 vector instructions a token, some of them of 64 bits, and 4.5 us of
-// launch, loads and exchanges), 9 for the cuts (a row's bins are read by one CU), 13 for
-// the race (logits and the noise's lines at 3 TB/s), 9 for the ends; distributions of
-// 144 x 32000 tokens 42.  The launches' shapes follow from how fast one CU goes, which is
+// launches of 3 to 5 us, whatever they do; 64 x 128001 fp16 logits under mixed rules 43:
+// 13 for the bins (some 18 vector instructions a token, and 4.5 us of launch, loads and
+// exchanges), 8 for the cuts (a row's bins are read by one CU), 13 for the race (logits
+// and the noise's lines at 3 TB/s), 9 for the ends; distributions of 144 x 32000 tokens
+// 40.  The launches' shapes follow from how fast one CU goes, which is
 // some 25 bytes a ns whatever the pattern.
 //
 // Longer lists are cut by a radix selection, and a bin that holds more tokens than the
@@ -1096,15 +1096,16 @@ hipError_t launch_share(const SampleArgs& a, hipStream_t s) {
 }  // namespace
 
 // Shares of 4096, 8192 or 16384 tokens: the first launch takes what the fullest CU has to
-// do (0.36 us per 1024 tokens), and a row's bins, written by one and read by the next,
-// 0.45 us per share (144 x 32000 tokens: 41.5 us in shares of 4096, 39.8 of 8192).  Rows of one group: shares whose bins take no more than 128 MiB.
+// do (0.36 us per 1024 tokens and 0.3 per workgroup), and the workgroup that sums a row's
+// bins 0.35 us per share (shares of 4096 and 8192: 2 x 32000 tokens 17.6 and 18.3 us,
+// 144 x 32000 41.5 and 39.8).  Rows of one group: shares whose bins take no more than 128 MiB.
 SampleShape sample_shape(const spear_sample_desc_t& d) {
   SampleShape s;
   constexpr int kCus = 256;
   double least = 0.0;
   for (int tokens = kSampleLeast; tokens <= 4 * kSampleLeast; tokens *= 2) {
     const int64_t shares = ceil_div(d.vocab, tokens);
-    const double us = 0.36 * (double)(ceil_div(d.batch * shares, kCus) * (tokens / 1024)) + 0.45 * (double)shares;
+    const double us = (0.36 * (tokens / 1024) + 0.3) * (double)ceil_div(d.batch * shares, kCus) + 0.35 * (double)shares;
     if (shares <= kSampleShares && (least == 0.0 || us < least)) {
       least = us;
       s.share_tokens = tokens;
