@@ -69,7 +69,7 @@ def spear_kv_plan(lens, new_tokens, held, block_table, free_pages, free_count, r
     _dense(free_pages, "free_pages", i32, 1, dev)
     _dense(free_count, "free_count", i32, 1, dev)
     B, pages = block_table.shape
-    if lens.shape[0] != B or new_tokens.shape[0] != B or held.shape[0] != B or free_count.shape[0] != 1:
+    if lens.numel() != B or new_tokens.numel() != B or held.numel() != B or free_count.numel() != 1:
         raise ValueError("need lens, new_tokens and held [B], block_table [B, max_pages], free_count [1]")
     rows = int(rows)
     if rows < 0:
@@ -86,9 +86,9 @@ def spear_kv_plan(lens, new_tokens, held, block_table, free_pages, free_count, r
         given = [_out(t, name, (n,), i32, dev) for t, name, n in zip(given, _PLANNED, sizes)]
     cu_q, kv_lens, positions, sequence, held_out, free_out = given
     lib, stream = _binding.load(), _stream(dev)
-    d = _plan(("kv_plan", B, rows, pages, int(page_size), free_pages.shape[0]), lambda: (
-        KvPlanDesc(B, rows, pages, int(page_size), free_pages.shape[0]), lib.spear_kv_plan_workspace_bytes,
-        "spear_kv_plan"))
+    page_size, free_slots = int(page_size), free_pages.numel()
+    d = _plan(("kv_plan", B, rows, pages, page_size, free_slots), lambda: (
+        KvPlanDesc(B, rows, pages, page_size, free_slots), lib.spear_kv_plan_workspace_bytes, "spear_kv_plan"))
     ws = _space(workspace, d[2], dev, stream)
     st = lib.spear_kv_plan(d[1], lens.data_ptr(), new_tokens.data_ptr(), held.data_ptr(), block_table.data_ptr(), pages,
                            free_pages.data_ptr(), free_count.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(),
@@ -101,10 +101,10 @@ def spear_kv_plan(lens, new_tokens, held, block_table, free_pages, free_count, r
 class AdapterPlan:
     """The rows of a batch by adapter: what spear_adapter_plan makes for a step and
     spear_adapter_add reads."""
-    __slots__ = ("data", "batch", "adapters", "rows")
+    __slots__ = ("data", "device", "batch", "adapters", "rows")
 
     def __init__(self, data, batch, adapters, rows):
-        self.data, self.batch, self.adapters, self.rows = data, batch, adapters, rows
+        self.data, self.device, self.batch, self.adapters, self.rows = data, data.device, batch, adapters, rows
 
 
 @functools.lru_cache(maxsize=4096)
@@ -124,15 +124,15 @@ def spear_adapter_plan(cu_q, adapter, adapters, rows, plan=None):
     dev = _gpu(cu_q, "cu_q")
     _dense(cu_q, "cu_q", torch.int32, 1, dev)
     _dense(adapter, "adapter", torch.int32, 1, dev)
-    B, adapters, rows = adapter.shape[0], int(adapters), int(rows)
-    if cu_q.shape[0] != B + 1:
+    B, adapters, rows = adapter.numel(), int(adapters), int(rows)
+    if cu_q.numel() != B + 1:
         raise ValueError("cu_q must have one entry more than adapter")
     lib, stream = _binding.load(), _stream(dev)
     if plan is None:
         plan = AdapterPlan(torch.empty(_plan_bytes(B, adapters, rows), dtype=torch.uint8, device=dev), B, adapters, rows)
     elif not isinstance(plan, AdapterPlan):
         raise TypeError("plan must come from spear_adapter_plan")
-    elif (plan.batch, plan.adapters, plan.rows) != (B, adapters, rows) or plan.data.device != dev:
+    elif (plan.batch, plan.adapters, plan.rows) != (B, adapters, rows) or plan.device != dev:
         raise ValueError("plan was made for other sizes")
     st = lib.spear_adapter_plan(B, adapters, rows, cu_q.data_ptr(), adapter.data_ptr(), plan.data.data_ptr(),
                                 plan.data.numel(), stream)
@@ -157,26 +157,26 @@ def spear_adapter_add(Y, X, A, B, plan, scale=None, workspace=None):
     _dense(B, "B", f16, 3, dev)
     if not isinstance(plan, AdapterPlan):
         raise TypeError("plan must come from spear_adapter_plan")
-    if plan.data.device != dev:
+    if plan.device != dev:
         raise ValueError(f"plan must be on {dev}")
     n, rank, K = A.shape
     rows, N = Y.shape
     if B.shape != (n, N, rank) or X.shape != (rows, K) or plan.adapters != n or plan.rows != rows:
         raise ValueError("need Y [rows, N], X [rows, K], A [adapters, rank, K], B [adapters, N, rank] and a plan of "
                          "these rows and adapters")
-    for t, name in ((X, "X"), (Y, "Y")):
-        if t.stride(1) != 1 and t.shape[1] > 1:
-            raise ValueError(f"{name} must be contiguous in its last dimension")
+    (xs, x1), (ys, y1) = X.stride(), Y.stride()
+    if (x1 != 1 and K > 1) or (y1 != 1 and N > 1):
+        raise ValueError("X and Y must be contiguous in their last dimension")
     if scale is not None:
         _dense(scale, "scale", torch.float32, 1, dev)
-        if scale.shape[0] != n:
+        if scale.numel() != n:
             raise ValueError("scale must be [adapters]")
     lib, stream = _binding.load(), _stream(dev)
     d = _plan(("adapter", dev.index, plan.batch, n, rows, K, N, rank), lambda: (
         AdapterDesc(plan.batch, n, rows, K, N, rank, 0), lib.spear_adapter_workspace_bytes, "spear_adapter_add"))
     ws = _space(workspace, d[2], dev, stream)
-    # (the strides of a single row say nothing)
-    xs, ys = (K, N) if rows == 1 else (X.stride(0), Y.stride(0))
+    if rows == 1:       # (the strides of a single row say nothing)
+        xs, ys = K, N
     st = lib.spear_adapter_add(d[1], X.data_ptr(), xs, A.data_ptr(), B.data_ptr(), _p(scale), plan.data.data_ptr(),
                                plan.data.numel(), Y.data_ptr(), ys, *ws, stream)
     _binding.check(st, "spear_adapter_add")
