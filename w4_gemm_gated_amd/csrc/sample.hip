@@ -64,7 +64,7 @@ typedef unsigned long long u64;
 
 enum Kind : int32_t { kEmpty, kOne, kRace };      // no token, the first one, a race of several
 
-// What a row's first launch leaves for the others.  t: kPer log2 of a weight, on the
+// What the cuts leave of a row for the launches after them.  t: kPer log2 of a weight, on the
 // row's grid; bins are counted from the one of the row's largest; masses are in units
 // of that bin's upper edge.  Every limit on t is a limit on the logit too: the least
 // fp32 number whose t reaches it (NaN: there is none).
@@ -74,7 +74,7 @@ struct RowInfo {
   double before, before_k;   // mass before bin `first`, and before bin_k
   double target;             // top-p's mass if that is known; else (with top-k) p
   double edge;               // weight at the upper edge of bin `first`
-  u64 end;                   // second launch: key of the last token kept (0: all)
+  u64 end;                   // from the row's end: key of the last token kept (0: all)
   double inv;                // 1 / mass of what is kept, in units of the largest weight
   int32_t first, last;       // tokens of bins before `first` are kept, those of bins past `last` are not ..
   int32_t bin_k;             // .. and top-k's cut lies in this bin (one of them, or past them; -1: no such cut)
@@ -271,7 +271,7 @@ __device__ __forceinline__ const void* row_of(const SampleArgs& a, int b) {
   return (const char*)a.logits + r * a.stride * (a.f16 ? 2 : 4);
 }
 
-// -------------------------------------------------------------- first launch
+// ------------------------------------------------------------- bins and cuts
 
 // (`step`: kSteps of the bin, the same for all of a thread's)
 static_assert(kThreads % kPer == 0, "a thread's bins have one place in their powers of two");
@@ -297,8 +297,7 @@ struct CutScratch {
   float limits[6];
 };
 
-// From a row's shares, when all of them are there: its largest, and the bins in which
-// the cuts lie.
+// From a row's shares: its largest, and the bins in which the cuts lie.
 __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rules& r, ShareInfo mine, double scale,
                                           double step, CutScratch& s) {
   const int tid = threadIdx.x;
@@ -564,7 +563,7 @@ __global__ void __launch_bounds__(kThreads) sample_cuts_kernel(SampleArgs a) {
   find_cuts(a, b, r, mine, scale_of(r), step, s);
 }
 
-// ------------------------------------------------------------- second launch
+// --------------------------------------------------------- race and its end
 
 // The race's key of a weight and its noise: the score's bits rise with it; 0 if it
 // takes no part.
@@ -860,7 +859,7 @@ __device__ Cut cut_selected(const SampleArgs& a, const RowInfo& o, const void* r
   return c;
 }
 
-// From a row's shares, when all of them are there: the list cut, and the race's end.
+// From a row's parts and list: the list cut, and the race's end.
 template <bool F16>
 __device__ __forceinline__ void end_race(const SampleArgs& a, int b, Scratch& s) {
   const int tid = threadIdx.x;
@@ -1033,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads) sample_end_kernel(SampleArgs a) {
   end_race<F16>(a, blockIdx.x, s);
 }
 
-// -------------------------------------------------------------- third launch
+// --------------------------------------------------------- the distributions
 
 template <bool F16>
 __global__ void __launch_bounds__(kThreads) sample_probs_kernel(SampleArgs a) {
@@ -1095,7 +1094,7 @@ hipError_t launch_share(const SampleArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Shares of 4096, 8192 or 16384 tokens: the first launch takes what the fullest CU has to
+// Shares of 4096, 8192 or 16384 tokens: the bins take what the fullest CU has to
 // do (0.36 us per 1024 tokens and 0.3 per workgroup), and the workgroup that sums a row's
 // bins 0.35 us per share (shares of 4096 and 8192: 2 x 32000 tokens 17.6 and 18.3 us,
 // 144 x 32000 41.5 and 39.8).  Rows of one group: shares whose bins take no more than 128 MiB.
