@@ -178,6 +178,29 @@ def test_special_values():
             check(l, rng.exponential(size=(8, V)).astype(np.float32), [rule] * 8)
 
 
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+@pytest.mark.parametrize("V", [3, 5000])
+def test_extreme_settings(V, dtype):
+    """Settings at the ends of their types, over logits of every size.  (No min-p of 1:
+    the oracle's weights round to 1 there, and the logits' order decides here.)"""
+    note(f"extreme settings, V {V} {np.dtype(dtype).name}")
+    rng = np.random.default_rng(V)
+    rules = [(np.inf, 0, 0.9, 0), (1e-45, 0, 0.9, 0), (1e-38, 50, 0.9, 0.1), (1e30, 5, 0.5, 0.1), (3e38, 0, 1, 0.99),
+             (1, -4, 1.5, -1), (1, 2**31 - 1, 1, 0.5), (-1, 0, 1, 0), (np.nan, 3, 0.5, 0), (1, 0, 1e-45, 0),
+             (1, 0, 1 - 2**-24, 0), (1, 0, 1, 1e-45), (1, 0, 1, 1e-38), (100, V - 1, 0.99999, 0)]
+    n, info = len(rules), np.finfo(dtype)
+    noise = rng.exponential(size=(n, V)).astype(np.float32)
+    alone = np.full((n, V), -np.inf, dtype)
+    alone[:, V // 2] = 3
+    wide = np.full((n, V), info.max, dtype)
+    wide[:, ::2] *= -1
+    small = np.full((n, V), info.tiny, dtype)
+    small[:, ::2] = info.smallest_subnormal
+    small[:, ::3] = -0.0
+    for l in (logits(rng, n, V, dtype), alone, np.full((n, V), np.inf, dtype), wide, small):
+        check(l, noise, rules)
+
+
 def test_noise_values():
     """Zero noise wins, infinite noise loses to any other, NaN takes no part; ties go to
     the lowest index."""
