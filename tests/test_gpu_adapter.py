@@ -169,6 +169,26 @@ def test_infinities_and_nan_stay_in_their_rows(rank):
     assert (np.abs(got[keep].astype(np.float64) - want[keep]) <= tol[keep]).all()
 
 
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 48, 64])
+@pytest.mark.parametrize("K,N", [(2048, 1000), (520, 4100)])
+def test_rows_that_fall_to_one_adapter(rank, K, N):
+    """A decode step with many adapters to choose from, whose requests want one of them
+    (tiles of 64, of 17 and of one row), or nearly all of them."""
+    note(f"one adapter of many, rank {rank} K {K} N {N}")
+    rng = np.random.default_rng(rank + K)
+    adapters = 40
+    X, A, B, Y = tensors(rng, 100, K, N, rank, adapters)
+    scale = rng.normal(size=adapters).astype(np.float32)
+    cu = np.arange(101, dtype=np.int32)
+    for of in (np.full(100, 7), np.where(np.arange(100) < 81, 7, 3), np.where(np.arange(100) % 5 == 0, -1, np.arange(100) % 40)):
+        of = of.astype(np.int32)
+        plan = sp.spear_adapter_plan(dev(cu), dev(of), adapters, 100)
+        got = sp.spear_adapter_add(dev(Y), dev(X), dev(A), dev(B), plan, dev(scale))
+        torch.cuda.synchronize()
+        want, slack = ref.adapter_add(Y, X, A, B, cu, of, scale)
+        compare(got.cpu().numpy(), want, slack, Y, cu, of, adapters)
+
+
 def test_a_row_does_not_depend_on_its_batch():
     """The same row alone, among others of its adapter, and among other adapters'
     (where K is cut alike)."""

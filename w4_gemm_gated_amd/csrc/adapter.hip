@@ -506,30 +506,42 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(AdapterArgs a)
 
 // Both products in one launch, for few rows and a short K: every workgroup of a tile forms
 // its H by itself (from the XCD's L2, after the first) and applies it to its columns,
-// whose B and Y come in meanwhile.  Tiles of more rows go sixteen at a time.
+// whose B and Y come in meanwhile.  Up to rank 32 a tile of more than 16 rows goes in one
+// pass (64 rows of one adapter of rank 16: 16 us, sixteen at a time 26).
+template <int RB, int ROWS, int STRIDE>
+struct FusedScratch {
+  f4_t red[(ROWS > 16 ? kShrinkWaves / 2 * 4 : kShrinkWaves) * RB * kWave];
+  float h[ROWS * 16 * RB];
+  __attribute__((aligned(16))) half_t halves[ROWS * STRIDE];
+  float factor[ROWS];
+};
+template <int RB, int SB, bool PACK, int SUB, int STRIDE, typename S>
+__device__ __forceinline__ void fused(const AdapterArgs& a, const Tile& t, int n0, int n_end, S& s) {
+  const int32_t* list = a.plan + kPlanHead + 4 * (int64_t)a.most_tiles;
+  Operands<SB, SUB> r;
+  if (n0 < n_end) request<SB, PACK, SUB>(a, t, n0, r);
+  shrink<RB, SUB>(a, t, list, 0, 0, a.K, s.red, [&](int row, int rank, const f4_t& v) { *(f4_t*)(s.h + row * a.rank + rank) = v; });
+  __syncthreads();
+  to_halves<16 * SUB>(a, t, s.h, s.factor, s.halves, STRIDE);
+  for (int n = n0; n < n_end; n += kShrinkWaves * kUnit) {
+    if (n > n0) request<SB, PACK, SUB>(a, t, n, r);
+    apply<SB, PACK, SUB>(a, t, n, r, s.halves, STRIDE, s.factor);
+  }
+}
 template <int RB, int SB, bool PACK>
 __global__ void __launch_bounds__(kShrinkThreads) adapter_fused_kernel(AdapterArgs a) {
   constexpr int kStride = (PACK ? 32 : 64 * SB) + 8;
-  __shared__ f4_t red[kShrinkWaves * RB * kWave];
-  __shared__ float h[16 * 16 * RB];
-  __shared__ __attribute__((aligned(16))) half_t halves[16 * kStride];
-  __shared__ float factor[16];
+  constexpr bool kWhole = RB <= 2;       // (LDS holds the sums of a whole tile's rows)
+  __shared__ FusedScratch<RB, kWhole ? kAdapterTile : 16, kStride> s;
   const int tile = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks, wave = threadIdx.x / kWave;
   if (tile >= min(a.plan[0], a.most_tiles)) return;
-  const Tile whole = tile_of(a, tile);
-  const int32_t* list = a.plan + kPlanHead + 4 * (int64_t)a.most_tiles;
+  const Tile t = tile_of(a, tile);
   const int n_end = min((chunk + 1) * a.chunk_columns, a.N), n0 = chunk * a.chunk_columns + wave * kUnit;
-  for (int row0 = 0; row0 < whole.rows; row0 += 16) {
-    const Tile t = {whole.adapter, whole.first + row0, min(whole.rows - row0, 16)};
-    Operands<SB, 1> r;
-    if (n0 < n_end) request<SB, PACK, 1>(a, t, n0, r);
-    shrink<RB, 1>(a, t, list, 0, 0, a.K, red, [&](int row, int rank, const f4_t& v) { *(f4_t*)(h + row * a.rank + rank) = v; });
-    __syncthreads();
-    to_halves<16>(a, t, h, factor, halves, kStride);
-    for (int n = n0; n < n_end; n += kShrinkWaves * kUnit) {
-      if (n > n0) request<SB, PACK, 1>(a, t, n, r);
-      apply<SB, PACK, 1>(a, t, n, r, halves, kStride, factor);
-    }
+  if (kWhole && t.rows > 16) {
+    fused<RB, SB, PACK, 4, kStride>(a, t, n0, n_end, s);
+  } else {
+    for (int row0 = 0; row0 < t.rows; row0 += 16)
+      fused<RB, SB, PACK, 1, kStride>(a, Tile{t.adapter, t.first + row0, min(t.rows - row0, 16)}, n0, n_end, s);
   }
 }
 
