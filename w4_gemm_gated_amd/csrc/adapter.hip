@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(kShrinkThreads) adapter_shrink_kernel(AdapterA
   extern __shared__ f4_t lds[];
   __shared__ float factor[kAdapterTile];
   __shared__ uint32_t arrived;
-  const int tile = blockIdx.x / a.slices, slice = blockIdx.x % a.slices, tid = threadIdx.x;
+  const int shares = a.slices * a.groups;
+  const int tile = blockIdx.x / shares, slice = blockIdx.x % shares / a.groups, tid = threadIdx.x;
   if (tile >= min(a.plan[0], a.most_tiles)) return;
   const Tile t = tile_of(a, tile);
   const int32_t* list = a.plan + kPlanHead + 4 * (int64_t)a.most_tiles;
@@ -318,17 +319,17 @@ __global__ void __launch_bounds__(kShrinkThreads) adapter_shrink_kernel(AdapterA
   char* parts = a.part + (size_t)tile * a.slices * tile_bytes;
   const __amdgpu_buffer_rsrc_t part = make_rsrc(parts + slice * tile_bytes, (uint32_t)tile_bytes);
   const int k_lo = slice * a.slice_k, k_hi = min(k_lo + a.slice_k, a.K);
-  for (int rank0 = 0; rank0 < a.rank; rank0 += 16 * RB) {
-    auto keep = [&](int row, int rank, const f4_t& v) { store_f4_dev(part, 4u * (uint32_t)(row * a.rank + rank), v); };
+  auto keep = [&](int row, int rank, const f4_t& v) { store_f4_dev(part, 4u * (uint32_t)(row * a.rank + rank), v); };
+  for (int rank0 = blockIdx.x % a.groups * 16 * RB; rank0 < a.rank; rank0 += a.groups * 16 * RB) {
     if (t.rows <= 16) shrink<RB, 1>(a, t, list, rank0, k_lo, k_hi, lds, keep);
     else shrink<RB, 4>(a, t, list, rank0, k_lo, k_hi, lds, keep);
   }
   drain_vm();
   __syncthreads();
-  if (a.slices > 1) {
+  if (shares > 1) {
     if (tid == 0) arrived = add_dev_u32(&a.counters[tile], 1u);
     __syncthreads();
-    if (arrived != (uint32_t)a.slices - 1) return;
+    if (arrived != (uint32_t)shares - 1) return;
     if (tid == 0) st_dev_u32(&a.counters[tile], 0u);
   }
   // The slices in order; then every row as two fp16 numbers per value.
@@ -549,7 +550,7 @@ template <int RB>
 hipError_t shrink_launch(const AdapterArgs& a, hipStream_t s) {
   const size_t red = (size_t)kShrinkWaves / 2 * 4 * RB * kWave * sizeof(f4_t), h = (size_t)kAdapterTile * a.rank * 4;
   const size_t bytes = red > h ? red : h;
-  adapter_shrink_kernel<RB><<<dim3((unsigned)(a.most_tiles * a.slices)), dim3(kShrinkThreads), bytes, s>>>(a);
+  adapter_shrink_kernel<RB><<<dim3((unsigned)(a.most_tiles * (int64_t)a.slices * a.groups)), dim3(kShrinkThreads), bytes, s>>>(a);
   return hipGetLastError();
 }
 
@@ -573,20 +574,26 @@ size_t adapter_plan_size(int64_t rows, int64_t batch, int64_t adapters) {
 // The launch shape by what a call is expected to take.  A workgroup reads its rows of X
 // and its ranks of A at about 25 bytes a ns, and workgroups past the CUs' number wait for
 // a place.  Two launches: slices of K (at least 512, joined in 2 us and the time in which
-// one workgroup reads them), and 4 us more than one.  One launch: all of K in every
+// one workgroup reads them), and 4 us more than one; ranks past 64 go to workgroups of
+// their own (2048 rows of rank 128, 4096 to 4096 columns: 40 us, one after the other 44; 16
+// rows of rank 256: 25 and 32).  One launch: all of K in every
 // workgroup, for as many columns as leave no more workgroups than CUs.
 AdapterShape adapter_shape(const spear_adapter_desc_t& d, int cus) {
   AdapterShape s;
   s.tiles = (int)adapter_most_tiles(d.rows, d.batch, d.adapters);
   s.rank_pad = d.rank <= 16 ? d.rank : d.rank <= 32 ? 32 : d.rank <= 64 ? 64 : d.rank <= 128 ? 128 : 256;
   const double rows = s.tiles > 0 ? (double)d.rows / s.tiles : 1.0;
-  auto reads = [&](double k, int64_t workgroups) { return k * 2.0 * (rows + d.rank) / 25e3 * (double)ceil_div(workgroups, cus); };
+  // (up to 64 ranks a workgroup, where there are counters to join them)
+  const bool joins = s.tiles <= (int)kMaxEcTiles;
+  s.groups = joins ? (int)ceil_div(d.rank, kAdapterRanks) : 1;
+  const double ranks = s.groups > 1 ? kAdapterRanks : d.rank;
+  auto reads = [&](double k, int64_t workgroups) { return k * 2.0 * (rows + ranks) / 25e3 * (double)ceil_div(workgroups, cus); };
   double least = 0.0;
   s.slices = 1;
   s.slice_k = (int)round_up(d.K, 512);
-  for (int64_t n = 1; n <= std::min<int64_t>(ceil_div(d.K, 512), 64) && s.tiles <= (int)kMaxEcTiles; ++n) {
+  for (int64_t n = 1; n <= std::min<int64_t>(ceil_div(d.K, 512), 64) && (joins || n == 1); ++n) {
     const int64_t k = round_up(ceil_div(d.K, n), 512), slices = ceil_div(d.K, k);
-    const double us = reads((double)k, s.tiles * slices) + (slices > 1 ? 2.0 + (double)slices * rows * d.rank * 4.0 / 80e3 : 0.0);
+    const double us = reads((double)k, s.tiles * slices * s.groups) + (slices > 1 ? 2.0 + (double)slices * rows * d.rank * 4.0 / 25e3 : 0.0);
     if (n == 1 || us < least) {
       least = us;
       s.slice_k = (int)k;
@@ -595,7 +602,7 @@ AdapterShape adapter_shape(const spear_adapter_desc_t& d, int cus) {
   }
   const int64_t units = ceil_div(d.N, 2 * kAdapterColumns), fit = s.tiles > 0 ? std::max<int64_t>(1, cus / s.tiles) : 1;
   const int64_t chunks = std::min(units, fit);
-  s.fused = d.rank <= 64 && rows <= 16.0 && reads((double)d.K, s.tiles * chunks) <= least + 4.0;
+  s.fused = d.rank <= kAdapterRanks && rows <= 16.0 && reads((double)d.K, s.tiles * chunks) <= least + 4.0;
   s.chunk_columns = s.fused ? (int)(2 * kAdapterColumns * ceil_div(units, chunks)) : kAdapterColumns;
   size_t at = kSyncHeaderBytes;
   s.H = at;

@@ -153,6 +153,7 @@ hipError_t launch_kv_plan(const KvPlanArgs& a, void* stream);
 // Adapters of many requests.
 constexpr int kMaxAdapters = 4096;   // counted in LDS by the plan
 constexpr int kAdapterTile = 64;     // rows of one adapter that a workgroup takes
+constexpr int kAdapterRanks = 64;    // most ranks of the first product that one takes at once
 constexpr int kAdapterColumns = 256; // columns of the output that one takes at once
 struct AdapterPlanArgs {
   int32_t batch, adapters, rows, most_tiles;
@@ -165,13 +166,13 @@ size_t adapter_plan_size(int64_t rows, int64_t batch, int64_t adapters);
 
 // Launch shape and workspace (offsets in bytes) of an adapter call.
 struct AdapterShape {
-  int tiles, rank_pad, slices, slice_k, chunk_columns;
+  int tiles, rank_pad, slices, slice_k, groups, chunk_columns;     // groups: of ranks
   bool fused;           // both products in one launch
   size_t H, factor, part, bytes;
 };
 AdapterShape adapter_shape(const spear_adapter_desc_t& d, int cus);
 struct AdapterArgs {
-  int32_t rows, adapters, K, N, rank, rank_pad, most_tiles, slices, slice_k, chunks, chunk_columns;
+  int32_t rows, adapters, K, N, rank, rank_pad, most_tiles, slices, slice_k, groups, chunks, chunk_columns;
   bool fused;
   const void *X, *A, *B;
   const float* scale;      // [adapters], or null: 1

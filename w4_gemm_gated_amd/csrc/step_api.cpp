@@ -154,7 +154,7 @@ spear_status_t spear_adapter_add(const spear_adapter_desc_t* desc, const void* X
   AdapterArgs a;
   a.rows = desc->rows; a.adapters = desc->adapters; a.K = desc->K; a.N = desc->N; a.rank = desc->rank;
   a.rank_pad = s.rank_pad; a.most_tiles = s.tiles; a.slices = s.slices; a.slice_k = s.slice_k;
-  a.fused = s.fused; a.chunk_columns = s.chunk_columns;
+  a.groups = s.groups; a.fused = s.fused; a.chunk_columns = s.chunk_columns;
   a.chunks = (int32_t)ceil_div(desc->N, s.chunk_columns);
   a.X = X; a.A = A; a.B = B; a.scale = scale; a.plan = plan; a.Y = Y;
   a.x_stride = x_stride; a.y_stride = y_stride;
