@@ -40,6 +40,7 @@
 // list (equal logits, a very high temperature) by the same selection over the row
 // itself, by one workgroup: 64 x 128001 tokens within 0.05 of each other take 290 us.
 #include <algorithm>
+#include <type_traits>
 
 #include "serve_internal.h"
 #include "wave_ops.h"
@@ -284,10 +285,9 @@ struct BinsScratch {
   u64 hist[kBins];
   u64 red[kWaves];
   double redd[kWaves];
-  uint32_t redc[kWaves];
+  uint32_t redc[kWaves], tokens[kWaves];
 };
 struct CutScratch {
-  double mass_to[kBins];        // the row's mass up to and with each bin
   double steps[kPer];
   double redd[kWaves];
   uint32_t redc[kWaves];
@@ -297,9 +297,12 @@ struct CutScratch {
   float limits[6];
 };
 
-// From a row's shares: its largest, and the bins in which the cuts lie.
+// From a row's shares: its largest, and the bins in which the cuts lie.  `mine`: the share of
+// this lane's number; bin_of_row(bin, n, def) adds what the shares have in a bin of the
+// row's; mass_to: the row's mass (the bits of a double) up to and with each bin.
+template <typename F>
 __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rules& r, ShareInfo mine, double scale,
-                                          double step, CutScratch& s) {
+                                          double step, CutScratch& s, u64* mass_to, F bin_of_row) {
   const int tid = threadIdx.x;
   const bool bins = !r.one && (r.k > 0 || r.p < 1.0f);
   // The row: its largest, ..
@@ -356,8 +359,7 @@ __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rule
     // .. and its bins from the top, one to a thread, until they hold all that the rules ask
     // for (one CU reads them: bins that need not be read are time saved).
     const double ask = r.p < 1.0f ? (double)r.p * total * (1.0 + kNear) : 0.0;
-    const u64* from = a.hist + (int64_t)b * a.shares * kBins;
-    constexpr int kTogether = 8;      // shares whose loads are in flight together
+    auto mass_up_to = [&](int bin) { return bin < 0 ? 0.0 : __longlong_as_double((long long)mass_to[bin]); };
     double mass_before = 0.0;
     uint32_t tokens_before = 0;
     int bins_read = 0;
@@ -365,25 +367,12 @@ __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rule
       const int bin = bins_read + tid;
       uint32_t n = 0;
       u64 def = 0;
-      for (int i0 = 0; i0 < a.shares; i0 += kTogether) {
-        u64 v[kTogether];
-#pragma unroll
-        for (int i = 0; i < kTogether; ++i) {
-          const int of = min(i0 + i, a.shares - 1), at = bin - s.share_off[of];
-          v[i] = i0 + i < a.shares && at >= 0 && at < s.share_used[of] ? from[(int64_t)of * kBins + at] : 0;
-        }
-#pragma unroll
-        for (int i = 0; i < kTogether; ++i) {
-          n += (uint32_t)(v[i] >> 48);
-          def += v[i] & ((1ull << 48) - 1);
-        }
-      }
-      double mass_to = mass_of(bin, step, n, def);
+      bin_of_row(bin, n, def);
+      double to = mass_of(bin, step, n, def);
       uint32_t tokens_to = n;
-      block_run(mass_to, tokens_to, s.redd, s.redc);
-      mass_to += mass_before;
+      block_run(to, tokens_to, s.redd, s.redc);
       tokens_to += tokens_before;
-      s.mass_to[bin] = mass_to;
+      mass_to[bin] = (u64)__double_as_longlong(to + mass_before);
       if (by_k && tokens_to >= (uint32_t)r.k && tokens_to - n < (uint32_t)r.k) {
         s.found = bin;
         s.found_before = tokens_to - n;
@@ -391,14 +380,13 @@ __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rule
       if (tid == kThreads - 1) s.tokens_all = tokens_to;
       __syncthreads();
       bins_read += kThreads;
-      mass_before = s.mass_to[bins_read - 1];
+      mass_before = mass_up_to(bins_read - 1);
       tokens_before = s.tokens_all;
       __syncthreads();
       // (uniform: all threads have the same sums)
     } while (bins_read < rows && (by_k ? tokens_before < (uint32_t)r.k : mass_before < ask));
     // (a share whose own largest is far below the row's counts tokens that weigh nothing here)
     by_k = by_k && tokens_before >= (uint32_t)r.k;
-    auto mass_up_to = [&](int bin) { return bin < 0 ? 0.0 : s.mass_to[bin]; };
     int bin_k = kBins, first = kBins, last = kBins;
     double low_sum = total, high_sum = total;
     if (by_k) {
@@ -475,9 +463,11 @@ __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rule
   }
 }
 
-template <bool F16, int EACH>
+// ONE: a row is a single share, whose cuts are found at once, from the bins in LDS.
+template <bool F16, int EACH, bool ONE>
 __global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
   __shared__ BinsScratch s;
+  __shared__ std::conditional_t<ONE, CutScratch, char> cut;
   const int b = blockIdx.x / a.shares, share = blockIdx.x % a.shares, tid = threadIdx.x;
   const Rules r = rules_of(a, b);
   const void* row = row_of(a, b);
@@ -519,7 +509,7 @@ __global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
     least = least < s.redc[i] ? least : s.redc[i];
   }
   const double scale = scale_of(r);
-  ShareInfo* mine = a.share + (int64_t)b * a.shares + share;
+  ShareInfo mine = {best, 0, 0, 0};
   if (bins && best != 0) {
     const double q = floor(t_of(logit_of(best), scale));
 #pragma unroll
@@ -531,36 +521,71 @@ __global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a) {
     }
     const double span = q - floor(t_of(logit_of((u64)least << 32), scale)) + 1.0;
     const int used = span < kBins ? (int)span : kBins;
-    u64* bins_out = a.hist + ((int64_t)b * a.shares + share) * kBins;
     __syncthreads();
     // The bins, and their sums: those of the row come from the shares' own.
     double mass = 0.0;
     uint32_t n = 0;
     for (int i = tid; i < used; i += kThreads) {
       const u64 v = s.hist[i];
-      bins_out[i] = v;
+      if constexpr (!ONE) a.hist[((int64_t)b * a.shares + share) * kBins + i] = v;
       mass += mass_of(i, step, (uint32_t)(v >> 48), v & ((1ull << 48) - 1));
       n += (uint32_t)(v >> 48);
     }
-    block_run(mass, n, s.redd, s.redc);
-    if (tid == kThreads - 1) {
-      mine->number = (u64)__double_as_longlong(q);
-      mine->mass = (u64)__double_as_longlong(mass);
-      mine->used = (u64)n << 32 | (u64)used;
+    mass = wave_sum(mass);
+    n = wave_sum(n);
+    if (tid % kWave == 0) {
+      s.redd[tid / kWave] = mass;
+      s.tokens[tid / kWave] = n;
     }
+    __syncthreads();
+    mass = s.redd[0];
+    n = s.tokens[0];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) {
+      mass += s.redd[i];
+      n += s.tokens[i];
+    }
+    mine = {best, (u64)__double_as_longlong(q), (u64)__double_as_longlong(mass), (u64)n << 32 | (u64)used};
   }
-  if (tid == 0) mine->best = best;
+  if constexpr (ONE) {
+    if (tid < kPer) cut.steps[tid] = step;
+    __syncthreads();
+    // (a thread's bins give way to the masses up to them)
+    find_cuts(a, b, r, mine, scale, step, cut, s.hist, [&](int bin, uint32_t& n, u64& def) {
+      n = (uint32_t)(s.hist[bin] >> 48);
+      def = s.hist[bin] & ((1ull << 48) - 1);
+    });
+  } else {
+    if (tid == 0) a.share[(int64_t)b * a.shares + share] = mine;
+  }
 }
 
 __global__ void __launch_bounds__(kThreads) sample_cuts_kernel(SampleArgs a) {
   __shared__ CutScratch s;
+  __shared__ u64 mass_to[kBins];
   const int b = blockIdx.x;
   const ShareInfo mine = a.share[(int64_t)b * a.shares + min((int)threadIdx.x % kWave, a.shares - 1)];
   const Rules r = rules_of(a, b);
   const double step = kSteps[threadIdx.x % kPer];
   if (threadIdx.x < kPer) s.steps[threadIdx.x] = step;
   __syncthreads();
-  find_cuts(a, b, r, mine, scale_of(r), step, s);
+  const u64* from = a.hist + (int64_t)b * a.shares * kBins;
+  find_cuts(a, b, r, mine, scale_of(r), step, s, mass_to, [&](int bin, uint32_t& n, u64& def) {
+    constexpr int kTogether = 8;      // shares whose loads are in flight together
+    for (int i0 = 0; i0 < a.shares; i0 += kTogether) {
+      u64 v[kTogether];
+#pragma unroll
+      for (int i = 0; i < kTogether; ++i) {
+        const int of = min(i0 + i, a.shares - 1), at = bin - s.share_off[of];
+        v[i] = i0 + i < a.shares && at >= 0 && at < s.share_used[of] ? from[(int64_t)of * kBins + at] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < kTogether; ++i) {
+        n += (uint32_t)(v[i] >> 48);
+        def += v[i] & ((1ull << 48) - 1);
+      }
+    }
+  });
 }
 
 // --------------------------------------------------------- race and its end
@@ -1092,8 +1117,12 @@ template <bool F16, int EACH>
 hipError_t launch(const SampleArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)(a.batch * a.shares)), parts((unsigned)(a.batch * a.parts)), rows((unsigned)a.batch),
       block(kThreads);
-  sample_bins_kernel<F16, EACH><<<grid, block, 0, s>>>(a);
-  sample_cuts_kernel<<<rows, dim3(kThreads), 0, s>>>(a);
+  if (a.shares == 1) {
+    sample_bins_kernel<F16, EACH, true><<<grid, block, 0, s>>>(a);
+  } else {
+    sample_bins_kernel<F16, EACH, false><<<grid, block, 0, s>>>(a);
+    sample_cuts_kernel<<<rows, block, 0, s>>>(a);
+  }
   if (!a.only_first) {
     sample_race_kernel<F16><<<parts, block, 0, s>>>(a);
     sample_end_kernel<F16><<<rows, block, 0, s>>>(a);
@@ -1114,14 +1143,16 @@ hipError_t launch_share(const SampleArgs& a, hipStream_t s) {
 // Shares of 4096, 8192 or 16384 tokens: the bins take what the fullest CU has to
 // do (0.36 us per 1024 tokens and 0.3 per workgroup), and the workgroup that sums a row's
 // bins 0.35 us per share (shares of 4096 and 8192: 2 x 32000 tokens 17.6 and 18.3 us,
-// 144 x 32000 41.5 and 39.8).  Rows of one group: shares whose bins take no more than 128 MiB.
+// 144 x 32000 41.5 and 39.8).  A row of one share saves that launch (16 x 1000 tokens 17.3
+// and 14.8 us, 16 x 8000 17.6 and 16.3, 16 x 16000 17.8 in four shares and 18.4 in one).  Rows of one group: shares whose bins take no more than 128 MiB.
 SampleShape sample_shape(const spear_sample_desc_t& d) {
   SampleShape s;
   constexpr int kCus = 256;
   double least = 0.0;
   for (int tokens = kSampleLeast; tokens <= 4 * kSampleLeast; tokens *= 2) {
     const int64_t shares = ceil_div(d.vocab, tokens);
-    const double us = (0.36 * (tokens / 1024) + 0.3) * (double)ceil_div(d.batch * shares, kCus) + 0.35 * (double)shares;
+    const double us = (0.36 * std::min(tokens, d.vocab) / 1024 + 0.3) * (double)ceil_div(d.batch * shares, kCus) +
+                      (shares > 1 ? 2.7 + 0.35 * (double)shares : 0.0);
     if (shares <= kSampleShares && (least == 0.0 || us < least)) {
       least = us;
       s.share_tokens = tokens;
