@@ -227,7 +227,9 @@ spear_status_t spear_kv_plan_workspace_bytes(const spear_kv_plan_desc_t* desc, s
  *     tokens, or with a value below zero gets nothing and keeps what it has, and
  *     the others are served as if it were not there.
  * Outputs, n being the new tokens that a sequence is given:
- *   cu_q      int32 [batch + 1], the running sum of n from 0.
+ *   cu_q      int32 [batch + 1], the running sum of n from 0: sequence b has rows
+ *             cu_q[b] .. cu_q[b + 1] - 1, and none where n = 0 (cu_q[b + 1] - 1 is
+ *             then a row of a sequence before it).
  *   kv_lens   int32 [batch], lens + n.
  *   slots     int64 [rows], positions and sequence int32 [rows]: slot in the
  *             cache, position and sequence of each new token; rows at and past
@@ -349,7 +351,8 @@ spear_status_t spear_sample_workspace_bytes(const spear_sample_desc_t* desc, siz
  *   logits   fp16 or fp32 [num_rows][V], the last dimension contiguous, row stride
  *            in elements.
  *   rows     int32 [batch]: the row of each draw, or NULL: draw b takes row b (batch
- *            at most num_rows); one outside the logits has no token.
+ *            at most num_rows); one outside the logits has no token, which is what a
+ *            sequence needs that a plan gave no rows.
  *   noise    fp32 [batch][V] drawn from Exp(1), contiguous; may be NULL where no
  *            tokens are asked for or the settings leave one token to every row.
  *   temperature, top_p, min_p  fp32 [batch], top_k int32 [batch], each NULL for the

@@ -3,8 +3,10 @@ host (no GPU): argument checks in the order in which they are documented, worksp
 sizes.  No call reaches a kernel."""
 import ctypes
 import os
+import re
 
 import pytest
+import torch
 
 from w4_gemm_gated_amd import _binding
 from w4_gemm_gated_amd._binding import AdapterDesc, KvPlanDesc, SampleDesc
@@ -198,3 +200,24 @@ def test_sample_workspaces_stay_bounded(lib):
         for batch in (1, 7, 64, 1000):
             st, need = size_of(f, SampleDesc(batch, V, 1, 1, 1.0, 0, 1.0, 0.0))
             assert st == OK and HEADER < need <= most, (batch, V)
+
+
+def documented_rows(text):
+    """The expression that a document's usage gives spear_sample for its rows: the argument
+    itself, or what the variable of that name is set to."""
+    call = re.search(r"sp\.spear_sample\((.*?)\n```", text, re.S).group(1)
+    given = re.search(r"\brows=(.*?), \w+=", re.sub(r" #.*", "", call)).group(1)
+    found = re.search(r"^%s = (.*?)(?: +#.*)?$" % re.escape(given), text, re.M)
+    return found.group(1) if found else given
+
+
+def test_documented_rows_leave_out_sequences_without_tokens(repo_root):
+    """Sequences that a plan gives nothing (they wait, have ended, or found no pages) own no
+    row of the logits: the usage shown maps them outside, not to a neighbour's row."""
+    with open(os.path.join(repo_root, "README.md")) as f:
+        rows = documented_rows(f.read())
+    for n in ([1, 0, 2], [0, 0, 1, 1, 0], [0], [3, 4, 5], [2, 0, 0]):
+        cu_q = torch.tensor([0] + n, dtype=torch.int32).cumsum(0, dtype=torch.int32)
+        got = eval(rows, {"torch": torch, "cu_q": cu_q})
+        assert got.dtype == torch.int32
+        assert got.tolist() == [sum(n[:b + 1]) - 1 if n[b] else -1 for b in range(len(n))]

@@ -202,7 +202,8 @@ def spear_sample(logits, noise=None, temperature=1.0, top_k=0, top_p=1.0, min_p=
     logits, and the distribution that it is drawn from.
 
     logits fp16 or fp32 [R, V] (last dimension contiguous); rows int32 [B]: the row of
-    each draw, or None: all in order; noise fp32 [B, V] from Exp(1): None if no tokens
+    each draw, or None: all in order (outside [0, R): token -1 and no distribution, for
+    sequences that a plan gave no rows); noise fp32 [B, V] from Exp(1): None if no tokens
     are wanted (tokens is then None, unless the settings below, given as numbers,
     leave a single token).  Settings are numbers, or a tensor [B] with one for each
     draw: temperature (0: the largest logit's token), top_k (int32; 0: off), top_p
