@@ -147,6 +147,20 @@ def test_tokens_too_light_to_count(V):
         check(l, rng.exponential(size=l.shape).astype(np.float32), rules)
 
 
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+def test_many_light_tokens_count_in_the_sum(dtype):
+    """One heavy token, and more equal light ones than any list holds, cut by top-k: each is
+    next to nothing, all of them a millionth or more of what is kept."""
+    note(f"many light tokens {np.dtype(dtype).name}")
+    V = 1 << 22
+    rng = np.random.default_rng(11)
+    l = np.full((3, V), -27.0378, dtype)          # weights of 1.99 2^-40, then of 2^-41, then of both
+    l[1] = -28.4
+    l[2, ::2] = -28.4
+    l[:, 12345] = 0
+    check(l, rng.exponential(size=l.shape).astype(np.float32), [(1.0, V - 1, 1.0, 0.0)] * 3)
+
+
 def test_flat_rows():
     """Distinct logits in a few bins: a selection over the row, step by step."""
     note("flat rows")

@@ -890,18 +890,27 @@ __device__ Cut cut_selected(const SampleArgs& a, const RowInfo& o, const void* r
       target *= o.before_k + ldexp((double)part, -kFixBits) * edge_of(s.steps, o.bin_k);
     }
   }
+  // The mass of what is kept.  A list has no order, so its terms are whole numbers, whose sum has
+  // none either (4094 of them lose 2^-28 of the row's largest at most).  Of a row every thread
+  // adds the same tokens in the same order, and their parts below 2^-40 count: a long row's
+  // light tokens, cut off there, are missed by all that they hold together (4 million of
+  // 1.99 2^-40 each: 2^-18).
+  const bool whole = listed <= kSampleList;
+  double sum = 0.0;
   each<F16>(a, row, list, listed, [&](u64 k) {
     const float l = logit_of(k);
     if (k >= c.end && !(l >= o.to) && l >= o.least) {
       const float w = weight_of(o, l);
       const int j = (int)~(uint32_t)k;
-      c.sum += (u64)((double)w * 0x1p40);     // (a sum in fixed point has no order, as the list has none)
+      const double term = (double)w * 0x1p40;
+      sum += whole ? floor(term) : term;
       if (a.noise) {
         const u64 v = race_key(w, a.noise[(int64_t)b * a.vocab + j], j);
         c.best = c.best > v ? c.best : v;
       }
     }
   });
+  c.sum = (u64)sum;
   return c;
 }
 
