@@ -161,6 +161,37 @@ def test_many_light_tokens_count_in_the_sum(dtype):
     check(l, rng.exponential(size=l.shape).astype(np.float32), [(1.0, V - 1, 1.0, 0.0)] * 3)
 
 
+@pytest.mark.parametrize("light", [-12.3, -17.1, -20.4, -22.9])
+@pytest.mark.parametrize("V", [3000, 131072])
+def test_top_p_among_light_tokens_below_a_heavy_one(V, light):
+    """Top-k ends among equal light tokens, top-p before or within them: its cut is looked
+    for from the heavy token's bin on, and the light ones enter the sums whole.
+
+    The sum before the cut may be off by 2^-31 of its mass, which is 2^-31 of the heavy
+    token (its own weight enters to 2^-33): that is one token's weight or less down to a
+    logit of -21.5, and four tokens' at -22.9, so the count lies between the oracle's for
+    masses 2^-31 below and above.  Given the count, the light tokens kept are the first
+    ones and the probabilities follow, as near as the others' are.
+    """
+    note(f"top-p among light tokens, V {V} logit {light}")
+    rng = np.random.default_rng(12)
+    w = np.exp(np.float64(np.float32(light)))
+    rules = []
+    for part in (0.1, 0.35, 0.6, 0.85):
+        p = np.float32((1 + part * (V - 2) * w) / (1 + (V - 2) * w))       # (V - 2 light tokens are left by top-k)
+        rules.append((1.0, V - 1, p, 0.0))
+    l = np.full((len(rules), V), light, np.float32)
+    l[:, 7] = 0
+    noise = rng.exponential(size=l.shape).astype(np.float32)
+    tokens, probs = sp.spear_sample(dev(l), dev(noise), probs=True, **settings(rules))
+    tokens, probs = tokens.cpu().numpy(), probs.cpu().numpy()
+    for b, rule in enumerate(rules):
+        least, most = (len(ref.kept_tokens(l[b], *rule, nudge=x)[0]) for x in (-2.0 ** -31, 2.0 ** -31))
+        kept = int((probs[b] > 0).sum())
+        assert least <= kept <= most, (b, rule, kept, least, most)
+        check_row(b, l[b], noise[b], (1.0, kept, 1.0, 0.0), int(tokens[b]), probs[b])
+
+
 def test_flat_rows():
     """Distinct logits in a few bins: a selection over the row, step by step."""
     note("flat rows")

@@ -79,6 +79,7 @@ struct RowInfo {
   double before, before_k;   // mass before bin `first`, and before bin_k
   double target;             // top-p's mass if that is known; else (with top-k) p
   double edge;               // weight at the upper edge of bin `first`
+  double fine;               // a selection by mass counts in units of 2^-kFixBits / fine of that edge
   u64 end;                   // from the row's end: key of the last token kept (0: all)
   double inv;                // 1 / mass of what is kept, in units of the largest weight
   int32_t first, last;       // tokens of bins before `first` are kept, those of bins past `last` are not ..
@@ -131,10 +132,10 @@ __device__ __forceinline__ double distance(double in) {
   return __builtin_fma(u, (double)(1ull << kDefBits), -(double)(h * (float)(1ull << kDefBits)));
 }
 // A weight in units of the upper edge of bin `bin`, its own or one above it, in fixed point.
-__device__ __forceinline__ u64 fixed_below(const RowInfo& o, const double* steps, float l, int bin) {
+__device__ __forceinline__ u64 fixed_below(const RowInfo& o, const double* steps, float l, int bin, double fine = 1.0) {
   const double t = t_of(l, o.scale), f = floor(t);
   const double w = (double)(1ull << kFixBits) - distance(t - f) * (double)(1 << (kFixBits - kDefBits));
-  return (u64)(w * edge_of(steps, min((int)(o.q - f) - bin, kBins - 1)));
+  return (u64)(w * edge_of(steps, min((int)(o.q - f) - bin, kBins - 1)) * fine);
 }
 // The weight relative to the row's largest, as fp32: the exponent's whole part apart, so
 // that the rest is exact to a few 2^-24.  (The difference of the logits first: that of
@@ -324,7 +325,7 @@ __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rule
   o.q = best ? floor(t_of(largest, scale)) : 0.0;
   o.largest = best ? finite(largest) : 0.0;
   o.before = o.before_k = o.target = 0.0;
-  o.edge = o.inv = 1.0;
+  o.edge = o.fine = o.inv = 1.0;
   o.end = 0;
   o.first = kBins;
   o.last = o.bin_k = -1;
@@ -419,6 +420,12 @@ __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rule
       }
       last = min(last, lo);
       o.target = by_k ? (double)r.p : (double)r.p * total;
+      // A selection adds the masses of bins `first` to `last`: below 2^62 of its units, which are
+      // no coarser than that asks for.  (With a top-k that cuts far below, light tokens by the
+      // thousand follow a heavy one: each of them may be a few 2^-40 of its bin's edge.)
+      const double most = (mass_up_to(last) * (1.0 + kNear) - mass_up_to(first - 1)) / edge_of(s.steps, first);
+      const int power = (int)(__double_as_longlong(fmax(most, 1.0)) >> 52) - 1023;
+      o.fine = (double)(1 << max(20 - power, 0));
     }
     o.by_k = by_k;
     o.by_p = r.p < 1.0f;
@@ -654,8 +661,7 @@ __device__ __forceinline__ int place_in_wave(u64 key, int n) {
 __device__ __forceinline__ uint32_t push(uint32_t v, int to) { return (uint32_t)__builtin_amdgcn_ds_permute(4 * to, (int)v); }
 __device__ __forceinline__ u64 push(u64 v, int to) { return (u64)push((uint32_t)(v >> 32), to) << 32 | push((uint32_t)v, to); }
 // Of the tokens of bins `first` to `last`, in falling order: the key of the one at which
-// the count reaches `count`, or the mass (in units of the upper edge, fixed point)
-// `mass`; the last one if it never does.  Each step splits the tokens that are
+// the count reaches `count`, or the mass (in the row's units, fixed point) `mass`; the last one if it never does.  Each step splits the tokens that are
 // left by the ten bits below those that they all share.
 template <bool F16>
 __device__ u64 select(const SampleArgs& a, const RowInfo& o, const void* row, const u64* list, uint32_t listed,
@@ -698,7 +704,7 @@ __device__ u64 select(const SampleArgs& a, const RowInfo& o, const void* row, co
       if (here(k)) {
         const int sub = kSubs - 1 - (int)((k >> shift) & (kSubs - 1));     // the largest first
         atomicAdd(&s.counts[sub], 1u);
-        if (!by_count) atomicAdd(&s.sums[sub], fixed_below(o, s.steps, logit_of(k), first));
+        if (!by_count) atomicAdd(&s.sums[sub], fixed_below(o, s.steps, logit_of(k), first, o.fine));
       }
     });
     __syncthreads();
@@ -754,7 +760,7 @@ __device__ u64 select(const SampleArgs& a, const RowInfo& o, const void* row, co
       const int lane = tid % kWave, n = (int)s.found_count;
       u64 key = lane < n ? s.sorted_key[lane] : 0;
       key = push(key, place_in_wave(key, n));
-      u64 before = lane < n && !by_count ? fixed_below(o, s.steps, logit_of(key), first) : 0;
+      u64 before = lane < n && !by_count ? fixed_below(o, s.steps, logit_of(key), first, o.fine) : 0;
       const u64 own = before;
       before = wave_run(before) - own;
       const bool in = lane < n && (by_count ? (uint32_t)lane < count : before < mass);
@@ -876,7 +882,7 @@ __device__ Cut cut_selected(const SampleArgs& a, const RowInfo& o, const void* r
     const bool by_count = rule == 0;
     if (!(by_count ? o.by_k : o.by_p)) continue;
     const double left = (target - o.before) / o.edge;     // top-p's mass in units of the bins' upper edge
-    const u64 mass = left > 0.0 ? (u64)fmin(ceil(left * (double)(1ull << kFixBits)), 0x1p62) : 1;
+    const u64 mass = left > 0.0 ? (u64)fmin(ceil(left * ((double)(1ull << kFixBits) * o.fine)), 0x1p62) : 1;
     const u64 end = select<F16>(a, o, row, list, listed, s, by_count ? o.bin_k : o.first, by_count ? o.bin_k : o.last,
                                 by_count, (uint32_t)o.left_k, mass);
     c.end = c.end > end ? c.end : end;
