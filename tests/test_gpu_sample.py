@@ -13,12 +13,16 @@ Tokens: the scores' weights are as near (2^-22 with the division), so the oracle
 score of the drawn token is within 2^-21 of its largest; it is the oracle's token
 where no other is that near.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 from oracle import spear_step as ref
 import w4_gemm_gated_amd as sp
+from w4_gemm_gated_amd import _binding
+from w4_gemm_gated_amd._binding import SampleDesc
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
@@ -357,6 +361,26 @@ def test_counters_repeats_and_streams():
         got = sp.spear_sample(l, noise, probs=True, **s)
     stream.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("B,V", [(40, 1000), (300, 4096), (300, 4097), (20, 16385), (4100, 50)])
+def test_a_workspace_of_just_the_bytes_asked_for(B, V):
+    """What stays within a workgroup has no place in the workspace: a call works in the
+    bytes that it asks for, and leaves what lies behind them."""
+    note(f"workspace of {B} draws of {V}")
+    rng = np.random.default_rng(V)
+    l, noise = dev(logits(rng, B, V)), dev(rng.exponential(size=(B, V)).astype(np.float32))
+    s = settings([RULES[b % len(RULES)] for b in range(B)])
+    want = sp.spear_sample(l, noise, probs=True, **s)
+    need = ctypes.c_size_t(0)
+    d = SampleDesc(B, V, B, 0, 0.0, 0, 0.0, 0.0)
+    assert _binding.load().spear_sample_workspace_bytes(ctypes.byref(d), ctypes.byref(need)) == 0
+    ws = torch.full((need.value + (4 << 20),), 77, dtype=torch.uint8, device=DEV)
+    ws[:need.value] = 0
+    got = sp.spear_sample(l, noise, probs=True, workspace=ws[:need.value], **s)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert bool((ws[need.value:] == 77).all()) and not ws[:1 << 20].any()
 
 
 def test_graph_replays():

@@ -202,6 +202,20 @@ def test_sample_workspaces_stay_bounded(lib):
             assert st == OK and HEADER < need <= most, (batch, V)
 
 
+def test_sample_workspaces_hold_only_what_leaves_a_workgroup(lib):
+    """A row of one share (up to 16384 tokens) has its bins in LDS, one of one part (up to
+    4096) its list too: neither has a place in the workspace.  The groups of rows that go
+    together bound the rest: 4096 shares' bins, and a list of 48 KiB a row."""
+    f = lib.spear_sample_workspace_bytes
+    size = lambda batch, V: size_of(f, SampleDesc(batch, V, batch, 0, 1.0, 0, 1.0, 0.0))[1] - HEADER  # noqa: E731
+    for V in (1, 40, 1000, 4096):
+        assert size(1000, V) <= 1000 * 512 and size(1 << 20, V) <= 4096 * 512
+    for V in (4097, 8000):                                      # (1000 rows of these go as single shares)
+        assert 1000 * (48 << 10) < size(1000, V) < 1000 * (49 << 10)
+    for V in (32000, 128001, 1 << 22):
+        assert size(1 << 20, V) < 4096 * ((32 << 10) + (48 << 10) + 1024) + (1 << 20)
+
+
 def documented_rows(text):
     """The expression that a document's usage gives spear_sample for its rows: the argument
     itself, or what the variable of that name is set to."""

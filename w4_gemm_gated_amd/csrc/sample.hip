@@ -1190,7 +1190,9 @@ hipError_t launch_share(const SampleArgs& a, hipStream_t s) {
 // do (0.36 us per 1024 tokens and 0.3 per workgroup), and the workgroup that sums a row's
 // bins 0.35 us per share (shares of 4096 and 8192: 2 x 32000 tokens 17.6 and 18.3 us,
 // 144 x 32000 41.5 and 39.8).  A row of one share saves that launch (16 x 1000 tokens 17.3
-// and 14.8 us, 16 x 8000 17.6 and 16.3, 16 x 16000 17.8 in four shares and 18.4 in one).  Rows of one group: shares whose bins take no more than 128 MiB.
+// and 14.8 us, 16 x 8000 17.6 and 16.3, 16 x 16000 17.8 in four shares and 18.4 in one).  Rows of one group: up to 4096 shares, whose bins take 128 MiB;
+// their lists take 48 KiB a row.  What stays in LDS (the bins of rows of one share, the lists
+// of rows of one part) has no place in the workspace.
 SampleShape sample_shape(const spear_sample_desc_t& d) {
   SampleShape s;
   constexpr int kCus = 256;
@@ -1210,17 +1212,18 @@ SampleShape sample_shape(const spear_sample_desc_t& d) {
   const size_t shares = (size_t)s.group * s.shares;
   s.info = at;
   at += (size_t)s.group * kSampleInfoBytes;
-  s.share = at;
-  at += shares * sizeof(ShareInfo);
   s.parts = (int)ceil_div(d.vocab, kSampleLeast);
+  const size_t listed = s.parts > 1 ? (size_t)s.group : 0, binned = s.shares > 1 ? shares : 0;      // rows, shares
+  s.share = at;
+  at += binned * sizeof(ShareInfo);
   s.part = at;
-  at += (size_t)s.group * s.parts * sizeof(PartInfo);
+  at += listed * s.parts * sizeof(PartInfo);
   s.list = at;
-  at += (size_t)s.group * kSampleList * 8;
+  at += listed * kSampleList * 8;
   s.hist = at;
-  at += shares * kBins * 8;
+  at += binned * kBins * 8;
   s.list_noise = at;
-  at += (size_t)s.group * kSampleList * 4;
+  at += listed * kSampleList * 4;
   s.bytes = at;
   return s;
 }

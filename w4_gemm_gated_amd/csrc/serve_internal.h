@@ -223,8 +223,8 @@ struct SampleArgs {
   int32_t* tokens;
   float* probs;
   void* info;
-  ShareInfo* share;                     // [batch][shares]
-  PartInfo* part;                       // [batch][parts]
+  ShareInfo* share;                     // [batch][shares], as hist where there are several
+  PartInfo* part;                       // [batch][parts], as list and list_noise where there are several
   unsigned long long *list, *hist;      // [batch][kSampleList], [batch][shares][bins]
   float* list_noise;                    // [batch][kSampleList]
 };
