@@ -21,7 +21,7 @@ import torch
 
 from oracle import spear_step as ref
 import w4_gemm_gated_amd as sp
-from w4_gemm_gated_amd import _binding
+from w4_gemm_gated_amd import _binding, serve
 from w4_gemm_gated_amd._binding import SampleDesc
 
 pytestmark = [pytest.mark.gpu,
@@ -286,6 +286,25 @@ def test_numbers_for_all_and_greedy_without_noise():
         assert torch.equal(tokens, first) and torch.equal(probs.argmax(1).int(), first)
         assert torch.equal(probs.sum(1), torch.ones(9, device=DEV))
     assert sp.spear_sample(dev(l), top_k=2**32 + 1, probs=True)[0] is None
+
+
+def test_numbers_that_change_from_call_to_call():
+    """What is kept for a call's sizes does not grow with its settings (NaN, which equals
+    nothing, among them), and each call goes by its own."""
+    note("settings that change")
+    rng = np.random.default_rng(13)
+    l = logits(rng, 5, 777)
+    noise = rng.exponential(size=l.shape).astype(np.float32)
+    d, n = dev(l), dev(noise)
+    sp.spear_sample(d, n)
+    kept = len(serve._plans)
+    calls = [dict(temperature=0.5 + i / 16, top_k=3 + i, top_p=0.5 + i / 64, min_p=i / 256) for i in range(20)]
+    for rule in calls + calls[::-1] + [dict(temperature=float("nan"))] * 2 + [dict(top_p=float("nan"))]:
+        got = sp.spear_sample(d, n, probs=True, **rule)
+        full = (rule.get("temperature", 1.0), rule.get("top_k", 0), rule.get("top_p", 1.0), rule.get("min_p", 0.0))
+        want = sp.spear_sample(d, n, probs=True, **settings([full] * 5))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert len(serve._plans) == kept
 
 
 def test_rows_and_strides():

@@ -196,6 +196,19 @@ def _setting(x, name, dtype, batch, device):
     return x.data_ptr(), 0
 
 
+# The last call's descriptor (never written to again): what a call needs beside it follows
+# from its sizes alone, and settings may change from one to the next.
+_last = ((), None)
+
+
+def _with_settings(fields):
+    global _last
+    last = _last
+    if last[0] != fields:
+        _last = last = (fields, ctypes.byref(SampleDesc(*fields)))
+    return last[1]
+
+
 def spear_sample(logits, noise=None, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, rows=None, probs=False,
                  tokens=None, workspace=None):
     """(tokens int32 [B], probs fp32 [B, V]): one token drawn for each row of the
@@ -240,10 +253,10 @@ def spear_sample(logits, noise=None, temperature=1.0, top_k=0, top_p=1.0, min_p=
     else:
         probs = None
     lib, stream = _binding.load(), _stream(dev)
-    d = _plan(("sample", B, V, R, dt, t, k, p, m), lambda: (
-        SampleDesc(B, V, R, _LOGITS[dt], t, k, p, m), lib.spear_sample_workspace_bytes, "spear_sample"))
+    d = _plan(("sample", B, V, R, dt), lambda: (
+        SampleDesc(B, V, R, _LOGITS[dt], 0.0, 0, 0.0, 0.0), lib.spear_sample_workspace_bytes, "spear_sample"))
     ws = _space(workspace, d[2], dev, stream)
-    st = lib.spear_sample(d[1], logits.data_ptr(), V if R == 1 else logits.stride(0), _p(rows), _p(noise), t_at, k_at,
+    st = lib.spear_sample(_with_settings((B, V, R, _LOGITS[dt], t, k, p, m)), logits.data_ptr(), V if R == 1 else logits.stride(0), _p(rows), _p(noise), t_at, k_at,
                           p_at, m_at, _p(tokens), _p(probs), *ws, stream)
     _binding.check(st, "spear_sample")
     return tokens, probs
