@@ -189,6 +189,31 @@ def test_rows_that_fall_to_one_adapter(rank, K, N):
         compare(got.cpu().numpy(), want, slack, Y, cu, of, adapters)
 
 
+@pytest.mark.parametrize("rank", [16, 72, 136])
+def test_more_tiles_than_there_are_counters(rank):
+    """Nearly as many adapters as a plan holds, so that there can be more tiles than the
+    workspace has counters.  Past rank 64 all of K and all ranks are then one workgroup's, 64
+    ranks at a time; up to it one launch does both products.  Most tiles are of one or two
+    rows, some of 16 and more and one of 64."""
+    note(f"many tiles, rank {rank}")
+    rng = np.random.default_rng(rank)
+    adapters = 4096
+    of = np.concatenate([rng.permutation(adapters), np.repeat([5, 9, 4001], [103, 16, 15]), [-1, adapters],
+                         rng.integers(0, adapters, 764)]).astype(np.int32)
+    rows = len(of)
+    cu = np.arange(rows + 1, dtype=np.int32)
+    for K, N in ((64, 72), (1096, 17)):
+        if K > 64 and rank > 72:
+            continue
+        X, A, B, Y = tensors(rng, rows, K, N, rank, adapters)
+        scale = rng.normal(size=adapters).astype(np.float32)
+        plan = sp.spear_adapter_plan(dev(cu), dev(of), adapters, rows)
+        got = sp.spear_adapter_add(dev(Y), dev(X), dev(A), dev(B), plan, dev(scale))
+        torch.cuda.synchronize()
+        want, slack = ref.adapter_add(Y, X, A, B, cu, of, scale)
+        compare(got.cpu().numpy(), want, slack, Y, cu, of, adapters)
+
+
 def test_a_row_does_not_depend_on_its_batch():
     """The same row alone, among others of its adapter, and among other adapters'
     (where K is cut alike)."""
