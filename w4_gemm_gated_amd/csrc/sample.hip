@@ -79,7 +79,6 @@ struct RowInfo {
   double before, before_k;   // mass before bin `first`, and before bin_k
   double target;             // top-p's mass if that is known; else (with top-k) p
   double edge;               // weight at the upper edge of bin `first`
-  double fine;               // a selection by mass counts in units of 2^-kFixBits / fine of that edge
   u64 end;                   // from the row's end: key of the last token kept (0: all)
   double inv;                // 1 / mass of what is kept, in units of the largest weight
   int32_t first, last;       // tokens of bins before `first` are kept, those of bins past `last` are not ..
@@ -92,6 +91,7 @@ struct RowInfo {
   int32_t left_k;            // tokens that top-k keeps of its bin
   int32_t by_k, by_p;        // which rules cut
   uint32_t listed;           // tokens in the list
+  int32_t finer;             // a selection by mass counts in units of 2^-(kFixBits + finer) of `edge`
 };
 
 __device__ __forceinline__ uint32_t rising(float l) {     // rises with l; -0 as +0
@@ -325,7 +325,7 @@ __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rule
   o.q = best ? floor(t_of(largest, scale)) : 0.0;
   o.largest = best ? finite(largest) : 0.0;
   o.before = o.before_k = o.target = 0.0;
-  o.edge = o.fine = o.inv = 1.0;
+  o.edge = o.inv = 1.0;
   o.end = 0;
   o.first = kBins;
   o.last = o.bin_k = -1;
@@ -333,6 +333,7 @@ __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rule
   o.token = best ? (int)~(uint32_t)best : -1;
   o.left_k = o.by_k = o.by_p = 0;
   o.listed = 0;
+  o.finer = 0;
   if (o.kind != kRace) {
     if (tid == 0) {
       if (a.tokens) a.tokens[b] = o.token;
@@ -420,12 +421,6 @@ __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rule
       }
       last = min(last, lo);
       o.target = by_k ? (double)r.p : (double)r.p * total;
-      // A selection adds the masses of bins `first` to `last`: below 2^62 of its units, which are
-      // no coarser than that asks for.  (With a top-k that cuts far below, light tokens by the
-      // thousand follow a heavy one: each of them may be a few 2^-40 of its bin's edge.)
-      const double most = (mass_up_to(last) * (1.0 + kNear) - mass_up_to(first - 1)) / edge_of(s.steps, first);
-      const int power = (int)(__double_as_longlong(fmax(most, 1.0)) >> 52) - 1023;
-      o.fine = (double)(1 << max(20 - power, 0));
     }
     o.by_k = by_k;
     o.by_p = r.p < 1.0f;
@@ -433,6 +428,14 @@ __device__ __forceinline__ void find_cuts(const SampleArgs& a, int b, const Rule
       o.first = first;
       o.last = last;
       o.edge = edge_of(s.steps, first);
+      // A selection adds the masses of bins `first` to `last`, and where these are several in
+      // units no coarser than keep the sum below 2^62.  (With a top-k that cuts far below, light
+      // tokens by the thousand may follow a heavy one, each a few 2^-40 of its bin's edge.)
+      if (first < last) {
+        const double most = fmax(mass_up_to(last) * (1.0 + kNear) - mass_up_to(first - 1), o.edge);
+        const int power = (int)((__double_as_longlong(most) >> 52) - (__double_as_longlong(o.edge) >> 52));
+        o.finer = max(20 - power, 0);
+      }
       if (by_k) o.bin_k = bin_k;
     }
   }
@@ -665,7 +668,7 @@ __device__ __forceinline__ u64 push(u64 v, int to) { return (u64)push((uint32_t)
 // left by the ten bits below those that they all share.
 template <bool F16>
 __device__ u64 select(const SampleArgs& a, const RowInfo& o, const void* row, const u64* list, uint32_t listed,
-                      Scratch& s, int first, int last, bool by_count, uint32_t count, u64 mass) {
+                      Scratch& s, int first, int last, bool by_count, uint32_t count, u64 mass, double fine) {
   const int tid = threadIdx.x;
   u64 mask = 0, value = 0;      // tokens left: key & mask == value
   // The bins as logits.  (Top-k's is one of several that top-p's cut may lie in, or past them.)
@@ -704,7 +707,7 @@ __device__ u64 select(const SampleArgs& a, const RowInfo& o, const void* row, co
       if (here(k)) {
         const int sub = kSubs - 1 - (int)((k >> shift) & (kSubs - 1));     // the largest first
         atomicAdd(&s.counts[sub], 1u);
-        if (!by_count) atomicAdd(&s.sums[sub], fixed_below(o, s.steps, logit_of(k), first, o.fine));
+        if (!by_count) atomicAdd(&s.sums[sub], fixed_below(o, s.steps, logit_of(k), first, fine));
       }
     });
     __syncthreads();
@@ -760,7 +763,7 @@ __device__ u64 select(const SampleArgs& a, const RowInfo& o, const void* row, co
       const int lane = tid % kWave, n = (int)s.found_count;
       u64 key = lane < n ? s.sorted_key[lane] : 0;
       key = push(key, place_in_wave(key, n));
-      u64 before = lane < n && !by_count ? fixed_below(o, s.steps, logit_of(key), first, o.fine) : 0;
+      u64 before = lane < n && !by_count ? fixed_below(o, s.steps, logit_of(key), first, fine) : 0;
       const u64 own = before;
       before = wave_run(before) - own;
       const bool in = lane < n && (by_count ? (uint32_t)lane < count : before < mass);
@@ -876,15 +879,16 @@ template <bool F16>
 __device__ Cut cut_selected(const SampleArgs& a, const RowInfo& o, const void* row, int b, const u64* list,
                             uint32_t listed, Scratch& s) {
   Cut c = {0, 0, 0};
+  const double fine = (double)(1 << o.finer);
   double target = o.target;
 #pragma unroll 1
   for (int rule = 0; rule < 2; ++rule) {       // top-k, then top-p
     const bool by_count = rule == 0;
     if (!(by_count ? o.by_k : o.by_p)) continue;
     const double left = (target - o.before) / o.edge;     // top-p's mass in units of the bins' upper edge
-    const u64 mass = left > 0.0 ? (u64)fmin(ceil(left * ((double)(1ull << kFixBits) * o.fine)), 0x1p62) : 1;
+    const u64 mass = left > 0.0 ? (u64)fmin(ceil(left * ((double)(1ull << kFixBits) * fine)), 0x1p62) : 1;
     const u64 end = select<F16>(a, o, row, list, listed, s, by_count ? o.bin_k : o.first, by_count ? o.bin_k : o.last,
-                                by_count, (uint32_t)o.left_k, mass);
+                                by_count, (uint32_t)o.left_k, mass, fine);
     c.end = c.end > end ? c.end : end;
     if (by_count && o.by_p) {
       // What top-k left of its bin, and with it top-p's mass.
