@@ -347,7 +347,8 @@ spear_status_t spear_sample_workspace_bytes(const spear_sample_desc_t* desc, siz
  *            left, the largest w(j) / noise[b][j] (fp32, ties to the lowest j); the
  *            first token where it is left alone; -1 for a row that has none.
  *   probs    fp32 [batch][V], contiguous, or NULL: w(j) / (sum of those left), 0 for
- *            the others (spear_verify_draft's target and draft rows).
+ *            the others (spear_verify_draft's target and draft rows).  Must not overlap
+ *            the logits.
  *   logits   fp16 or fp32 [num_rows][V], the last dimension contiguous, row stride
  *            in elements.
  *   rows     int32 [batch]: the row of each draw, or NULL: draw b takes row b (batch
@@ -358,8 +359,9 @@ spear_status_t spear_sample_workspace_bytes(const spear_sample_desc_t* desc, siz
  *   temperature, top_p, min_p  fp32 [batch], top_k int32 [batch], each NULL for the
  *            descriptor's value.
  * Which tokens are left is decided in 64 bits (weights enter the sums to 2^-33 of
- * themselves); the weights of the race and of the probabilities are fp32.  The result
- * does not depend on scheduling.
+ * themselves while |l| / temperature is below 2^20, and to 2^-53 |l| / temperature past
+ * it); the weights of the race and of the probabilities are fp32 and follow from the
+ * logits' differences.  The result does not depend on scheduling.
  * Errors: NULL_POINTER, INVALID_SHAPE, INVALID_ARGUMENT, UNSUPPORTED,
  *         MISALIGNED, WORKSPACE_TOO_SMALL, HIP.
  */

@@ -250,6 +250,18 @@ def test_extreme_settings(V, dtype):
         check(l, noise, rules)
 
 
+@pytest.mark.parametrize("offset", [-3e4, 1000.0, 65000.0])
+def test_logits_far_from_zero(offset):
+    """Rows whose logits share a large offset: their place on the bins' grid is a product
+    rounded to 64 bits, 2^-53 |l| / temperature of a weight, which 2^-33 of itself holds up
+    to a quotient of 2^20.  (Steps of fp32 there: 2^-8; of the weights at 0.07: 5 %.)"""
+    note(f"offset {offset}")
+    rng = np.random.default_rng(14)
+    rules = [(0.07, 0, 0.9, 0.0), (0.07, 40, 0.6, 0.0), (0.5, 3000, 0.95, 0.01), (1.0, 0, 0.3, 0.0), (2.0, 7000, 0.999, 0.0)]
+    l = (logits(rng, len(rules), 9001, np.float32) + np.float32(offset)).astype(np.float32)
+    check(l, rng.exponential(size=l.shape).astype(np.float32), rules)
+
+
 def test_noise_values():
     """Zero noise wins, infinite noise loses to any other, NaN takes no part; ties go to
     the lowest index."""

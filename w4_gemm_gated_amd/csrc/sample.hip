@@ -30,7 +30,8 @@
 //
 // The sums decide which token is the last one, and in a flat distribution that token
 // has a millionth of the total: weights enter the sums to 2^-33 of themselves (five fp32
-// roundings of a term below 2^-12), and sums are held in 64 bits.
+// roundings of a term below 2^-12; past |l| / T = 2^20 the product t, rounded to 64 bits, is
+// off by more), and sums are held in 64 bits.
 //
 // What a call takes (replayed from a graph): 2 x 32000 tokens 18 us, a chain of four
 // launches of 3 to 5 us, whatever they do; 64 x 128001 fp16 logits under mixed rules 43:
