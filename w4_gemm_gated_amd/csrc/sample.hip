@@ -35,8 +35,8 @@
 //
 // What a call takes (replayed from a graph): 2 x 32000 tokens 18 us, a chain of four
 // launches of 3 to 5 us, whatever they do; 64 x 128001 fp16 logits under mixed rules 43:
-// 13 for the bins (some 18 vector instructions a token, and 4.5 us of launch, loads and
-// exchanges), 8 for the cuts (a row's bins are read by one CU), 13 for the race (logits
+// 13 for the bins (23 vector instructions a token for the histogram, 14 of them in 64 bits,
+// some ten for the row's largest and least, and 4.5 us of launch, loads and exchanges), 8 for the cuts (a row's bins are read by one CU), 13 for the race (logits
 // and the noise's lines at 3 TB/s), 9 for the ends; distributions of 144 x 32000 tokens
 // 40.  The launches' shapes follow from how fast one CU goes, which is
 // some 25 bytes a ns whatever the pattern.
