@@ -39,7 +39,8 @@
  * read as the last page, slots outside the cache are not written.  With offsets
  * that do not rise, a row that comes before its sequence's first is read back as
  * zeros, and an attention call so large that the rows they repeat could pass its
- * 32-bit counts computes nothing.
+ * 32-bit counts computes nothing.  A plan of adapters that was made for other sizes
+ * gives wrong rows, within the tensors.
  */
 #ifndef SPEAR_SERVE_H
 #define SPEAR_SERVE_H

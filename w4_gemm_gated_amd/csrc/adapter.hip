@@ -165,12 +165,10 @@ __device__ __forceinline__ void store_f4_dev(__amdgpu_buffer_rsrc_t r, uint32_t 
   __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), r, byte_offset, 0, kCachePolicySc1);
 }
 
-struct Tile {
-  int adapter, first, rows;
-};
+using Tile = AdapterTile;
 __device__ __forceinline__ Tile tile_of(const AdapterArgs& a, int tile) {
   const int4 q = plan_tiles(a.plan)[tile];
-  return {min(max(q.x, 0), a.adapters - 1), min(max(q.y, 0), a.rows - 1), min(max(q.z, 1), kAdapterTile)};
+  return adapter_tile(q.x, q.y, q.z, a.adapters, a.rows);
 }
 
 // Ranks [rank0, rank0 + 16 RB) of one slice of K for a tile of up to 16 SUB rows: the

@@ -164,6 +164,18 @@ hipError_t launch_adapter_plan(const AdapterPlanArgs& a, void* stream);
 int64_t adapter_most_tiles(int64_t rows, int64_t batch, int64_t adapters);
 size_t adapter_plan_size(int64_t rows, int64_t batch, int64_t adapters);
 
+// A tile: rows [first, first + rows) of the plan's list belong to `adapter`.  Within the
+// list and the adapters whatever the plan holds (one that was made for other sizes, or not
+// yet).
+struct AdapterTile {
+  int32_t adapter, first, rows;
+};
+constexpr AdapterTile adapter_tile(int32_t adapter, int32_t first, int32_t rows, int32_t adapters, int32_t all_rows) {
+  first = first < 0 ? 0 : first < all_rows ? first : all_rows - 1;
+  const int32_t most = all_rows - first < kAdapterTile ? all_rows - first : kAdapterTile;
+  return {adapter < 0 ? 0 : adapter < adapters ? adapter : adapters - 1, first, rows < 1 ? 1 : rows < most ? rows : most};
+}
+
 // Launch shape and workspace (offsets in bytes) of an adapter call.
 struct AdapterShape {
   int tiles, rank_pad, slices, slice_k, groups, chunk_columns;     // groups: of ranks
